@@ -60,6 +60,9 @@
  *                              are not valid (bf16 keeps its range, fp16
  *                              does not; the tensor-core path uses fp16 for
  *                              its 3 extra mantissa bits).
+ *       MLA_STATUS_BAD_POSITION  a rope position outside the rope table was
+ *                              met (mla_append_latent): nothing was written
+ *                              for that token.
  */
 #ifndef MLA_CHUNKED_CONTEXT_H
 #define MLA_CHUNKED_CONTEXT_H
@@ -92,7 +95,11 @@ enum {
 enum { MLA_DTYPE_F32 = 0, MLA_DTYPE_BF16 = 1, MLA_DTYPE_F16 = 2 };
 
 /* Bits of the caller's dev_status word (see the conventions above). */
-enum { MLA_STATUS_BAD_BLOCK = 1, MLA_STATUS_FP16_RANGE = 2 };
+enum {
+  MLA_STATUS_BAD_BLOCK = 1,
+  MLA_STATUS_FP16_RANGE = 2,
+  MLA_STATUS_BAD_POSITION = 4
+};
 
 /* Bits of mla_device_error_flags(). */
 enum { MLA_DEVICE_ERR_WAIT_TIMEOUT = 1 };
@@ -498,6 +505,111 @@ int mla_chunked_prefill_equal_window(
     int32_t num_blocks, const int32_t *block_table, int32_t block_table_stride,
     const void *w_kv_b, void *workspace, size_t workspace_bytes, void *out,
     float *out_lse, int32_t *dev_status, mla_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Decode: writing the paged latent cache, and attending single new tokens to
+ * it in the absorbed form (the queries are taken into the latent space, keys
+ * and values are the cache rows themselves, nothing is up-projected).  One
+ * decode step of a layer is, in order,
+ *   mla_append_latent    new rows -> cache (norm, rotation), q_pe rotated
+ *   mla_absorb_query     q -> q_latent
+ *   mla_latent_attn      q_latent x cache -> o_latent, LSE
+ *   mla_expand_output    o_latent -> O
+ * mla_append_latent also prepares a prefill: it fills the cache, and its
+ * new_latent and rotated queries are the inputs of mla_chunked_prefill.
+ *
+ * The batch is described on the device, so that a captured graph can be
+ * replayed with other lengths:
+ *   query_start_loc  device int32 [num_seqs+1], non-decreasing: sequence r's
+ *                    new tokens are rows [qsl[r], qsl[r+1]) of the token
+ *                    arrays.  Entries are clamped to [0, num_tokens]; rows
+ *                    before qsl[0] and from qsl[num_seqs] on belong to no
+ *                    sequence and what is stored for them is left as it was.
+ *   seq_lens         device int32 [num_seqs]: the sequence's tokens, its new
+ *                    ones included; <= 0: none.  New token i of n sits at
+ *                    cache position seq_lens[r] - n + i.
+ *   block_table      device int32 [num_seqs, block_table_stride].
+ * A position whose block id is outside [0, num_blocks), or whose block index
+ * is outside the block table's row, sets MLA_STATUS_BAD_BLOCK; it is not
+ * written, and is read as zeros.
+ * All four calls only enqueue kernels on `stream` and may be captured into a
+ * graph.  Two calls that may run at the same time (two streams, two graphs)
+ * need a workspace each.
+ *
+ * mla_append_latent: per new token t of sequence r at position p
+ *   row[0:L)   = kv_a[t][0:L) * norm_weight / sqrt(mean of squares + norm_eps)
+ *                (norm_weight device [L] in dtype; NULL: no norm, copied)
+ *   row[L:L+P) = rotation of kv_a[t][L:L+P) by the angles of the token's
+ *                rope position
+ *   kv_cache[block_table[r][p / bs]][p % bs] = row; new_latent[t] = row
+ *   (device [T, L+P], nullable); q_pe_out[t, h] = rotation of the rope
+ *   columns of q[t, h].
+ *   kv_a       device [T, kv_a_ld] in dtype, kv_a_ld >= L+P; any element
+ *              alignment (16-byte aligned rows move as 16-byte vectors)
+ *   positions  device int32 [T], the rope positions; NULL: the cache
+ *              positions.  One outside [0, max_positions) sets
+ *              MLA_STATUS_BAD_POSITION, and nothing is written for the token.
+ *   rope_table device float32 [max_positions, P]: cos of the P/2 angles, then
+ *              sin.  NULL: no rotation, the rope columns are copied.
+ *   interleaved  0: dimension i is rotated with i + P/2; 1: 2i with 2i+1.
+ *   q, q_pe_out  both or neither (NULL): q device [T, H, Dn+P]; row (t, h) of
+ *              the result starts at q_pe_out + (t*H + h) * q_pe_ld elements,
+ *              q_pe_ld >= P.  q_pe_out = q + Dn with q_pe_ld = Dn+P rotates in
+ *              place; q_pe_out = q_latent + L with q_pe_ld = L+P writes the
+ *              rope columns of the absorbed queries.
+ *   Arithmetic is float32, rounded once to dtype.  A token with a negative
+ *   cache position (more new tokens than seq_lens) is skipped like a row of
+ *   no sequence.  kv_cache must not overlap the inputs, new_latent not kv_a.
+ *   Errors: MLA_ERR_UNSUPPORTED for an odd P with a rope table. */
+int mla_append_latent(const mla_dims_t *d, const void *kv_a, int64_t kv_a_ld,
+                      const void *norm_weight, float norm_eps,
+                      int32_t num_tokens, int32_t num_seqs,
+                      const int32_t *query_start_loc, const int32_t *seq_lens,
+                      const int32_t *positions, const float *rope_table,
+                      int32_t max_positions, int32_t interleaved,
+                      void *kv_cache, int32_t num_blocks,
+                      const int32_t *block_table, int32_t block_table_stride,
+                      void *new_latent, const void *q, void *q_pe_out,
+                      int64_t q_pe_ld, int32_t *dev_status,
+                      mla_stream_t stream);
+
+/* mla_absorb_query: q_latent[t, h, 0:L) = sum_d q[t, h, d] w_kv_b[h*(Dn+Dv)+d]
+ *   over the Dn nope columns; with rope_columns = 1 also q_latent[t, h, L:L+P)
+ *   = q[t, h, Dn:Dn+P) (0: left as they are, for mla_append_latent to write).
+ *   q device [T, H, Dn+P], w_kv_b device [H*(Dn+Dv), L], q_latent device
+ *   [T, H, L+P], all in dtype; float32 sums, rounded once.
+ * mla_expand_output: out[t, h, v] = sum_l o_latent[t, h, l] w_kv_b[h*(Dn+Dv)
+ *   + Dn + v][l].  o_latent device [T, H, L], out device [T, H, Dv], in dtype.
+ *   Tensor-core shape: 16-byte aligned pointers, else MLA_ERR_UNSUPPORTED. */
+int mla_absorb_query(const mla_dims_t *d, const void *q, int32_t num_tokens,
+                     const void *w_kv_b, int32_t rope_columns, void *q_latent,
+                     mla_stream_t stream);
+int mla_expand_output(const mla_dims_t *d, const void *o_latent,
+                      int32_t num_tokens, const void *w_kv_b, void *out,
+                      mla_stream_t stream);
+
+/* mla_latent_attn: per new token t of sequence r and head h, over the cache
+ *   rows c_j of the sequence's positions j (causal = 1: j up to the token's
+ *   own position; causal = 0: all j < seq_lens[r])
+ *     s_j = softmax_scale * q_latent[t, h] . c_j       (L+P columns)
+ *     o_latent[t, h] = sum_j softmax(s)_j c_j[0:L),  lse[h, t] = ln sum e^s_j
+ *   q_latent device [T, H, L+P], o_latent device [T, H, L], both in dtype;
+ *   lse device float32 [H, T], nullable.  A row that sees no key gets 0 and
+ *   -inf.  Cache rows past seq_lens are never used.
+ *   workspace: device, 16-byte aligned, mla_latent_attn_workspace_bytes bytes
+ *   (partial results of key ranges: one size for the tensor-core shape,
+ *   whatever the batch; 0 bytes and NULL otherwise); nothing in it has to be
+ *   initialised, and nothing in it is kept from call to call.
+ *   Errors: MLA_ERR_UNSUPPORTED for L+P > 1024 off the tensor-core shape. */
+int mla_latent_attn_workspace_bytes(const mla_dims_t *d, int32_t num_tokens,
+                                    int32_t num_seqs, size_t *bytes);
+int mla_latent_attn(const mla_dims_t *d, int32_t causal, int32_t num_seqs,
+                    const int32_t *query_start_loc, const int32_t *seq_lens,
+                    int32_t num_tokens, const void *q_latent,
+                    const void *kv_cache, int32_t num_blocks,
+                    const int32_t *block_table, int32_t block_table_stride,
+                    void *workspace, size_t workspace_bytes, void *o_latent,
+                    float *lse, int32_t *dev_status, mla_stream_t stream);
 
 /* 1 when the current device runs the tcgen05 (sm_103a) kernels of this
  * library. */

@@ -17,7 +17,9 @@ from ._lib import (Chunk, Dims, MlaError, lib, merge_attn_states, mla_chunk_kv_d
                    mla_selftest_bounded_wait, mla_kernel_launches,
                    mla_fused_attn_workspace_bytes, mla_fused_context_attn,
                    mla_fused_attn_plan, mla_prefill_pinned_bytes, mla_profile_begin,
-                   mla_profile_end, mla_set_pipeline_overlap, MLA_STATUS_FP16_RANGE)
+                   mla_profile_end, mla_set_pipeline_overlap, MLA_STATUS_FP16_RANGE,
+                   MLA_STATUS_BAD_POSITION, mla_append_latent, mla_absorb_query,
+                   mla_expand_output, mla_latent_attn, mla_latent_attn_workspace_bytes)
 
 __all__ = ["Chunk", "Dims", "MlaError", "lib", "merge_attn_states", "mla_chunk_kv_dtype",
            "mla_chunk_workspace_bytes", "mla_device_error_flags",
@@ -30,7 +32,9 @@ __all__ = ["Chunk", "Dims", "MlaError", "lib", "merge_attn_states", "mla_chunk_k
            "mla_selftest_bounded_wait", "mla_kernel_launches", "mla_fused_attn_workspace_bytes",
            "mla_fused_context_attn", "mla_fused_attn_plan", "mla_prefill_pinned_bytes",
            "mla_profile_begin", "mla_profile_end", "mla_set_pipeline_overlap",
-           "MLA_STATUS_FP16_RANGE", "ChunkedPrefill"]
+           "MLA_STATUS_FP16_RANGE", "ChunkedPrefill", "MLA_STATUS_BAD_POSITION",
+           "mla_append_latent", "mla_absorb_query", "mla_expand_output", "mla_latent_attn",
+           "mla_latent_attn_workspace_bytes", "LatentDecode"]
 
 
 class ChunkedPrefill:
@@ -63,4 +67,43 @@ class ChunkedPrefill:
                             self.max_context_chunk, self.split_alignment, q, new_latent,
                             kv_cache, block_table, w_kv_b, self.workspace, out, out_lse,
                             dev_status, stream, pinned_scratch=self.pinned)
+        return out
+
+
+class LatentDecode:
+    """Holds the absorbed queries, latent outputs and workspace for decode
+    steps of up to max_tokens new tokens and max_seqs sequences, and runs a
+    layer's step on them: append to the cache, absorb the queries, attend,
+    expand.  The lengths are read on the device, so one captured step can be
+    replayed as they grow.  One instance serves one step at a time."""
+
+    def __init__(self, dims: Dims, max_tokens: int, max_seqs: int, device="cuda"):
+        import torch
+        self.dims, self.max_tokens, self.max_seqs = dims, int(max_tokens), int(max_seqs)
+        H, L, P = dims.num_heads, dims.kv_lora_rank, dims.qk_rope_dim
+        self.q_latent = torch.empty(self.max_tokens, H, L + P, dtype=dims.dtype, device=device)
+        self.o_latent = torch.empty(self.max_tokens, H, L, dtype=dims.dtype, device=device)
+        self.workspace = torch.empty(
+            max(16, mla_latent_attn_workspace_bytes(dims, self.max_tokens, self.max_seqs)),
+            dtype=torch.uint8, device=device)
+
+    def __call__(self, q, kv_a, query_start_loc, seq_lens, rope_table, kv_cache, block_table,
+                 w_kv_b, out, lse=None, norm_weight=None, norm_eps=1e-6, positions=None,
+                 interleaved=False, causal=True, dev_status=None, stream=None):
+        """q [T, H, Dn+P] before rotation, kv_a [T, L+P] before norm and
+        rotation; out [T, H, Dv], lse [H, T].  Rows of no sequence are left
+        out of the cache; what out holds for them is not specified."""
+        T, dims = q.shape[0], self.dims
+        if T > self.max_tokens or seq_lens.shape[0] > self.max_seqs:
+            raise ValueError(f"LatentDecode: {T} tokens of {seq_lens.shape[0]} sequences, room "
+                             f"for {self.max_tokens} of {self.max_seqs}")
+        q_lat, o_lat = self.q_latent[:T], self.o_latent[:T]
+        mla_append_latent(dims, kv_a, query_start_loc, seq_lens, rope_table, kv_cache,
+                          block_table, norm_weight, norm_eps, positions, interleaved, q=q,
+                          q_pe_out=q_lat[..., dims.kv_lora_rank:], dev_status=dev_status,
+                          stream=stream)
+        mla_absorb_query(dims, q, w_kv_b, q_lat, rope_columns=False, stream=stream)
+        mla_latent_attn(dims, causal, query_start_loc, seq_lens, q_lat, kv_cache, block_table,
+                        self.workspace, o_lat, lse, dev_status, stream)
+        mla_expand_output(dims, o_lat, w_kv_b, out, stream)
         return out

@@ -23,7 +23,7 @@ HEADER = os.path.join(HERE, "..", "include", "mla_chunked_context.h")
 MLA_OK, MLA_ERR_INVALID, MLA_ERR_TOO_SMALL, MLA_ERR_PLANNER_STUCK, MLA_ERR_CUDA, \
     MLA_ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5
 MLA_DTYPE_F32, MLA_DTYPE_BF16, MLA_DTYPE_F16 = 0, 1, 2
-MLA_STATUS_BAD_BLOCK, MLA_STATUS_FP16_RANGE = 1, 2
+MLA_STATUS_BAD_BLOCK, MLA_STATUS_FP16_RANGE, MLA_STATUS_BAD_POSITION = 1, 2, 4
 
 _ERRORS = {MLA_ERR_INVALID: "invalid argument", MLA_ERR_TOO_SMALL: "buffer too small",
            MLA_ERR_PLANNER_STUCK: "planner cannot progress (budget below one aligned split)",
@@ -38,7 +38,9 @@ EXPORTED = ("mla_plan_context_chunks", "merge_attn_states", "mla_gather_context_
             "mla_chunked_prefill_equal_window", "mla_selftest_bounded_wait",
             "mla_kernel_launches", "mla_fused_attn_workspace_bytes",
             "mla_fused_context_attn", "mla_fused_attn_plan", "mla_prefill_pinned_bytes",
-            "mla_profile_begin", "mla_profile_end", "mla_set_pipeline_overlap")
+            "mla_profile_begin", "mla_profile_end", "mla_set_pipeline_overlap",
+            "mla_append_latent", "mla_absorb_query", "mla_expand_output",
+            "mla_latent_attn_workspace_bytes", "mla_latent_attn")
 MLA_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 
@@ -113,6 +115,12 @@ def lib() -> C.CDLL:
             "mla_prefill_equal_window_workspace_bytes": [P, P, P, I32, I32, I32, P],
             "mla_chunked_prefill_equal_window": [P, P, P, I32, I32, I32, P, P, P, I32, P, I32, P,
                                                  P, SZ, P, P, P, P],
+            "mla_append_latent": [P, P, I64, P, C.c_float, I32, I32, P, P, P, P, I32, I32, P, I32,
+                                  P, I32, P, P, P, I64, P, P],
+            "mla_absorb_query": [P, P, I32, P, I32, P, P],
+            "mla_expand_output": [P, P, I32, P, P, P],
+            "mla_latent_attn_workspace_bytes": [P, I32, I32, P],
+            "mla_latent_attn": [P, I32, I32, P, P, I32, P, P, I32, P, I32, P, SZ, P, P, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -521,3 +529,134 @@ def mla_selftest_bounded_wait(limit_us: int, gave_up, stream=None) -> None:
     """Run the bounded-wait self test (gave_up: device int32 tensor)."""
     _check(lib().mla_selftest_bounded_wait(int(limit_us), _ptr(gave_up), _stream(stream)),
            "mla_selftest_bounded_wait")
+
+
+# ------------------------------------------------------------------ decode --
+def _on_device(where: str, first: torch.Tensor, *others) -> None:
+    """The C calls work on the current device: every tensor has to be there
+    (host tensors, or another GPU's, are refused before anything runs)."""
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in (first, *others):
+        if t is not None and (not t.is_cuda or t.device.index != cur):
+            raise ValueError(f"{where}: tensor on {t.device}, the current device is "
+                             f"{'none' if cur is None else f'cuda:{cur}'}")
+
+
+def _want(where: str, name: str, t: Optional[torch.Tensor], dtype, *shape) -> None:
+    """t (if given) has this dtype and shape (None: any size) and is contiguous."""
+    if t is None:
+        return
+    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        want = "x".join("*" if n is None else str(n) for n in shape)
+        raise ValueError(f"{where}: {name} has to be contiguous {want} {dtype}, got "
+                         f"{'x'.join(map(str, t.shape))} {t.dtype}")
+
+
+def _batch(where: str, query_start_loc, seq_lens, block_table) -> int:
+    R = seq_lens.shape[0]
+    _want(where, "seq_lens", seq_lens, torch.int32, None)
+    _want(where, "query_start_loc", query_start_loc, torch.int32, R + 1)
+    _want(where, "block_table", block_table, torch.int32, R, None)
+    return R
+
+
+def mla_append_latent(dims: Dims, kv_a, query_start_loc, seq_lens, rope_table, kv_cache,
+                      block_table, norm_weight=None, norm_eps: float = 1e-6, positions=None,
+                      interleaved: bool = False, new_latent=None, q=None, q_pe_out=None,
+                      dev_status=None, stream=None) -> None:
+    """Norm, rotation and paged append of the new tokens' rows kv_a [T, L+P]
+    (rows may be columns of a wider tensor), and the rotation of the queries'
+    rope columns.  q_pe_out: a [T, H, P] view, e.g. ``q[..., Dn:]`` (in place)
+    or ``q_latent[..., L:]``.  rope_table: float32 [positions, P], cos then
+    sin, or None."""
+    w = "mla_append_latent"
+    LP, H, P = dims.kv_lora_rank + dims.qk_rope_dim, dims.num_heads, dims.qk_rope_dim
+    T = kv_a.shape[0]
+    _on_device(w, kv_a, query_start_loc, seq_lens, rope_table, kv_cache, block_table, norm_weight,
+               positions, new_latent, q, q_pe_out, dev_status)
+    R = _batch(w, query_start_loc, seq_lens, block_table)
+    if kv_a.dtype != dims.dtype or kv_a.dim() != 2 or kv_a.shape[1] != LP or \
+            (T > 0 and kv_a.stride(1) != 1):
+        raise ValueError(f"{w}: kv_a has to be [T, {LP}] {dims.dtype} with contiguous rows")
+    _want(w, "kv_cache", kv_cache, dims.dtype, None, dims.block_size, LP)
+    _want(w, "norm_weight", norm_weight, dims.dtype, dims.kv_lora_rank)
+    _want(w, "positions", positions, torch.int32, T)
+    _want(w, "rope_table", rope_table, torch.float32, None, P)
+    _want(w, "new_latent", new_latent, dims.dtype, T, LP)
+    _want(w, "q", q, dims.dtype, T, H, dims.qk_nope_dim + P)
+    _want(w, "dev_status", dev_status, torch.int32, 1)
+    q_ld = P
+    if q_pe_out is not None:
+        q_ld = q_pe_out.stride(1) if H > 1 else q_pe_out.stride(0)
+        if q_pe_out.dtype != dims.dtype or q_pe_out.shape != (T, H, P) or \
+                (P > 1 and q_pe_out.stride(2) != 1) or \
+                (T > 1 and q_pe_out.stride(0) != H * q_ld):
+            raise ValueError(f"{w}: q_pe_out has to be a [{T}, {H}, {P}] {dims.dtype} view of "
+                             "evenly spaced rows")
+    d = dims.c()
+    _check(lib().mla_append_latent(
+        C.byref(d), _ptr(kv_a), kv_a.stride(0) if T > 1 else max(LP, kv_a.stride(0)),
+        _ptr(norm_weight), norm_eps, T, R, _ptr(query_start_loc), _ptr(seq_lens), _ptr(positions),
+        _ptr(rope_table), 0 if rope_table is None else rope_table.shape[0], int(interleaved),
+        _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table), block_table.shape[1],
+        _ptr(new_latent), _ptr(q), _ptr(q_pe_out), q_ld, _ptr(dev_status), _stream(stream)), w)
+
+
+def mla_absorb_query(dims: Dims, q, w_kv_b, q_latent, rope_columns: bool = True,
+                     stream=None) -> None:
+    """q [T, H, Dn+P] -> q_latent [T, H, L+P]; rope_columns False leaves the
+    rope columns of q_latent as they are."""
+    w, T, H = "mla_absorb_query", q.shape[0], dims.num_heads
+    _on_device(w, q, w_kv_b, q_latent)
+    _want(w, "q", q, dims.dtype, T, H, dims.qk_nope_dim + dims.qk_rope_dim)
+    _want(w, "w_kv_b", w_kv_b, dims.dtype, H * (dims.qk_nope_dim + dims.v_dim), dims.kv_lora_rank)
+    _want(w, "q_latent", q_latent, dims.dtype, T, H, dims.kv_lora_rank + dims.qk_rope_dim)
+    d = dims.c()
+    _check(lib().mla_absorb_query(C.byref(d), _ptr(q), T, _ptr(w_kv_b), int(rope_columns),
+                                  _ptr(q_latent), _stream(stream)), w)
+
+
+def mla_expand_output(dims: Dims, o_latent, w_kv_b, out, stream=None) -> None:
+    """o_latent [T, H, L] -> out [T, H, Dv]."""
+    w, T, H = "mla_expand_output", o_latent.shape[0], dims.num_heads
+    _on_device(w, o_latent, w_kv_b, out)
+    _want(w, "o_latent", o_latent, dims.dtype, T, H, dims.kv_lora_rank)
+    _want(w, "w_kv_b", w_kv_b, dims.dtype, H * (dims.qk_nope_dim + dims.v_dim), dims.kv_lora_rank)
+    _want(w, "out", out, dims.dtype, T, H, dims.v_dim)
+    d = dims.c()
+    _check(lib().mla_expand_output(C.byref(d), _ptr(o_latent), T, _ptr(w_kv_b), _ptr(out),
+                                   _stream(stream)), w)
+
+
+def mla_latent_attn_workspace_bytes(dims: Dims, num_tokens: int, num_seqs: int) -> int:
+    d = dims.c()
+    n = C.c_size_t(0)
+    _check(lib().mla_latent_attn_workspace_bytes(C.byref(d), int(num_tokens), int(num_seqs),
+                                                 C.byref(n)), "mla_latent_attn_workspace_bytes")
+    return int(n.value)
+
+
+def mla_latent_attn(dims: Dims, causal: bool, query_start_loc, seq_lens, q_latent, kv_cache,
+                    block_table, workspace, o_latent, lse=None, dev_status=None,
+                    stream=None) -> None:
+    """Absorbed attention over the paged latent cache: q_latent [T, H, L+P] ->
+    o_latent [T, H, L], lse [H, T].  workspace: a uint8 device tensor of
+    mla_latent_attn_workspace_bytes bytes."""
+    w, T, H, L = "mla_latent_attn", q_latent.shape[0], dims.num_heads, dims.kv_lora_rank
+    _on_device(w, q_latent, query_start_loc, seq_lens, kv_cache, block_table, workspace, o_latent,
+               lse, dev_status)
+    R = _batch(w, query_start_loc, seq_lens, block_table)
+    LP = L + dims.qk_rope_dim
+    _want(w, "q_latent", q_latent, dims.dtype, T, H, LP)
+    _want(w, "kv_cache", kv_cache, dims.dtype, None, dims.block_size, LP)
+    _want(w, "workspace", workspace, torch.uint8, None)
+    _want(w, "o_latent", o_latent, dims.dtype, T, H, L)
+    _want(w, "lse", lse, torch.float32, H, T)
+    _want(w, "dev_status", dev_status, torch.int32, 1)
+    d = dims.c()
+    _check(lib().mla_latent_attn(
+        C.byref(d), int(causal), R, _ptr(query_start_loc), _ptr(seq_lens), T, _ptr(q_latent),
+        _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table), block_table.shape[1],
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(o_latent),
+        _ptr(lse), _ptr(dev_status), _stream(stream)), w)

@@ -382,3 +382,97 @@ def equal_window_prefill(q, new_latent, cache, block_table, w_kv_b,
     pnt = _planner.prefix_num_tokens(context_lens, query_lens)
     out, out_lse = merge_attn_states(pO, pL, sO, sL, pnt)
     return out, out_lse, len(starts)
+
+
+# --------------------------------------------------------------------------
+# decode: paged append, absorbed attention
+# --------------------------------------------------------------------------
+def rope_table(positions: int, P: int, base: float = 10000.0):
+    """[positions, P]: cos of the P/2 angles position * base^(-2i/P), then sin."""
+    ang = np.arange(positions)[:, None] * base ** (-2.0 * np.arange(P // 2) / P)
+    return np.concatenate([np.cos(ang), np.sin(ang)], axis=1)
+
+
+def rotate(x, table_row, interleaved: bool):
+    """Rotates the pairs of x [..., P] by the angles of one table row."""
+    x = np.asarray(x, dtype=np.float64)
+    half = x.shape[-1] // 2
+    c, s = table_row[:half], table_row[half:]
+    out = np.empty_like(x)
+    if interleaved:
+        a, b = x[..., 0::2], x[..., 1::2]
+        out[..., 0::2], out[..., 1::2] = a * c - b * s, b * c + a * s
+    else:
+        a, b = x[..., :half], x[..., half:]
+        out[..., :half], out[..., half:] = a * c - b * s, b * c + a * s
+    return out
+
+
+def token_positions(query_start_loc, seq_lens):
+    """(token, request, cache position) of every new token: the last n of a
+    request's seq_lens tokens are its n new ones."""
+    out = []
+    for r, n in enumerate(seq_lens):
+        lo, hi = int(query_start_loc[r]), int(query_start_loc[r + 1])
+        for t in range(lo, hi):
+            out.append((t, r, int(n) - (hi - lo) + (t - lo)))
+    return out
+
+
+def latent_row(x, dims: MlaDims, norm_weight, eps: float, table_row, interleaved: bool):
+    """The cache row of one token: RMS norm of the latent part (None: none),
+    rotation of the rope part (None: none)."""
+    x = np.asarray(x, dtype=np.float64)
+    lat, pe = x[:dims.kv_lora_rank], x[dims.kv_lora_rank:]
+    if norm_weight is not None:
+        lat = lat / np.sqrt(np.mean(lat * lat) + eps) * norm_weight
+    if table_row is not None:
+        pe = rotate(pe, table_row, interleaved)
+    return np.concatenate([lat, pe])
+
+
+def absorb_query(q, w_kv_b, dims: MlaDims):
+    """q [T, H, Dn+P] -> [T, H, L+P]: q_nope W_uk per head, q_pe as it is."""
+    q = np.asarray(q, dtype=np.float64)
+    H, Dn, Dv, L = dims.num_heads, dims.qk_nope_dim, dims.v_dim, dims.kv_lora_rank
+    w = np.asarray(w_kv_b, dtype=np.float64).reshape(H, Dn + Dv, L)[:, :Dn]
+    return np.concatenate([np.einsum("thd,hdl->thl", q[..., :Dn], w, optimize=True),
+                           q[..., Dn:]], axis=2)
+
+
+def expand_output(o_latent, w_kv_b, dims: MlaDims):
+    """o_latent [T, H, L] -> [T, H, Dv]: W_uv o per head."""
+    H, Dn, Dv, L = dims.num_heads, dims.qk_nope_dim, dims.v_dim, dims.kv_lora_rank
+    w = np.asarray(w_kv_b, dtype=np.float64).reshape(H, Dn + Dv, L)[:, Dn:]
+    return np.einsum("thl,hvl->thv", np.asarray(o_latent, dtype=np.float64), w, optimize=True)
+
+
+def latent_attention(q_latent, cache, block_table, query_start_loc, seq_lens, dims: MlaDims,
+                     causal: bool):
+    """Absorbed attention: keys are whole cache rows, values their first L
+    columns.  Returns O [T, H, L], LSE [H, T] (0 and -inf for a row that sees
+    no key; NaN for rows of no request) and two sizes that error bounds need:
+    sum_j p_j |c_j| [T, H, L] and max_j scale * sum |q||c_j| [H, T]."""
+    q = np.asarray(q_latent, dtype=np.float64)
+    T, H, _ = q.shape
+    L = dims.kv_lora_rank
+    o = np.full((T, H, L), np.nan)
+    lse = np.full((H, T), np.nan)
+    mass = np.zeros((T, H, L))
+    size = np.zeros((H, T))
+    for t, r, pos in token_positions(query_start_loc, seq_lens):
+        n = max(0, (pos + 1) if causal else int(seq_lens[r]))
+        if n == 0:
+            o[t], lse[:, t] = 0.0, NEG_INF
+            continue
+        c = np.stack([context_row(cache, block_table, r, j, dims.block_size)
+                      for j in range(n)]).astype(np.float64)
+        s = q[t] @ c.T * dims.softmax_scale
+        size[:, t] = (np.abs(q[t]) @ np.abs(c).T).max(axis=1) * dims.softmax_scale
+        mx = s.max(axis=1, keepdims=True)
+        e = np.exp(s - mx)
+        tot = e.sum(axis=1, keepdims=True)
+        lse[:, t] = (mx + np.log(tot))[:, 0]
+        o[t] = (e / tot) @ c[:, :L]
+        mass[t] = (e / tot) @ np.abs(c[:, :L])
+    return o, lse, mass, size
