@@ -23,6 +23,12 @@ int launch_latent_attn_simt(const mla_dims_t &d, int causal, int R, const int32_
                             const int32_t *seq_lens, int T, const void *q, const void *cache,
                             int num_blocks, const int32_t *block_table, int bt_stride, void *o,
                             float *lse, int32_t *status, cudaStream_t s);
+// sm103_latent.cu
+int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t *qsl,
+                          const int32_t *seq_lens, int T, const void *q, const void *cache,
+                          int num_blocks, const int32_t *block_table, int bt_stride, float *part_o,
+                          float *part_lse, void *desc, int max_ctas, void *o, float *lse,
+                          int32_t *status, cudaStream_t s);
 
 namespace {
 
@@ -38,12 +44,17 @@ int check_rows(const mla_dims_t &d, int T) {
 // key ranges.  A CTA has at most two (the unit it starts in the middle of and
 // the one it leaves unfinished), each 64 rows of 512 float32 and a log-sum.
 constexpr int kMaxCtas = 160;
-size_t latent_workspace(const mla_dims_t &d) {
+struct LatentWorkspace {
+  float *part_o = nullptr, *part_lse = nullptr;
+  void *desc = nullptr;  // two int4 a cluster: its unfinished unit
+};
+size_t latent_workspace(const mla_dims_t &d, void *base, LatentWorkspace &w) {
   if (!tc_shape(d)) return 0;
-  Carve cv(nullptr);
-  cv.take(size_t(2) * kMaxCtas * 64 * 512 * sizeof(float));
-  cv.take(size_t(2) * kMaxCtas * 64 * sizeof(float));
-  cv.take(size_t(kMaxCtas) * 8 * sizeof(int32_t));
+  // 16-byte aligned bases are enough: every part is a multiple of 256 bytes
+  Carve cv(base);
+  w.part_o = static_cast<float *>(cv.take(size_t(2) * kMaxCtas * 64 * 512 * sizeof(float)));
+  w.part_lse = static_cast<float *>(cv.take(size_t(2) * kMaxCtas * 64 * sizeof(float)));
+  w.desc = cv.take(size_t(kMaxCtas) * 8 * sizeof(int32_t));
   return cv.off;
 }
 
@@ -135,7 +146,8 @@ extern "C" int mla_latent_attn_workspace_bytes(const mla_dims_t *d, int32_t num_
   rc = check_rows(*d, num_tokens);
   if (rc) return rc;
   if (num_seqs < 0 || !bytes) return MLA_ERR_INVALID;
-  *bytes = latent_workspace(*d);
+  LatentWorkspace w;
+  *bytes = latent_workspace(*d, nullptr, w);
   return MLA_OK;
 }
 
@@ -160,10 +172,17 @@ extern "C" int mla_latent_attn(const mla_dims_t *d, int32_t causal, int32_t num_
       !aligned16(kv_cache))
     return MLA_ERR_INVALID;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (const size_t need = latent_workspace(*d)) {
+  if (tc_shape(*d)) {
+    LatentWorkspace w;
+    const size_t need = latent_workspace(*d, workspace, w);
     if (!workspace || !aligned16(workspace)) return MLA_ERR_INVALID;
     if (workspace_bytes < need) return MLA_ERR_TOO_SMALL;
-    if (!tc_available()) return MLA_ERR_UNSUPPORTED;
+    if (!aligned16(q_latent) || !aligned16(o_latent) || !tc_available())
+      return MLA_ERR_UNSUPPORTED;
+    return launch_latent_attn_tc(*d, causal, num_seqs, query_start_loc, seq_lens, num_tokens,
+                                 q_latent, kv_cache, num_blocks, block_table, block_table_stride,
+                                 w.part_o, w.part_lse, w.desc, kMaxCtas, o_latent, lse, dev_status,
+                                 s);
   }
   if (!latent_simt_ok(*d)) return MLA_ERR_UNSUPPORTED;
   return launch_latent_attn_simt(*d, causal, num_seqs, query_start_loc, seq_lens, num_tokens,

@@ -1,0 +1,910 @@
+// Latent (absorbed) attention over the paged cache on the 5th-generation
+// tensor cores (sm_103a), DeepSeek-V3 head shape, bf16:
+//   s_j = scale * q . c_j (576 columns), o = sum_j softmax(s)_j c_j[0:512), lse
+// for every row (new token, head); the rows of a sequence share its cache rows.
+//
+// A row reads 1152 bytes and spends 2 * (576 + 512) FLOP per key: with 128
+// rows that is 242 FLOP/byte, just under the GPU's bf16 : HBM ratio of 289, so
+// both the tensor pipe and HBM have to be kept near their limits, and what
+// limits the tensor pipe is how its operands fit on chip:
+//   * O (rows x 512 float32) lives in tensor memory.  128 rows would take all
+//     512 columns and leave none for S, so an SM holds 64 rows: 256 columns,
+//     in the layout where lanes 0-63 have the rows with one half of D's
+//     columns and lanes 64-127 the same rows with the other half.  Softmax
+//     threads of lanes l and l+64 share row l, each with half of the keys.
+//   * an MMA of K=16 takes at least 44.6 clocks whatever its size (measured),
+//     and the operands' shared-memory reads 1 clock per 128 bytes.
+// Two forms (template parameter):
+//   single (rows of a unit: 64)  one CTA, weight-stationary MMAs of M=64;
+//          tiles of 64 keys, two stages; a stage serves as K (K-major, 9
+//          blocks of 64 columns) and as V (the first 8 blocks, MN-major).
+//   pair   (rows: 128)  a cluster of two CTAs, cta_group::2 MMAs of M=128 (64
+//          rows in each), tiles of 128 keys.  Each CTA holds its 64 keys of K
+//          (9 blocks) and its 256 columns of V for all 128 keys, in two rings
+//          refilled block by block as the MMAs release them (one tile's worth
+//          each: there is no room for two).
+// Work split: the keys of all units (sequence, 64 or 128 rows) are laid end to
+// end in tiles and dealt out in equal contiguous shares, one per cluster, by
+// the kernel itself from the lengths on the device.  A unit that lies in one
+// share is written directly; the pieces of a cut one go to scratch as
+// normalised float32 with their log-sums, and latent_combine_kernel joins
+// them.
+// Warps: 0 K loads, 1 V loads (pair), 2 MMA issue, 3 query loads, 4-7 softmax
+// and epilogue (tensor-memory lanes 0-127).
+#include <algorithm>
+#include <atomic>
+
+#include "sm103.cuh"
+
+namespace mla {
+namespace sm103 {
+namespace {
+
+constexpr int LAT = 512, WIDTH = 576, NBLK = 9;  // row: 9 blocks of 64 columns
+constexpr int CROWS = 64;                        // rows of O in a CTA
+constexpr int BLK_BYTES = 64 * 128;              // 64 rows x 64 columns, 128-byte swizzled
+constexpr int Q_BYTES = NBLK * BLK_BYTES;
+constexpr int THREADS = 256;
+constexpr int MAPS = 6;  // cache boxes of 1, 2, 4, 8, 16 and 32 rows
+constexpr uint32_t TMEM_COLS = 512, S_COL = 256;
+constexpr float LN2 = 0.69314718055994531f;
+// O is rescaled only when a row's maximum has grown by more than this (log2):
+// until then p is at most 2^8, which float32 sums and bf16's exponent hold
+// without loss.
+constexpr float RESCALE = 8.f;
+
+template <bool PAIR>
+struct Cfg {
+  static constexpr int TILE = PAIR ? 128 : 64;  // keys
+  static constexpr int UROWS = PAIR ? 128 : 64; // rows of a unit
+  static constexpr int NC = TILE / 2;           // S columns of a softmax thread
+  static constexpr int KV_BYTES = PAIR ? NBLK * BLK_BYTES + 4 * 2 * BLK_BYTES : 2 * NBLK * BLK_BYTES;
+  static constexpr int P_BYTES = CROWS * TILE * 2;
+  static constexpr int SMEM = 1024 + Q_BYTES + KV_BYTES + P_BYTES + 1024 + 512;
+  // a share has at least this many tiles: shorter ones cost more in scratch
+  // traffic and joining than they save
+  static constexpr int MIN_TILES = PAIR ? 2 : 4;
+};
+constexpr int V_CHUNK = 4 * 32 * 128;  // pair: 32 keys x 256 columns of V
+
+struct Maps {
+  CUtensorMap q;
+  CUtensorMap c[MAPS];
+};
+
+struct LatentArgs {
+  const int32_t *qsl, *seq_lens, *block_table;
+  __nv_bfloat16 *o;
+  float *lse, *part_o, *part_lse;
+  int4 *desc;
+  int32_t *status;
+  int T, R, H, bs, num_blocks, bt_stride, causal, box_log2;
+  float scale_log2;
+};
+
+// ---- the work split ---------------------------------------------------------
+struct Seq {
+  int q0, nq, len, nrt, tiles;
+};
+
+template <bool PAIR>
+__device__ __forceinline__ Seq load_seq(const LatentArgs &a, int r) {
+  Seq s;
+  s.q0 = min(max(__ldg(a.qsl + r), 0), a.T);
+  s.nq = max(min(__ldg(a.qsl + r + 1), a.T) - s.q0, 0);
+  s.len = max(__ldg(a.seq_lens + r), 0);
+  s.nrt = (s.nq * a.H + Cfg<PAIR>::UROWS - 1) / Cfg<PAIR>::UROWS;
+  // a unit without keys still has its rows to write
+  s.tiles = max(1, (s.len + Cfg<PAIR>::TILE - 1) / Cfg<PAIR>::TILE);
+  return s;
+}
+
+struct Share {  // of a cluster, in shared memory
+  long long len, share;
+  int r, rt, tile;
+};
+
+// Piece of a unit: row tile rt of sequence r, key tiles [t0, t1).
+template <bool PAIR>
+struct Walk {
+  const LatentArgs &a;
+  Seq s;
+  int r, rt, t0, t1, next_tile;
+  long long left;
+  __device__ __forceinline__ Walk(const LatentArgs &args, const Share &sh)
+      : a(args), r(sh.r), rt(sh.rt), t0(0), t1(0), next_tile(sh.tile), left(sh.len) {
+    if (left > 0) s = load_seq<PAIR>(a, r);
+  }
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    if (t1 > 0 && t1 == s.tiles) {  // the previous piece ended its unit
+      next_tile = 0;
+      if (++rt == s.nrt) {
+        rt = 0;
+        do {
+          if (++r >= a.R) return false;
+          s = load_seq<PAIR>(a, r);
+        } while (s.nrt == 0);
+      }
+    }
+    t0 = next_tile;
+    t1 = int(min((long long)s.tiles, t0 + left));
+    left -= t1 - t0;
+    return true;
+  }
+};
+
+// All threads: this cluster's share of the tiles of all units.
+template <bool PAIR>
+__device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int clusters,
+                                           Share *out, long long *scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int NW = THREADS / 32;
+  auto work = [&](int r) -> long long {
+    if (r >= a.R) return 0;
+    const Seq s = load_seq<PAIR>(a, r);
+    return (long long)s.nrt * s.tiles;
+  };
+  long long mine = 0;
+  const long long first = work(threadIdx.x);
+  mine = first;
+  for (int r = threadIdx.x + THREADS; r < a.R; r += THREADS) mine += work(r);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) scratch[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) total += scratch[w];
+  long long share = (total + clusters - 1) / clusters;
+  if (share < Cfg<PAIR>::MIN_TILES) share = Cfg<PAIR>::MIN_TILES;
+  const long long start = share * cluster;
+  if (threadIdx.x == 0) {
+    out->share = share;
+    out->len = max(0LL, min(share, total - start));
+    out->r = out->rt = out->tile = 0;
+  }
+  __syncthreads();
+  if (start >= total) return;
+  long long base = 0;
+  for (int r0 = 0; r0 < a.R; r0 += THREADS) {
+    const int r = r0 + threadIdx.x;
+    const long long w = r0 == 0 ? first : work(r);
+    long long inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    long long before = base, all = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      if (i < warp) before += scratch[i];
+      all += scratch[i];
+    }
+    const long long lo = before + inc - w;
+    if (w > 0 && start >= lo && start < lo + w) {
+      const int tiles = load_seq<PAIR>(a, r).tiles;
+      out->r = r;
+      out->rt = int((start - lo) / tiles);
+      out->tile = int((start - lo) % tiles);
+    }
+    base += all;
+    __syncthreads();
+    if (base > start) return;
+  }
+}
+
+// ---- cache loads --------------------------------------------------------------
+// Cache row of position j of a sequence (block table row bt): num_rows (which
+// the loads fill with zeros) past its length and for a bad block.
+__device__ __forceinline__ int cache_row(const LatentArgs &a, const int32_t *bt, int len, int j) {
+  const int none = a.num_blocks * a.bs;
+  if (j >= len) return none;
+  const int b = j / a.bs;
+  const int blk = b < a.bt_stride ? __ldg(bt + b) : -1;
+  if (blk < 0 || blk >= a.num_blocks) {
+    if (a.status) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
+    return none;
+  }
+  return blk * a.bs + (j - b * a.bs);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
+                                         int y) {
+  if (PAIR)
+    tma_load_2d_pair(dst, m, bar, x, y);
+  else
+    tma_load_2d(dst, m, bar, x, y);
+}
+
+// `rows` (at most a box) cache rows from `row`, the first `valid` of them
+// real and the others zeros, to dst and, `count` times, on to the next column
+// block `step` bytes further.  A whole box is one copy a block; a ragged one
+// is put together from the smaller boxes (128-byte rows: any row is a legal
+// destination, and the swizzle goes by the address).
+template <bool PAIR>
+__device__ __forceinline__ void load_rows(const Maps &m, int box_log2, uint32_t dst, uint32_t step,
+                                          int count, int x, int row, int valid, int none,
+                                          uint32_t bar) {
+  const int rows = 1 << box_log2;
+  if (valid <= 0 || valid >= rows) {
+    const int y = valid <= 0 ? none : row;
+    for (int b = 0; b < count; ++b)
+      load_box<PAIR>(dst + b * step, &m.c[box_log2], bar, x + b * 64, y);
+    return;
+  }
+  int off = 0;
+  for (int k = box_log2 - 1; k >= 0; --k)
+    if (valid & (1 << k)) {
+      for (int b = 0; b < count; ++b)
+        load_box<PAIR>(dst + b * step + off * 128, &m.c[k], bar, x + b * 64, row + off);
+      off += 1 << k;
+    }
+  for (int k = box_log2 - 1; k >= 0; --k)
+    if ((rows - valid) & (1 << k)) {
+      for (int b = 0; b < count; ++b)
+        load_box<PAIR>(dst + b * step + off * 128, &m.c[k], bar, x + b * 64, none);
+      off += 1 << k;
+    }
+}
+
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t mn_block_bytes) {
+  return desc_mnmajor_sw128(saddr, mn_block_bytes);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void softmax_barrier() {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+template <bool PAIR>
+__global__ void __launch_bounds__(THREADS, 1)
+    latent_attn_kernel(const __grid_constant__ Maps m, const LatentArgs a) {
+  using C = Cfg<PAIR>;
+  constexpr int TILE = C::TILE, NC = C::NC;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sQ = smem_u32(smem), sK = sQ + Q_BYTES, sV = sK + NBLK * BLK_BYTES,
+                 sP = sK + C::KV_BYTES;
+  float *xmax = reinterpret_cast<float *>(smem + Q_BYTES + C::KV_BYTES + C::P_BYTES);  // [2][128]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(xmax + 256);
+  // k_full[9] k_empty[9] v_full[4] v_empty[4] (single: k_*[2] are the stages),
+  // q_full q_empty, s_full[2] s_empty[2], p_full, pv_done, done
+  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 72, v_full = k_full + 144,
+                 v_empty = v_full + 32, q_full = v_empty + 32, q_empty = q_full + 8,
+                 s_full = q_empty + 8, s_empty = s_full + 16, p_full = s_empty + 16,
+                 pv_done = p_full + 8, done = pv_done + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 35);
+  Share *share = reinterpret_cast<Share *>(bars + 36);        // 28 bytes
+  long long *scan = reinterpret_cast<long long *>(bars + 40);  // [8]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+  const int cluster = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int clusters = PAIR ? gridDim.x >> 1 : gridDim.x;
+  auto lead = [&](uint32_t bar) { return PAIR ? mapa_shared(bar, 0) : bar; };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NBLK; ++i) {
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(v_full + 8 * i, 1);
+      mbar_init(v_empty + 8 * i, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_empty + 8 * i, PAIR ? 8 : 4);
+    }
+    mbar_init(p_full, PAIR ? 8 : 4);
+    mbar_init(pv_done, 1);
+    mbar_init(done, 1);
+    fence_mbar_init();
+    prefetch_map(&m.q);
+    prefetch_map(&m.c[a.box_log2]);
+  }
+  if (warp == 2) {
+    if (PAIR)
+      tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    else
+      tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+  }
+  find_share<PAIR>(a, cluster, clusters, share, scan);
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int box = 1 << a.box_log2, none = a.num_blocks * a.bs;
+
+  if (warp == 0) {
+    // ---------------- K (single: and V) loads, whole warp
+    Walk<PAIR> w(a, *share);
+    int g = 0;
+    bool ok = true;
+    const uint32_t bar0 = lead(k_full);
+    while (ok && w.next()) {
+      const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
+      for (int t = w.t0; t < w.t1 && ok; ++t, ++g) {
+        const int key0 = t * TILE + int(rank) * 64;  // this CTA's 64 keys
+        int row[2], valid[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // lane l: row groups l and l + 32
+          const int off = (lane + 32 * i) << a.box_log2;
+          row[i] = off < 64 ? cache_row(a, bt, w.s.len, key0 + off) : none;
+          valid[i] = row[i] == none ? 0 : min(box, w.s.len - key0 - off);
+        }
+        const int st = PAIR ? 0 : g & 1;
+        const uint32_t free_parity = PAIR ? (g & 1) ^ 1 : ((g >> 1) & 1) ^ 1;
+        if (PAIR) {
+          for (int kb = 0; kb < NBLK && ok; ++kb) {
+            ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * kb, free_parity));
+            if (!ok) break;
+            if (rank == 0 && lane == 0) mbar_expect_tx(k_full + 8 * kb, 2 * BLK_BYTES);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int off = (lane + 32 * i) << a.box_log2;
+              // rows past the length only make scores that are masked
+              if (off < 64)
+                tma_load_2d_pair(sK + kb * BLK_BYTES + off * 128, &m.c[a.box_log2], bar0 + 8 * kb,
+                                 kb * 64, row[i]);
+            }
+          }
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * st, free_parity));
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(k_full + 8 * st, NBLK * BLK_BYTES);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int off = (lane + 32 * i) << a.box_log2;
+            if (off < 64)
+              load_rows<PAIR>(m, a.box_log2, sK + st * NBLK * BLK_BYTES + off * 128, BLK_BYTES,
+                              NBLK, 0, row[i], valid[i], none, k_full + 8 * st);
+          }
+        }
+      }
+    }
+    // the loads issued here have landed before the CTA may exit
+    if (g > 0) {
+      if (PAIR) {
+        for (int kb = 0; kb < NBLK; ++kb)
+          mbar_wait((rank == 0 ? k_full : k_empty) + 8 * kb, (g - 1) & 1);
+      } else {
+        for (int i = max(0, g - 2); i < g; ++i) mbar_wait(k_full + 8 * (i & 1), (i >> 1) & 1);
+      }
+    }
+  } else if (warp == 1 && PAIR) {
+    // ---------------- V loads: 256 columns of all keys, 32 keys at a time
+    Walk<PAIR> w(a, *share);
+    int g = 0;
+    bool ok = true;
+    const uint32_t bar0 = lead(v_full);
+    while (ok && w.next()) {
+      const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
+      for (int t = w.t0; t < w.t1 && ok; ++t, ++g) {
+        for (int c = 0; c < 4 && ok; ++c) {
+          const int key0 = t * TILE + c * 32, off = lane << a.box_log2;
+          int row = none, valid = 0;
+          if (off < 32) {
+            row = cache_row(a, bt, w.s.len, key0 + off);
+            valid = row == none ? 0 : min(box, w.s.len - key0 - off);
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(v_empty + 8 * c, (g & 1) ^ 1));
+          if (!ok) break;
+          if (rank == 0 && lane == 0) mbar_expect_tx(v_full + 8 * c, 2 * V_CHUNK);
+          __syncwarp();
+          if (off < 32)
+            load_rows<PAIR>(m, a.box_log2, sV + c * V_CHUNK + off * 128, 32 * 128, 4,
+                            int(rank) * 256, row, valid, none, bar0 + 8 * c);
+        }
+      }
+    }
+    if (g > 0)
+      for (int c = 0; c < 4; ++c) mbar_wait((rank == 0 ? v_full : v_empty) + 8 * c, (g - 1) & 1);
+  } else if (warp == 3) {
+    // ---------------- query loads
+    if (lane == 0) {
+      Walk<PAIR> w(a, *share);
+      int n = 0;
+      const uint32_t bar = lead(q_full);
+      while (w.next()) {
+        if (!mbar_wait(q_empty, (n & 1) ^ 1)) break;
+        if (rank == 0) mbar_expect_tx(q_full, (PAIR ? 2 : 1) * Q_BYTES);
+        const int row = w.s.q0 * a.H + w.rt * C::UROWS + int(rank) * CROWS;
+        for (int kb = 0; kb < NBLK; ++kb)
+          load_box<PAIR>(sQ + kb * BLK_BYTES, &m.q, bar, kb * 64, row);
+        ++n;
+      }
+      if (n > 0) mbar_wait(rank == 0 ? q_full : q_empty, (n - 1) & 1);
+    }
+  } else if (warp == 2) {
+    // ---------------- MMA issue (pair: the even CTA)
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t id_s = idesc_f16kind(PAIR ? 128 : 64, TILE, false, false, true);
+      constexpr uint32_t id_o = idesc_f16kind(PAIR ? 128 : 64, 256, false, true, true);
+      auto mma = [](uint32_t d, uint64_t x, uint64_t y, uint32_t id, uint32_t acc) {
+        if (PAIR)
+          mma_bf16_pair(d, x, y, id, acc);
+        else
+          mma_bf16_ws(d, x, y, id, acc);
+      };
+      auto commit = [](uint32_t bar) {
+        if (PAIR)
+          mma_commit_pair_mc(bar, uint16_t(3));
+        else
+          mma_commit(bar);
+      };
+      // O (+)= P V of tile g
+      auto second = [&](int g, bool first) -> bool {
+        if (!(PAIR ? mbar_wait_cluster(p_full, g & 1) : mbar_wait(p_full, g & 1))) return false;
+        tc_fence_after();
+        if (PAIR) {
+          for (int c = 0; c < 4; ++c) {
+            if (!mbar_wait(v_full + 8 * c, g & 1)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+              const int k16 = c * 2 + ks;
+              const uint64_t pd = desc_kmajor_sw128(sP + (k16 >> 2) * BLK_BYTES + (k16 & 3) * 32);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma(tmem + j * 128, pd,
+                    desc_mn(sV + c * V_CHUNK + 2 * j * 32 * 128 + ks * 2048, 32 * 128), id_o,
+                    !(first && k16 == 0));
+            }
+            commit(v_empty + 8 * c);
+          }
+        } else {
+          const uint32_t v = sK + (g & 1) * NBLK * BLK_BYTES;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              mma(tmem + j * 128, desc_kmajor_sw128(sP + ks * 32),
+                  desc_mn(v + 4 * j * BLK_BYTES + ks * 2048, BLK_BYTES), id_o,
+                  !(first && ks == 0));
+          commit(k_empty + 8 * (g & 1));
+        }
+        commit(pv_done);
+        return true;
+      };
+      Walk<PAIR> w(a, *share);
+      int g = 0, n = 0;
+      bool ok = true;
+      while (ok && w.next()) {
+        if (!mbar_wait(q_full, n & 1)) break;
+        tc_fence_after();
+        for (int t = w.t0; t < w.t1; ++t, ++g) {
+          const int sb = g & 1;
+          ok = mbar_wait(s_empty + 8 * sb, ((g >> 1) & 1) ^ 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + S_COL + sb * NC;
+          if (!PAIR) {
+            ok = mbar_wait(k_full + 8 * sb, (g >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          const uint32_t k = PAIR ? sK : sK + sb * NBLK * BLK_BYTES;
+          for (int kb = 0; kb < NBLK; ++kb) {
+            if (PAIR) {
+              ok = mbar_wait(k_full + 8 * kb, g & 1);
+              if (!ok) break;
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma(d, desc_kmajor_sw128(sQ + kb * BLK_BYTES + ks * 32),
+                  desc_kmajor_sw128(k + kb * BLK_BYTES + ks * 32), id_s, (kb | ks) != 0);
+            if (PAIR) commit(k_empty + 8 * kb);
+          }
+          if (!ok) break;
+          commit(s_full + 8 * sb);
+          if (t + 1 == w.t1) commit(q_empty);
+          if (t > w.t0) {
+            ok = second(g - 1, t - 1 == w.t0);
+            if (!ok) break;
+          }
+        }
+        if (ok) ok = second(g - 1, w.t1 - 1 == w.t0);
+        ++n;
+      }
+      // every MMA has completed before tensor memory is released
+      commit(done);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------- softmax and epilogue
+    const int tid = threadIdx.x - 128;      // tensor-memory lane
+    const int half = tid >> 6, rl = tid & 63;
+    const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
+    const uint32_t s_empty_lead = lead(s_empty), p_full_lead = lead(p_full);
+    auto arrive = [&](uint32_t bar) {
+      if (PAIR)
+        mbar_arrive_cluster(bar);
+      else
+        mbar_arrive(bar);
+    };
+    if (tid == 0 && rank == 0) a.desc[2 * cluster] = make_int4(0, 0, 0, 0);
+    Walk<PAIR> w(a, *share);
+    int g = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      const int rows = w.s.nq * a.H - w.rt * C::UROWS;  // of the unit (may exceed it)
+      const int urow = int(rank) * CROWS + rl;
+      const int i = (w.rt * C::UROWS + urow) / a.H;     // token of the sequence
+      const int vis = a.causal ? min(w.s.len, w.s.len - w.s.nq + i + 1) : w.s.len;
+      float mref = neg_inf(), l = 0.f;
+      for (int t = w.t0; t < w.t1; ++t, ++g) {
+        const int sb = g & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * sb, (g >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[NC];
+#pragma unroll
+        for (int c = 0; c < NC; c += 32)
+          tmem_ld32(t_lane + S_COL + sb * NC + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster_relaxed(s_empty_lead + 8 * sb);
+          else
+            mbar_arrive(s_empty + 8 * sb);
+        }
+        const int nvis = vis - t * TILE - half * NC;
+        if (nvis < NC) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if (c >= nvis) s[c] = __float_as_uint(neg_inf());
+        }
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        xmax[sb * 128 + tid] = mine;
+        softmax_barrier();
+        const float mt = fmaxf(mine, xmax[sb * 128 + (tid ^ 64)]) * a.scale_log2;
+        // both threads of a row see the same maxima and decide alike
+        float f = 1.f;
+        if (mt > mref + RESCALE || (is_neg_inf(mref) && mt > mref)) {
+          f = exp2_fast(mref - mt);  // 0 from -inf
+          mref = mt;
+          l *= f;
+        }
+        const float base = is_neg_inf(mref) ? 0.f : mref;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t p[NC / 2];
+#pragma unroll
+        for (int c = 0; c < NC; c += 2) {
+          const float x = exp2_fast(fmaf(__uint_as_float(s[c]), a.scale_log2, -base));
+          const float y = exp2_fast(fmaf(__uint_as_float(s[c + 1]), a.scale_log2, -base));
+          sum[(c >> 1) & 3] += x + y;
+          p[c / 2] = pack_bf16(x, y);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // P V of the tile before is done: P and O may be written
+        if (g > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1));
+          if (!ok) break;
+        }
+        tc_fence_after();
+        if (t > w.t0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_lane + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(t_lane + c, o);
+          }
+          tmem_wait_st();
+        }
+        // P, K-major with 128-byte swizzle, 64 keys a block
+        const uint32_t prow = sP + (PAIR ? half * BLK_BYTES : 0) + rl * 128;
+        const int c0 = PAIR ? 0 : half * 4;
+#pragma unroll
+        for (int c = 0; c < NC / 8; ++c)
+          st_shared_v4(prow + (((c0 + c) ^ (rl & 7)) << 4),
+                       make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]));
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(p_full_lead);
+      }
+      if (!ok) break;
+      // ---- the piece's rows
+      xmax[((g & 1) * 128) + tid] = l;  // (the other buffer may still be read)
+      softmax_barrier();
+      l += xmax[((g & 1) * 128) + (tid ^ 64)];
+      softmax_barrier();
+      ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
+      const bool live = urow < rows;
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f || l != l ? mref + log2f(l) : neg_inf();
+      const int64_t grow = int64_t(w.s.q0) * a.H + w.rt * C::UROWS + urow;
+      const int slot = 2 * cluster + (w.t0 == 0 ? 1 : 0);
+      // scratch of a slot and CTA: [512/4][64 rows][4], so that the lanes of a
+      // warp write one contiguous piece
+      const int64_t srow = int64_t(slot) * C::UROWS + int(rank) * CROWS;
+      float4 *part = reinterpret_cast<float4 *>(a.part_o + srow * LAT) + rl;
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(t_lane + c, o);
+        tmem_wait_ld();
+        const int j = c >> 7, cc = c & 127;
+        const int dim = PAIR ? half * 256 + j * 128 + cc : j * 256 + half * 128 + cc;
+        if (whole) {
+          if (live) {
+            __nv_bfloat16 *dst = a.o + grow * LAT + dim;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float x = __uint_as_float(o[e + 2 * k]), y = __uint_as_float(o[e + 2 * k + 1]);
+                v[k] = inv == 0.f ? 0u : pack_bf16(x * inv, y * inv);
+              }
+              *reinterpret_cast<uint4 *>(dst + e) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = inv == 0.f ? 0.f : __uint_as_float(o[e + k]) * inv;
+            part[((dim + e) / 4) * CROWS] = make_float4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+      tc_fence_before();  // the reads of O come before the next piece's P is handed over
+      if (half == 0) {
+        if (whole) {
+          if (live && a.lse) a.lse[int64_t(grow % a.H) * a.T + grow / a.H] = lse2 * LN2;
+        } else {
+          a.part_lse[srow + rl] = lse2;
+        }
+      }
+      if (!whole && w.t0 == 0 && tid == 0 && rank == 0) {
+        // the unit's first piece: its others are in the shares that follow
+        const long long rest = w.s.tiles - w.t1;
+        a.desc[2 * cluster] =
+            make_int4(1 + int((rest + share->share - 1) / share->share), min(rows, C::UROWS), 0, 0);
+        *reinterpret_cast<long long *>(a.desc + 2 * cluster + 1) =
+            int64_t(w.s.q0) * a.H + w.rt * C::UROWS;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) mbar_wait(done, 0);
+  __syncthreads();
+  if (PAIR) cluster_sync();  // neither CTA leaves while the pair's MMAs or arrives may touch it
+  tc_fence_after();
+  if (warp == 2) {
+    __syncwarp();
+    if (PAIR)
+      tmem_dealloc_pair(tmem, TMEM_COLS);
+    else
+      tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the pieces of cut units: o = sum_i w_i o_i / sum_i w_i with w_i =
+// 2^(lse_i - max).  An item is 16 rows x 16 columns of one unit; the block's
+// threads are 16 rows x 4 float4 columns x 4 quarters of the pieces.  The
+// blocks find the cut units from the clusters' descriptors.
+constexpr int CT = 256;
+__global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, int clusters,
+                                                            int urows, const float *part_o,
+                                                            const float *part_lse,
+                                                            __nv_bfloat16 *o, float *lse, int H,
+                                                            int T) {
+  __shared__ int units[256];
+  __shared__ float4 sacc[3][64];
+  __shared__ float smax[3][64], ssum[3][64];
+  // the cut units, in cluster order whatever the order of the warps
+  const bool cut = int(threadIdx.x) < clusters && desc[2 * threadIdx.x].x > 0;
+  const uint32_t b = __ballot_sync(0xffffffffu, cut);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int per_warp[CT / 32];
+  if (lane == 0) per_warp[warp] = __popc(b);
+  __syncthreads();
+  int base = 0, total = 0;
+  for (int i = 0; i < CT / 32; ++i) {
+    if (i < warp) base += per_warp[i];
+    total += per_warp[i];
+  }
+  if (cut) units[base + __popc(b & ((1u << lane) - 1))] = threadIdx.x;
+  __syncthreads();
+  const int row_groups = urows / 16, items = row_groups * 32;
+  const int quarter = threadIdx.x >> 6, k = threadIdx.x & 63, rr = k & 15, cq = k >> 4;
+  for (int it = blockIdx.x; it < total * items; it += gridDim.x) {
+    const int c0 = units[it / items], sub = it % items;
+    const int row = (sub >> 5) * 16 + rr, col4 = (sub & 31) * 4 + cq;
+    const int4 d = desc[2 * c0];
+    const int n = d.x;
+    const int64_t grow0 = *reinterpret_cast<const long long *>(desc + 2 * c0 + 1);
+    auto slot_row = [&](int i) {
+      return int64_t(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * urows + (row & ~63);
+    };
+    float mx = neg_inf(), sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = quarter; i0 < n; i0 += 16) {  // four pieces at a time
+      float ls[4];
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + 4 * u;
+        ls[u] = neg_inf();
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+          const int64_t s = slot_row(i);
+          ls[u] = part_lse[s + (row & 63)];
+          v[u] = *(reinterpret_cast<const float4 *>(part_o + s * LAT) + col4 * CROWS + (row & 63));
+        }
+      }
+      float mn = mx;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ls[u]);
+      const float bs = is_neg_inf(mn) ? 0.f : mn;
+      const float f = exp2_fast(mx - bs);
+      sum *= f;
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float w = exp2_fast(ls[u] - bs);
+        sum += w;
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
+      mx = mn;
+    }
+    if (quarter > 0) {
+      sacc[quarter - 1][k] = acc;
+      smax[quarter - 1][k] = mx;
+      ssum[quarter - 1][k] = sum;
+    }
+    __syncthreads();
+    if (quarter == 0) {
+      float mn = mx;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) mn = fmaxf(mn, smax[i][k]);
+      const float bs = is_neg_inf(mn) ? 0.f : mn;
+      float f = exp2_fast(mx - bs);
+      sum *= f;
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        f = exp2_fast(smax[i][k] - bs);
+        sum = fmaf(f, ssum[i][k], sum);
+        acc.x = fmaf(f, sacc[i][k].x, acc.x);
+        acc.y = fmaf(f, sacc[i][k].y, acc.y);
+        acc.z = fmaf(f, sacc[i][k].z, acc.z);
+        acc.w = fmaf(f, sacc[i][k].w, acc.w);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      if (row < d.y) {
+        const int64_t grow = grow0 + row;
+        const uint2 out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
+                                     pack_bf16(acc.z * inv, acc.w * inv));
+        *reinterpret_cast<uint2 *>(o + grow * LAT + col4 * 4) = out;
+        if (lse && col4 == 0)
+          lse[int64_t(grow % H) * T + grow / H] = sum == 0.f ? neg_inf() : (bs + log2f(sum)) * LN2;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <bool PAIR>
+int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaStream_t s) {
+  constexpr int MAX_DEV = 64;
+  static std::atomic<int> grid_of[MAX_DEV];  // CTAs that fit the device, 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEV) return MLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = Cfg<PAIR>::SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int grid = grid_of[dev].load(std::memory_order_acquire);
+  if (grid == 0) {
+    if (cudaFuncSetAttribute(latent_attn_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<PAIR>::SMEM) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    const int cs = PAIR ? 2 : 1;
+    cfg.gridDim = dim3(cs * (num_sms() / cs));
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<PAIR>, &cfg) != cudaSuccess || n < 1)
+      n = num_sms() / cs;
+    grid = std::min(cs * n, urows_limit);
+    grid_of[dev].store(grid, std::memory_order_release);
+  }
+  cfg.gridDim = dim3(grid);
+  launch_begin(s);
+  if (cudaLaunchKernelEx(&cfg, latent_attn_kernel<PAIR>, maps, a) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  int rc = launch_status(s, "latent_attn_kernel");
+  if (rc) return rc;
+  const int clusters = PAIR ? grid / 2 : grid;
+  launch_begin(s);
+  latent_combine_kernel<<<2 * num_sms(), CT, 0, s>>>(a.desc, clusters, Cfg<PAIR>::UROWS, a.part_o,
+                                                     a.part_lse, a.o, a.lse, a.H, a.T);
+  return launch_status(s, "latent_combine_kernel");
+}
+
+}  // namespace
+}  // namespace sm103
+
+// part_o [2 * max_ctas * 64 * 512], part_lse [2 * max_ctas * 64], desc
+// [2 * max_ctas] int4.
+int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t *qsl,
+                          const int32_t *seq_lens, int T, const void *q, const void *cache,
+                          int num_blocks, const int32_t *block_table, int bt_stride, float *part_o,
+                          float *part_lse, void *desc, int max_ctas, void *o, float *lse,
+                          int32_t *status, cudaStream_t s) {
+  using namespace sm103;
+  const int64_t cache_rows = int64_t(num_blocks) * d.block_size;
+  if (cache_rows >= (int64_t(1) << 31) - 64) return MLA_ERR_UNSUPPORTED;
+  Maps maps;
+  if (!make_tmap_2d_16(&maps.q, false, q, WIDTH, uint64_t(T) * d.num_heads, WIDTH * 2, 64, CROWS,
+                       true))
+    return MLA_ERR_CUDA;
+  // the largest box (at most 32 rows) that never crosses a page
+  int box_log2 = 0;
+  while (box_log2 < MAPS - 1 && d.block_size % (2 << box_log2) == 0) ++box_log2;
+  for (int i = 0; i <= box_log2; ++i)
+    if (!make_tmap_2d_16(&maps.c[i], false, cache, WIDTH, uint64_t(std::max<int64_t>(1, cache_rows)),
+                         WIDTH * 2, 64, 1u << i, true))
+      return MLA_ERR_CUDA;
+  for (int i = box_log2 + 1; i < MAPS; ++i) maps.c[i] = maps.c[box_log2];
+  LatentArgs a{qsl, seq_lens, block_table, static_cast<__nv_bfloat16 *>(o), lse, part_o, part_lse,
+               static_cast<int4 *>(desc), status, T, R, d.num_heads, d.block_size, num_blocks,
+               bt_stride, causal, box_log2, d.softmax_scale * 1.4426950408889634f};
+  // rows of an average sequence beyond one CTA's 64: pairs
+  const bool pair = int64_t(T) * d.num_heads > int64_t(64) * R;
+  return pair ? launch_latent<true>(maps, a, max_ctas, s) : launch_latent<false>(maps, a, max_ctas, s);
+}
+
+int latent_take_errors() { return sm103::take_error_flags_here(); }
+
+}  // namespace mla
