@@ -44,7 +44,8 @@ constexpr int LAT = 512, WIDTH = 576, NBLK = 9;  // row: 9 blocks of 64 columns
 constexpr int CROWS = 64;                        // rows of O in a CTA
 constexpr int BLK_BYTES = 64 * 128;              // 64 rows x 64 columns, 128-byte swizzled
 constexpr int Q_BYTES = NBLK * BLK_BYTES;
-constexpr int THREADS = 256;
+constexpr int SWARPS = 8, STHREADS = 32 * SWARPS;  // softmax
+constexpr int THREADS = 128 + STHREADS;
 constexpr int MAPS = 6;  // cache boxes of 1, 2, 4, 8, 16 and 32 rows
 constexpr uint32_t TMEM_COLS = 512, S_COL = 256;
 constexpr float LN2 = 0.69314718055994531f;
@@ -57,14 +58,17 @@ template <bool PAIR>
 struct Cfg {
   static constexpr int TILE = PAIR ? 128 : 64;  // keys
   static constexpr int UROWS = PAIR ? 128 : 64; // rows of a unit
-  static constexpr int NC = TILE / 2;           // S columns of a softmax thread
+  static constexpr int SC = TILE / 2;           // S columns in tensor memory
+  static constexpr int NC = SC / 2;             // of a softmax thread
   static constexpr int KV_BYTES = PAIR ? NBLK * BLK_BYTES + 4 * 2 * BLK_BYTES : 2 * NBLK * BLK_BYTES;
   static constexpr int P_BYTES = CROWS * TILE * 2;
-  static constexpr int SMEM = 1024 + Q_BYTES + KV_BYTES + P_BYTES + 1024 + 512;
+  static constexpr int USED = Q_BYTES + KV_BYTES + P_BYTES + 2048 + 52 * 8;
+  static constexpr int SMEM = 232448;  // all of it; the rest is room for alignment
   // a share has at least this many tiles: shorter ones cost more in scratch
   // traffic and joining than they save
   static constexpr int MIN_TILES = PAIR ? 2 : 4;
 };
+constexpr int KG = 3;  // pair: K is loaded and released in groups of 3 column blocks
 constexpr int V_CHUNK = 4 * 32 * 128;  // pair: 32 keys x 256 columns of V
 
 struct Maps {
@@ -252,8 +256,36 @@ __device__ __forceinline__ void load_rows(const Maps &m, int box_log2, uint32_t 
     }
 }
 
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t mn_block_bytes) {
-  return desc_mnmajor_sw128(saddr, mn_block_bytes);
+// One MMA from the low words of its operands' descriptors; the high words are
+// the same for all of them here (8-row groups 1024 bytes apart, 128-byte
+// swizzle).  An MMA of these shapes takes 45-80 clocks, so the issuing thread
+// can afford few instructions for each: descriptors differ by constants added
+// to a low word (with 64-bit descriptors put together for every MMA it issued
+// one in 129 clocks).
+constexpr uint32_t DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_k(uint32_t saddr) {
+  return ((saddr >> 4) & 0x3FFF) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t mn_block_bytes) {
+  return ((saddr >> 4) & 0x3FFF) | ((mn_block_bytes >> 4) << 16);
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma_lo(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc,
+                                       uint32_t acc) {
+  if (PAIR)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n"
+        " mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(DESC_HI), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n"
+        " mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.ws.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(DESC_HI), "r"(idesc), "r"(acc)
+        : "memory");
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -263,21 +295,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 __device__ __forceinline__ void softmax_barrier() {
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(STHREADS) : "memory");
 }
 
 template <bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ Maps m, const LatentArgs a) {
   using C = Cfg<PAIR>;
-  constexpr int TILE = C::TILE, NC = C::NC;
+  constexpr int TILE = C::TILE, SC = C::SC, NC = C::NC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  static_assert(C::USED <= C::SMEM, "shared memory");
+  if (smem + C::USED > smem_raw + C::SMEM) {  // (the base is 1024-byte aligned in practice)
+    if (threadIdx.x == 0) atomicOr(&g_error_flags, kErrWaitTimeout);
+    return;
+  }
   const uint32_t sQ = smem_u32(smem), sK = sQ + Q_BYTES, sV = sK + NBLK * BLK_BYTES,
                  sP = sK + C::KV_BYTES;
-  float *xmax = reinterpret_cast<float *>(smem + Q_BYTES + C::KV_BYTES + C::P_BYTES);  // [2][128]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(xmax + 256);
+  float *xmax = reinterpret_cast<float *>(smem + Q_BYTES + C::KV_BYTES + C::P_BYTES);  // [2][256]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(xmax + 512);
   // k_full[9] k_empty[9] v_full[4] v_empty[4] (single: k_*[2] are the stages),
   // q_full q_empty, s_full[2] s_empty[2], p_full, pv_done, done
   const uint32_t k_full = smem_u32(bars), k_empty = k_full + 72, v_full = k_full + 144,
@@ -286,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                  pv_done = p_full + 8, done = pv_done + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 35);
   Share *share = reinterpret_cast<Share *>(bars + 36);        // 28 bytes
-  long long *scan = reinterpret_cast<long long *>(bars + 40);  // [8]
+  long long *scan = reinterpret_cast<long long *>(bars + 40);  // [12]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;
@@ -307,9 +344,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(s_empty + 8 * i, PAIR ? 8 : 4);
+      mbar_init(s_empty + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
     }
-    mbar_init(p_full, PAIR ? 8 : 4);
+    mbar_init(p_full, PAIR ? 2 * SWARPS : SWARPS);
     mbar_init(pv_done, 1);
     mbar_init(done, 1);
     fence_mbar_init();
@@ -350,18 +387,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int st = PAIR ? 0 : g & 1;
         const uint32_t free_parity = PAIR ? (g & 1) ^ 1 : ((g >> 1) & 1) ^ 1;
         if (PAIR) {
-          for (int kb = 0; kb < NBLK && ok; ++kb) {
-            ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * kb, free_parity));
+          for (int kg = 0; kg < NBLK / KG && ok; ++kg) {
+            ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * kg, free_parity));
             if (!ok) break;
-            if (rank == 0 && lane == 0) mbar_expect_tx(k_full + 8 * kb, 2 * BLK_BYTES);
+            if (rank == 0 && lane == 0) mbar_expect_tx(k_full + 8 * kg, 2 * KG * BLK_BYTES);
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int off = (lane + 32 * i) << a.box_log2;
               // rows past the length only make scores that are masked
               if (off < 64)
-                tma_load_2d_pair(sK + kb * BLK_BYTES + off * 128, &m.c[a.box_log2], bar0 + 8 * kb,
-                                 kb * 64, row[i]);
+                for (int kb = kg * KG; kb < kg * KG + KG; ++kb)
+                  tma_load_2d_pair(sK + kb * BLK_BYTES + off * 128, &m.c[a.box_log2],
+                                   bar0 + 8 * kg, kb * 64, row[i]);
             }
           }
         } else {
@@ -382,8 +420,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // the loads issued here have landed before the CTA may exit
     if (g > 0) {
       if (PAIR) {
-        for (int kb = 0; kb < NBLK; ++kb)
-          mbar_wait((rank == 0 ? k_full : k_empty) + 8 * kb, (g - 1) & 1);
+        for (int kg = 0; kg < NBLK / KG; ++kg)
+          mbar_wait((rank == 0 ? k_full : k_empty) + 8 * kg, (g - 1) & 1);
       } else {
         for (int i = max(0, g - 2); i < g; ++i) mbar_wait(k_full + 8 * (i & 1), (i >> 1) & 1);
       }
@@ -433,51 +471,50 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (n > 0) mbar_wait(rank == 0 ? q_full : q_empty, (n - 1) & 1);
     }
   } else if (warp == 2) {
-    // ---------------- MMA issue (pair: the even CTA)
-    if (lane == 0 && rank == 0) {
+    // ---------------- MMA issue (pair: the even CTA).
+    if (rank == 0 && elect_one()) {
       constexpr uint32_t id_s = idesc_f16kind(PAIR ? 128 : 64, TILE, false, false, true);
       constexpr uint32_t id_o = idesc_f16kind(PAIR ? 128 : 64, 256, false, true, true);
-      auto mma = [](uint32_t d, uint64_t x, uint64_t y, uint32_t id, uint32_t acc) {
-        if (PAIR)
-          mma_bf16_pair(d, x, y, id, acc);
-        else
-          mma_bf16_ws(d, x, y, id, acc);
-      };
+      constexpr uint32_t BLK = BLK_BYTES >> 4;  // steps of descriptor addresses (16 bytes)
       auto commit = [](uint32_t bar) {
         if (PAIR)
           mma_commit_pair_mc(bar, uint16_t(3));
         else
           mma_commit(bar);
       };
+      const uint32_t q_lo = desc_lo_k(sQ), k_lo = desc_lo_k(sK), p_lo = desc_lo_k(sP);
+      const uint32_t v_lo = PAIR ? desc_lo_mn(sV, 32 * 128) : desc_lo_mn(sK, BLK_BYTES);
       // O (+)= P V of tile g
       auto second = [&](int g, bool first) -> bool {
-        if (!(PAIR ? mbar_wait_cluster(p_full, g & 1) : mbar_wait(p_full, g & 1))) return false;
+        if (!mbar_wait(p_full, g & 1)) return false;
         tc_fence_after();
+        const uint32_t acc0 = first ? 0 : 1;
         if (PAIR) {
+#pragma unroll
           for (int c = 0; c < 4; ++c) {
             if (!mbar_wait(v_full + 8 * c, g & 1)) return false;
             tc_fence_after();
+            {
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-              const int k16 = c * 2 + ks;
-              const uint64_t pd = desc_kmajor_sw128(sP + (k16 >> 2) * BLK_BYTES + (k16 & 3) * 32);
+              for (int ks = 0; ks < 2; ++ks) {
+                const int k16 = c * 2 + ks;
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                mma(tmem + j * 128, pd,
-                    desc_mn(sV + c * V_CHUNK + 2 * j * 32 * 128 + ks * 2048, 32 * 128), id_o,
-                    !(first && k16 == 0));
+                for (int j = 0; j < 2; ++j)
+                  mma_lo<PAIR>(tmem + j * 128, p_lo + (k16 >> 2) * BLK + (k16 & 3) * 2,
+                               v_lo + c * (V_CHUNK >> 4) + j * (2 * 32 * 128 >> 4) + ks * 128, id_o,
+                               k16 == 0 ? acc0 : 1);
+              }
+              commit(v_empty + 8 * c);
             }
-            commit(v_empty + 8 * c);
           }
         } else {
-          const uint32_t v = sK + (g & 1) * NBLK * BLK_BYTES;
+          const uint32_t v = v_lo + (g & 1) * NBLK * BLK;
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              mma(tmem + j * 128, desc_kmajor_sw128(sP + ks * 32),
-                  desc_mn(v + 4 * j * BLK_BYTES + ks * 2048, BLK_BYTES), id_o,
-                  !(first && ks == 0));
+              mma_lo<PAIR>(tmem + j * 128, p_lo + ks * 2, v + 4 * j * BLK + ks * 128, id_o,
+                           ks == 0 ? acc0 : 1);
           commit(k_empty + 8 * (g & 1));
         }
         commit(pv_done);
@@ -493,30 +530,49 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int sb = g & 1;
           ok = mbar_wait(s_empty + 8 * sb, ((g >> 1) & 1) ^ 1);
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + S_COL + sb * NC;
-          if (!PAIR) {
-            ok = mbar_wait(k_full + 8 * sb, (g >> 1) & 1);
+          const uint32_t d = tmem + S_COL + sb * SC;
+          // S of this tile goes ahead of P V of the one before, so that the
+          // softmax has the tensor pipe's time, unless its keys have yet to
+          // land: the P V that could run then also releases room for loads
+          // (waiting here first left the loads of one tile in flight at a time:
+          // 6000 clocks a tile against 3500)
+          bool behind = t > w.t0;
+          if (behind && !mbar_test(k_full + 8 * (PAIR ? 0 : sb), PAIR ? g & 1 : (g >> 1) & 1)) {
+            ok = second(g - 1, t - 1 == w.t0);
             if (!ok) break;
-            tc_fence_after();
+            behind = false;
           }
-          const uint32_t k = PAIR ? sK : sK + sb * NBLK * BLK_BYTES;
-          for (int kb = 0; kb < NBLK; ++kb) {
-            if (PAIR) {
-              ok = mbar_wait(k_full + 8 * kb, g & 1);
+          if (PAIR) {
+#pragma unroll
+            for (int kg = 0; kg < NBLK / KG; ++kg) {
+              ok = ok && mbar_wait(k_full + 8 * kg, g & 1);
               if (!ok) break;
               tc_fence_after();
-            }
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma(d, desc_kmajor_sw128(sQ + kb * BLK_BYTES + ks * 32),
-                  desc_kmajor_sw128(k + kb * BLK_BYTES + ks * 32), id_s, (kb | ks) != 0);
-            if (PAIR) commit(k_empty + 8 * kb);
+              for (int kb = kg * KG; kb < kg * KG + KG; ++kb)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  mma_lo<PAIR>(d, q_lo + kb * BLK + ks * 2, k_lo + kb * BLK + ks * 2, id_s,
+                               (kb | ks) != 0);
+              commit(k_empty + 8 * kg);
+            }
+          } else {
+            ok = mbar_wait(k_full + 8 * sb, (g >> 1) & 1);
+            tc_fence_after();
+            if (ok) {
+              const uint32_t k = k_lo + sb * NBLK * BLK;
+#pragma unroll
+              for (int kb = 0; kb < NBLK; ++kb)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  mma_lo<PAIR>(d, q_lo + kb * BLK + ks * 2, k + kb * BLK + ks * 2, id_s,
+                               (kb | ks) != 0);
+            }
           }
           if (!ok) break;
           commit(s_full + 8 * sb);
           if (t + 1 == w.t1) commit(q_empty);
-          if (t > w.t0) {
+          if (behind) {
             ok = second(g - 1, t - 1 == w.t0);
             if (!ok) break;
           }
@@ -529,18 +585,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= 4) {
-    // ---------------- softmax and epilogue
-    const int tid = threadIdx.x - 128;      // tensor-memory lane
-    const int half = tid >> 6, rl = tid & 63;
+    // ---------------- softmax and epilogue: four threads a row, each a
+    // quarter of the tile's keys (half: which half of D's columns its lanes
+    // hold; part: which half of those is this warp's)
+    const int tid = threadIdx.x - 128, tl = tid & 127;  // tl: tensor-memory lane
+    const int part = tid >> 7, half = tl >> 6, rl = tl & 63;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t s_empty_lead = lead(s_empty), p_full_lead = lead(p_full);
-    auto arrive = [&](uint32_t bar) {
-      if (PAIR)
-        mbar_arrive_cluster(bar);
-      else
-        mbar_arrive(bar);
-    };
     if (tid == 0 && rank == 0) a.desc[2 * cluster] = make_int4(0, 0, 0, 0);
+    // the value of the four threads of a row, by f
+    auto row_join = [&](float *x, float v, auto f) {
+      x[tid] = v;
+      softmax_barrier();
+      return f(f(v, x[tid ^ 64]), f(x[tid ^ 128], x[tid ^ 192]));
+    };
     Walk<PAIR> w(a, *share);
     int g = 0;
     bool ok = true;
@@ -556,9 +614,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         uint32_t s[NC];
-#pragma unroll
-        for (int c = 0; c < NC; c += 32)
-          tmem_ld32(t_lane + S_COL + sb * NC + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
+        const uint32_t t_s = t_lane + S_COL + sb * SC + part * NC;
+        if constexpr (PAIR)
+          tmem_ld32(t_s, s);
+        else
+          tmem_ld16(t_s, s);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
@@ -568,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           else
             mbar_arrive(s_empty + 8 * sb);
         }
-        const int nvis = vis - t * TILE - half * NC;
+        const int nvis = vis - t * TILE - half * SC - part * NC;
         if (nvis < NC) {
 #pragma unroll
           for (int c = 0; c < NC; ++c)
@@ -577,11 +637,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
         for (int c = 0; c < NC; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        xmax[sb * 128 + tid] = mine;
-        softmax_barrier();
-        const float mt = fmaxf(mine, xmax[sb * 128 + (tid ^ 64)]) * a.scale_log2;
-        // both threads of a row see the same maxima and decide alike
+        const float mt = row_join(xmax + sb * 256, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                  [](float x, float y) { return fmaxf(x, y); }) *
+                         a.scale_log2;
+        // the threads of a row see the same maxima and decide alike
         float f = 1.f;
         if (mt > mref + RESCALE || (is_neg_inf(mref) && mt > mref)) {
           f = exp2_fast(mref - mt);  // 0 from -inf
@@ -607,19 +666,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         if (t > w.t0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
+          for (int c = 0; c < 128; c += 32) {
             uint32_t o[32];
-            tmem_ld32(t_lane + c, o);
+            tmem_ld32(t_lane + part * 128 + c, o);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(t_lane + c, o);
+            tmem_st32(t_lane + part * 128 + c, o);
           }
           tmem_wait_st();
         }
         // P, K-major with 128-byte swizzle, 64 keys a block
         const uint32_t prow = sP + (PAIR ? half * BLK_BYTES : 0) + rl * 128;
-        const int c0 = PAIR ? 0 : half * 4;
+        const int c0 = (PAIR ? 0 : half * 4) + part * (NC / 8);
 #pragma unroll
         for (int c = 0; c < NC / 8; ++c)
           st_shared_v4(prow + (((c0 + c) ^ (rl & 7)) << 4),
@@ -627,74 +686,98 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive(p_full_lead);
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_remote(p_full_lead);
+          else
+            mbar_arrive(p_full);
+        }
       }
       if (!ok) break;
       // ---- the piece's rows
-      xmax[((g & 1) * 128) + tid] = l;  // (the other buffer may still be read)
-      softmax_barrier();
-      l += xmax[((g & 1) * 128) + (tid ^ 64)];
-      softmax_barrier();
+      l = row_join(xmax + (g & 1) * 256, l, [](float x, float y) { return x + y; });
+      const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f || l != l ? mref + log2f(l) : neg_inf();
+      const int64_t grow0 = int64_t(w.s.q0) * a.H + w.rt * C::UROWS;  // the unit's first row
+      const int slot = 2 * cluster + (w.t0 == 0 ? 1 : 0);
+      const int64_t srow = int64_t(slot) * C::UROWS + int(rank) * CROWS;
+      if (half == 0 && part == 0) {
+        const int64_t grow = grow0 + urow;
+        if (!whole)
+          a.part_lse[srow + rl] = lse2;
+        else if (urow < rows && a.lse)
+          a.lse[int64_t(grow % a.H) * a.T + grow / a.H] = lse2 * LN2;
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1));
       if (!ok) break;
       tc_fence_after();
-      const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
-      const bool live = urow < rows;
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f || l != l ? mref + log2f(l) : neg_inf();
-      const int64_t grow = int64_t(w.s.q0) * a.H + w.rt * C::UROWS + urow;
-      const int slot = 2 * cluster + (w.t0 == 0 ? 1 : 0);
-      // scratch of a slot and CTA: [512/4][64 rows][4], so that the lanes of a
-      // warp write one contiguous piece
-      const int64_t srow = int64_t(slot) * C::UROWS + int(rank) * CROWS;
-      float4 *part = reinterpret_cast<float4 *>(a.part_o + srow * LAT) + rl;
+      // D's columns: part 0 holds the first MMA's, part 1 the second's
+      const int dim0 = PAIR ? half * 256 + part * 128 : part * 256 + half * 128;
+      if (whole) {
+        // through shared memory (P's room), EC columns of all four quarters at
+        // a time, so that whole sectors are written
+        constexpr int EC = PAIR ? 32 : 16, PIECES = EC / 8;
+        const uint32_t stage = sP + (tid >> 6) * (64 * EC * 2);
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(t_lane + c, o);
-        tmem_wait_ld();
-        const int j = c >> 7, cc = c & 127;
-        const int dim = PAIR ? half * 256 + j * 128 + cc : j * 256 + half * 128 + cc;
-        if (whole) {
-          if (live) {
-            __nv_bfloat16 *dst = a.o + grow * LAT + dim;
+        for (int c = 0; c < 128; c += EC) {
+          uint32_t o[EC];
+          if constexpr (PAIR)
+            tmem_ld32(t_lane + part * 128 + c, o);
+          else
+            tmem_ld16(t_lane + part * 128 + c, o);
+          tmem_wait_ld();
+          if (c > 0) softmax_barrier();  // the stage has been read
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t v[4];
+          for (int e = 0; e < PIECES; ++e) {
+            uint32_t v[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float x = __uint_as_float(o[e + 2 * k]), y = __uint_as_float(o[e + 2 * k + 1]);
-                v[k] = inv == 0.f ? 0u : pack_bf16(x * inv, y * inv);
-              }
-              *reinterpret_cast<uint4 *>(dst + e) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int k = 0; k < 4; ++k) {
+              const float x = __uint_as_float(o[8 * e + 2 * k]), y = __uint_as_float(o[8 * e + 2 * k + 1]);
+              v[k] = inv == 0.f ? 0u : pack_bf16(x * inv, y * inv);
             }
+            const int sw = PAIR ? (rl >> 1) & 3 : (rl >> 2) & 1;  // spreads the banks
+            st_shared_v4(stage + rl * (EC * 2) + ((e ^ sw) << 4), make_uint4(v[0], v[1], v[2], v[3]));
           }
-        } else {
+          softmax_barrier();
+#pragma unroll
+          for (int k = 0; k < PIECES; ++k) {
+            const int x = k * STHREADS + tid;  // quarter, row, piece
+            const int qt = x / (64 * PIECES), r = x / PIECES % 64, e = x % PIECES;
+            const int row = int(rank) * CROWS + r;
+            const int sw = PAIR ? (r >> 1) & 3 : (r >> 2) & 1;
+            const int d = PAIR ? (qt & 1) * 256 + (qt >> 1) * 128 : (qt >> 1) * 256 + (qt & 1) * 128;
+            if (row < rows)
+              *reinterpret_cast<uint4 *>(a.o + (grow0 + row) * LAT + d + c + e * 8) =
+                  ld_shared_v4(sP + qt * (64 * EC * 2) + r * (EC * 2) + ((e ^ sw) << 4));
+          }
+        }
+      } else {
+        // scratch of a slot and CTA: [512/4][64 rows][4], so that the lanes of
+        // a warp write one contiguous piece
+        float4 *dst = reinterpret_cast<float4 *>(a.part_o + srow * LAT) + rl;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(t_lane + part * 128 + c, o);
+          tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = inv == 0.f ? 0.f : __uint_as_float(o[e + k]) * inv;
-            part[((dim + e) / 4) * CROWS] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[((dim0 + c + e) / 4) * CROWS] = make_float4(v[0], v[1], v[2], v[3]);
           }
+        }
+        if (w.t0 == 0 && tid == 0 && rank == 0) {
+          // the unit's first piece: its others are in the shares that follow
+          const long long rest = w.s.tiles - w.t1;
+          a.desc[2 * cluster] =
+              make_int4(1 + int((rest + share->share - 1) / share->share), min(rows, C::UROWS), 0, 0);
+          *reinterpret_cast<long long *>(a.desc + 2 * cluster + 1) = grow0;
         }
       }
       tc_fence_before();  // the reads of O come before the next piece's P is handed over
-      if (half == 0) {
-        if (whole) {
-          if (live && a.lse) a.lse[int64_t(grow % a.H) * a.T + grow / a.H] = lse2 * LN2;
-        } else {
-          a.part_lse[srow + rl] = lse2;
-        }
-      }
-      if (!whole && w.t0 == 0 && tid == 0 && rank == 0) {
-        // the unit's first piece: its others are in the shares that follow
-        const long long rest = w.s.tiles - w.t1;
-        a.desc[2 * cluster] =
-            make_int4(1 + int((rest + share->share - 1) / share->share), min(rows, C::UROWS), 0, 0);
-        *reinterpret_cast<long long *>(a.desc + 2 * cluster + 1) =
-            int64_t(w.s.q0) * a.H + w.rt * C::UROWS;
-      }
     }
   }
   tc_fence_before();
@@ -713,117 +796,139 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Joins the pieces of cut units: o = sum_i w_i o_i / sum_i w_i with w_i =
-// 2^(lse_i - max).  An item is 16 rows x 16 columns of one unit; the block's
-// threads are 16 rows x 4 float4 columns x 4 quarters of the pieces.  The
-// blocks find the cut units from the clusters' descriptors.
-constexpr int CT = 256;
+// 2^(lse_i - max).  A warp takes 32 rows and 4 * W columns of a unit, U pieces
+// at a time: W * U = 16 loads of 16 bytes a thread in flight, which is what
+// this kernel lives on.  Units of few pieces take wide items, those of many
+// pieces (one long sequence) narrow ones, of which there are more.
+template <int W, int U>
+__device__ __forceinline__ void join(const float *part_o, const float *part_lse, int c0, int n,
+                                     int urows, int row, int col4, bool live, int64_t grow,
+                                     __nv_bfloat16 *o, float *lse, int H, int T) {
+  float mx = neg_inf(), sum = 0.f;
+  float4 acc[W];
+#pragma unroll
+  for (int k = 0; k < W; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += U) {
+    float ls[U];
+    float4 v[U][W];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u;
+      ls[u] = neg_inf();
+      if (i < n) {
+        const int64_t s = int64_t(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * urows + (row & ~63);
+        ls[u] = part_lse[s + (row & 63)];
+        const float4 *src = reinterpret_cast<const float4 *>(part_o + s * LAT) + (row & 63);
+#pragma unroll
+        for (int k = 0; k < W; ++k) v[u][k] = src[(col4 + k) * CROWS];
+      } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k) v[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    float mn = mx;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, ls[u]);
+    const float bs = is_neg_inf(mn) ? 0.f : mn;
+    const float f = exp2_fast(mx - bs);
+    mx = mn;
+    sum *= f;
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+      acc[k] = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = exp2_fast(ls[u] - bs);
+      sum += w;
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        acc[k].x = fmaf(w, v[u][k].x, acc[k].x);
+        acc[k].y = fmaf(w, v[u][k].y, acc[k].y);
+        acc[k].z = fmaf(w, v[u][k].z, acc[k].z);
+        acc[k].w = fmaf(w, v[u][k].w, acc[k].w);
+      }
+    }
+  }
+  if (!live) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint2 out[W];
+#pragma unroll
+  for (int k = 0; k < W; ++k)
+    out[k] = make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv),
+                        pack_bf16(acc[k].z * inv, acc[k].w * inv));
+  __nv_bfloat16 *dst = o + grow * LAT + col4 * 4;
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int k = 0; k < W; k += 2)
+      *reinterpret_cast<uint4 *>(dst + 4 * k) =
+          make_uint4(out[k].x, out[k].y, out[k + 1].x, out[k + 1].y);
+  } else {
+    *reinterpret_cast<uint2 *>(dst) = out[0];
+  }
+  if (lse && col4 == 0)
+    lse[int64_t(grow % H) * T + grow / H] =
+        sum == 0.f ? neg_inf() : ((is_neg_inf(mx) ? 0.f : mx) + log2f(sum)) * LN2;
+}
+
+constexpr int CT = 256;          // threads of a combine block; clusters <= CT
+constexpr int WIDE_PIECES = 8;   // units of at most this many pieces take wide items
 __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, int clusters,
                                                             int urows, const float *part_o,
                                                             const float *part_lse,
                                                             __nv_bfloat16 *o, float *lse, int H,
                                                             int T) {
-  __shared__ int units[256];
-  __shared__ float4 sacc[3][64];
-  __shared__ float smax[3][64], ssum[3][64];
-  // the cut units, in cluster order whatever the order of the warps
-  const bool cut = int(threadIdx.x) < clusters && desc[2 * threadIdx.x].x > 0;
-  const uint32_t b = __ballot_sync(0xffffffffu, cut);
+  // the cut units (cluster of the first piece) and the items before each
+  __shared__ int units[CT], first[CT + 1], warp_units[CT / 32], warp_items[CT / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ int per_warp[CT / 32];
-  if (lane == 0) per_warp[warp] = __popc(b);
-  __syncthreads();
-  int base = 0, total = 0;
-  for (int i = 0; i < CT / 32; ++i) {
-    if (i < warp) base += per_warp[i];
-    total += per_warp[i];
+  const int n_here = int(threadIdx.x) < clusters ? desc[2 * threadIdx.x].x : 0;
+  const int items = n_here == 0 ? 0 : (urows / 32) * (n_here <= WIDE_PIECES ? 16 : 128);
+  int inc = items;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += v;
   }
-  if (cut) units[base + __popc(b & ((1u << lane) - 1))] = threadIdx.x;
+  const uint32_t b = __ballot_sync(0xffffffffu, items > 0);
+  if (lane == 31) {
+    warp_units[warp] = __popc(b);
+    warp_items[warp] = inc;
+  }
   __syncthreads();
-  const int row_groups = urows / 16, items = row_groups * 32;
-  const int quarter = threadIdx.x >> 6, k = threadIdx.x & 63, rr = k & 15, cq = k >> 4;
-  for (int it = blockIdx.x; it < total * items; it += gridDim.x) {
-    const int c0 = units[it / items], sub = it % items;
-    const int row = (sub >> 5) * 16 + rr, col4 = (sub & 31) * 4 + cq;
+  int ubase = 0, ibase = 0, num = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < CT / 32; ++i) {
+    if (i < warp) {
+      ubase += warp_units[i];
+      ibase += warp_items[i];
+    }
+    num += warp_units[i];
+    total += warp_items[i];
+  }
+  if (items > 0) {
+    const int u = ubase + __popc(b & ((1u << lane) - 1));
+    units[u] = threadIdx.x;
+    first[u] = ibase + inc - items;
+  }
+  __syncthreads();
+  for (int it = blockIdx.x * (CT / 32) + warp; it < total; it += gridDim.x * (CT / 32)) {
+    int lo = 0, hi = num - 1;  // the unit of this item
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= it)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int c0 = units[lo], sub = it - first[lo];
     const int4 d = desc[2 * c0];
-    const int n = d.x;
     const int64_t grow0 = *reinterpret_cast<const long long *>(desc + 2 * c0 + 1);
-    auto slot_row = [&](int i) {
-      return int64_t(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * urows + (row & ~63);
-    };
-    float mx = neg_inf(), sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = quarter; i0 < n; i0 += 16) {  // four pieces at a time
-      float ls[4];
-      float4 v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + 4 * u;
-        ls[u] = neg_inf();
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < n) {
-          const int64_t s = slot_row(i);
-          ls[u] = part_lse[s + (row & 63)];
-          v[u] = *(reinterpret_cast<const float4 *>(part_o + s * LAT) + col4 * CROWS + (row & 63));
-        }
-      }
-      float mn = mx;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ls[u]);
-      const float bs = is_neg_inf(mn) ? 0.f : mn;
-      const float f = exp2_fast(mx - bs);
-      sum *= f;
-      acc.x *= f;
-      acc.y *= f;
-      acc.z *= f;
-      acc.w *= f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float w = exp2_fast(ls[u] - bs);
-        sum += w;
-        acc.x = fmaf(w, v[u].x, acc.x);
-        acc.y = fmaf(w, v[u].y, acc.y);
-        acc.z = fmaf(w, v[u].z, acc.z);
-        acc.w = fmaf(w, v[u].w, acc.w);
-      }
-      mx = mn;
-    }
-    if (quarter > 0) {
-      sacc[quarter - 1][k] = acc;
-      smax[quarter - 1][k] = mx;
-      ssum[quarter - 1][k] = sum;
-    }
-    __syncthreads();
-    if (quarter == 0) {
-      float mn = mx;
-#pragma unroll
-      for (int i = 0; i < 3; ++i) mn = fmaxf(mn, smax[i][k]);
-      const float bs = is_neg_inf(mn) ? 0.f : mn;
-      float f = exp2_fast(mx - bs);
-      sum *= f;
-      acc.x *= f;
-      acc.y *= f;
-      acc.z *= f;
-      acc.w *= f;
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        f = exp2_fast(smax[i][k] - bs);
-        sum = fmaf(f, ssum[i][k], sum);
-        acc.x = fmaf(f, sacc[i][k].x, acc.x);
-        acc.y = fmaf(f, sacc[i][k].y, acc.y);
-        acc.z = fmaf(f, sacc[i][k].z, acc.z);
-        acc.w = fmaf(f, sacc[i][k].w, acc.w);
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (row < d.y) {
-        const int64_t grow = grow0 + row;
-        const uint2 out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
-                                     pack_bf16(acc.z * inv, acc.w * inv));
-        *reinterpret_cast<uint2 *>(o + grow * LAT + col4 * 4) = out;
-        if (lse && col4 == 0)
-          lse[int64_t(grow % H) * T + grow / H] = sum == 0.f ? neg_inf() : (bs + log2f(sum)) * LN2;
-      }
-    }
-    __syncthreads();
+    const bool wide = d.x <= WIDE_PIECES;
+    const int cols = wide ? 16 : 128;
+    const int row = (sub / cols) * 32 + lane, cg = sub % cols;
+    if (wide)
+      join<8, 2>(part_o, part_lse, c0, d.x, urows, row, cg * 8, row < d.y, grow0 + row, o, lse, H, T);
+    else
+      join<1, 16>(part_o, part_lse, c0, d.x, urows, row, cg, row < d.y, grow0 + row, o, lse, H, T);
   }
 }
 
@@ -867,7 +972,7 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
   if (rc) return rc;
   const int clusters = PAIR ? grid / 2 : grid;
   launch_begin(s);
-  latent_combine_kernel<<<2 * num_sms(), CT, 0, s>>>(a.desc, clusters, Cfg<PAIR>::UROWS, a.part_o,
+  latent_combine_kernel<<<4 * num_sms(), CT, 0, s>>>(a.desc, clusters, Cfg<PAIR>::UROWS, a.part_o,
                                                      a.part_lse, a.o, a.lse, a.H, a.T);
   return launch_status(s, "latent_combine_kernel");
 }
