@@ -12,20 +12,25 @@
 //     in the layout where lanes 0-63 have the rows with one half of D's
 //     columns and lanes 64-127 the same rows with the other half.  Softmax
 //     threads of lanes l and l+64 share row l, each with half of the keys.
-//   * an MMA of K=16 takes at least 44.6 clocks whatever its size (measured),
-//     and the operands' shared-memory reads 1 clock per 128 bytes.
+//   * an MMA takes a clock per 128 bytes that it reads from shared memory, when
+//     that is more than its products do (measured: M=64, N=64, K=16 of the
+//     single form 32 clocks, N=256 80; pair M=128 N=64 25, N=256 64), so S,
+//     with its small N, is bound by re-reading the queries.
 // Two forms (template parameter):
-//   single (rows of a unit: 64)  one CTA, weight-stationary MMAs of M=64;
-//          tiles of 64 keys, two stages; a stage serves as K (K-major, 9
-//          blocks of 64 columns) and as V (the first 8 blocks, MN-major).
+//   single (rows of a unit: 64)  one CTA, weight-stationary MMAs of M=64; a
+//          stage serves as K (K-major, 9 blocks of 64 columns) and as V (the
+//          first 8 blocks, MN-major).
 //   pair   (rows: 128)  a cluster of two CTAs, cta_group::2 MMAs of M=128 (64
-//          rows in each), tiles of 128 keys.  Each CTA holds its 64 keys of K
-//          (9 blocks) and its 256 columns of V for all 128 keys, in two rings
-//          refilled block by block as the MMAs release them (one tile's worth
-//          each: there is no room for two).
-// Work split: the keys of all units (sequence, 64 or 128 rows) are laid end to
-// end in tiles and dealt out in equal contiguous shares, one per cluster, by
-// the kernel itself from the lengths on the device.  A unit that lies in one
+//          rows in each).  An operand of such an MMA sits at the same offset
+//          in both CTAs, so V (each CTA 256 columns of all keys) cannot share
+//          the place of K (each CTA all columns of half of the keys).
+//   Both take 64 keys at a time from two stages.  (128 keys a tile halve the
+//   reads of the queries in the pair form, but leave room for one stage: S,
+//   softmax and P V then follow each other, 4840 clocks per 128 keys.)
+// Work split: the units (sequence, 64 or 128 rows) are laid end to end, each
+// as long as its key tiles and a constant for its start and end, and dealt out
+// in equal contiguous shares, one per cluster, by the kernel itself from the
+// lengths on the device.  A unit that lies in one
 // share is written directly; the pieces of a cut one go to scratch as
 // normalised float32 with their log-sums, and latent_combine_kernel joins
 // them.
@@ -54,22 +59,25 @@ constexpr float LN2 = 0.69314718055994531f;
 // without loss.
 constexpr float RESCALE = 8.f;
 
+constexpr int TILE = 64;     // keys
+constexpr int SC = TILE / 2; // S columns in tensor memory
+constexpr int NC = SC / 2;   // of a softmax thread
 template <bool PAIR>
 struct Cfg {
-  static constexpr int TILE = PAIR ? 128 : 64;  // keys
-  static constexpr int UROWS = PAIR ? 128 : 64; // rows of a unit
-  static constexpr int SC = TILE / 2;           // S columns in tensor memory
-  static constexpr int NC = SC / 2;             // of a softmax thread
-  static constexpr int KV_BYTES = PAIR ? NBLK * BLK_BYTES + 4 * 2 * BLK_BYTES : 2 * NBLK * BLK_BYTES;
-  static constexpr int P_BYTES = CROWS * TILE * 2;
-  static constexpr int USED = Q_BYTES + KV_BYTES + P_BYTES + 2048 + 52 * 8;
+  static constexpr int UROWS = PAIR ? 128 : 64;     // rows of a unit
+  static constexpr int KROWS = PAIR ? 32 : 64;      // keys of a tile in a CTA's K
+  static constexpr int K_STAGE = NBLK * KROWS * 128;
+  static constexpr int V_STAGE = PAIR ? 4 * BLK_BYTES : 0;
+  static constexpr int NP = PAIR ? 2 : 1;           // P buffers
+  static constexpr int KV_BYTES = 2 * (K_STAGE + V_STAGE);
+  static constexpr int P_BYTES = NP * BLK_BYTES;
+  static constexpr int USED = Q_BYTES + KV_BYTES + P_BYTES + 2048 + 40 * 8;
   static constexpr int SMEM = 232448;  // all of it; the rest is room for alignment
-  // a share has at least this many tiles: shorter ones cost more in scratch
-  // traffic and joining than they save
-  static constexpr int MIN_TILES = PAIR ? 2 : 4;
 };
-constexpr int KG = 3;  // pair: K is loaded and released in groups of 3 column blocks
-constexpr int V_CHUNK = 4 * 32 * 128;  // pair: 32 keys x 256 columns of V
+// What a unit costs beyond its tiles (queries in, rows out: about 4500 clocks),
+// in tiles (2500-3700 clocks), and the least that a share is worth: shorter
+// ones cost more in scratch traffic and joining than they save.
+constexpr int UNIT_COST = 2, MIN_SHARE = 6;
 
 struct Maps {
   CUtensorMap q;
@@ -99,30 +107,32 @@ __device__ __forceinline__ Seq load_seq(const LatentArgs &a, int r) {
   s.len = max(__ldg(a.seq_lens + r), 0);
   s.nrt = (s.nq * a.H + Cfg<PAIR>::UROWS - 1) / Cfg<PAIR>::UROWS;
   // a unit without keys still has its rows to write
-  s.tiles = max(1, (s.len + Cfg<PAIR>::TILE - 1) / Cfg<PAIR>::TILE);
+  s.tiles = max(1, (s.len + TILE - 1) / TILE);
   return s;
 }
 
 struct Share {  // of a cluster, in shared memory
   long long len, share;
-  int r, rt, tile;
+  int r, rt, pos;
 };
 
-// Piece of a unit: row tile rt of sequence r, key tiles [t0, t1).
+// Piece of a unit: row tile rt of sequence r, key tiles [t0, t1).  Position v
+// of a unit is its tile v - UNIT_COST: a share that ends (or starts) in the
+// first UNIT_COST positions has none (or all) of the unit's tiles.
 template <bool PAIR>
 struct Walk {
   const LatentArgs &a;
   Seq s;
-  int r, rt, t0, t1, next_tile;
+  int r, rt, t0, t1, pos;
   long long left;
   __device__ __forceinline__ Walk(const LatentArgs &args, const Share &sh)
-      : a(args), r(sh.r), rt(sh.rt), t0(0), t1(0), next_tile(sh.tile), left(sh.len) {
+      : a(args), r(sh.r), rt(sh.rt), t0(0), t1(0), pos(sh.pos), left(sh.len) {
     if (left > 0) s = load_seq<PAIR>(a, r);
   }
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
-    if (t1 > 0 && t1 == s.tiles) {  // the previous piece ended its unit
-      next_tile = 0;
+    if (t1 > 0) {  // the previous piece ended its unit (or left would be 0)
+      pos = 0;
       if (++rt == s.nrt) {
         rt = 0;
         do {
@@ -131,10 +141,11 @@ struct Walk {
         } while (s.nrt == 0);
       }
     }
-    t0 = next_tile;
-    t1 = int(min((long long)s.tiles, t0 + left));
-    left -= t1 - t0;
-    return true;
+    const int take = int(min((long long)(s.tiles + UNIT_COST - pos), left));
+    t0 = max(0, pos - UNIT_COST);
+    t1 = max(0, pos + take - UNIT_COST);
+    left -= take;
+    return t1 > t0;
   }
 };
 
@@ -147,7 +158,7 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
   auto work = [&](int r) -> long long {
     if (r >= a.R) return 0;
     const Seq s = load_seq<PAIR>(a, r);
-    return (long long)s.nrt * s.tiles;
+    return (long long)s.nrt * (s.tiles + UNIT_COST);
   };
   long long mine = 0;
   const long long first = work(threadIdx.x);
@@ -161,12 +172,12 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
 #pragma unroll
   for (int w = 0; w < NW; ++w) total += scratch[w];
   long long share = (total + clusters - 1) / clusters;
-  if (share < Cfg<PAIR>::MIN_TILES) share = Cfg<PAIR>::MIN_TILES;
+  if (share < MIN_SHARE) share = MIN_SHARE;
   const long long start = share * cluster;
   if (threadIdx.x == 0) {
     out->share = share;
     out->len = max(0LL, min(share, total - start));
-    out->r = out->rt = out->tile = 0;
+    out->r = out->rt = out->pos = 0;
   }
   __syncthreads();
   if (start >= total) return;
@@ -190,10 +201,10 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
     }
     const long long lo = before + inc - w;
     if (w > 0 && start >= lo && start < lo + w) {
-      const int tiles = load_seq<PAIR>(a, r).tiles;
+      const int length = load_seq<PAIR>(a, r).tiles + UNIT_COST;
       out->r = r;
-      out->rt = int((start - lo) / tiles);
-      out->tile = int((start - lo) % tiles);
+      out->rt = int((start - lo) / length);
+      out->pos = int((start - lo) % length);
     }
     base += all;
     __syncthreads();
@@ -302,7 +313,6 @@ template <bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ Maps m, const LatentArgs a) {
   using C = Cfg<PAIR>;
-  constexpr int TILE = C::TILE, SC = C::SC, NC = C::NC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -311,19 +321,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) atomicOr(&g_error_flags, kErrWaitTimeout);
     return;
   }
-  const uint32_t sQ = smem_u32(smem), sK = sQ + Q_BYTES, sV = sK + NBLK * BLK_BYTES,
+  const uint32_t sQ = smem_u32(smem), sK = sQ + Q_BYTES, sV = sK + 2 * C::K_STAGE,
                  sP = sK + C::KV_BYTES;
   float *xmax = reinterpret_cast<float *>(smem + Q_BYTES + C::KV_BYTES + C::P_BYTES);  // [2][256]
   uint64_t *bars = reinterpret_cast<uint64_t *>(xmax + 512);
-  // k_full[9] k_empty[9] v_full[4] v_empty[4] (single: k_*[2] are the stages),
-  // q_full q_empty, s_full[2] s_empty[2], p_full, pv_done, done
-  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 72, v_full = k_full + 144,
-                 v_empty = v_full + 32, q_full = v_empty + 32, q_empty = q_full + 8,
-                 s_full = q_empty + 8, s_empty = s_full + 16, p_full = s_empty + 16,
-                 pv_done = p_full + 8, done = pv_done + 8;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 35);
-  Share *share = reinterpret_cast<Share *>(bars + 36);        // 28 bytes
-  long long *scan = reinterpret_cast<long long *>(bars + 40);  // [12]
+  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 16, v_full = k_full + 32,
+                 v_empty = k_full + 48, s_full = k_full + 64, s_empty = k_full + 80,
+                 p_full = k_full + 96, pv_done = k_full + 112, q_full = k_full + 128,
+                 q_empty = k_full + 136, done = k_full + 144;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
+  Share *share = reinterpret_cast<Share *>(bars + 20);         // 28 bytes
+  long long *scan = reinterpret_cast<long long *>(bars + 24);  // [12]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;
@@ -332,22 +340,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto lead = [&](uint32_t bar) { return PAIR ? mapa_shared(bar, 0) : bar; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NBLK; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_empty + 8 * i, 1);
-    }
-    for (int i = 0; i < 4; ++i) {
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_empty + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
+      mbar_init(p_full + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
+      mbar_init(pv_done + 8 * i, 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(s_empty + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
-    }
-    mbar_init(p_full, PAIR ? 2 * SWARPS : SWARPS);
-    mbar_init(pv_done, 1);
     mbar_init(done, 1);
     fence_mbar_init();
     prefetch_map(&m.q);
@@ -367,93 +371,47 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   const int box = 1 << a.box_log2, none = a.num_blocks * a.bs;
 
-  if (warp == 0) {
-    // ---------------- K (single: and V) loads, whole warp
+  if (warp == 0 || (PAIR && warp == 1)) {
+    // ---------------- K loads (single: which are V too) and V loads, one warp
+    // each: a lane has the boxes of row groups lane and lane + 32
+    const bool is_v = PAIR && warp == 1;
+    const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
+    const uint32_t full_lead = lead(full);
+    const uint32_t dst0 = is_v ? sV : sK, stage_bytes = is_v ? C::V_STAGE : C::K_STAGE;
+    const int nrows = is_v ? 64 : C::KROWS, blocks = is_v ? 4 : NBLK;
+    const int skip = PAIR && !is_v ? int(rank) * C::KROWS : 0;  // first key of the tile here
+    const int x0 = is_v ? int(rank) * 256 : 0;
     Walk<PAIR> w(a, *share);
     int g = 0;
     bool ok = true;
-    const uint32_t bar0 = lead(k_full);
     while (ok && w.next()) {
       const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
-      for (int t = w.t0; t < w.t1 && ok; ++t, ++g) {
-        const int key0 = t * TILE + int(rank) * 64;  // this CTA's 64 keys
+      for (int t = w.t0; t < w.t1; ++t, ++g) {
+        const int key0 = t * TILE + skip, st = g & 1;
         int row[2], valid[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // lane l: row groups l and l + 32
+        for (int i = 0; i < 2; ++i) {
           const int off = (lane + 32 * i) << a.box_log2;
-          row[i] = off < 64 ? cache_row(a, bt, w.s.len, key0 + off) : none;
-          valid[i] = row[i] == none ? 0 : min(box, w.s.len - key0 - off);
+          row[i] = off < nrows ? cache_row(a, bt, w.s.len, key0 + off) : none;
+          // (a row past the length in K alone only makes scores that are masked)
+          valid[i] = row[i] == none ? 0 : PAIR && !is_v ? box : min(box, w.s.len - key0 - off);
         }
-        const int st = PAIR ? 0 : g & 1;
-        const uint32_t free_parity = PAIR ? (g & 1) ^ 1 : ((g >> 1) & 1) ^ 1;
-        if (PAIR) {
-          for (int kg = 0; kg < NBLK / KG && ok; ++kg) {
-            ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * kg, free_parity));
-            if (!ok) break;
-            if (rank == 0 && lane == 0) mbar_expect_tx(k_full + 8 * kg, 2 * KG * BLK_BYTES);
-            __syncwarp();
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((g >> 1) & 1) ^ 1));
+        if (!ok) break;
+        if (rank == 0 && lane == 0) mbar_expect_tx(full + 8 * st, (PAIR ? 2 : 1) * stage_bytes);
+        __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int off = (lane + 32 * i) << a.box_log2;
-              // rows past the length only make scores that are masked
-              if (off < 64)
-                for (int kb = kg * KG; kb < kg * KG + KG; ++kb)
-                  tma_load_2d_pair(sK + kb * BLK_BYTES + off * 128, &m.c[a.box_log2],
-                                   bar0 + 8 * kg, kb * 64, row[i]);
-            }
-          }
-        } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * st, free_parity));
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(k_full + 8 * st, NBLK * BLK_BYTES);
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int off = (lane + 32 * i) << a.box_log2;
-            if (off < 64)
-              load_rows<PAIR>(m, a.box_log2, sK + st * NBLK * BLK_BYTES + off * 128, BLK_BYTES,
-                              NBLK, 0, row[i], valid[i], none, k_full + 8 * st);
-          }
+        for (int i = 0; i < 2; ++i) {
+          const int off = (lane + 32 * i) << a.box_log2;
+          if (off < nrows)
+            load_rows<PAIR>(m, a.box_log2, dst0 + st * stage_bytes + off * 128, nrows * 128, blocks,
+                            x0, row[i], valid[i], none, full_lead + 8 * st);
         }
       }
     }
     // the loads issued here have landed before the CTA may exit
-    if (g > 0) {
-      if (PAIR) {
-        for (int kg = 0; kg < NBLK / KG; ++kg)
-          mbar_wait((rank == 0 ? k_full : k_empty) + 8 * kg, (g - 1) & 1);
-      } else {
-        for (int i = max(0, g - 2); i < g; ++i) mbar_wait(k_full + 8 * (i & 1), (i >> 1) & 1);
-      }
-    }
-  } else if (warp == 1 && PAIR) {
-    // ---------------- V loads: 256 columns of all keys, 32 keys at a time
-    Walk<PAIR> w(a, *share);
-    int g = 0;
-    bool ok = true;
-    const uint32_t bar0 = lead(v_full);
-    while (ok && w.next()) {
-      const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
-      for (int t = w.t0; t < w.t1 && ok; ++t, ++g) {
-        for (int c = 0; c < 4 && ok; ++c) {
-          const int key0 = t * TILE + c * 32, off = lane << a.box_log2;
-          int row = none, valid = 0;
-          if (off < 32) {
-            row = cache_row(a, bt, w.s.len, key0 + off);
-            valid = row == none ? 0 : min(box, w.s.len - key0 - off);
-          }
-          ok = __all_sync(0xffffffffu, mbar_wait(v_empty + 8 * c, (g & 1) ^ 1));
-          if (!ok) break;
-          if (rank == 0 && lane == 0) mbar_expect_tx(v_full + 8 * c, 2 * V_CHUNK);
-          __syncwarp();
-          if (off < 32)
-            load_rows<PAIR>(m, a.box_log2, sV + c * V_CHUNK + off * 128, 32 * 128, 4,
-                            int(rank) * 256, row, valid, none, bar0 + 8 * c);
-        }
-      }
-    }
-    if (g > 0)
-      for (int c = 0; c < 4; ++c) mbar_wait((rank == 0 ? v_full : v_empty) + 8 * c, (g - 1) & 1);
+    for (int i = max(0, g - 2); i < g; ++i)
+      mbar_wait((rank == 0 ? full : empty) + 8 * (i & 1), (i >> 1) & 1);
   } else if (warp == 3) {
     // ---------------- query loads
     if (lane == 0) {
@@ -483,103 +441,79 @@ __global__ void __launch_bounds__(THREADS, 1)
           mma_commit(bar);
       };
       const uint32_t q_lo = desc_lo_k(sQ), k_lo = desc_lo_k(sK), p_lo = desc_lo_k(sP);
-      const uint32_t v_lo = PAIR ? desc_lo_mn(sV, 32 * 128) : desc_lo_mn(sK, BLK_BYTES);
+      // V: blocks of 64 columns BLK_BYTES apart, MN-major
+      const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, BLK_BYTES);
+      constexpr uint32_t K_STEP = C::K_STAGE >> 4, V_STEP = (PAIR ? C::V_STAGE : C::K_STAGE) >> 4;
+      constexpr uint32_t KBLK = C::KROWS * 128 >> 4;
       // O (+)= P V of tile g
       auto second = [&](int g, bool first) -> bool {
-        if (!mbar_wait(p_full, g & 1)) return false;
+        const int st = g & 1;
+        const uint32_t parity = (g >> 1) & 1;
+        if (PAIR && !mbar_wait(v_full + 8 * st, parity)) return false;
+        if (!mbar_wait(p_full + 8 * st, parity)) return false;
         tc_fence_after();
         const uint32_t acc0 = first ? 0 : 1;
-        if (PAIR) {
+        const uint32_t v = v_lo + st * V_STEP, p = p_lo + (PAIR ? st * BLK : 0);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (!mbar_wait(v_full + 8 * c, g & 1)) return false;
-            tc_fence_after();
-            {
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-              for (int ks = 0; ks < 2; ++ks) {
-                const int k16 = c * 2 + ks;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  mma_lo<PAIR>(tmem + j * 128, p_lo + (k16 >> 2) * BLK + (k16 & 3) * 2,
-                               v_lo + c * (V_CHUNK >> 4) + j * (2 * 32 * 128 >> 4) + ks * 128, id_o,
-                               k16 == 0 ? acc0 : 1);
-              }
-              commit(v_empty + 8 * c);
-            }
-          }
-        } else {
-          const uint32_t v = v_lo + (g & 1) * NBLK * BLK;
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              mma_lo<PAIR>(tmem + j * 128, p_lo + ks * 2, v + 4 * j * BLK + ks * 128, id_o,
-                           ks == 0 ? acc0 : 1);
-          commit(k_empty + 8 * (g & 1));
-        }
-        commit(pv_done);
+          for (int j = 0; j < 2; ++j)
+            mma_lo<PAIR>(tmem + j * 128, p + ks * 2, v + (PAIR ? 2 : 4) * j * BLK + ks * 128, id_o,
+                         ks == 0 ? acc0 : 1);
+        commit((PAIR ? v_empty : k_empty) + 8 * st);
+        commit(pv_done + 8 * st);
         return true;
       };
       Walk<PAIR> w(a, *share);
       int g = 0, n = 0;
-      bool ok = true;
-      while (ok && w.next()) {
-        if (!mbar_wait(q_full, n & 1)) break;
-        tc_fence_after();
+      bool ok = true, first = false;  // first: the pending P V starts a unit's O
+      for (; ok && w.next(); ++n) {
         for (int t = w.t0; t < w.t1; ++t, ++g) {
-          const int sb = g & 1;
-          ok = mbar_wait(s_empty + 8 * sb, ((g >> 1) & 1) ^ 1);
-          if (!ok) break;
-          const uint32_t d = tmem + S_COL + sb * SC;
+          const int st = g & 1;
+          const uint32_t parity = (g >> 1) & 1;
           // S of this tile goes ahead of P V of the one before, so that the
-          // softmax has the tensor pipe's time, unless its keys have yet to
-          // land: the P V that could run then also releases room for loads
-          // (waiting here first left the loads of one tile in flight at a time:
-          // 6000 clocks a tile against 3500)
-          bool behind = t > w.t0;
-          if (behind && !mbar_test(k_full + 8 * (PAIR ? 0 : sb), PAIR ? g & 1 : (g >> 1) & 1)) {
-            ok = second(g - 1, t - 1 == w.t0);
-            if (!ok) break;
-            behind = false;
-          }
-          if (PAIR) {
-#pragma unroll
-            for (int kg = 0; kg < NBLK / KG; ++kg) {
-              ok = ok && mbar_wait(k_full + 8 * kg, g & 1);
+          // softmax has the tensor pipe's time, unless its keys (or queries)
+          // have yet to land.  Then the single form waits for that P V, which
+          // releases room for loads, its bottleneck (S always first: 6000
+          // clocks a tile, this: 3700); the pair form takes whichever is ready
+          // first (2810 to 2550).
+          auto ready = [&] {
+            return mbar_test(k_full + 8 * st, parity) && (t > w.t0 || mbar_test(q_full, n & 1));
+          };
+          bool behind = g > 0;
+          if (behind && !ready()) {
+            const long long c0 = clock64();
+            while (PAIR && !mbar_test(p_full + 8 * (st ^ 1), ((g - 1) >> 1) & 1) && !ready() &&
+                   clock64() - c0 < kWaitCycles) {
+            }
+            if (!PAIR || !ready()) {
+              ok = second(g - 1, first);
               if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int kb = kg * KG; kb < kg * KG + KG; ++kb)
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  mma_lo<PAIR>(d, q_lo + kb * BLK + ks * 2, k_lo + kb * BLK + ks * 2, id_s,
-                               (kb | ks) != 0);
-              commit(k_empty + 8 * kg);
-            }
-          } else {
-            ok = mbar_wait(k_full + 8 * sb, (g >> 1) & 1);
-            tc_fence_after();
-            if (ok) {
-              const uint32_t k = k_lo + sb * NBLK * BLK;
-#pragma unroll
-              for (int kb = 0; kb < NBLK; ++kb)
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  mma_lo<PAIR>(d, q_lo + kb * BLK + ks * 2, k + kb * BLK + ks * 2, id_s,
-                               (kb | ks) != 0);
+              behind = false;
             }
           }
+          ok = (t > w.t0 || mbar_wait(q_full, n & 1)) &&
+               mbar_wait(s_empty + 8 * st, parity ^ 1) && mbar_wait(k_full + 8 * st, parity);
           if (!ok) break;
-          commit(s_full + 8 * sb);
+          tc_fence_after();
+          const uint32_t d = tmem + S_COL + st * SC, k = k_lo + st * K_STEP;
+#pragma unroll
+          for (int kb = 0; kb < NBLK; ++kb)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_lo<PAIR>(d, q_lo + kb * BLK + ks * 2, k + kb * KBLK + ks * 2, id_s,
+                           (kb | ks) != 0);
+          if (PAIR) commit(k_empty + 8 * st);
+          commit(s_full + 8 * st);
           if (t + 1 == w.t1) commit(q_empty);
           if (behind) {
-            ok = second(g - 1, t - 1 == w.t0);
+            ok = second(g - 1, first);
             if (!ok) break;
           }
+          first = t == w.t0;
         }
-        if (ok) ok = second(g - 1, w.t1 - 1 == w.t0);
-        ++n;
       }
+      if (ok && g > 0) second(g - 1, first);
       // every MMA has completed before tensor memory is released
       commit(done);
     }
@@ -615,10 +549,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         uint32_t s[NC];
         const uint32_t t_s = t_lane + S_COL + sb * SC + part * NC;
-        if constexpr (PAIR)
-          tmem_ld32(t_s, s);
-        else
-          tmem_ld16(t_s, s);
+        tmem_ld16(t_s, s);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
@@ -658,13 +589,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           p[c / 2] = pack_bf16(x, y);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        // P V of the tile before is done: P and O may be written
-        if (g > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1));
+        // O is rescaled once P V of the tile before is done; P's room is free
+        // once that of NP tiles before is
+        const bool rescale = t > w.t0 && __any_sync(0xffffffffu, f != 1.f);
+        const int wait_for = rescale ? g - 1 : g - C::NP;
+        if (wait_for >= 0) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(pv_done + 8 * (wait_for & 1), (wait_for >> 1) & 1));
           if (!ok) break;
         }
-        tc_fence_after();
-        if (t > w.t0 && __any_sync(0xffffffffu, f != 1.f)) {
+        if (rescale) {
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
             uint32_t o[32];
@@ -676,9 +611,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           tmem_wait_st();
         }
-        // P, K-major with 128-byte swizzle, 64 keys a block
-        const uint32_t prow = sP + (PAIR ? half * BLK_BYTES : 0) + rl * 128;
-        const int c0 = (PAIR ? 0 : half * 4) + part * (NC / 8);
+        // P, K-major with 128-byte swizzle
+        const uint32_t prow = sP + (PAIR ? sb * BLK_BYTES : 0) + rl * 128;
+        const int c0 = half * 4 + part * 2;
 #pragma unroll
         for (int c = 0; c < NC / 8; ++c)
           st_shared_v4(prow + (((c0 + c) ^ (rl & 7)) << 4),
@@ -688,9 +623,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) {
           if (PAIR)
-            mbar_arrive_remote(p_full_lead);
+            mbar_arrive_remote(p_full_lead + 8 * sb);
           else
-            mbar_arrive(p_full);
+            mbar_arrive(p_full + 8 * sb);
         }
       }
       if (!ok) break;
@@ -709,7 +644,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         else if (urow < rows && a.lse)
           a.lse[int64_t(grow % a.H) * a.T + grow / a.H] = lse2 * LN2;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
       // D's columns: part 0 holds the first MMA's, part 1 the second's
