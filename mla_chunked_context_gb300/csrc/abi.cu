@@ -71,6 +71,7 @@ int launch_attn_fused(const mla_dims_t &d, int num_seqs, const int32_t *q_loc,
 int fused_take_errors();
 int gather_take_errors();
 int latent_take_errors();
+int heads_take_errors();
 
 namespace {
 
@@ -985,9 +986,10 @@ extern "C" int mla_device_error_flags(int32_t *flags) {
   if (!flags) return MLA_ERR_INVALID;
   if (cudaDeviceSynchronize() != cudaSuccess) return MLA_ERR_CUDA;
   const int a = gemm_take_errors(), b = attn_take_errors(), c = fused_take_errors(),
-            e = gather_take_errors(), f = latent_take_errors();
-  if (a < 0 || b < 0 || c < 0 || e < 0 || f < 0) return MLA_ERR_CUDA;
-  *flags = a | b | c | e | f;
+            e = gather_take_errors(), f = latent_take_errors(),
+            g = heads_take_errors();
+  if (a < 0 || b < 0 || c < 0 || e < 0 || f < 0 || g < 0) return MLA_ERR_CUDA;
+  *flags = a | b | c | e | f | g;
   return MLA_OK;
 }
 

@@ -23,7 +23,11 @@ int launch_latent_attn_simt(const mla_dims_t &d, int causal, int R, const int32_
                             const int32_t *seq_lens, int T, const void *q, const void *cache,
                             int num_blocks, const int32_t *block_table, int bt_stride, void *o,
                             float *lse, int32_t *status, cudaStream_t s);
-// sm103_latent.cu
+// sm103_heads.cu, sm103_latent.cu
+int launch_absorb_tc(const mla_dims_t &d, const void *q, int T, const void *w, int rope_columns,
+                     void *q_latent, cudaStream_t s);
+int launch_expand_tc(const mla_dims_t &d, const void *o_latent, int T, const void *w, void *out,
+                     cudaStream_t s);
 int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t *qsl,
                           const int32_t *seq_lens, int T, const void *q, const void *cache,
                           int num_blocks, const int32_t *block_table, int bt_stride, float *part_o,
@@ -116,8 +120,12 @@ extern "C" int mla_absorb_query(const mla_dims_t *d, const void *q, int32_t num_
   if (!q || !w_kv_b || !q_latent || !aligned_to(q, es) || !aligned_to(w_kv_b, es) ||
       !aligned_to(q_latent, es))
     return MLA_ERR_INVALID;
-  if (tc_shape(*d) && (!aligned16(q) || !aligned16(w_kv_b) || !aligned16(q_latent)))
-    return MLA_ERR_UNSUPPORTED;
+  if (tc_shape(*d)) {
+    if (!aligned16(q) || !aligned16(w_kv_b) || !aligned16(q_latent) || !tc_available())
+      return MLA_ERR_UNSUPPORTED;
+    return launch_absorb_tc(*d, q, num_tokens, w_kv_b, rope_columns, q_latent,
+                            static_cast<cudaStream_t>(stream));
+  }
   return launch_absorb_simt(*d, q, num_tokens, w_kv_b, rope_columns, q_latent,
                             static_cast<cudaStream_t>(stream));
 }
@@ -133,8 +141,12 @@ extern "C" int mla_expand_output(const mla_dims_t *d, const void *o_latent, int3
   if (!o_latent || !w_kv_b || !out || !aligned_to(o_latent, es) || !aligned_to(w_kv_b, es) ||
       !aligned_to(out, es))
     return MLA_ERR_INVALID;
-  if (tc_shape(*d) && (!aligned16(o_latent) || !aligned16(w_kv_b) || !aligned16(out)))
-    return MLA_ERR_UNSUPPORTED;
+  if (tc_shape(*d)) {
+    if (!aligned16(o_latent) || !aligned16(w_kv_b) || !aligned16(out) || !tc_available())
+      return MLA_ERR_UNSUPPORTED;
+    return launch_expand_tc(*d, o_latent, num_tokens, w_kv_b, out,
+                            static_cast<cudaStream_t>(stream));
+  }
   return launch_expand_simt(*d, o_latent, num_tokens, w_kv_b, out,
                             static_cast<cudaStream_t>(stream));
 }
