@@ -532,33 +532,44 @@ def mla_selftest_bounded_wait(limit_us: int, gave_up, stream=None) -> None:
 
 
 # ------------------------------------------------------------------ decode --
-def _on_device(where: str, first: torch.Tensor, *others) -> None:
-    """The C calls work on the current device: every tensor has to be there
-    (host tensors, or another GPU's, are refused before anything runs)."""
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in (first, *others):
-        if t is not None and (not t.is_cuda or t.device.index != cur):
-            raise ValueError(f"{where}: tensor on {t.device}, the current device is "
-                             f"{'none' if cur is None else f'cuda:{cur}'}")
+# These calls are made once a layer and token, so their checks are kept to a
+# few comparisons a tensor.
+def _refuse(where, name, t, dtype, shape):
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        cur = f"cuda:{torch.cuda.current_device()}" if torch.cuda.is_available() else "none"
+        raise ValueError(f"{where}: {name} is on {t.device}, the current device is {cur}")
+    raise ValueError(f"{where}: {name} has to be contiguous {list(shape)} {dtype}, got "
+                     f"{list(t.shape)} {t.dtype}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _want(where: str, name: str, t: Optional[torch.Tensor], dtype, *shape) -> None:
-    """t (if given) has this dtype and shape (None: any size) and is contiguous."""
-    if t is None:
-        return
-    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        want = "x".join("*" if n is None else str(n) for n in shape)
-        raise ValueError(f"{where}: {name} has to be contiguous {want} {dtype}, got "
-                         f"{'x'.join(map(str, t.shape))} {t.dtype}")
+def _take(where: str, *specs) -> None:
+    """Every (name, tensor or None, dtype, shape) is contiguous, of that type
+    and shape, and on the current device, where the C calls work."""
+    cur = None
+    for name, t, dtype, shape in specs:
+        if t is None:
+            continue
+        dev = t.get_device()
+        if cur is None and dev >= 0:
+            cur = torch.cuda.current_device()
+        if dev != cur or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            _refuse(where, name, t, dtype, shape)
 
 
-def _batch(where: str, query_start_loc, seq_lens, block_table) -> int:
-    R = seq_lens.shape[0]
-    _want(where, "seq_lens", seq_lens, torch.int32, None)
-    _want(where, "query_start_loc", query_start_loc, torch.int32, R + 1)
-    _want(where, "block_table", block_table, torch.int32, R, None)
-    return R
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _dim(t: torch.Tensor, i: int, n: int, where: str, name: str) -> int:
+    if t.dim() != n:
+        raise ValueError(f"{where}: {name} has to have {n} dimensions, got {t.dim()}")
+    return t.shape[i]
 
 
 def mla_append_latent(dims: Dims, kv_a, query_start_loc, seq_lens, rope_table, kv_cache,
@@ -571,62 +582,61 @@ def mla_append_latent(dims: Dims, kv_a, query_start_loc, seq_lens, rope_table, k
     or ``q_latent[..., L:]``.  rope_table: float32 [positions, P], cos then
     sin, or None."""
     w = "mla_append_latent"
-    LP, H, P = dims.kv_lora_rank + dims.qk_rope_dim, dims.num_heads, dims.qk_rope_dim
-    T = kv_a.shape[0]
-    _on_device(w, kv_a, query_start_loc, seq_lens, rope_table, kv_cache, block_table, norm_weight,
-               positions, new_latent, q, q_pe_out, dev_status)
-    R = _batch(w, query_start_loc, seq_lens, block_table)
-    if kv_a.dtype != dims.dtype or kv_a.dim() != 2 or kv_a.shape[1] != LP or \
-            (T > 0 and kv_a.stride(1) != 1):
-        raise ValueError(f"{w}: kv_a has to be [T, {LP}] {dims.dtype} with contiguous rows")
-    _want(w, "kv_cache", kv_cache, dims.dtype, None, dims.block_size, LP)
-    _want(w, "norm_weight", norm_weight, dims.dtype, dims.kv_lora_rank)
-    _want(w, "positions", positions, torch.int32, T)
-    _want(w, "rope_table", rope_table, torch.float32, None, P)
-    _want(w, "new_latent", new_latent, dims.dtype, T, LP)
-    _want(w, "q", q, dims.dtype, T, H, dims.qk_nope_dim + P)
-    _want(w, "dev_status", dev_status, torch.int32, 1)
+    dt, H, P, L = dims.dtype, dims.num_heads, dims.qk_rope_dim, dims.kv_lora_rank
+    T, R = _dim(kv_a, 0, 2, w, "kv_a"), _dim(seq_lens, 0, 1, w, "seq_lens")
+    blocks, stride = _dim(kv_cache, 0, 3, w, "kv_cache"), _dim(block_table, 1, 2, w, "block_table")
+    n_pos = 0 if rope_table is None else rope_table.shape[0]
+    i32 = torch.int32
+    ld = kv_a.stride(0) if T > 1 else L + P
+    if kv_a.dtype is not dt or kv_a.shape[1] != L + P or kv_a.stride(1) != 1 or ld < L + P:
+        raise ValueError(f"{w}: kv_a has to be [T, {L + P}] {dt} with contiguous rows")
+    _take(w, ("query_start_loc", query_start_loc, i32, (R + 1,)), ("seq_lens", seq_lens, i32, (R,)),
+          ("block_table", block_table, i32, (R, stride)),
+          ("kv_cache", kv_cache, dt, (blocks, dims.block_size, L + P)),
+          ("norm_weight", norm_weight, dt, (L,)), ("positions", positions, i32, (T,)),
+          ("rope_table", rope_table, torch.float32, (n_pos, P)),
+          ("new_latent", new_latent, dt, (T, L + P)),
+          ("q", q, dt, (T, H, dims.qk_nope_dim + P)), ("dev_status", dev_status, i32, (1,)))
+    if kv_a.get_device() != kv_cache.get_device():
+        _refuse(w, "kv_a", kv_a, dt, (T, L + P))
     q_ld = P
     if q_pe_out is not None:
-        q_ld = q_pe_out.stride(1) if H > 1 else q_pe_out.stride(0)
-        if q_pe_out.dtype != dims.dtype or q_pe_out.shape != (T, H, P) or \
-                (P > 1 and q_pe_out.stride(2) != 1) or \
-                (T > 1 and q_pe_out.stride(0) != H * q_ld):
-            raise ValueError(f"{w}: q_pe_out has to be a [{T}, {H}, {P}] {dims.dtype} view of "
-                             "evenly spaced rows")
-    d = dims.c()
+        st = q_pe_out.stride()
+        q_ld = st[1] if H > 1 else st[0] if T > 1 else P
+        if q_pe_out.dtype is not dt or q_pe_out.shape != (T, H, P) or (P > 1 and st[2] != 1) or \
+                (T > 1 and st[0] != H * q_ld) or q_pe_out.get_device() != kv_a.get_device():
+            raise ValueError(f"{w}: q_pe_out has to be a [{T}, {H}, {P}] {dt} view of evenly "
+                             "spaced rows on the same device")
     _check(lib().mla_append_latent(
-        C.byref(d), _ptr(kv_a), kv_a.stride(0) if T > 1 else max(LP, kv_a.stride(0)),
-        _ptr(norm_weight), norm_eps, T, R, _ptr(query_start_loc), _ptr(seq_lens), _ptr(positions),
-        _ptr(rope_table), 0 if rope_table is None else rope_table.shape[0], int(interleaved),
-        _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table), block_table.shape[1],
-        _ptr(new_latent), _ptr(q), _ptr(q_pe_out), q_ld, _ptr(dev_status), _stream(stream)), w)
+        C.byref(dims.c()), kv_a.data_ptr(), ld, _p(norm_weight),
+        norm_eps, T, R, query_start_loc.data_ptr(), seq_lens.data_ptr(), _p(positions),
+        _p(rope_table), n_pos, 1 if interleaved else 0, kv_cache.data_ptr(), blocks,
+        block_table.data_ptr(), stride, _p(new_latent), _p(q), _p(q_pe_out), q_ld,
+        _p(dev_status), _raw_stream(stream)), w)
 
 
 def mla_absorb_query(dims: Dims, q, w_kv_b, q_latent, rope_columns: bool = True,
                      stream=None) -> None:
     """q [T, H, Dn+P] -> q_latent [T, H, L+P]; rope_columns False leaves the
     rope columns of q_latent as they are."""
-    w, T, H = "mla_absorb_query", q.shape[0], dims.num_heads
-    _on_device(w, q, w_kv_b, q_latent)
-    _want(w, "q", q, dims.dtype, T, H, dims.qk_nope_dim + dims.qk_rope_dim)
-    _want(w, "w_kv_b", w_kv_b, dims.dtype, H * (dims.qk_nope_dim + dims.v_dim), dims.kv_lora_rank)
-    _want(w, "q_latent", q_latent, dims.dtype, T, H, dims.kv_lora_rank + dims.qk_rope_dim)
-    d = dims.c()
-    _check(lib().mla_absorb_query(C.byref(d), _ptr(q), T, _ptr(w_kv_b), int(rope_columns),
-                                  _ptr(q_latent), _stream(stream)), w)
+    w, dt, H = "mla_absorb_query", dims.dtype, dims.num_heads
+    T, L, P, Dn = _dim(q, 0, 3, w, "q"), dims.kv_lora_rank, dims.qk_rope_dim, dims.qk_nope_dim
+    _take(w, ("q", q, dt, (T, H, Dn + P)), ("w_kv_b", w_kv_b, dt, (H * (Dn + dims.v_dim), L)),
+          ("q_latent", q_latent, dt, (T, H, L + P)))
+    _check(lib().mla_absorb_query(C.byref(dims.c()), q.data_ptr(), T, w_kv_b.data_ptr(),
+                                  1 if rope_columns else 0, q_latent.data_ptr(),
+                                  _raw_stream(stream)), w)
 
 
 def mla_expand_output(dims: Dims, o_latent, w_kv_b, out, stream=None) -> None:
     """o_latent [T, H, L] -> out [T, H, Dv]."""
-    w, T, H = "mla_expand_output", o_latent.shape[0], dims.num_heads
-    _on_device(w, o_latent, w_kv_b, out)
-    _want(w, "o_latent", o_latent, dims.dtype, T, H, dims.kv_lora_rank)
-    _want(w, "w_kv_b", w_kv_b, dims.dtype, H * (dims.qk_nope_dim + dims.v_dim), dims.kv_lora_rank)
-    _want(w, "out", out, dims.dtype, T, H, dims.v_dim)
-    d = dims.c()
-    _check(lib().mla_expand_output(C.byref(d), _ptr(o_latent), T, _ptr(w_kv_b), _ptr(out),
-                                   _stream(stream)), w)
+    w, dt, H = "mla_expand_output", dims.dtype, dims.num_heads
+    T, L = _dim(o_latent, 0, 3, w, "o_latent"), dims.kv_lora_rank
+    _take(w, ("o_latent", o_latent, dt, (T, H, L)),
+          ("w_kv_b", w_kv_b, dt, (H * (dims.qk_nope_dim + dims.v_dim), L)),
+          ("out", out, dt, (T, H, dims.v_dim)))
+    _check(lib().mla_expand_output(C.byref(dims.c()), o_latent.data_ptr(), T, w_kv_b.data_ptr(),
+                                   out.data_ptr(), _raw_stream(stream)), w)
 
 
 def mla_latent_attn_workspace_bytes(dims: Dims, num_tokens: int, num_seqs: int) -> int:
@@ -643,20 +653,19 @@ def mla_latent_attn(dims: Dims, causal: bool, query_start_loc, seq_lens, q_laten
     """Absorbed attention over the paged latent cache: q_latent [T, H, L+P] ->
     o_latent [T, H, L], lse [H, T].  workspace: a uint8 device tensor of
     mla_latent_attn_workspace_bytes bytes."""
-    w, T, H, L = "mla_latent_attn", q_latent.shape[0], dims.num_heads, dims.kv_lora_rank
-    _on_device(w, q_latent, query_start_loc, seq_lens, kv_cache, block_table, workspace, o_latent,
-               lse, dev_status)
-    R = _batch(w, query_start_loc, seq_lens, block_table)
+    w, dt, H, L = "mla_latent_attn", dims.dtype, dims.num_heads, dims.kv_lora_rank
     LP = L + dims.qk_rope_dim
-    _want(w, "q_latent", q_latent, dims.dtype, T, H, LP)
-    _want(w, "kv_cache", kv_cache, dims.dtype, None, dims.block_size, LP)
-    _want(w, "workspace", workspace, torch.uint8, None)
-    _want(w, "o_latent", o_latent, dims.dtype, T, H, L)
-    _want(w, "lse", lse, torch.float32, H, T)
-    _want(w, "dev_status", dev_status, torch.int32, 1)
-    d = dims.c()
+    T, R = _dim(q_latent, 0, 3, w, "q_latent"), _dim(seq_lens, 0, 1, w, "seq_lens")
+    blocks, stride = _dim(kv_cache, 0, 3, w, "kv_cache"), _dim(block_table, 1, 2, w, "block_table")
+    ws = 0 if workspace is None else workspace.numel()
+    i32 = torch.int32
+    _take(w, ("q_latent", q_latent, dt, (T, H, LP)),
+          ("query_start_loc", query_start_loc, i32, (R + 1,)), ("seq_lens", seq_lens, i32, (R,)),
+          ("block_table", block_table, i32, (R, stride)),
+          ("kv_cache", kv_cache, dt, (blocks, dims.block_size, LP)),
+          ("workspace", workspace, torch.uint8, (ws,)), ("o_latent", o_latent, dt, (T, H, L)),
+          ("lse", lse, torch.float32, (H, T)), ("dev_status", dev_status, i32, (1,)))
     _check(lib().mla_latent_attn(
-        C.byref(d), int(causal), R, _ptr(query_start_loc), _ptr(seq_lens), T, _ptr(q_latent),
-        _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table), block_table.shape[1],
-        _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(o_latent),
-        _ptr(lse), _ptr(dev_status), _stream(stream)), w)
+        C.byref(dims.c()), 1 if causal else 0, R, query_start_loc.data_ptr(), seq_lens.data_ptr(),
+        T, q_latent.data_ptr(), kv_cache.data_ptr(), blocks, block_table.data_ptr(), stride,
+        _p(workspace), ws, o_latent.data_ptr(), _p(lse), _p(dev_status), _raw_stream(stream)), w)

@@ -9,15 +9,17 @@
 // Every value is read once and written once (the row twice, when the dense
 // copy is asked for), so the kernel is bound by HBM when there are many
 // tokens and by the chain of dependent loads (sequence, length, block id)
-// when there are few.  A block serves one token: warp 0 of its first block
-// the row, all other warps the heads of the queries, 32 lanes over 16-byte
-// pieces.  Few tokens spread their heads over several blocks.
+// when there are few.  So the row and the first pieces of the queries are read
+// before that chain is walked.  A block serves one token: warp 0 of its first
+// block the row, all other threads the heads of the queries, each the same
+// columns (and angles) of several heads.  Few tokens spread their heads over
+// several blocks.
 #include "common.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 4;
 
 struct AppendArgs {
   const void *kv_a, *norm_weight, *q;
@@ -89,53 +91,81 @@ __device__ __forceinline__ void rotate_pair(const T *src, T *d0, T *d1, const fl
   }
 }
 
-// The same for the 16-byte pieces of piece number `k`: interleaved, one piece
-// holds N/2 pairs; half-split, piece k goes with piece k + P/(2N).
+// 16-byte pieces: interleaved, one piece holds N/2 pairs; half-split, piece k
+// (x) goes with piece k + P/(2N) (y).  c, s: the pairs' cosines and sines.
 template <typename T>
-__device__ __forceinline__ void rotate_piece(const T *src, T *d0, T *d1, const float *rope, int P,
-                                             int k, bool interleaved) {
+__device__ __forceinline__ void rotate_piece(Piece<T> &x, Piece<T> &y, const float *c,
+                                             const float *s, bool interleaved) {
   constexpr int N = Piece<T>::N;
-  const int half = P / 2;
   if (interleaved) {
-    Piece<T> x;
-    x.load(src + k * N);
 #pragma unroll
     for (int e = 0; e < N / 2; ++e) {
-      const float c = __ldg(rope + k * (N / 2) + e), s = __ldg(rope + half + k * (N / 2) + e);
       const float a = x.v[2 * e], b = x.v[2 * e + 1];
-      x.v[2 * e] = a * c - b * s;
-      x.v[2 * e + 1] = b * c + a * s;
+      x.v[2 * e] = a * c[e] - b * s[e];
+      x.v[2 * e + 1] = b * c[e] + a * s[e];
     }
-    if (d0) x.store(d0 + k * N);
-    if (d1) x.store(d1 + k * N);
   } else {
-    Piece<T> x, y;
-    x.load(src + k * N);
-    y.load(src + half + k * N);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const float c = __ldg(rope + k * N + e), s = __ldg(rope + half + k * N + e);
       const float a = x.v[e], b = y.v[e];
-      x.v[e] = a * c - b * s;
-      y.v[e] = b * c + a * s;
-    }
-    if (d0) {
-      x.store(d0 + k * N);
-      y.store(d0 + half + k * N);
-    }
-    if (d1) {
-      x.store(d1 + k * N);
-      y.store(d1 + half + k * N);
+      x.v[e] = a * c[e] - b * s[e];
+      y.v[e] = b * c[e] + a * s[e];
     }
   }
 }
 
-template <typename T>
+
+template <typename T, bool EARLY>
 __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
   constexpr int N = Piece<T>::N;
+  constexpr int ROW_PRE = EARLY ? 4 : 0;  // pieces of a row a lane reads ahead
+  constexpr int Q_PRE = EARLY ? 2 : 0;    // heads a thread reads ahead
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x;
-  // the token's sequence and position
+  const bool row_warp = blockIdx.y == 0 && warp == 0;
+  chain_release();
+  chain_wait();
+
+  // ---- what does not depend on the token's sequence is read first
+  const T *x = static_cast<const T *>(a.kv_a) + t * a.kv_a_ld;
+  const T *w = static_cast<const T *>(a.norm_weight);
+  const int n_pieces = a.L / N;
+  Piece<T> row[EARLY ? ROW_PRE : 1];
+  // the queries: this block's share of the heads; a thread has columns k of
+  // heads qh, qh + q_step, ...
+  const int h0 = int(int64_t(a.H) * blockIdx.y / gridDim.y);
+  const int h1 = int(int64_t(a.H) * (blockIdx.y + 1) / gridDim.y);
+  const int q_tid = int(threadIdx.x) - (blockIdx.y == 0 ? 32 : 0);  // < 0: the row's warp
+  const int q_threads = int(blockDim.x) - (blockIdx.y == 0 ? 32 : 0);
+  const int units = a.P / (a.interleaved ? N : 2 * N);  // of a head, as pieces
+  const int qk = a.Dn + a.P;
+  const T *q = static_cast<const T *>(a.q) + int64_t(t) * a.H * qk + a.Dn;
+  T *qo = static_cast<T *>(a.q_pe) + int64_t(t) * a.H * a.q_pe_ld;
+  const int y_off = a.P / 2;
+  int k = 0, qh = h1, q_step = 1;
+  Piece<T> qx[EARLY ? Q_PRE : 1], qy[EARLY ? Q_PRE : 1];
+  if (row_warp) {
+    if (a.vec_row) {
+#pragma unroll
+      for (int i = 0; i < ROW_PRE; ++i)
+        if (lane + 32 * i < n_pieces) row[i].load(x + (lane + 32 * i) * N);
+    }
+  } else if (a.vec_q) {
+    q_step = q_threads / units;
+    if (q_tid < q_step * units) {
+      k = q_tid % units;
+      qh = h0 + q_tid / units;
+    }
+#pragma unroll
+    for (int i = 0; i < Q_PRE; ++i)
+      if (qh + i * q_step < h1) {
+        const T *src = q + int64_t(qh + i * q_step) * qk + k * N;
+        qx[i].load(src);
+        if (!a.interleaved) qy[i].load(src + y_off);
+      }
+  }
+
+  // ---- the token's sequence and position
   const int first = max(__ldg(a.qsl), 0);
   if (t < first || t >= min(__ldg(a.qsl + a.R), a.T)) return;
   const int r = find_seq_warp(a.qsl, a.R, t);
@@ -150,88 +180,124 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
   }
   const float *rope = a.rope ? a.rope + int64_t(rpos) * a.P : nullptr;
 
-  if (blockIdx.y == 0 && warp == 0) {
-    // ---- the row
+  if (row_warp) {
     const int blk_i = pos / a.bs;
     const int blk = blk_i < a.bt_stride ? __ldg(a.block_table + int64_t(r) * a.bt_stride + blk_i) : -1;
     const bool good = blk >= 0 && blk < a.num_blocks;
     if (!good && lane == 0 && a.status) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
     const int LP = a.L + a.P;
-    const T *x = static_cast<const T *>(a.kv_a) + t * a.kv_a_ld;
-    const T *w = static_cast<const T *>(a.norm_weight);
     T *d0 = good ? static_cast<T *>(a.kv_cache) + (int64_t(blk) * a.bs + pos % a.bs) * LP : nullptr;
     T *d1 = a.new_latent ? static_cast<T *>(a.new_latent) + int64_t(t) * LP : nullptr;
-    float ss = 0.f;
+    float inv = 1.f;
     if (w) {
-      if (a.vec_row) {
-        for (int k = lane; k < a.L / N; k += 32) {
-          Piece<T> p;
-          p.load(x + k * N);
+      float ss = 0.f;
+      auto square = [&](const Piece<T> &p) {
 #pragma unroll
-          for (int e = 0; e < N; ++e) ss = fmaf(p.v[e], p.v[e], ss);
+        for (int e = 0; e < N; ++e) ss = fmaf(p.v[e], p.v[e], ss);
+      };
+      if (a.vec_row) {
+#pragma unroll
+        for (int i = 0; i < ROW_PRE; ++i)
+          if (lane + 32 * i < n_pieces) square(row[i]);
+        for (int j = lane + 32 * ROW_PRE; j < n_pieces; j += 32) {
+          Piece<T> p;
+          p.load(x + j * N);
+          square(p);
         }
       } else {
-        for (int k = lane; k < a.L; k += 32) {
-          const float v = to_f32(x[k]);
+        for (int j = lane; j < a.L; j += 32) {
+          const float v = to_f32(x[j]);
           ss = fmaf(v, v, ss);
         }
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      inv = 1.f / sqrtf(ss / float(a.L) + a.eps);
     }
-    const float inv = w ? 1.f / sqrtf(ss / float(a.L) + a.eps) : 1.f;
     if (a.vec_row) {
-      for (int k = lane; k < a.L / N; k += 32) {
-        Piece<T> p, g;
-        p.load(x + k * N);
+      auto put = [&](Piece<T> p, int j) {
         if (w) {
-          g.load(w + k * N);
+          Piece<T> g;
+          g.load(w + j * N);
 #pragma unroll
           for (int e = 0; e < N; ++e) p.v[e] = p.v[e] * inv * g.v[e];
         }
-        if (d0) p.store(d0 + k * N);
-        if (d1) p.store(d1 + k * N);
+        if (d0) p.store(d0 + j * N);
+        if (d1) p.store(d1 + j * N);
+      };
+#pragma unroll
+      for (int i = 0; i < ROW_PRE; ++i)
+        if (lane + 32 * i < n_pieces) put(row[i], lane + 32 * i);
+      for (int j = lane + 32 * ROW_PRE; j < n_pieces; j += 32) {
+        Piece<T> p;
+        p.load(x + j * N);
+        put(p, j);
       }
     } else {
-      for (int k = lane; k < a.L; k += 32) {
-        float v = to_f32(x[k]);
-        if (w) v = v * inv * to_f32(w[k]);
+      for (int j = lane; j < a.L; j += 32) {
+        float v = to_f32(x[j]);
+        if (w) v = v * inv * to_f32(w[j]);
         const T o = from_f32<T>(v);
-        if (d0) d0[k] = o;
-        if (d1) d1[k] = o;
+        if (d0) d0[j] = o;
+        if (d1) d1[j] = o;
       }
     }
     T *p0 = d0 ? d0 + a.L : nullptr, *p1 = d1 ? d1 + a.L : nullptr;
     if (!rope) {
-      for (int k = lane; k < a.P; k += 32) {
-        const T v = x[a.L + k];
-        if (p0) p0[k] = v;
-        if (p1) p1[k] = v;
+      for (int j = lane; j < a.P; j += 32) {
+        const T v = x[a.L + j];
+        if (p0) p0[j] = v;
+        if (p1) p1[j] = v;
       }
     } else {
-      for (int k = lane; k < a.P / 2; k += 32)
-        rotate_pair<T>(x + a.L, p0, p1, rope, a.P, k, a.interleaved);
+      for (int j = lane; j < a.P / 2; j += 32)
+        rotate_pair<T>(x + a.L, p0, p1, rope, a.P, j, a.interleaved);
     }
     return;
   }
   if (!a.q) return;
-  // ---- the queries' rope columns: this block's share of the heads
-  const int h0 = int(int64_t(a.H) * blockIdx.y / gridDim.y);
-  const int h1 = int(int64_t(a.H) * (blockIdx.y + 1) / gridDim.y);
-  const T *q = static_cast<const T *>(a.q) + int64_t(t) * a.H * (a.Dn + a.P) + a.Dn;
-  T *o = static_cast<T *>(a.q_pe) + int64_t(t) * a.H * a.q_pe_ld;
-  const int units = !rope ? a.P : a.vec_q ? a.P / (a.interleaved ? N : 2 * N) : a.P / 2;
-  const int skip = blockIdx.y == 0 ? 32 : 0;  // warp 0 of the first block has the row
-  for (int u = threadIdx.x - skip; u < (h1 - h0) * units; u += int(blockDim.x) - skip) {
-    const int h = h0 + u / units, k = u % units;
-    const T *src = q + int64_t(h) * (a.Dn + a.P);
-    T *dst = o + h * a.q_pe_ld;
-    if (!rope)
-      dst[k] = src[k];
-    else if (a.vec_q)
-      rotate_piece<T>(src, dst, nullptr, rope, a.P, k, a.interleaved);
+  if (a.vec_q) {
+    if (qh >= h1) return;
+    // the angles of this thread's columns, for all of its heads
+    constexpr int NA = N;
+    const int n_ang = a.interleaved ? N / 2 : N;
+    float c[NA], sn[NA];
+#pragma unroll
+    for (int e = 0; e < NA; e += 2)  // (the table's rows are 8-byte aligned here)
+      if (e < n_ang) {
+        const float2 u = __ldg(reinterpret_cast<const float2 *>(rope + k * n_ang + e));
+        const float2 v = __ldg(reinterpret_cast<const float2 *>(rope + y_off + k * n_ang + e));
+        c[e] = u.x;
+        c[e + 1] = u.y;
+        sn[e] = v.x;
+        sn[e + 1] = v.y;
+      }
+    auto put = [&](Piece<T> px, Piece<T> py, int h) {
+      rotate_piece<T>(px, py, c, sn, a.interleaved);
+      T *dst = qo + h * a.q_pe_ld + k * N;
+      px.store(dst);
+      if (!a.interleaved) py.store(dst + y_off);
+    };
+#pragma unroll
+    for (int i = 0; i < Q_PRE; ++i)
+      if (qh + i * q_step < h1) put(qx[i], qy[i], qh + i * q_step);
+#pragma unroll 1
+    for (int h = qh + Q_PRE * q_step; h < h1; h += q_step) {
+      const T *src = q + int64_t(h) * qk + k * N;
+      Piece<T> px, py;
+      px.load(src);
+      if (!a.interleaved) py.load(src + y_off);
+      put(px, py, h);
+    }
+    return;
+  }
+  const int per_head = rope ? a.P / 2 : a.P;
+  for (int u = q_tid; u < (h1 - h0) * per_head; u += q_threads) {
+    const int h = h0 + u / per_head, j = u % per_head;
+    if (rope)
+      rotate_pair<T>(q + int64_t(h) * qk, qo + h * a.q_pe_ld, nullptr, rope, a.P, j, a.interleaved);
     else
-      rotate_pair<T>(src, dst, nullptr, rope, a.P, k, a.interleaved);
+      qo[h * a.q_pe_ld + j] = q[int64_t(h) * qk + j];
   }
 }
 
@@ -252,21 +318,23 @@ int launch_append(const mla_dims_t &d, const void *kv_a, int64_t kv_a_ld, const 
   a.vec_row = (L * es) % 16 == 0 && (kv_a_ld * es) % 16 == 0 && al(kv_a) && al(norm_weight) &&
               al(kv_cache) && al(new_latent);
   const int pair_bytes = interleaved ? P * es : P / 2 * es;  // a rotation's 16-byte pieces
-  a.vec_q = q && pair_bytes % 16 == 0 && (d.qk_nope_dim * es) % 16 == 0 && (q_pe_ld * es) % 16 == 0 &&
+  const int units = P * es / (interleaved ? 16 : 32);  // of a head
+  a.vec_q = q && rope && (reinterpret_cast<uintptr_t>(rope) & 7) == 0 && units >= 1 &&
+            units <= 32 * (WARPS - 1) && pair_bytes % 16 == 0 && (d.qk_nope_dim * es) % 16 == 0 && (q_pe_ld * es) % 16 == 0 &&
             al(q) && al(q_pe);
   // enough blocks for every SM where there are heads to share out
   const int want = 2 * num_sms();
   const int most = q ? (d.num_heads + 7) / 8 : 1;
   int ys = T >= want ? 1 : (want + T - 1) / T;
   if (ys > most) ys = most;
-  launch_begin(s);
   const dim3 grid(T, ys);
   const int threads = q ? 32 * WARPS : 32;
+  const bool early = T < want;
   if (d.dtype == MLA_DTYPE_BF16)
-    append_kernel<__nv_bfloat16><<<grid, threads, 0, s>>>(a);
-  else
-    append_kernel<float><<<grid, threads, 0, s>>>(a);
-  return launch_status(s, "append_kernel");
+    return launch_chained(early ? append_kernel<__nv_bfloat16, true> : append_kernel<__nv_bfloat16, false>,
+                          grid, threads, 0, 1, s, "append_kernel", a);
+  return launch_chained(early ? append_kernel<float, true> : append_kernel<float, false>, grid,
+                        threads, 0, 1, s, "append_kernel", a);
 }
 
 }  // namespace mla

@@ -124,6 +124,42 @@ inline int launch_status(cudaStream_t s, const char *name) {
   return err == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
+// Programmatic dependent launch, for the chains of short decode kernels: a
+// kernel launched with launch_chained may start while the one before it on the
+// stream is still running (once all of that one's blocks have called
+// chain_release or exited), and calls chain_wait before it touches any global
+// memory: there it waits until the kernels before it have completed and their
+// writes are visible.
+__device__ __forceinline__ void chain_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void chain_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... Params, typename... Args>
+inline int launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                          int cluster, cudaStream_t s, const char *name, Args &&...args) {
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  launch_begin(s);
+  if (cudaLaunchKernelEx(&cfg, kernel, Params(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  return launch_status(s, name);
+}
+
 inline int elem_bytes(int32_t dtype) { return dtype == MLA_DTYPE_F32 ? 4 : 2; }
 
 // storage types of the inputs and of the final output

@@ -77,6 +77,17 @@ __global__ void __launch_bounds__(THREADS, 2)
     prefetch_map(&tm_o);
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), cols);
+  chain_release();
+  if (warp == 0 && lane == 0) {
+    // the weights on their way to L2 while the kernels before this one finish
+    for (int k = 0; k < C::K; k += 64) {
+      if (EXPAND)
+        prefetch_2d(&tm_w, k, h * 2 * HEAD + HEAD + n0);
+      else
+        for (int j = 0; j < g.nc; j += 64) prefetch_2d(&tm_w, n0 + j, h * 2 * HEAD + k);
+    }
+  }
+  chain_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -193,10 +204,9 @@ int launch_heads(const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap
       return MLA_ERR_CUDA;
     ready[dev].store(1, std::memory_order_release);
   }
-  launch_begin(s);
-  head_gemm_kernel<EXPAND><<<dim3(C::N / g.nc, (g.T + TM - 1) / TM, g.H), THREADS, C::SMEM, s>>>(
-      ta, tw, to, g);
-  return launch_status(s, EXPAND ? "expand_kernel" : "absorb_kernel");
+  return launch_chained(head_gemm_kernel<EXPAND>, dim3(C::N / g.nc, (g.T + TM - 1) / TM, g.H),
+                        THREADS, C::SMEM, 1, s, EXPAND ? "expand_kernel" : "absorb_kernel", ta, tw,
+                        to, g);
 }
 
 // Columns of a CTA: the most (up to `top`) that still gives every SM two CTAs,

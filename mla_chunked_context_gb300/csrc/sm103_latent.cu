@@ -363,6 +363,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     else
       tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
   }
+  chain_release();
+  chain_wait();
   find_share<PAIR>(a, cluster, clusters, share, scan);
   tc_fence_before();
   __syncthreads();
@@ -815,6 +817,8 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
   // the cut units (cluster of the first piece) and the items before each
   __shared__ int units[CT], first[CT + 1], warp_units[CT / 32], warp_items[CT / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  chain_release();
+  chain_wait();
   const int n_here = int(threadIdx.x) < clusters ? desc[2 * threadIdx.x].x : 0;
   const int items = n_here == 0 ? 0 : (urows / 32) * (n_here <= WIDE_PIECES ? 16 : 128);
   int inc = items;
@@ -897,19 +901,12 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
     grid = std::min(cs * n, urows_limit);
     grid_of[dev].store(grid, std::memory_order_release);
   }
-  cfg.gridDim = dim3(grid);
-  launch_begin(s);
-  if (cudaLaunchKernelEx(&cfg, latent_attn_kernel<PAIR>, maps, a) != cudaSuccess) {
-    cudaGetLastError();
-    return MLA_ERR_CUDA;
-  }
-  int rc = launch_status(s, "latent_attn_kernel");
+  int rc = launch_chained(latent_attn_kernel<PAIR>, grid, THREADS, Cfg<PAIR>::SMEM, PAIR ? 2 : 1, s,
+                          "latent_attn_kernel", maps, a);
   if (rc) return rc;
-  const int clusters = PAIR ? grid / 2 : grid;
-  launch_begin(s);
-  latent_combine_kernel<<<4 * num_sms(), CT, 0, s>>>(a.desc, clusters, Cfg<PAIR>::UROWS, a.part_o,
-                                                     a.part_lse, a.o, a.lse, a.H, a.T);
-  return launch_status(s, "latent_combine_kernel");
+  return launch_chained(latent_combine_kernel, 4 * num_sms(), CT, 0, 1, s, "latent_combine_kernel",
+                        a.desc, PAIR ? grid / 2 : grid, Cfg<PAIR>::UROWS, a.part_o, a.part_lse, a.o,
+                        a.lse, a.H, a.T);
 }
 
 }  // namespace
