@@ -17,16 +17,17 @@
 //     single form 32 clocks, N=256 80; pair M=128 N=64 25, N=256 64), so S,
 //     with its small N, is bound by re-reading the queries.
 // Two forms (template parameter):
-//   single (rows of a unit: 64)  one CTA, weight-stationary MMAs of M=64; a
-//          stage serves as K (K-major, 9 blocks of 64 columns) and as V (the
-//          first 8 blocks, MN-major).
+//   single (rows of a unit: 64)  one CTA, weight-stationary MMAs of M=64; 64
+//          keys at a time from two stages, each of which serves as K (K-major,
+//          9 blocks of 64 columns) and as V (the first 8 blocks, MN-major).
 //   pair   (rows: 128)  a cluster of two CTAs, cta_group::2 MMAs of M=128 (64
-//          rows in each).  An operand of such an MMA sits at the same offset
-//          in both CTAs, so V (each CTA 256 columns of all keys) cannot share
-//          the place of K (each CTA all columns of half of the keys).
-//   Both take 64 keys at a time from two stages.  (128 keys a tile halve the
-//   reads of the queries in the pair form, but leave room for one stage: S,
-//   softmax and P V then follow each other, 4840 clocks per 128 keys.)
+//          rows in each), 128 keys at a time.  An operand of such an MMA sits
+//          at the same offset in both CTAs, so V (each CTA 256 columns of all
+//          keys) cannot share the place of K (each CTA all columns of half of
+//          the keys), and there is room for one tile: K is released and
+//          refilled in three groups of columns, V in two halves of the keys.
+//          (64 keys at a time from two stages read the queries twice as often:
+//          2500 clocks per 64 keys, the shared memory's limit being 1860.)
 // Work split: the units (sequence, 64 or 128 rows) are laid end to end, each
 // as long as its key tiles and a constant for its start and end, and dealt out
 // in equal contiguous shares, one per cluster, by the kernel itself from the
@@ -59,25 +60,24 @@ constexpr float LN2 = 0.69314718055994531f;
 // without loss.
 constexpr float RESCALE = 8.f;
 
-constexpr int TILE = 64;     // keys
-constexpr int SC = TILE / 2; // S columns in tensor memory
-constexpr int NC = SC / 2;   // of a softmax thread
 template <bool PAIR>
 struct Cfg {
+  static constexpr int TILE = PAIR ? 128 : 64;      // keys
+  static constexpr int SC = TILE / 2;               // S columns in tensor memory
+  static constexpr int NC = SC / 2;                 // of a softmax thread
   static constexpr int UROWS = PAIR ? 128 : 64;     // rows of a unit
-  static constexpr int KROWS = PAIR ? 32 : 64;      // keys of a tile in a CTA's K
-  static constexpr int K_STAGE = NBLK * KROWS * 128;
-  static constexpr int V_STAGE = PAIR ? 4 * BLK_BYTES : 0;
-  static constexpr int NP = PAIR ? 2 : 1;           // P buffers
-  static constexpr int KV_BYTES = 2 * (K_STAGE + V_STAGE);
-  static constexpr int P_BYTES = NP * BLK_BYTES;
+  static constexpr int KG = PAIR ? 3 : 1;           // K groups of 3 blocks / whole stages
+  static constexpr int STAGE = NBLK * BLK_BYTES;    // 64 keys, all columns
+  static constexpr int V_CHUNK = 4 * BLK_BYTES;     // pair: 64 keys, 256 columns
+  static constexpr int KV_BYTES = PAIR ? STAGE + 2 * V_CHUNK : 2 * STAGE;
+  static constexpr int P_BYTES = TILE * 128;
   static constexpr int USED = Q_BYTES + KV_BYTES + P_BYTES + 2048 + 40 * 8;
   static constexpr int SMEM = 232448;  // all of it; the rest is room for alignment
+  // what a unit costs beyond its tiles (queries in, rows out: about 4500
+  // clocks), in tiles, and the least that a share is worth: shorter ones cost
+  // more in scratch traffic and joining than they save
+  static constexpr int UNIT_COST = PAIR ? 1 : 2, MIN_SHARE = PAIR ? 3 : 6;
 };
-// What a unit costs beyond its tiles (queries in, rows out: about 4500 clocks),
-// in tiles (2500-3700 clocks), and the least that a share is worth: shorter
-// ones cost more in scratch traffic and joining than they save.
-constexpr int UNIT_COST = 2, MIN_SHARE = 6;
 
 struct Maps {
   CUtensorMap q;
@@ -107,7 +107,7 @@ __device__ __forceinline__ Seq load_seq(const LatentArgs &a, int r) {
   s.len = max(__ldg(a.seq_lens + r), 0);
   s.nrt = (s.nq * a.H + Cfg<PAIR>::UROWS - 1) / Cfg<PAIR>::UROWS;
   // a unit without keys still has its rows to write
-  s.tiles = max(1, (s.len + TILE - 1) / TILE);
+  s.tiles = max(1, (s.len + Cfg<PAIR>::TILE - 1) / Cfg<PAIR>::TILE);
   return s;
 }
 
@@ -141,9 +141,9 @@ struct Walk {
         } while (s.nrt == 0);
       }
     }
-    const int take = int(min((long long)(s.tiles + UNIT_COST - pos), left));
-    t0 = max(0, pos - UNIT_COST);
-    t1 = max(0, pos + take - UNIT_COST);
+    const int take = int(min((long long)(s.tiles + Cfg<PAIR>::UNIT_COST - pos), left));
+    t0 = max(0, pos - Cfg<PAIR>::UNIT_COST);
+    t1 = max(0, pos + take - Cfg<PAIR>::UNIT_COST);
     left -= take;
     return t1 > t0;
   }
@@ -158,7 +158,7 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
   auto work = [&](int r) -> long long {
     if (r >= a.R) return 0;
     const Seq s = load_seq<PAIR>(a, r);
-    return (long long)s.nrt * (s.tiles + UNIT_COST);
+    return (long long)s.nrt * (s.tiles + Cfg<PAIR>::UNIT_COST);
   };
   long long mine = 0;
   const long long first = work(threadIdx.x);
@@ -172,7 +172,7 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
 #pragma unroll
   for (int w = 0; w < NW; ++w) total += scratch[w];
   long long share = (total + clusters - 1) / clusters;
-  if (share < MIN_SHARE) share = MIN_SHARE;
+  if (share < Cfg<PAIR>::MIN_SHARE) share = Cfg<PAIR>::MIN_SHARE;
   const long long start = share * cluster;
   if (threadIdx.x == 0) {
     out->share = share;
@@ -201,7 +201,7 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
     }
     const long long lo = before + inc - w;
     if (w > 0 && start >= lo && start < lo + w) {
-      const int length = load_seq<PAIR>(a, r).tiles + UNIT_COST;
+      const int length = load_seq<PAIR>(a, r).tiles + Cfg<PAIR>::UNIT_COST;
       out->r = r;
       out->rt = int((start - lo) / length);
       out->pos = int((start - lo) % length);
@@ -313,6 +313,7 @@ template <bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ Maps m, const LatentArgs a) {
   using C = Cfg<PAIR>;
+  constexpr int TILE = C::TILE, SC = C::SC, NC = C::NC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -321,13 +322,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) atomicOr(&g_error_flags, kErrWaitTimeout);
     return;
   }
-  const uint32_t sQ = smem_u32(smem), sK = sQ + Q_BYTES, sV = sK + 2 * C::K_STAGE,
+  const uint32_t sQ = smem_u32(smem), sK = sQ + Q_BYTES, sV = sK + C::STAGE,
                  sP = sK + C::KV_BYTES;
   float *xmax = reinterpret_cast<float *>(smem + Q_BYTES + C::KV_BYTES + C::P_BYTES);  // [2][256]
   uint64_t *bars = reinterpret_cast<uint64_t *>(xmax + 512);
-  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 16, v_full = k_full + 32,
-                 v_empty = k_full + 48, s_full = k_full + 64, s_empty = k_full + 80,
-                 p_full = k_full + 96, pv_done = k_full + 112, q_full = k_full + 128,
+  // (pair: k_* one for each of 3 column groups, v_* of 2 key halves; single:
+  // k_* one for each of 2 stages)
+  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 24, v_full = k_full + 48,
+                 v_empty = k_full + 64, s_full = k_full + 80, s_empty = k_full + 96,
+                 p_full = k_full + 112, pv_done = k_full + 120, q_full = k_full + 128,
                  q_empty = k_full + 136, done = k_full + 144;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
   Share *share = reinterpret_cast<Share *>(bars + 20);         // 28 bytes
@@ -340,16 +343,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto lead = [&](uint32_t bar) { return PAIR ? mapa_shared(bar, 0) : bar; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(s_empty + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
-      mbar_init(p_full + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
-      mbar_init(pv_done + 8 * i, 1);
     }
+    mbar_init(p_full, PAIR ? 2 * SWARPS : SWARPS);
+    mbar_init(pv_done, 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(done, 1);
@@ -373,47 +378,91 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   const int box = 1 << a.box_log2, none = a.num_blocks * a.bs;
 
-  if (warp == 0 || (PAIR && warp == 1)) {
-    // ---------------- K loads (single: which are V too) and V loads, one warp
-    // each: a lane has the boxes of row groups lane and lane + 32
-    const bool is_v = PAIR && warp == 1;
-    const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
-    const uint32_t full_lead = lead(full);
-    const uint32_t dst0 = is_v ? sV : sK, stage_bytes = is_v ? C::V_STAGE : C::K_STAGE;
-    const int nrows = is_v ? 64 : C::KROWS, blocks = is_v ? 4 : NBLK;
-    const int skip = PAIR && !is_v ? int(rank) * C::KROWS : 0;  // first key of the tile here
-    const int x0 = is_v ? int(rank) * 256 : 0;
+  // Cache rows of 64 keys from key0 on: a lane has those of row groups lane and
+  // lane + 32 (of a box each).
+  auto find_rows = [&](const int32_t *bt, int len, int key0, int (&row)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int off = (lane + 32 * i) << a.box_log2;
+      row[i] = off < 64 ? cache_row(a, bt, len, key0 + off) : none;
+    }
+  };
+  // `count` column blocks from x on of those keys, to blocks of 64 rows
+  auto load_keys = [&](uint32_t dst, int count, int x, const int (&row)[2], int len, int key0,
+                       bool exact, uint32_t bar) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int off = (lane + 32 * i) << a.box_log2;
+      const int valid = row[i] == none ? 0 : exact ? min(box, len - key0 - off) : box;
+      if (off < 64)
+        load_rows<PAIR>(m, a.box_log2, dst + off * 128, BLK_BYTES, count, x, row[i], valid, none, bar);
+    }
+  };
+
+  if (warp == 0) {
+    // ---------------- K loads (single: which are V too)
     Walk<PAIR> w(a, *share);
     int g = 0;
     bool ok = true;
+    const uint32_t full_lead = lead(k_full);
     while (ok && w.next()) {
       const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
-      for (int t = w.t0; t < w.t1; ++t, ++g) {
-        const int key0 = t * TILE + skip, st = g & 1;
-        int row[2], valid[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int off = (lane + 32 * i) << a.box_log2;
-          row[i] = off < nrows ? cache_row(a, bt, w.s.len, key0 + off) : none;
-          // (a row past the length in K alone only makes scores that are masked)
-          valid[i] = row[i] == none ? 0 : PAIR && !is_v ? box : min(box, w.s.len - key0 - off);
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((g >> 1) & 1) ^ 1));
-        if (!ok) break;
-        if (rank == 0 && lane == 0) mbar_expect_tx(full + 8 * st, (PAIR ? 2 : 1) * stage_bytes);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int off = (lane + 32 * i) << a.box_log2;
-          if (off < nrows)
-            load_rows<PAIR>(m, a.box_log2, dst0 + st * stage_bytes + off * 128, nrows * 128, blocks,
-                            x0, row[i], valid[i], none, full_lead + 8 * st);
+      for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+        const int key0 = t * TILE + int(rank) * 64;
+        int row[2];
+        find_rows(bt, w.s.len, key0, row);
+        if (PAIR) {
+          for (int kg = 0; kg < 3; ++kg) {
+            ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * kg, (g & 1) ^ 1));
+            if (!ok) break;
+            if (rank == 0 && lane == 0) mbar_expect_tx(k_full + 8 * kg, 2 * 3 * BLK_BYTES);
+            __syncwarp();
+            // (rows past the length only make scores that are masked)
+            load_keys(sK + kg * 3 * BLK_BYTES, 3, kg * 192, row, w.s.len, key0, false,
+                      full_lead + 8 * kg);
+          }
+        } else {
+          const int st = g & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * st, ((g >> 1) & 1) ^ 1));
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(k_full + 8 * st, C::STAGE);
+          __syncwarp();
+          load_keys(sK + st * C::STAGE, NBLK, 0, row, w.s.len, key0, true, k_full + 8 * st);
         }
       }
     }
     // the loads issued here have landed before the CTA may exit
-    for (int i = max(0, g - 2); i < g; ++i)
-      mbar_wait((rank == 0 ? full : empty) + 8 * (i & 1), (i >> 1) & 1);
+    if (PAIR) {
+      for (int kg = 0; g > 0 && kg < 3; ++kg)
+        mbar_wait((rank == 0 ? k_full : k_empty) + 8 * kg, (g - 1) & 1);
+    } else {
+      for (int i = max(0, g - 2); i < g; ++i) mbar_wait(k_full + 8 * (i & 1), (i >> 1) & 1);
+    }
+  } else if (PAIR && warp == 1) {
+    // ---------------- V loads
+    Walk<PAIR> w(a, *share);
+    int g = 0;
+    bool ok = true;
+    const uint32_t full_lead = lead(v_full);
+    while (ok && w.next()) {
+      const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
+      for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+        int row[2][2];
+        find_rows(bt, w.s.len, t * TILE, row[0]);
+        find_rows(bt, w.s.len, t * TILE + 64, row[1]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(v_empty + 8 * c, (g & 1) ^ 1));
+          if (!ok) break;
+          if (rank == 0 && lane == 0) mbar_expect_tx(v_full + 8 * c, 2 * C::V_CHUNK);
+          __syncwarp();
+          load_keys(sV + c * C::V_CHUNK, 4, int(rank) * 256, row[c], w.s.len, t * TILE + c * 64, true,
+                    full_lead + 8 * c);
+        }
+      }
+    }
+    for (int c = 0; g > 0 && c < 2; ++c)
+      mbar_wait((rank == 0 ? v_full : v_empty) + 8 * c, (g - 1) & 1);
   } else if (warp == 3) {
     // ---------------- query loads
     if (lane == 0) {
@@ -445,25 +494,28 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t q_lo = desc_lo_k(sQ), k_lo = desc_lo_k(sK), p_lo = desc_lo_k(sP);
       // V: blocks of 64 columns BLK_BYTES apart, MN-major
       const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, BLK_BYTES);
-      constexpr uint32_t K_STEP = C::K_STAGE >> 4, V_STEP = (PAIR ? C::V_STAGE : C::K_STAGE) >> 4;
-      constexpr uint32_t KBLK = C::KROWS * 128 >> 4;
       // O (+)= P V of tile g
       auto second = [&](int g, bool first) -> bool {
-        const int st = g & 1;
-        const uint32_t parity = (g >> 1) & 1;
-        if (PAIR && !mbar_wait(v_full + 8 * st, parity)) return false;
-        if (!mbar_wait(p_full + 8 * st, parity)) return false;
+        if (!mbar_wait(p_full, g & 1)) return false;
         tc_fence_after();
         const uint32_t acc0 = first ? 0 : 1;
-        const uint32_t v = v_lo + st * V_STEP, p = p_lo + (PAIR ? st * BLK : 0);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+        for (int c = 0; c < (PAIR ? 2 : 1); ++c) {
+          if (PAIR) {
+            if (!mbar_wait(v_full + 8 * c, g & 1)) return false;
+            tc_fence_after();
+          }
+          const uint32_t p = p_lo + c * BLK;
+          const uint32_t v = v_lo + (PAIR ? c * (C::V_CHUNK >> 4) : (g & 1) * (C::STAGE >> 4));
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            mma_lo<PAIR>(tmem + j * 128, p + ks * 2, v + (PAIR ? 2 : 4) * j * BLK + ks * 128, id_o,
-                         ks == 0 ? acc0 : 1);
-        commit((PAIR ? v_empty : k_empty) + 8 * st);
-        commit(pv_done + 8 * st);
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              mma_lo<PAIR>(tmem + j * 128, p + ks * 2, v + (PAIR ? 2 : 4) * j * BLK + ks * 128, id_o,
+                           c + ks == 0 ? acc0 : 1);
+          commit(PAIR ? v_empty + 8 * c : k_empty + 8 * (g & 1));
+        }
+        commit(pv_done);
         return true;
       };
       Walk<PAIR> w(a, *share);
@@ -472,7 +524,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (; ok && w.next(); ++n) {
         for (int t = w.t0; t < w.t1; ++t, ++g) {
           const int st = g & 1;
-          const uint32_t parity = (g >> 1) & 1;
+          const uint32_t parity = (g >> 1) & 1;           // of things with two stages
+          const uint32_t k_parity = PAIR ? g & 1 : parity, k_first = PAIR ? k_full : k_full + 8 * st;
           // S of this tile goes ahead of P V of the one before, so that the
           // softmax has the tensor pipe's time, unless its keys (or queries)
           // have yet to land.  Then the single form waits for that P V, which
@@ -480,12 +533,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           // clocks a tile, this: 3700); the pair form takes whichever is ready
           // first (2810 to 2550).
           auto ready = [&] {
-            return mbar_test(k_full + 8 * st, parity) && (t > w.t0 || mbar_test(q_full, n & 1));
+            return mbar_test(k_first, k_parity) && (t > w.t0 || mbar_test(q_full, n & 1));
           };
           bool behind = g > 0;
           if (behind && !ready()) {
             const long long c0 = clock64();
-            while (PAIR && !mbar_test(p_full + 8 * (st ^ 1), ((g - 1) >> 1) & 1) && !ready() &&
+            while (PAIR && !mbar_test(p_full, (g - 1) & 1) && !ready() &&
                    clock64() - c0 < kWaitCycles) {
             }
             if (!PAIR || !ready()) {
@@ -494,18 +547,22 @@ __global__ void __launch_bounds__(THREADS, 1)
               behind = false;
             }
           }
-          ok = (t > w.t0 || mbar_wait(q_full, n & 1)) &&
-               mbar_wait(s_empty + 8 * st, parity ^ 1) && mbar_wait(k_full + 8 * st, parity);
+          ok = (t > w.t0 || mbar_wait(q_full, n & 1)) && mbar_wait(s_empty + 8 * st, parity ^ 1);
+          const uint32_t d = tmem + S_COL + st * SC, k = k_lo + (PAIR ? 0 : st * (C::STAGE >> 4));
+#pragma unroll
+          for (int kg = 0; kg < C::KG; ++kg) {
+            ok = ok && mbar_wait(k_first + 8 * kg, k_parity);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kb = kg * (NBLK / C::KG); kb < (kg + 1) * (NBLK / C::KG); ++kb)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_lo<PAIR>(d, q_lo + kb * BLK + ks * 2, k + kb * BLK + ks * 2, id_s,
+                             (kb | ks) != 0);
+            if (PAIR) commit(k_empty + 8 * kg);
+          }
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + S_COL + st * SC, k = k_lo + st * K_STEP;
-#pragma unroll
-          for (int kb = 0; kb < NBLK; ++kb)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_lo<PAIR>(d, q_lo + kb * BLK + ks * 2, k + kb * KBLK + ks * 2, id_s,
-                           (kb | ks) != 0);
-          if (PAIR) commit(k_empty + 8 * st);
           commit(s_full + 8 * st);
           if (t + 1 == w.t1) commit(q_empty);
           if (behind) {
@@ -551,7 +608,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         uint32_t s[NC];
         const uint32_t t_s = t_lane + S_COL + sb * SC + part * NC;
-        tmem_ld16(t_s, s);
+        if constexpr (PAIR)
+          tmem_ld32(t_s, s);
+        else
+          tmem_ld16(t_s, s);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
@@ -591,16 +651,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           p[c / 2] = pack_bf16(x, y);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        // O is rescaled once P V of the tile before is done; P's room is free
-        // once that of NP tiles before is
-        const bool rescale = t > w.t0 && __any_sync(0xffffffffu, f != 1.f);
-        const int wait_for = rescale ? g - 1 : g - C::NP;
-        if (wait_for >= 0) {
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(pv_done + 8 * (wait_for & 1), (wait_for >> 1) & 1));
+        // P V of the tile before is done: P and O may be written
+        if (g > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1));
           if (!ok) break;
         }
-        if (rescale) {
+        if (t > w.t0 && __any_sync(0xffffffffu, f != 1.f)) {
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
@@ -613,9 +669,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           tmem_wait_st();
         }
-        // P, K-major with 128-byte swizzle
-        const uint32_t prow = sP + (PAIR ? sb * BLK_BYTES : 0) + rl * 128;
-        const int c0 = half * 4 + part * 2;
+        // P, K-major with 128-byte swizzle, 64 keys a block
+        const uint32_t prow = sP + (PAIR ? half * BLK_BYTES : 0) + rl * 128;
+        const int c0 = (PAIR ? 0 : half * 4) + part * (NC / 8);
 #pragma unroll
         for (int c = 0; c < NC / 8; ++c)
           st_shared_v4(prow + (((c0 + c) ^ (rl & 7)) << 4),
@@ -625,9 +681,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) {
           if (PAIR)
-            mbar_arrive_remote(p_full_lead + 8 * sb);
+            mbar_arrive_remote(p_full_lead);
           else
-            mbar_arrive(p_full + 8 * sb);
+            mbar_arrive(p_full);
         }
       }
       if (!ok) break;
@@ -646,7 +702,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         else if (urow < rows && a.lse)
           a.lse[int64_t(grow % a.H) * a.T + grow / a.H] = lse2 * LN2;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1));
       if (!ok) break;
       tc_fence_after();
       // D's columns: part 0 holds the first MMA's, part 1 the second's
