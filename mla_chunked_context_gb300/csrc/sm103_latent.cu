@@ -17,17 +17,16 @@
 //     single form 32 clocks, N=256 80; pair M=128 N=64 25, N=256 64), so S,
 //     with its small N, is bound by re-reading the queries.
 // Two forms (template parameter):
-//   single (rows of a unit: 64)  one CTA, weight-stationary MMAs of M=64; 64
-//          keys at a time from two stages, each of which serves as K (K-major,
-//          9 blocks of 64 columns) and as V (the first 8 blocks, MN-major).
+//   single (rows of a unit: 64)  one CTA, weight-stationary MMAs of M=64; a
+//          stage serves as K (K-major, 9 blocks of 64 columns) and as V (the
+//          first 8 blocks, MN-major).
 //   pair   (rows: 128)  a cluster of two CTAs, cta_group::2 MMAs of M=128 (64
-//          rows in each), 128 keys at a time.  An operand of such an MMA sits
-//          at the same offset in both CTAs, so V (each CTA 256 columns of all
-//          keys) cannot share the place of K (each CTA all columns of half of
-//          the keys), and there is room for one tile: K is released and
-//          refilled in three groups of columns, V in two halves of the keys.
-//          (64 keys at a time from two stages read the queries twice as often:
-//          2500 clocks per 64 keys, the shared memory's limit being 1860.)
+//          rows in each).  An operand of such an MMA sits at the same offset
+//          in both CTAs, so V (each CTA 256 columns of all keys) cannot share
+//          the place of K (each CTA all columns of half of the keys).
+//   Both take 64 keys at a time from two stages.  (128 keys a tile halve the
+//   reads of the queries in the pair form, but leave room for one stage: S,
+//   softmax and P V then follow each other, 4840 clocks per 128 keys.)
 // Work split: the units (sequence, 64 or 128 rows) are laid end to end, each
 // as long as its key tiles and a constant for its start and end, and dealt out
 // in equal contiguous shares, one per cluster, by the kernel itself from the
@@ -39,6 +38,7 @@
 // and epilogue (tensor-memory lanes 0-127).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "sm103.cuh"
 
@@ -52,7 +52,7 @@ constexpr int BLK_BYTES = 64 * 128;              // 64 rows x 64 columns, 128-by
 constexpr int Q_BYTES = NBLK * BLK_BYTES;
 constexpr int SWARPS = 8, STHREADS = 32 * SWARPS;  // softmax
 constexpr int THREADS = 128 + STHREADS;
-constexpr int MAPS = 6;  // cache boxes of 1, 2, 4, 8, 16 and 32 rows
+constexpr int MAPS = 7;  // cache boxes of 1, 2, 4 .. 64 rows
 constexpr uint32_t TMEM_COLS = 512, S_COL = 256;
 constexpr float LN2 = 0.69314718055994531f;
 // O is rescaled only when a row's maximum has grown by more than this (log2):
@@ -60,24 +60,25 @@ constexpr float LN2 = 0.69314718055994531f;
 // without loss.
 constexpr float RESCALE = 8.f;
 
+constexpr int TILE = 64;     // keys
+constexpr int SC = TILE / 2; // S columns in tensor memory
+constexpr int NC = SC / 2;   // of a softmax thread
 template <bool PAIR>
 struct Cfg {
-  static constexpr int TILE = PAIR ? 128 : 64;      // keys
-  static constexpr int SC = TILE / 2;               // S columns in tensor memory
-  static constexpr int NC = SC / 2;                 // of a softmax thread
   static constexpr int UROWS = PAIR ? 128 : 64;     // rows of a unit
-  static constexpr int KG = PAIR ? 3 : 1;           // K groups of 3 blocks / whole stages
-  static constexpr int STAGE = NBLK * BLK_BYTES;    // 64 keys, all columns
-  static constexpr int V_CHUNK = 4 * BLK_BYTES;     // pair: 64 keys, 256 columns
-  static constexpr int KV_BYTES = PAIR ? STAGE + 2 * V_CHUNK : 2 * STAGE;
-  static constexpr int P_BYTES = TILE * 128;
+  static constexpr int KROWS = PAIR ? 32 : 64;      // keys of a tile in a CTA's K
+  static constexpr int K_STAGE = NBLK * KROWS * 128;
+  static constexpr int V_STAGE = PAIR ? 4 * BLK_BYTES : 0;
+  static constexpr int NP = PAIR ? 2 : 1;           // P buffers
+  static constexpr int KV_BYTES = 2 * (K_STAGE + V_STAGE);
+  static constexpr int P_BYTES = NP * BLK_BYTES;
   static constexpr int USED = Q_BYTES + KV_BYTES + P_BYTES + 2048 + 40 * 8;
   static constexpr int SMEM = 232448;  // all of it; the rest is room for alignment
-  // what a unit costs beyond its tiles (queries in, rows out: about 4500
-  // clocks), in tiles, and the least that a share is worth: shorter ones cost
-  // more in scratch traffic and joining than they save
-  static constexpr int UNIT_COST = PAIR ? 1 : 2, MIN_SHARE = PAIR ? 3 : 6;
 };
+// What a unit costs beyond its tiles (queries in, rows out: about 4500 clocks),
+// in tiles (2500-3700 clocks), and the least that a share is worth: shorter
+// ones cost more in scratch traffic and joining than they save.
+constexpr int UNIT_COST = 2, MIN_SHARE = 6;
 
 struct Maps {
   CUtensorMap q;
@@ -107,7 +108,7 @@ __device__ __forceinline__ Seq load_seq(const LatentArgs &a, int r) {
   s.len = max(__ldg(a.seq_lens + r), 0);
   s.nrt = (s.nq * a.H + Cfg<PAIR>::UROWS - 1) / Cfg<PAIR>::UROWS;
   // a unit without keys still has its rows to write
-  s.tiles = max(1, (s.len + Cfg<PAIR>::TILE - 1) / Cfg<PAIR>::TILE);
+  s.tiles = max(1, (s.len + TILE - 1) / TILE);
   return s;
 }
 
@@ -141,74 +142,89 @@ struct Walk {
         } while (s.nrt == 0);
       }
     }
-    const int take = int(min((long long)(s.tiles + Cfg<PAIR>::UNIT_COST - pos), left));
-    t0 = max(0, pos - Cfg<PAIR>::UNIT_COST);
-    t1 = max(0, pos + take - Cfg<PAIR>::UNIT_COST);
+    const int take = int(min((long long)(s.tiles + UNIT_COST - pos), left));
+    t0 = max(0, pos - UNIT_COST);
+    t1 = max(0, pos + take - UNIT_COST);
     left -= take;
     return t1 > t0;
   }
 };
 
-// All threads: this cluster's share of the tiles of all units.
+// All threads: this cluster's share of the positions of all units.
 template <bool PAIR>
 __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int clusters,
                                            Share *out, long long *scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int NW = THREADS / 32;
-  auto work = [&](int r) -> long long {
-    if (r >= a.R) return 0;
-    const Seq s = load_seq<PAIR>(a, r);
-    return (long long)s.nrt * (s.tiles + Cfg<PAIR>::UNIT_COST);
+  struct {
+    long long work;
+    int length;
+  } mine;
+  auto look = [&](int r) {
+    mine.work = 0;
+    mine.length = 1;
+    if (r < a.R) {
+      const Seq s = load_seq<PAIR>(a, r);
+      mine.length = s.tiles + UNIT_COST;
+      mine.work = (long long)s.nrt * mine.length;
+    }
   };
-  long long mine = 0;
-  const long long first = work(threadIdx.x);
-  mine = first;
-  for (int r = threadIdx.x + THREADS; r < a.R; r += THREADS) mine += work(r);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) scratch[warp] = mine;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) total += scratch[w];
-  long long share = (total + clusters - 1) / clusters;
-  if (share < Cfg<PAIR>::MIN_SHARE) share = Cfg<PAIR>::MIN_SHARE;
-  const long long start = share * cluster;
-  if (threadIdx.x == 0) {
-    out->share = share;
-    out->len = max(0LL, min(share, total - start));
-    out->r = out->rt = out->pos = 0;
-  }
-  __syncthreads();
-  if (start >= total) return;
-  long long base = 0;
-  for (int r0 = 0; r0 < a.R; r0 += THREADS) {
-    const int r = r0 + threadIdx.x;
-    const long long w = r0 == 0 ? first : work(r);
-    long long inc = w;
+  // inclusive scan over the block's threads: (own sum, all)
+  auto scan = [&](long long v, long long &all) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
     }
-    if (lane == 31) scratch[warp] = inc;
+    if (lane == 31) scratch[warp] = v;
     __syncthreads();
-    long long before = base, all = 0;
+    all = 0;
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-      if (i < warp) before += scratch[i];
+      if (i == warp) v += all;
       all += scratch[i];
     }
-    const long long lo = before + inc - w;
-    if (w > 0 && start >= lo && start < lo + w) {
-      const int length = load_seq<PAIR>(a, r).tiles + Cfg<PAIR>::UNIT_COST;
-      out->r = r;
-      out->rt = int((start - lo) / length);
-      out->pos = int((start - lo) % length);
+    return v;
+  };
+  // more sequences than threads: their total first
+  long long total = 0;
+  if (a.R > THREADS) {
+    long long sum = 0;
+    for (int r = threadIdx.x; r < a.R; r += THREADS) {
+      look(r);
+      sum += mine.work;
+    }
+    scan(sum, total);
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {  // no work, unless a thread finds some below
+    out->len = 0;
+    out->r = out->rt = out->pos = 0;
+  }
+  long long base = 0;
+  for (int r0 = 0; r0 < a.R; r0 += THREADS) {
+    look(r0 + threadIdx.x);
+    long long all;
+    const long long hi = base + scan(mine.work, all), lo = hi - mine.work;
+    if (a.R <= THREADS) total = all;
+    // (64-bit divisions only where 32 bits do not hold the numbers)
+    long long share = total <= 0x7fffffff ? (unsigned(total) + clusters - 1) / unsigned(clusters)
+                                          : (total + clusters - 1) / clusters;
+    if (share < MIN_SHARE) share = MIN_SHARE;
+    const long long start = share * cluster;
+    if (start >= lo && start < hi) {
+      const long long off = start - lo;
+      const int rt = off <= 0x7fffffff ? int(unsigned(off) / unsigned(mine.length))
+                                       : int(off / mine.length);
+      out->share = share;
+      out->len = min(share, total - start);
+      out->r = r0 + threadIdx.x;
+      out->rt = rt;
+      out->pos = int(off - (long long)rt * mine.length);
     }
     base += all;
+    if (base > start || r0 + THREADS >= a.R) break;
     __syncthreads();
-    if (base > start) return;
   }
 }
 
@@ -236,11 +252,11 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
     tma_load_2d(dst, m, bar, x, y);
 }
 
-// `rows` (at most a box) cache rows from `row`, the first `valid` of them
-// real and the others zeros, to dst and, `count` times, on to the next column
-// block `step` bytes further.  A whole box is one copy a block; a ragged one
-// is put together from the smaller boxes (128-byte rows: any row is a legal
-// destination, and the swizzle goes by the address).
+// A box of cache rows from `row`, the first `valid` of them real and the others
+// zeros, to dst and, `count` times, on to the next column block `step` bytes
+// further; called by one thread.  A whole box is one copy a block; a ragged
+// one is put together from the smaller boxes (128-byte rows: any row is a
+// legal destination, and the swizzle goes by the address).
 template <bool PAIR>
 __device__ __forceinline__ void load_rows(const Maps &m, int box_log2, uint32_t dst, uint32_t step,
                                           int count, int x, int row, int valid, int none,
@@ -248,23 +264,20 @@ __device__ __forceinline__ void load_rows(const Maps &m, int box_log2, uint32_t 
   const int rows = 1 << box_log2;
   if (valid <= 0 || valid >= rows) {
     const int y = valid <= 0 ? none : row;
-    for (int b = 0; b < count; ++b)
-      load_box<PAIR>(dst + b * step, &m.c[box_log2], bar, x + b * 64, y);
+    const CUtensorMap *map = &m.c[box_log2];
+#pragma unroll 3
+    for (int b = 0; b < count; ++b) load_box<PAIR>(dst + b * step, map, bar, x + b * 64, y);
     return;
   }
   int off = 0;
-  for (int k = box_log2 - 1; k >= 0; --k)
-    if (valid & (1 << k)) {
-      for (int b = 0; b < count; ++b)
-        load_box<PAIR>(dst + b * step + off * 128, &m.c[k], bar, x + b * 64, row + off);
-      off += 1 << k;
-    }
-  for (int k = box_log2 - 1; k >= 0; --k)
-    if ((rows - valid) & (1 << k)) {
-      for (int b = 0; b < count; ++b)
-        load_box<PAIR>(dst + b * step + off * 128, &m.c[k], bar, x + b * 64, none);
-      off += 1 << k;
-    }
+  for (int part = 0; part < 2; ++part)  // the real rows, then zeros
+    for (int k = box_log2 - 1; k >= 0; --k)
+      if ((part == 0 ? valid : rows - valid) & (1 << k)) {
+        for (int b = 0; b < count; ++b)
+          load_box<PAIR>(dst + b * step + off * 128, &m.c[k], bar, x + b * 64,
+                         part == 0 ? row + off : none);
+        off += 1 << k;
+      }
 }
 
 // One MMA from the low words of its operands' descriptors; the high words are
@@ -313,7 +326,6 @@ template <bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ Maps m, const LatentArgs a) {
   using C = Cfg<PAIR>;
-  constexpr int TILE = C::TILE, SC = C::SC, NC = C::NC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -322,15 +334,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) atomicOr(&g_error_flags, kErrWaitTimeout);
     return;
   }
-  const uint32_t sQ = smem_u32(smem), sK = sQ + Q_BYTES, sV = sK + C::STAGE,
+  const uint32_t sQ = smem_u32(smem), sK = sQ + Q_BYTES, sV = sK + 2 * C::K_STAGE,
                  sP = sK + C::KV_BYTES;
   float *xmax = reinterpret_cast<float *>(smem + Q_BYTES + C::KV_BYTES + C::P_BYTES);  // [2][256]
   uint64_t *bars = reinterpret_cast<uint64_t *>(xmax + 512);
-  // (pair: k_* one for each of 3 column groups, v_* of 2 key halves; single:
-  // k_* one for each of 2 stages)
-  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 24, v_full = k_full + 48,
-                 v_empty = k_full + 64, s_full = k_full + 80, s_empty = k_full + 96,
-                 p_full = k_full + 112, pv_done = k_full + 120, q_full = k_full + 128,
+  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 16, v_full = k_full + 32,
+                 v_empty = k_full + 48, s_full = k_full + 64, s_empty = k_full + 80,
+                 p_full = k_full + 96, pv_done = k_full + 112, q_full = k_full + 128,
                  q_empty = k_full + 136, done = k_full + 144;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
   Share *share = reinterpret_cast<Share *>(bars + 20);         // 28 bytes
@@ -343,18 +353,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto lead = [&](uint32_t bar) { return PAIR ? mapa_shared(bar, 0) : bar; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_empty + 8 * i, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(s_empty + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
+      mbar_init(p_full + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
+      mbar_init(pv_done + 8 * i, 1);
     }
-    mbar_init(p_full, PAIR ? 2 * SWARPS : SWARPS);
-    mbar_init(pv_done, 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(done, 1);
@@ -368,101 +376,63 @@ __global__ void __launch_bounds__(THREADS, 1)
     else
       tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
   }
+  tc_fence_before();
+  if (PAIR) cluster_arrive();  // both CTAs' barriers exist before any load or arrive
   chain_release();
   chain_wait();
   find_share<PAIR>(a, cluster, clusters, share, scan);
-  tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();
+  if (PAIR) cluster_wait();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int box = 1 << a.box_log2, none = a.num_blocks * a.bs;
+  const int none = a.num_blocks * a.bs;
 
-  // Cache rows of 64 keys from key0 on: a lane has those of row groups lane and
-  // lane + 32 (of a box each).
-  auto find_rows = [&](const int32_t *bt, int len, int key0, int (&row)[2]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int off = (lane + 32 * i) << a.box_log2;
-      row[i] = off < 64 ? cache_row(a, bt, len, key0 + off) : none;
-    }
-  };
-  // `count` column blocks from x on of those keys, to blocks of 64 rows
-  auto load_keys = [&](uint32_t dst, int count, int x, const int (&row)[2], int len, int key0,
-                       bool exact, uint32_t bar) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int off = (lane + 32 * i) << a.box_log2;
-      const int valid = row[i] == none ? 0 : exact ? min(box, len - key0 - off) : box;
-      if (off < 64)
-        load_rows<PAIR>(m, a.box_log2, dst + off * 128, BLK_BYTES, count, x, row[i], valid, none, bar);
-    }
-  };
-
-  if (warp == 0) {
-    // ---------------- K loads (single: which are V too)
+  if (warp == 0 || (PAIR && warp == 1)) {
+    // ---------------- K loads (single: which are V too) and V loads, one warp
+    // each.  A lane finds the cache rows of row groups lane and lane + 32; one
+    // thread issues the copies, from values that are the same in all lanes (a
+    // copy issued by several lanes, each with its own operands, took 120-150
+    // clocks, and the loads of a tile 2500 to 4000).
+    const bool is_v = PAIR && warp == 1;
+    const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
+    const uint32_t full_lead = lead(full);
+    const uint32_t dst0 = is_v ? sV : sK, stage_bytes = is_v ? C::V_STAGE : C::K_STAGE;
+    const int nrows = is_v ? 64 : C::KROWS, blocks = is_v ? 4 : NBLK;
+    const int bl = min(a.box_log2, is_v || !PAIR ? 6 : 5), bx = 1 << bl;  // box of at most nrows
+    const int skip = PAIR && !is_v ? int(rank) * C::KROWS : 0;  // first key of the tile here
+    const int x0 = is_v ? int(rank) * 256 : 0;
     Walk<PAIR> w(a, *share);
     int g = 0;
     bool ok = true;
-    const uint32_t full_lead = lead(k_full);
     while (ok && w.next()) {
       const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
-      for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
-        const int key0 = t * TILE + int(rank) * 64;
+      for (int t = w.t0; t < w.t1; ++t, ++g) {
+        const int key0 = t * TILE + skip, st = g & 1;
         int row[2];
-        find_rows(bt, w.s.len, key0, row);
-        if (PAIR) {
-          for (int kg = 0; kg < 3; ++kg) {
-            ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * kg, (g & 1) ^ 1));
-            if (!ok) break;
-            if (rank == 0 && lane == 0) mbar_expect_tx(k_full + 8 * kg, 2 * 3 * BLK_BYTES);
-            __syncwarp();
-            // (rows past the length only make scores that are masked)
-            load_keys(sK + kg * 3 * BLK_BYTES, 3, kg * 192, row, w.s.len, key0, false,
-                      full_lead + 8 * kg);
-          }
-        } else {
-          const int st = g & 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * st, ((g >> 1) & 1) ^ 1));
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(k_full + 8 * st, C::STAGE);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int off = (lane + 32 * i) << bl;
+          row[i] = off < nrows ? cache_row(a, bt, w.s.len, key0 + off) : none;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((g >> 1) & 1) ^ 1));
+        if (!ok) break;
+        if (rank == 0 && lane == 0) mbar_expect_tx(full + 8 * st, (PAIR ? 2 : 1) * stage_bytes);
+        __syncwarp();
+        for (int i = 0; i < nrows >> bl; ++i) {
+          const int r = __shfl_sync(0xffffffffu, i < 32 ? row[0] : row[1], i & 31);
+          const int off = i << bl;
+          // (a row past the length in K alone only makes scores that are masked)
+          const int valid = r == none ? 0 : PAIR && !is_v ? bx : min(bx, w.s.len - key0 - off);
+          if (elect_one())
+            load_rows<PAIR>(m, bl, dst0 + st * stage_bytes + off * 128, nrows * 128, blocks, x0, r,
+                            valid, none, full_lead + 8 * st);
           __syncwarp();
-          load_keys(sK + st * C::STAGE, NBLK, 0, row, w.s.len, key0, true, k_full + 8 * st);
         }
       }
     }
     // the loads issued here have landed before the CTA may exit
-    if (PAIR) {
-      for (int kg = 0; g > 0 && kg < 3; ++kg)
-        mbar_wait((rank == 0 ? k_full : k_empty) + 8 * kg, (g - 1) & 1);
-    } else {
-      for (int i = max(0, g - 2); i < g; ++i) mbar_wait(k_full + 8 * (i & 1), (i >> 1) & 1);
-    }
-  } else if (PAIR && warp == 1) {
-    // ---------------- V loads
-    Walk<PAIR> w(a, *share);
-    int g = 0;
-    bool ok = true;
-    const uint32_t full_lead = lead(v_full);
-    while (ok && w.next()) {
-      const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
-      for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
-        int row[2][2];
-        find_rows(bt, w.s.len, t * TILE, row[0]);
-        find_rows(bt, w.s.len, t * TILE + 64, row[1]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(v_empty + 8 * c, (g & 1) ^ 1));
-          if (!ok) break;
-          if (rank == 0 && lane == 0) mbar_expect_tx(v_full + 8 * c, 2 * C::V_CHUNK);
-          __syncwarp();
-          load_keys(sV + c * C::V_CHUNK, 4, int(rank) * 256, row[c], w.s.len, t * TILE + c * 64, true,
-                    full_lead + 8 * c);
-        }
-      }
-    }
-    for (int c = 0; g > 0 && c < 2; ++c)
-      mbar_wait((rank == 0 ? v_full : v_empty) + 8 * c, (g - 1) & 1);
+    for (int i = max(0, g - 2); i < g; ++i)
+      mbar_wait((rank == 0 ? full : empty) + 8 * (i & 1), (i >> 1) & 1);
   } else if (warp == 3) {
     // ---------------- query loads
     if (lane == 0) {
@@ -494,28 +464,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t q_lo = desc_lo_k(sQ), k_lo = desc_lo_k(sK), p_lo = desc_lo_k(sP);
       // V: blocks of 64 columns BLK_BYTES apart, MN-major
       const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, BLK_BYTES);
+      constexpr uint32_t K_STEP = C::K_STAGE >> 4, V_STEP = (PAIR ? C::V_STAGE : C::K_STAGE) >> 4;
+      constexpr uint32_t KBLK = C::KROWS * 128 >> 4;
       // O (+)= P V of tile g
       auto second = [&](int g, bool first) -> bool {
-        if (!mbar_wait(p_full, g & 1)) return false;
+        const int st = g & 1;
+        const uint32_t parity = (g >> 1) & 1;
+        if (PAIR && !mbar_wait(v_full + 8 * st, parity)) return false;
+        if (!mbar_wait(p_full + 8 * st, parity)) return false;
         tc_fence_after();
         const uint32_t acc0 = first ? 0 : 1;
+        const uint32_t v = v_lo + st * V_STEP, p = p_lo + (PAIR ? st * BLK : 0);
 #pragma unroll
-        for (int c = 0; c < (PAIR ? 2 : 1); ++c) {
-          if (PAIR) {
-            if (!mbar_wait(v_full + 8 * c, g & 1)) return false;
-            tc_fence_after();
-          }
-          const uint32_t p = p_lo + c * BLK;
-          const uint32_t v = v_lo + (PAIR ? c * (C::V_CHUNK >> 4) : (g & 1) * (C::STAGE >> 4));
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              mma_lo<PAIR>(tmem + j * 128, p + ks * 2, v + (PAIR ? 2 : 4) * j * BLK + ks * 128, id_o,
-                           c + ks == 0 ? acc0 : 1);
-          commit(PAIR ? v_empty + 8 * c : k_empty + 8 * (g & 1));
-        }
-        commit(pv_done);
+          for (int j = 0; j < 2; ++j)
+            mma_lo<PAIR>(tmem + j * 128, p + ks * 2, v + (PAIR ? 2 : 4) * j * BLK + ks * 128, id_o,
+                         ks == 0 ? acc0 : 1);
+        commit((PAIR ? v_empty : k_empty) + 8 * st);
+        commit(pv_done + 8 * st);
         return true;
       };
       Walk<PAIR> w(a, *share);
@@ -524,8 +491,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (; ok && w.next(); ++n) {
         for (int t = w.t0; t < w.t1; ++t, ++g) {
           const int st = g & 1;
-          const uint32_t parity = (g >> 1) & 1;           // of things with two stages
-          const uint32_t k_parity = PAIR ? g & 1 : parity, k_first = PAIR ? k_full : k_full + 8 * st;
+          const uint32_t parity = (g >> 1) & 1;
           // S of this tile goes ahead of P V of the one before, so that the
           // softmax has the tensor pipe's time, unless its keys (or queries)
           // have yet to land.  Then the single form waits for that P V, which
@@ -533,12 +499,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           // clocks a tile, this: 3700); the pair form takes whichever is ready
           // first (2810 to 2550).
           auto ready = [&] {
-            return mbar_test(k_first, k_parity) && (t > w.t0 || mbar_test(q_full, n & 1));
+            return mbar_test(k_full + 8 * st, parity) && (t > w.t0 || mbar_test(q_full, n & 1));
           };
           bool behind = g > 0;
           if (behind && !ready()) {
             const long long c0 = clock64();
-            while (PAIR && !mbar_test(p_full, (g - 1) & 1) && !ready() &&
+            while (PAIR && !mbar_test(p_full + 8 * (st ^ 1), ((g - 1) >> 1) & 1) && !ready() &&
                    clock64() - c0 < kWaitCycles) {
             }
             if (!PAIR || !ready()) {
@@ -547,22 +513,18 @@ __global__ void __launch_bounds__(THREADS, 1)
               behind = false;
             }
           }
-          ok = (t > w.t0 || mbar_wait(q_full, n & 1)) && mbar_wait(s_empty + 8 * st, parity ^ 1);
-          const uint32_t d = tmem + S_COL + st * SC, k = k_lo + (PAIR ? 0 : st * (C::STAGE >> 4));
-#pragma unroll
-          for (int kg = 0; kg < C::KG; ++kg) {
-            ok = ok && mbar_wait(k_first + 8 * kg, k_parity);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kb = kg * (NBLK / C::KG); kb < (kg + 1) * (NBLK / C::KG); ++kb)
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma_lo<PAIR>(d, q_lo + kb * BLK + ks * 2, k + kb * BLK + ks * 2, id_s,
-                             (kb | ks) != 0);
-            if (PAIR) commit(k_empty + 8 * kg);
-          }
+          ok = (t > w.t0 || mbar_wait(q_full, n & 1)) &&
+               mbar_wait(s_empty + 8 * st, parity ^ 1) && mbar_wait(k_full + 8 * st, parity);
           if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + S_COL + st * SC, k = k_lo + st * K_STEP;
+#pragma unroll
+          for (int kb = 0; kb < NBLK; ++kb)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_lo<PAIR>(d, q_lo + kb * BLK + ks * 2, k + kb * KBLK + ks * 2, id_s,
+                           (kb | ks) != 0);
+          if (PAIR) commit(k_empty + 8 * st);
           commit(s_full + 8 * st);
           if (t + 1 == w.t1) commit(q_empty);
           if (behind) {
@@ -608,10 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         uint32_t s[NC];
         const uint32_t t_s = t_lane + S_COL + sb * SC + part * NC;
-        if constexpr (PAIR)
-          tmem_ld32(t_s, s);
-        else
-          tmem_ld16(t_s, s);
+        tmem_ld16(t_s, s);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
@@ -651,12 +610,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           p[c / 2] = pack_bf16(x, y);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        // P V of the tile before is done: P and O may be written
-        if (g > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1));
+        // O is rescaled once P V of the tile before is done; P's room is free
+        // once that of NP tiles before is
+        const bool rescale = t > w.t0 && __any_sync(0xffffffffu, f != 1.f);
+        const int wait_for = rescale ? g - 1 : g - C::NP;
+        if (wait_for >= 0) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(pv_done + 8 * (wait_for & 1), (wait_for >> 1) & 1));
           if (!ok) break;
         }
-        if (t > w.t0 && __any_sync(0xffffffffu, f != 1.f)) {
+        if (rescale) {
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
@@ -669,9 +632,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           tmem_wait_st();
         }
-        // P, K-major with 128-byte swizzle, 64 keys a block
-        const uint32_t prow = sP + (PAIR ? half * BLK_BYTES : 0) + rl * 128;
-        const int c0 = (PAIR ? 0 : half * 4) + part * (NC / 8);
+        // P, K-major with 128-byte swizzle
+        const uint32_t prow = sP + (PAIR ? sb * BLK_BYTES : 0) + rl * 128;
+        const int c0 = half * 4 + part * 2;
 #pragma unroll
         for (int c = 0; c < NC / 8; ++c)
           st_shared_v4(prow + (((c0 + c) ^ (rl & 7)) << 4),
@@ -681,9 +644,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) {
           if (PAIR)
-            mbar_arrive_remote(p_full_lead);
+            mbar_arrive_remote(p_full_lead + 8 * sb);
           else
-            mbar_arrive(p_full);
+            mbar_arrive(p_full + 8 * sb);
         }
       }
       if (!ok) break;
@@ -702,7 +665,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         else if (urow < rows && a.lse)
           a.lse[int64_t(grow % a.H) * a.T + grow / a.H] = lse2 * LN2;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
       // D's columns: part 0 holds the first MMA's, part 1 the second's
@@ -789,66 +752,90 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Joins the pieces of cut units: o = sum_i w_i o_i / sum_i w_i with w_i =
-// 2^(lse_i - max).  A warp takes 32 rows and 4 * W columns of a unit, U pieces
-// at a time: W * U = 16 loads of 16 bytes a thread in flight, which is what
-// this kernel lives on.  Units of few pieces take wide items, those of many
-// pieces (one long sequence) narrow ones, of which there are more.
-template <int W, int U>
-__device__ __forceinline__ void join(const float *part_o, const float *part_lse, int c0, int n,
-                                     int urows, int row, int col4, bool live, int64_t grow,
-                                     __nv_bfloat16 *o, float *lse, int H, int T) {
-  float mx = neg_inf(), sum = 0.f;
+// 2^(lse_i - max).  It lives on loads in flight: a thread has 16 of 16 bytes,
+// U pieces of W float4 columns.  Units of at most FEW pieces: a warp takes 32
+// rows x 4 W columns, W the widest that still takes all pieces at once (two
+// columns of eight pieces for units of two or three cost 5-8 us more where
+// there are a hundred of them).  Units of more (a long sequence spread over
+// many clusters): a block takes 32 rows x 4 columns, its warps every eighth
+// piece, and joins theirs in shared memory (a warp for all of 70 pieces: 3 us
+// more).
+constexpr int CT = 256, CW = CT / 32;  // threads, warps of a block; clusters <= CT
+constexpr int FEW = 8, COMBINE_BLOCKS = 2;
+
+__device__ __forceinline__ int few_columns(int pieces) { return pieces <= 2 ? 8 : pieces <= 4 ? 4 : 2; }
+
+template <int W>
+struct Joined {
+  float mx, sum;
   float4 acc[W];
+};
+
+template <int W>
+__device__ __forceinline__ void join_more(Joined<W> &j, float ls, const float4 (&v)[W], float bs) {
+  const float w = exp2_fast(ls - bs);
+  j.sum += w;
 #pragma unroll
-  for (int k = 0; k < W; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += U) {
+  for (int k = 0; k < W; ++k) {
+    j.acc[k].x = fmaf(w, v[k].x, j.acc[k].x);
+    j.acc[k].y = fmaf(w, v[k].y, j.acc[k].y);
+    j.acc[k].z = fmaf(w, v[k].z, j.acc[k].z);
+    j.acc[k].w = fmaf(w, v[k].w, j.acc[k].w);
+  }
+}
+
+// pieces first, first + step, ... of n
+template <int W, int U>
+__device__ __forceinline__ Joined<W> join_pieces(const float *part_o, const float *part_lse, int c0,
+                                                 int first, int step, int n, int urows, int row,
+                                                 int col4) {
+  Joined<W> j;
+  j.mx = neg_inf();
+  j.sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < W; ++k) j.acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = first; i0 < n; i0 += U * step) {
     float ls[U];
     float4 v[U][W];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u;
+      const int i = i0 + u * step;
       ls[u] = neg_inf();
+#pragma unroll
+      for (int k = 0; k < W; ++k) v[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
         const int64_t s = int64_t(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * urows + (row & ~63);
         ls[u] = part_lse[s + (row & 63)];
         const float4 *src = reinterpret_cast<const float4 *>(part_o + s * LAT) + (row & 63);
 #pragma unroll
         for (int k = 0; k < W; ++k) v[u][k] = src[(col4 + k) * CROWS];
-      } else {
-#pragma unroll
-        for (int k = 0; k < W; ++k) v[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
-    float mn = mx;
+    float mn = j.mx;
 #pragma unroll
     for (int u = 0; u < U; ++u) mn = fmaxf(mn, ls[u]);
     const float bs = is_neg_inf(mn) ? 0.f : mn;
-    const float f = exp2_fast(mx - bs);
-    mx = mn;
-    sum *= f;
+    const float f = exp2_fast(j.mx - bs);
+    j.mx = mn;
+    j.sum *= f;
 #pragma unroll
     for (int k = 0; k < W; ++k)
-      acc[k] = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+      j.acc[k] = make_float4(j.acc[k].x * f, j.acc[k].y * f, j.acc[k].z * f, j.acc[k].w * f);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float w = exp2_fast(ls[u] - bs);
-      sum += w;
-#pragma unroll
-      for (int k = 0; k < W; ++k) {
-        acc[k].x = fmaf(w, v[u][k].x, acc[k].x);
-        acc[k].y = fmaf(w, v[u][k].y, acc[k].y);
-        acc[k].z = fmaf(w, v[u][k].z, acc[k].z);
-        acc[k].w = fmaf(w, v[u][k].w, acc[k].w);
-      }
-    }
+    for (int u = 0; u < U; ++u) join_more<W>(j, ls[u], v[u], bs);
   }
-  if (!live) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  return j;
+}
+
+template <int W>
+__device__ __forceinline__ void join_store(const Joined<W> &j, int64_t grow, int col4,
+                                           __nv_bfloat16 *o, float *lse, int H, int T) {
+  const float inv = j.sum == 0.f ? 0.f : 1.f / j.sum;
   uint2 out[W];
 #pragma unroll
   for (int k = 0; k < W; ++k)
-    out[k] = make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv),
-                        pack_bf16(acc[k].z * inv, acc[k].w * inv));
+    out[k] = make_uint2(pack_bf16(j.acc[k].x * inv, j.acc[k].y * inv),
+                        pack_bf16(j.acc[k].z * inv, j.acc[k].w * inv));
   __nv_bfloat16 *dst = o + grow * LAT + col4 * 4;
   if constexpr (W > 1) {
 #pragma unroll
@@ -860,53 +847,95 @@ __device__ __forceinline__ void join(const float *part_o, const float *part_lse,
   }
   if (lse && col4 == 0)
     lse[int64_t(grow % H) * T + grow / H] =
-        sum == 0.f ? neg_inf() : ((is_neg_inf(mx) ? 0.f : mx) + log2f(sum)) * LN2;
+        j.sum == 0.f ? neg_inf() : ((is_neg_inf(j.mx) ? 0.f : j.mx) + log2f(j.sum)) * LN2;
 }
 
-constexpr int CT = 256;          // threads of a combine block; clusters <= CT
-constexpr int WIDE_PIECES = 8;   // units of at most this many pieces take wide items
 __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, int clusters,
                                                             int urows, const float *part_o,
                                                             const float *part_lse,
                                                             __nv_bfloat16 *o, float *lse, int H,
                                                             int T) {
-  // the cut units (cluster of the first piece) and the items before each
-  __shared__ int units[CT], first[CT + 1], warp_units[CT / 32], warp_items[CT / 32];
+  // cut units (cluster of the first piece) of many pieces, and of few with the
+  // items before each
+  __shared__ int few[CT], many[CT], first[CT], warp_few[CW], warp_many[CW], warp_items[CW];
+  __shared__ float4 sacc[CW][32];
+  __shared__ float smax[CW][32], ssum[CW][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   chain_release();
   chain_wait();
   const int n_here = int(threadIdx.x) < clusters ? desc[2 * threadIdx.x].x : 0;
-  const int items = n_here == 0 ? 0 : (urows / 32) * (n_here <= WIDE_PIECES ? 16 : 128);
+  const bool is_few = n_here > 0 && n_here <= FEW;
+  const int items = is_few ? urows / 32 * (128 / few_columns(n_here)) : 0;
   int inc = items;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += v;
   }
-  const uint32_t b = __ballot_sync(0xffffffffu, items > 0);
+  const uint32_t bf = __ballot_sync(0xffffffffu, is_few);
+  const uint32_t bm = __ballot_sync(0xffffffffu, n_here > FEW);
   if (lane == 31) {
-    warp_units[warp] = __popc(b);
+    warp_few[warp] = __popc(bf);
+    warp_many[warp] = __popc(bm);
     warp_items[warp] = inc;
   }
   __syncthreads();
-  int ubase = 0, ibase = 0, num = 0, total = 0;
+  int base_f = 0, base_m = 0, base_i = 0, num_f = 0, num_m = 0, num_i = 0;
 #pragma unroll
-  for (int i = 0; i < CT / 32; ++i) {
+  for (int i = 0; i < CW; ++i) {
     if (i < warp) {
-      ubase += warp_units[i];
-      ibase += warp_items[i];
+      base_f += warp_few[i];
+      base_m += warp_many[i];
+      base_i += warp_items[i];
     }
-    num += warp_units[i];
-    total += warp_items[i];
+    num_f += warp_few[i];
+    num_m += warp_many[i];
+    num_i += warp_items[i];
   }
-  if (items > 0) {
-    const int u = ubase + __popc(b & ((1u << lane) - 1));
-    units[u] = threadIdx.x;
-    first[u] = ibase + inc - items;
+  const uint32_t below = (1u << lane) - 1;
+  if (n_here > FEW) {
+    many[base_m + __popc(bm & below)] = threadIdx.x;
+  } else if (is_few) {
+    const int u = base_f + __popc(bf & below);
+    few[u] = threadIdx.x;
+    first[u] = base_i + inc - items;
   }
   __syncthreads();
-  for (int it = blockIdx.x * (CT / 32) + warp; it < total; it += gridDim.x * (CT / 32)) {
-    int lo = 0, hi = num - 1;  // the unit of this item
+  const int groups = urows / 32;
+  for (int it = blockIdx.x; it < num_m * groups * 128; it += gridDim.x) {
+    const int c0 = many[it / (groups * 128)], sub = it % (groups * 128);
+    const int row = (sub / 128) * 32 + lane, col4 = sub % 128;
+    const int4 d = desc[2 * c0];
+    const int64_t grow0 = *reinterpret_cast<const long long *>(desc + 2 * c0 + 1);
+    Joined<1> j = join_pieces<1, 16>(part_o, part_lse, c0, warp, CW, d.x, urows, row, col4);
+    sacc[warp][lane] = j.acc[0];
+    smax[warp][lane] = j.mx;
+    ssum[warp][lane] = j.sum;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 1; i < CW; ++i) j.mx = fmaxf(j.mx, smax[i][lane]);
+      const float bs = is_neg_inf(j.mx) ? 0.f : j.mx;
+      j.sum = 0.f;
+      j.acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < CW; ++i) {
+        const float f = exp2_fast(smax[i][lane] - bs);
+        const float4 v = sacc[i][lane];
+        j.sum = fmaf(f, ssum[i][lane], j.sum);
+        j.acc[0].x = fmaf(f, v.x, j.acc[0].x);
+        j.acc[0].y = fmaf(f, v.y, j.acc[0].y);
+        j.acc[0].z = fmaf(f, v.z, j.acc[0].z);
+        j.acc[0].w = fmaf(f, v.w, j.acc[0].w);
+      }
+      if (row < d.y) join_store<1>(j, grow0 + row, col4, o, lse, H, T);
+    }
+    __syncthreads();
+  }
+  // (from the block after the last that had an item above)
+  const int turn = (blockIdx.x + gridDim.x - num_m * groups * 128 % gridDim.x) % gridDim.x;
+  for (int it = turn * CW + warp; it < num_i; it += gridDim.x * CW) {
+    int lo = 0, hi = num_f - 1;  // the unit of this item
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (first[mid] <= it)
@@ -914,16 +943,21 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
       else
         hi = mid - 1;
     }
-    const int c0 = units[lo], sub = it - first[lo];
+    const int c0 = few[lo], sub = it - first[lo];
     const int4 d = desc[2 * c0];
     const int64_t grow0 = *reinterpret_cast<const long long *>(desc + 2 * c0 + 1);
-    const bool wide = d.x <= WIDE_PIECES;
-    const int cols = wide ? 16 : 128;
-    const int row = (sub / cols) * 32 + lane, cg = sub % cols;
-    if (wide)
-      join<8, 2>(part_o, part_lse, c0, d.x, urows, row, cg * 8, row < d.y, grow0 + row, o, lse, H, T);
+    const int w = few_columns(d.x), row = sub / (128 / w) * 32 + lane, col4 = sub % (128 / w) * w;
+    auto one = [&](auto width, auto pieces) {
+      constexpr int W = decltype(width)::value, U = decltype(pieces)::value;
+      const Joined<W> j = join_pieces<W, U>(part_o, part_lse, c0, 0, 1, d.x, urows, row, col4);
+      if (row < d.y) join_store<W>(j, grow0 + row, col4, o, lse, H, T);
+    };
+    if (w == 8)
+      one(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
+    else if (w == 4)
+      one(std::integral_constant<int, 4>(), std::integral_constant<int, 4>());
     else
-      join<1, 16>(part_o, part_lse, c0, d.x, urows, row, cg, row < d.y, grow0 + row, o, lse, H, T);
+      one(std::integral_constant<int, 2>(), std::integral_constant<int, 8>());
   }
 }
 
@@ -960,7 +994,7 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
   int rc = launch_chained(latent_attn_kernel<PAIR>, grid, THREADS, Cfg<PAIR>::SMEM, PAIR ? 2 : 1, s,
                           "latent_attn_kernel", maps, a);
   if (rc) return rc;
-  return launch_chained(latent_combine_kernel, 4 * num_sms(), CT, 0, 1, s, "latent_combine_kernel",
+  return launch_chained(latent_combine_kernel, COMBINE_BLOCKS * num_sms(), CT, 0, 1, s, "latent_combine_kernel",
                         a.desc, PAIR ? grid / 2 : grid, Cfg<PAIR>::UROWS, a.part_o, a.part_lse, a.o,
                         a.lse, a.H, a.T);
 }
