@@ -529,9 +529,10 @@ int mla_chunked_prefill_equal_window(
  *                    ones included; <= 0: none.  New token i of n sits at
  *                    cache position seq_lens[r] - n + i.
  *   block_table      device int32 [num_seqs, block_table_stride].
- * A position whose block id is outside [0, num_blocks), or whose block index
- * is outside the block table's row, sets MLA_STATUS_BAD_BLOCK; it is not
- * written, and is read as zeros.
+ * A position whose block id is outside [0, num_blocks) sets
+ * MLA_STATUS_BAD_BLOCK; it is not written, and is read as zeros.  A position
+ * past the block table's row (block_table_stride * block_size) sets the same
+ * bit; it is not written, and is no key.
  * All four calls only enqueue kernels on `stream` and may be captured into a
  * graph.  Two calls that may run at the same time (two streams, two graphs)
  * need a workspace each.
@@ -595,7 +596,10 @@ int mla_expand_output(const mla_dims_t *d, const void *o_latent,
  *     o_latent[t, h] = sum_j softmax(s)_j c_j[0:L),  lse[h, t] = ln sum e^s_j
  *   q_latent device [T, H, L+P], o_latent device [T, H, L], both in dtype;
  *   lse device float32 [H, T], nullable.  A row that sees no key gets 0 and
- *   -inf.  Cache rows past seq_lens are never used.
+ *   -inf.  Cache rows past seq_lens are never used.  A cache row that is not
+ *   finite makes the tokens that see it NaN, and on the tensor-core path (where
+ *   its weight of 0 multiplies it) may make so the sequence's new tokens before
+ *   it.  No output may overlap an input.
  *   workspace: device, 16-byte aligned, mla_latent_attn_workspace_bytes bytes
  *   (partial results of key ranges: one size for the tensor-core shape,
  *   whatever the batch; 0 bytes and NULL otherwise); nothing in it has to be

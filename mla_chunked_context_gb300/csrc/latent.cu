@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
   const int q0 = max(__ldg(a.qsl + r), 0), q1 = min(__ldg(a.qsl + r + 1), a.T);
   if (t >= q1) return;
   const int len = max(__ldg(a.seq_lens + r), 0);
-  const int nk = a.causal ? max(0, len - (q1 - q0) + (t - q0) + 1) : len;
+  const int keys = int(min((long long)len, (long long)a.bt_stride * a.bs));
+  const int nk = a.causal ? max(0, min(keys, len - (q1 - q0) + (t - q0) + 1)) : keys;
   const int LP = a.L + a.P;
   const T *q = static_cast<const T *>(a.q) + (int64_t(t) * a.H + h) * LP;
   const T *cache = static_cast<const T *>(a.cache);
@@ -120,13 +121,13 @@ __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
     acc[e] = 0.f;
   }
   float m = neg_inf(), l = 0.f;
-  bool bad = false;
+  bool bad = keys < len;
   // lane i < KB finds the cache row of key j0 + i; -1: past the end or bad
   auto find = [&](int j0) -> int64_t {
     const int j = j0 + lane;
     if (lane >= KB || j >= nk) return -1;
     const int b = j / a.bs;
-    const int blk = b < a.bt_stride ? __ldg(bt + b) : -1;
+    const int blk = __ldg(bt + b);
     if (blk < 0 || blk >= a.num_blocks) {
       bad = true;
       return -1;

@@ -109,6 +109,14 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map,
+                                                 uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 // L2 eviction-priority policies for the cache-hinted copies below.
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;
@@ -420,9 +428,9 @@ static inline int take_error_flags_here() {
 // bounds.  Returns false when cuTensorMapEncodeTiled rejects it.
 bool make_tmap_2d_16(CUtensorMap *map, bool fp16, const void *base, uint64_t dim0, uint64_t dim1,
                      uint64_t row_stride_bytes, uint32_t box0, uint32_t box1, bool swizzle128);
-// 3-D variant (dim0 contiguous; box depth 1 along dim2).
+// 3-D variant (dim0 contiguous; box of depth box2 along dim2).
 bool make_tmap_3d_16(CUtensorMap *map, bool fp16, const void *base, uint64_t dim0, uint64_t dim1,
                      uint64_t dim2, uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0,
-                     uint32_t box1, bool swizzle128);
+                     uint32_t box1, bool swizzle128, uint32_t box2 = 1);
 
 }  // namespace mla

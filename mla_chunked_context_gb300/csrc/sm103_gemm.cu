@@ -351,12 +351,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 bool make_tmap_3d_16(CUtensorMap *map, bool fp16, const void *base, uint64_t dim0, uint64_t dim1,
                      uint64_t dim2, uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0,
-                     uint32_t box1, bool swizzle128) {
+                     uint32_t box1, bool swizzle128, uint32_t box2) {
   auto fn = sm103::encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {dim0, dim1, dim2};
   const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
-  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint32_t box[3] = {box0, box1, box2};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                         3, const_cast<void *>(base), dims, strides, box, estr,

@@ -72,32 +72,48 @@ struct Cfg {
   static constexpr int NP = PAIR ? 2 : 1;           // P buffers
   static constexpr int KV_BYTES = 2 * (K_STAGE + V_STAGE);
   static constexpr int P_BYTES = NP * BLK_BYTES;
-  static constexpr int USED = Q_BYTES + KV_BYTES + P_BYTES + 2048 + 40 * 8;
+  static constexpr int USED = Q_BYTES + KV_BYTES + P_BYTES + 2048 + 44 * 8;
   static constexpr int SMEM = 232448;  // all of it; the rest is room for alignment
 };
-// What a unit costs beyond its tiles (queries in, rows out: about 4500 clocks),
-// in tiles (2500-3700 clocks), and the least that a share is worth: shorter
-// ones cost more in scratch traffic and joining than they save.
-constexpr int UNIT_COST = 2, MIN_SHARE = 6;
+// Work split, in positions of a tile.  UNIT_COST: what a unit costs beyond its
+// tiles (queries in, rows out: about 5000 clocks, a tile taking 1700 to 3400).
+// MIN_SHARE: the least that a share is worth; shorter ones cost more in scratch
+// traffic and joining than they save.
+template <bool PAIR>
+constexpr int UNIT_COST = PAIR ? 3 : 2;
+constexpr int MIN_SHARE = 4;
+// A cut costs another UNIT_COST and the joining, some 10 tiles' time of the
+// whole GPU when it is the only one.  So: no cut nearer than SNAP to a unit's
+// end; none at all through units of up to SHORT positions; and where there are
+// no more units than clusters, one each, unless the longest is more than
+// WHOLE_SLACK beyond an equal share.
+constexpr int SNAP = 1, SHORT = 10, WHOLE_SLACK = 8;
+
+// Tiles between asking for keys in L2 and copying them to shared memory, whose
+// two stages do not cover HBM's latency.
+constexpr int AHEAD = 1;
 
 struct Maps {
   CUtensorMap q;
+  CUtensorMap v;  // pair: 16 rows x 4 column blocks
   CUtensorMap c[MAPS];
 };
 
 struct LatentArgs {
   const int32_t *qsl, *seq_lens, *block_table;
+  const uint8_t *cache;
   __nv_bfloat16 *o;
   float *lse, *part_o, *part_lse;
   int4 *desc;
   int32_t *status;
-  int T, R, H, bs, num_blocks, bt_stride, causal, box_log2;
+  int T, R, H, bs, num_blocks, none, bt_stride, causal, box_log2;  // none: a row past the cache
+  uint32_t bs_mul, bs_shift;  // division by bs, see page_of
   float scale_log2;
 };
 
 // ---- the work split ---------------------------------------------------------
 struct Seq {
-  int q0, nq, len, nrt, tiles;
+  int q0, nq, len, keys, nrt, tiles;  // keys: len, cut to the block table's row
 };
 
 template <bool PAIR>
@@ -106,15 +122,17 @@ __device__ __forceinline__ Seq load_seq(const LatentArgs &a, int r) {
   s.q0 = min(max(__ldg(a.qsl + r), 0), a.T);
   s.nq = max(min(__ldg(a.qsl + r + 1), a.T) - s.q0, 0);
   s.len = max(__ldg(a.seq_lens + r), 0);
+  s.keys = int(min((long long)s.len, (long long)a.bt_stride * a.bs));
   s.nrt = (s.nq * a.H + Cfg<PAIR>::UROWS - 1) / Cfg<PAIR>::UROWS;
   // a unit without keys still has its rows to write
-  s.tiles = max(1, (s.len + TILE - 1) / TILE);
+  s.tiles = max(1, (s.keys + TILE - 1) / TILE);
   return s;
 }
 
 struct Share {  // of a cluster, in shared memory
-  long long len, share;
-  int r, rt, pos;
+  long long start, end;  // the positions [start, end)
+  int share;             // of all clusters, before cuts were moved
+  int r, rt, pos, snap;  // of the start; how far cuts were moved
 };
 
 // Piece of a unit: row tile rt of sequence r, key tiles [t0, t1).  Position v
@@ -122,123 +140,182 @@ struct Share {  // of a cluster, in shared memory
 // first UNIT_COST positions has none (or all) of the unit's tiles.
 template <bool PAIR>
 struct Walk {
+  static constexpr int COST = UNIT_COST<PAIR>;
   const LatentArgs &a;
   Seq s;
   int r, rt, t0, t1, pos;
   long long left;
   __device__ __forceinline__ Walk(const LatentArgs &args, const Share &sh)
-      : a(args), r(sh.r), rt(sh.rt), t0(0), t1(0), pos(sh.pos), left(sh.len) {
-    if (left > 0) s = load_seq<PAIR>(a, r);
+      : a(args), r(sh.r), rt(sh.rt), t0(0), t1(0), pos(sh.pos), left(sh.end - sh.start) {
+    if (left > 0) {
+      s = load_seq<PAIR>(a, r);
+      if (rt >= s.nrt) next_seq();  // the share starts behind the sequence
+    }
+  }
+  __device__ __forceinline__ void next_seq() {
+    rt = 0;
+    do {
+      if (++r >= a.R) {
+        left = 0;
+        return;
+      }
+      s = load_seq<PAIR>(a, r);
+    } while (s.nrt == 0);
   }
   __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
-    if (t1 > 0) {  // the previous piece ended its unit (or left would be 0)
+    if (t1 > 0) {  // the previous piece ended its unit (or left is 0)
       pos = 0;
-      if (++rt == s.nrt) {
-        rt = 0;
-        do {
-          if (++r >= a.R) return false;
-          s = load_seq<PAIR>(a, r);
-        } while (s.nrt == 0);
-      }
+      if (left > 0 && ++rt == s.nrt) next_seq();
     }
-    const int take = int(min((long long)(s.tiles + UNIT_COST - pos), left));
-    t0 = max(0, pos - UNIT_COST);
-    t1 = max(0, pos + take - UNIT_COST);
+    if (left <= 0) return false;
+    const int take = int(min((long long)(s.tiles + COST - pos), left));
+    t0 = max(0, pos - COST);
+    pos += take;
+    t1 = max(0, pos - COST);
     left -= take;
     return t1 > t0;
   }
+  // shares after this one that have a piece of this unit, which this one cuts
+  __device__ __forceinline__ int others(const Share &sh) const {
+    return 1 + int((s.tiles + COST - pos - sh.snap - 1) / sh.share);
+  }
 };
 
-// All threads: this cluster's share of the positions of all units.
+// All threads: this cluster's share of the positions of all units.  Cluster c
+// of n starts at position c * share, moved to the end of a unit where one is
+// near.  (Sequences' units and positions are summed in one 64-bit scan, 24 and
+// 40 bits: there are at most 2^24 units, and 2^40 positions would take years.)
+constexpr int POS_BITS = 40;
 template <bool PAIR>
 __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int clusters,
                                            Share *out, long long *scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int NW = THREADS / 32;
-  struct {
-    long long work;
-    int length;
-  } mine;
-  auto look = [&](int r) {
-    mine.work = 0;
-    mine.length = 1;
-    if (r < a.R) {
-      const Seq s = load_seq<PAIR>(a, r);
-      mine.length = s.tiles + UNIT_COST;
-      mine.work = (long long)s.nrt * mine.length;
-    }
+  constexpr long long MASK = (1LL << POS_BITS) - 1;
+  int *most = reinterpret_cast<int *>(scratch + NW);  // [NW]
+  int nrt, length;
+  auto look = [&](int r) -> long long {
+    nrt = 0;
+    length = 1;
+    if (r >= a.R) return 0;
+    const Seq s = load_seq<PAIR>(a, r);
+    nrt = s.nrt;
+    length = s.tiles + UNIT_COST<PAIR>;
+    return ((long long)nrt << POS_BITS) | ((long long)nrt * length);
   };
-  // inclusive scan over the block's threads: (own sum, all)
-  auto scan = [&](long long v, long long &all) {
+  // inclusive scan over the block's threads, the total, and the longest unit
+  int longest = 0;
+  auto scan = [&](long long v, int len, long long &all) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long u = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += u;
     }
-    if (lane == 31) scratch[warp] = v;
+    len = __reduce_max_sync(0xffffffffu, len);
+    if (lane == 31) {
+      scratch[warp] = v;
+      most[warp] = len;
+    }
     __syncthreads();
     all = 0;
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
       if (i == warp) v += all;
       all += scratch[i];
+      longest = max(longest, most[i]);
     }
     return v;
   };
-  // more sequences than threads: their total first
-  long long total = 0;
-  if (a.R > THREADS) {
-    long long sum = 0;
-    for (int r = threadIdx.x; r < a.R; r += THREADS) {
-      look(r);
-      sum += mine.work;
-    }
-    scan(sum, total);
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {  // no work, unless a thread finds some below
-    out->len = 0;
+  if (threadIdx.x == 0) {  // no work, unless threads find some below
+    out->start = out->end = 0;
     out->r = out->rt = out->pos = 0;
+  }
+  // more sequences than threads: their totals first
+  const bool many = a.R > THREADS;
+  long long total = 0;
+  if (many) {
+    long long sum = 0;
+    int len = 0;
+    for (int r = threadIdx.x; r < a.R; r += THREADS) {
+      sum += look(r);
+      if (nrt > 0) len = max(len, length);
+    }
+    scan(sum, len, total);
+    __syncthreads();
   }
   long long base = 0;
   for (int r0 = 0; r0 < a.R; r0 += THREADS) {
-    look(r0 + threadIdx.x);
+    const long long mine = look(r0 + threadIdx.x);
     long long all;
-    const long long hi = base + scan(mine.work, all), lo = hi - mine.work;
-    if (a.R <= THREADS) total = all;
+    const long long sum = base + scan(mine, nrt > 0 ? length : 0, all);
+    if (!many) total = all;
+    const long long positions = total & MASK;
+    const int units = int(total >> POS_BITS);
     // (64-bit divisions only where 32 bits do not hold the numbers)
-    long long share = total <= 0x7fffffff ? (unsigned(total) + clusters - 1) / unsigned(clusters)
-                                          : (total + clusters - 1) / clusters;
-    if (share < MIN_SHARE) share = MIN_SHARE;
-    const long long start = share * cluster;
-    if (start >= lo && start < hi) {
-      const long long off = start - lo;
-      const int rt = off <= 0x7fffffff ? int(unsigned(off) / unsigned(mine.length))
-                                       : int(off / mine.length);
-      out->share = share;
-      out->len = min(share, total - start);
-      out->r = r0 + threadIdx.x;
-      out->rt = rt;
-      out->pos = int(off - (long long)rt * mine.length);
+    int share = positions <= 0x7fffffff
+                    ? int((unsigned(positions) + clusters - 1) / unsigned(clusters))
+                    : int(min((positions + clusters - 1) / clusters, 0x7fffffffLL));
+    if (nrt > 0) {
+      const long long lo = (sum - mine) & MASK, hi = sum & MASK;
+      if (units <= clusters && longest <= share + WHOLE_SLACK) {
+        const int u = cluster - int((sum - mine) >> POS_BITS);  // of this sequence's
+        if (u >= 0 && u < nrt) {
+          out->end = out->share = length;
+          out->r = r0 + threadIdx.x;
+          out->rt = u;
+        }
+      } else {
+        if (share < MIN_SHARE) share = MIN_SHARE;
+        const int snap = longest <= SHORT ? SHORT / 2 : SNAP;
+        const long long start = (long long)share * cluster, end = start + share;
+        // the cut nearest to position p of this sequence (from its start)
+        int rt, pos;
+        auto cut = [&](long long p) {
+          rt = p <= 0x7fffffff ? int(unsigned(p) / unsigned(length)) : int(p / length);
+          pos = int(p - (long long)rt * length);
+          if (pos <= snap) {
+            pos = 0;
+          } else if (length - pos <= snap) {
+            pos = 0;
+            ++rt;
+          }
+          return lo + (long long)rt * length + pos;
+        };
+        if (start >= lo && start < hi) {
+          out->start = cut(start - lo);
+          out->share = share;
+          out->snap = snap;
+          out->r = r0 + threadIdx.x;
+          out->rt = rt;
+          out->pos = pos;
+          if (end >= positions) out->end = positions;
+        }
+        if (end < positions && end >= lo && end < hi) out->end = cut(end - lo);
+      }
     }
     base += all;
-    if (base > start || r0 + THREADS >= a.R) break;
     __syncthreads();
   }
+}
+
+// n / bs for 0 <= n < 2^31 without a division, which would take the loading
+// warps some 200 clocks a piece: with l = ceil(log2 bs) and m = floor(2^32 (2^l
+// - bs) / bs) + 1, n / bs = (n + floor(m n / 2^32)) >> l (Granlund and
+// Montgomery, Division by invariant integers using multiplication, 1994).
+__device__ __forceinline__ int page_of(const LatentArgs &a, int n) {
+  return int((__umulhi(a.bs_mul, uint32_t(n)) + uint32_t(n)) >> a.bs_shift);
 }
 
 // ---- cache loads --------------------------------------------------------------
 // Cache row of position j of a sequence (block table row bt): num_rows (which
 // the loads fill with zeros) past its length and for a bad block.
 __device__ __forceinline__ int cache_row(const LatentArgs &a, const int32_t *bt, int len, int j) {
-  const int none = a.num_blocks * a.bs;
-  if (j >= len) return none;
-  const int b = j / a.bs;
-  const int blk = b < a.bt_stride ? __ldg(bt + b) : -1;
+  if (j >= len) return a.none;
+  const int b = page_of(a, j);
+  const int blk = __ldg(bt + b);
   if (blk < 0 || blk >= a.num_blocks) {
     if (a.status) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
-    return none;
+    return a.none;
   }
   return blk * a.bs + (j - b * a.bs);
 }
@@ -251,6 +328,11 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
   else
     tma_load_2d(dst, m, bar, x, y);
 }
+
+// V of the pair form lies in groups of 16 keys (an MMA's K): [4 column blocks][16
+// keys][64 columns], so that one copy brings a group whatever the page size
+// (a multiple of 16).
+constexpr int V_GROUP = 4 * 16 * 128;
 
 // A box of cache rows from `row`, the first `valid` of them real and the others
 // zeros, to dst and, `count` times, on to the next column block `step` bytes
@@ -343,8 +425,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                  p_full = k_full + 96, pv_done = k_full + 112, q_full = k_full + 128,
                  q_empty = k_full + 136, done = k_full + 144;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
-  Share *share = reinterpret_cast<Share *>(bars + 20);         // 28 bytes
-  long long *scan = reinterpret_cast<long long *>(bars + 24);  // [12]
+  volatile int *progress = reinterpret_cast<volatile int *>(bars + 43);  // tiles K was loaded of
+  Share *share = reinterpret_cast<Share *>(bars + 20);         // 40 bytes
+  long long *scan = reinterpret_cast<long long *>(bars + 25);  // [18]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;
@@ -363,6 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(p_full + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
       mbar_init(pv_done + 8 * i, 1);
     }
+    *progress = 0;
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(done, 1);
@@ -380,12 +464,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (PAIR) cluster_arrive();  // both CTAs' barriers exist before any load or arrive
   chain_release();
   chain_wait();
-  find_share<PAIR>(a, cluster, clusters, share, scan);
-  __syncthreads();
+  find_share<PAIR>(a, cluster, clusters, share, scan);  // (ends with a barrier)
   if (PAIR) cluster_wait();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int none = a.num_blocks * a.bs;
+  const int none = a.none;
 
   if (warp == 0 || (PAIR && warp == 1)) {
     // ---------------- K loads (single: which are V too) and V loads, one warp
@@ -398,9 +481,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t full_lead = lead(full);
     const uint32_t dst0 = is_v ? sV : sK, stage_bytes = is_v ? C::V_STAGE : C::K_STAGE;
     const int nrows = is_v ? 64 : C::KROWS, blocks = is_v ? 4 : NBLK;
-    const int bl = min(a.box_log2, is_v || !PAIR ? 6 : 5), bx = 1 << bl;  // box of at most nrows
+    const int bl = min(a.box_log2, is_v ? 4 : PAIR ? 5 : 6), bx = 1 << bl;  // rows at once
     const int skip = PAIR && !is_v ? int(rank) * C::KROWS : 0;  // first key of the tile here
-    const int x0 = is_v ? int(rank) * 256 : 0;
     Walk<PAIR> w(a, *share);
     int g = 0;
     bool ok = true;
@@ -412,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int off = (lane + 32 * i) << bl;
-          row[i] = off < nrows ? cache_row(a, bt, w.s.len, key0 + off) : none;
+          row[i] = off < nrows ? cache_row(a, bt, w.s.keys, key0 + off) : none;
         }
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((g >> 1) & 1) ^ 1));
         if (!ok) break;
@@ -422,33 +504,78 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int r = __shfl_sync(0xffffffffu, i < 32 ? row[0] : row[1], i & 31);
           const int off = i << bl;
           // (a row past the length in K alone only makes scores that are masked)
-          const int valid = r == none ? 0 : PAIR && !is_v ? bx : min(bx, w.s.len - key0 - off);
-          if (elect_one())
-            load_rows<PAIR>(m, bl, dst0 + st * stage_bytes + off * 128, nrows * 128, blocks, x0, r,
-                            valid, none, full_lead + 8 * st);
+          const int valid = r == none ? 0 : PAIR && !is_v ? bx : min(bx, w.s.keys - key0 - off);
+          if (elect_one()) {
+            const uint32_t dst = dst0 + st * stage_bytes, bar = full_lead + 8 * st;
+            if (!is_v)
+              load_rows<PAIR>(m, bl, dst + off * 128, nrows * 128, blocks, 0, r, valid, none, bar);
+            else if (bl == 4 && (valid == 0 || valid == 16))
+              tma_load_3d_pair(dst + (off >> 4) * V_GROUP, &m.v, bar, 0, r, int(rank) * 4);
+            else
+              load_rows<PAIR>(m, bl, dst + (off >> 4) * V_GROUP + (off & 15) * 128, 16 * 128, 4,
+                              int(rank) * 256, r, valid, none, bar);
+          }
           __syncwarp();
         }
+        if (!is_v && lane == 0) *progress = g + 1;
       }
     }
     // the loads issued here have landed before the CTA may exit
     for (int i = max(0, g - 2); i < g; ++i)
       mbar_wait((rank == 0 ? full : empty) + 8 * (i & 1), (i >> 1) & 1);
   } else if (warp == 3) {
-    // ---------------- query loads
-    if (lane == 0) {
-      Walk<PAIR> w(a, *share);
-      int n = 0;
-      const uint32_t bar = lead(q_full);
-      while (w.next()) {
-        if (!mbar_wait(q_empty, (n & 1) ^ 1)) break;
-        if (rank == 0) mbar_expect_tx(q_full, (PAIR ? 2 : 1) * Q_BYTES);
-        const int row = w.s.q0 * a.H + w.rt * C::UROWS + int(rank) * CROWS;
-        for (int kb = 0; kb < NBLK; ++kb)
-          load_box<PAIR>(sQ + kb * BLK_BYTES, &m.q, bar, kb * 64, row);
-        ++n;
+    // ---------------- query loads, and this CTA's keys on their way to L2
+    // AHEAD tiles before the K loads come to them, whose progress paces this
+    // warp (nothing waits for it but the queries)
+    const int bl = min(a.box_log2, PAIR ? 5 : 6);
+    Walk<PAIR> w(a, *share);
+    int g = 0, n = 0;
+    bool ok = true;
+    const uint32_t bar = lead(q_full);
+    for (; ok && w.next(); ++n) {
+      const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
+      bool queries = false;
+      auto load_queries = [&] {
+        queries = true;
+        if (elect_one()) {
+          if (rank == 0) mbar_expect_tx(q_full, (PAIR ? 2 : 1) * Q_BYTES);
+          const int row = w.s.q0 * a.H + w.rt * C::UROWS + int(rank) * CROWS;
+          for (int kb = 0; kb < NBLK; ++kb)
+            load_box<PAIR>(sQ + kb * BLK_BYTES, &m.q, bar, kb * 64, row);
+        }
+        __syncwarp();
+      };
+      for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+        const long long c0 = clock64();
+        int at;
+        for (;;) {
+          at = __shfl_sync(0xffffffffu, *progress, 0);
+          if (!queries && __all_sync(0xffffffffu, mbar_test(q_empty, (n & 1) ^ 1))) load_queries();
+          if (at >= g - AHEAD) break;
+          ok = __all_sync(0xffffffffu, clock64() - c0 < kWaitCycles);
+          if (!ok) break;
+          __nanosleep(64);
+        }
+        if (at >= g) continue;  // already being loaded
+        const int key0 = t * TILE + (PAIR ? int(rank) * C::KROWS : 0);
+        for (int i = 0; i < C::KROWS >> bl; i += 32) {
+          const int j = key0 + ((lane + i) << bl);
+          int row = none;
+          if (((lane + i) << bl) < C::KROWS) row = cache_row(a, bt, w.s.keys, j);
+          if (row != none)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             a.cache + int64_t(row) * (WIDTH * 2)),
+                         "r"(min(1 << bl, w.s.keys - j) * WIDTH * 2)
+                         : "memory");
+        }
+        __syncwarp();
       }
-      if (n > 0) mbar_wait(rank == 0 ? q_full : q_empty, (n - 1) & 1);
+      if (ok && !queries) {
+        ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (n & 1) ^ 1));
+        if (ok) load_queries();
+      }
     }
+    if (n > 0) mbar_wait(rank == 0 ? q_full : q_empty, (n - 1) & 1);
   } else if (warp == 2) {
     // ---------------- MMA issue (pair: the even CTA).
     if (rank == 0 && elect_one()) {
@@ -462,8 +589,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           mma_commit(bar);
       };
       const uint32_t q_lo = desc_lo_k(sQ), k_lo = desc_lo_k(sK), p_lo = desc_lo_k(sP);
-      // V: blocks of 64 columns BLK_BYTES apart, MN-major
-      const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, BLK_BYTES);
+      // V, MN-major: blocks of 64 columns BLK_BYTES (pair: 16 rows) apart
+      const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, PAIR ? 16 * 128 : BLK_BYTES);
+      constexpr uint32_t V_KS = (PAIR ? V_GROUP : 2048) >> 4;  // 16 keys
+      constexpr uint32_t V_J = PAIR ? 2 * 16 * 128 >> 4 : 4 * BLK;  // second MMA's columns
       constexpr uint32_t K_STEP = C::K_STAGE >> 4, V_STEP = (PAIR ? C::V_STAGE : C::K_STAGE) >> 4;
       constexpr uint32_t KBLK = C::KROWS * 128 >> 4;
       // O (+)= P V of tile g
@@ -479,7 +608,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            mma_lo<PAIR>(tmem + j * 128, p + ks * 2, v + (PAIR ? 2 : 4) * j * BLK + ks * 128, id_o,
+            mma_lo<PAIR>(tmem + j * 128, p + ks * 2, v + j * V_J + ks * V_KS, id_o,
                          ks == 0 ? acc0 : 1);
         commit((PAIR ? v_empty : k_empty) + 8 * st);
         commit(pv_done + 8 * st);
@@ -561,7 +690,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int rows = w.s.nq * a.H - w.rt * C::UROWS;  // of the unit (may exceed it)
       const int urow = int(rank) * CROWS + rl;
       const int i = (w.rt * C::UROWS + urow) / a.H;     // token of the sequence
-      const int vis = a.causal ? min(w.s.len, w.s.len - w.s.nq + i + 1) : w.s.len;
+      const int vis = a.causal ? min(w.s.keys, w.s.len - w.s.nq + i + 1) : w.s.keys;
+      if (w.s.keys < w.s.len && a.status && tid == 0) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
       float mref = neg_inf(), l = 0.f;
       for (int t = w.t0; t < w.t1; ++t, ++g) {
         const int sb = g & 1;
@@ -727,9 +857,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (w.t0 == 0 && tid == 0 && rank == 0) {
           // the unit's first piece: its others are in the shares that follow
-          const long long rest = w.s.tiles - w.t1;
-          a.desc[2 * cluster] =
-              make_int4(1 + int((rest + share->share - 1) / share->share), min(rows, C::UROWS), 0, 0);
+          a.desc[2 * cluster] = make_int4(1 + w.others(*share), min(rows, C::UROWS), 0, 0);
           *reinterpret_cast<long long *>(a.desc + 2 * cluster + 1) = grow0;
         }
       }
@@ -1010,23 +1138,32 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
                           float *part_lse, void *desc, int max_ctas, void *o, float *lse,
                           int32_t *status, cudaStream_t s) {
   using namespace sm103;
-  const int64_t cache_rows = int64_t(num_blocks) * d.block_size;
+  // (a cache without blocks gets a map of one row, which nothing asks for)
+  const int64_t cache_rows = std::max<int64_t>(1, int64_t(num_blocks) * d.block_size);
   if (cache_rows >= (int64_t(1) << 31) - 64) return MLA_ERR_UNSUPPORTED;
   Maps maps;
   if (!make_tmap_2d_16(&maps.q, false, q, WIDTH, uint64_t(T) * d.num_heads, WIDTH * 2, 64, CROWS,
                        true))
     return MLA_ERR_CUDA;
-  // the largest box (at most 32 rows) that never crosses a page
+  if (!make_tmap_3d_16(&maps.v, false, cache, 64, uint64_t(cache_rows), NBLK,
+                       WIDTH * 2, 128, 64, 16, true, 4))
+    return MLA_ERR_CUDA;
+  // the largest box (at most 64 rows) that never crosses a page
   int box_log2 = 0;
   while (box_log2 < MAPS - 1 && d.block_size % (2 << box_log2) == 0) ++box_log2;
   for (int i = 0; i <= box_log2; ++i)
-    if (!make_tmap_2d_16(&maps.c[i], false, cache, WIDTH, uint64_t(std::max<int64_t>(1, cache_rows)),
+    if (!make_tmap_2d_16(&maps.c[i], false, cache, WIDTH, uint64_t(cache_rows),
                          WIDTH * 2, 64, 1u << i, true))
       return MLA_ERR_CUDA;
   for (int i = box_log2 + 1; i < MAPS; ++i) maps.c[i] = maps.c[box_log2];
-  LatentArgs a{qsl, seq_lens, block_table, static_cast<__nv_bfloat16 *>(o), lse, part_o, part_lse,
+  uint32_t bs_shift = 0;
+  while ((uint64_t(1) << bs_shift) < uint64_t(d.block_size)) ++bs_shift;
+  const uint32_t bs_mul = uint32_t(
+      (uint64_t(1) << 32) * ((uint64_t(1) << bs_shift) - d.block_size) / d.block_size + 1);
+  LatentArgs a{qsl, seq_lens, block_table, static_cast<const uint8_t *>(cache),
+               static_cast<__nv_bfloat16 *>(o), lse, part_o, part_lse,
                static_cast<int4 *>(desc), status, T, R, d.num_heads, d.block_size, num_blocks,
-               bt_stride, causal, box_log2, d.softmax_scale * 1.4426950408889634f};
+               int(cache_rows), bt_stride, causal, box_log2, bs_mul, bs_shift, d.softmax_scale * 1.4426950408889634f};
   // rows of an average sequence beyond one CTA's 64: pairs
   const bool pair = int64_t(T) * d.num_heads > int64_t(64) * R;
   return pair ? launch_latent<true>(maps, a, max_ctas, s) : launch_latent<false>(maps, a, max_ctas, s);

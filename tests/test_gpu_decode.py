@@ -227,8 +227,8 @@ def test_latent_attention_many_requests_and_rows_of_no_sequence():
 
 @pytest.mark.parametrize("shape,dtype", [(LARGE, "bf16"), (SMALL, "f32")])
 def test_latent_attention_bad_blocks(shape, dtype):
-    """Bad block ids and lengths past the block table: a status bit, the rows
-    read as zeros."""
+    """Bad block ids: a status bit, the rows read as zeros; a length past the
+    block table's row: the bit, and the keys end with the row."""
     rng = np.random.default_rng(12)
     dims, od = make_dims(shape, 4, 16, dtype)
     lens, qsl = [100, 50, 60], [0, 1, 2, 3]
@@ -236,18 +236,24 @@ def test_latent_attention_bad_blocks(shape, dtype):
     q = normal(rng, 3, 4, shape[0] + shape[1], std=0.4, dtype=dims.dtype)
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     o, lse = run_attn(dims, True, qsl, lens, q, cache, table, status=status)
-    assert status.item() == 0
     bad = table.clone()
     bad[0, 2] = cache.shape[0]
     bad[1, 0] = -1
-    long = [100, 50, 16 * table.shape[1] + 20]  # 20 positions past the table's row
+    assert status.item() == 0
     bad[2] = table[2, 0]
-    o, lse = run_attn(dims, True, qsl, long, q, cache, bad, status=status)
+    row = [100, 50, 16 * table.shape[1]]
+    o, lse = run_attn(dims, True, qsl, row, q, cache, bad, status=status)
     assert status.item() == M.MLA_STATUS_BAD_BLOCK
+    status.zero_()
+    far = table.clone()
+    far[2] = table[2, 0]  # (a full block of sequence 2, as often as the row is long)
+    o2, lse2 = run_attn(dims, True, qsl, [100, 50, row[2] + 20], q, cache, far, status=status)
+    assert status.item() == M.MLA_STATUS_BAD_BLOCK
+    check_attn(dims, od, True, qsl, row, q, cache, far, o2, lse2)
     zero = torch.cat([cache, torch.zeros_like(cache[:1])])  # the same with zero blocks
-    ztab = torch.cat([bad, torch.full((3, 2), len(cache), dtype=torch.int32)], 1)
+    ztab = bad.clone()
     ztab[(ztab < 0) | (ztab > len(cache))] = len(cache)
-    check_attn(dims, od, True, qsl, long, q, zero, ztab, o, lse)
+    check_attn(dims, od, True, qsl, row, q, zero, ztab, o, lse)
 
 
 def test_latent_attention_far_offsets():
