@@ -6,10 +6,14 @@
 // so the kernel is there to stream: the weight halves (16.8 MB each at 128
 // heads) once for few tokens, the activations once for many.
 //
-// A CTA computes 128 tokens x NC columns of one head; two CTAs an SM, so that
-// one's loads run beside the other's epilogue.  NC is 256 (absorb) or 128
-// (expand) where that gives every SM its two CTAs, and smaller where heads and
-// tokens are few, to spread the weights' loads over more SMs.
+// A CTA computes 128 tokens x NC columns of one head; two (expand) or three
+// (absorb) CTAs an SM, so that one's loads run beside another's epilogue.  NC
+// is 128, and 64 where heads and tokens are too few to give every SM two CTAs,
+// to spread the weights' loads over more SMs.  (Absorb with 256 columns, two
+// CTAs an SM: 27.0 us for 500 tokens and 128 heads, with 128 columns 26.0, with
+// 64 34.3; expand with 64: 21.7 against 19.6.)  Both move their bytes at 4.4
+// and 5.0 TB/s then, rows of 256 bytes of each token's 147 (131) KB; 16 tokens
+// take 6.6 us, the host's time for the call.
 //   warp 0     TMA loads: per 64 columns of the contraction, the tokens' box
 //              (only as many rows as there are tokens: what the others' rows of
 //              the accumulator hold is never stored) and the weight's: absorb's
@@ -36,11 +40,12 @@ constexpr int THREADS = 192;
 template <bool EXPAND>
 struct Cfg {
   static constexpr int K = EXPAND ? LAT : HEAD, N = EXPAND ? HEAD : LAT;
-  static constexpr int MAX_NC = EXPAND ? 128 : 256;
+  static constexpr int MAX_NC = 128;
   static constexpr int KBLOCKS = K / 64;
   static constexpr int STAGES = EXPAND ? 3 : 2;
   static constexpr int STAGE = A_BYTES + MAX_NC * 128;
-  static constexpr int SMEM = 1024 + STAGES * STAGE + 128;  // two CTAs an SM
+  static constexpr int CTAS = EXPAND ? 2 : 3;       // an SM
+  static constexpr int SMEM = 1024 + STAGES * STAGE + 128;
 };
 
 struct HeadArgs {
@@ -50,7 +55,7 @@ struct HeadArgs {
 };
 
 template <bool EXPAND>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                      const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_o, const HeadArgs g) {
@@ -63,7 +68,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * C::STAGES + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * g.nc, t0 = blockIdx.y * TM, h = blockIdx.z;
-  const uint32_t cols = uint32_t(g.nc);  // 64, 128 or 256
+  const uint32_t cols = uint32_t(g.nc);  // 64 or 128
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
@@ -209,13 +214,10 @@ int launch_heads(const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap
                         to, g);
 }
 
-// Columns of a CTA: the most (up to `top`) that still gives every SM two CTAs,
-// at least 64.
-int pick_nc(int T, int H, int n, int top) {
+// Columns of a CTA.
+int pick_nc(int T, int H, int n) {
   const int64_t tiles = int64_t((T + TM - 1) / TM) * H;
-  int nc = top;
-  while (nc > 64 && tiles * (n / nc) < 2 * num_sms()) nc /= 2;
-  return nc;
+  return tiles * (n / 128) < 2 * num_sms() ? 64 : 128;
 }
 
 }  // namespace
@@ -226,7 +228,7 @@ int launch_absorb_tc(const mla_dims_t &d, const void *q, int T, const void *w, i
   using namespace sm103;
   const int H = d.num_heads, QK = HEAD + ROPE, LP = LAT + ROPE;
   HeadArgs g{rope_columns ? static_cast<const __nv_bfloat16 *>(q) : nullptr,
-             static_cast<__nv_bfloat16 *>(q_latent), T, H, pick_nc(T, H, LAT, 256),
+             static_cast<__nv_bfloat16 *>(q_latent), T, H, pick_nc(T, H, LAT),
              std::min(TM, (T + 7) / 8 * 8)};
   CUtensorMap ta, tw, to;
   if (!make_tmap_2d_16(&ta, false, q, uint64_t(H) * QK, T, uint64_t(H) * QK * 2, 64, g.box_rows,
@@ -242,7 +244,7 @@ int launch_expand_tc(const mla_dims_t &d, const void *o_latent, int T, const voi
                      cudaStream_t s) {
   using namespace sm103;
   const int H = d.num_heads;
-  HeadArgs g{nullptr, nullptr, T, H, pick_nc(T, H, HEAD, 128), std::min(TM, (T + 7) / 8 * 8)};
+  HeadArgs g{nullptr, nullptr, T, H, pick_nc(T, H, HEAD), std::min(TM, (T + 7) / 8 * 8)};
   CUtensorMap ta, tw, to;
   if (!make_tmap_2d_16(&ta, false, o_latent, uint64_t(H) * LAT, T, uint64_t(H) * LAT * 2, 64,
                        g.box_rows, true) ||

@@ -72,7 +72,8 @@ struct Cfg {
   static constexpr int NP = PAIR ? 2 : 1;           // P buffers
   static constexpr int KV_BYTES = 2 * (K_STAGE + V_STAGE);
   static constexpr int P_BYTES = NP * BLK_BYTES;
-  static constexpr int USED = Q_BYTES + KV_BYTES + P_BYTES + 2048 + 44 * 8;
+  static constexpr int USED = Q_BYTES + KV_BYTES + P_BYTES + 2048 + 48 * 8;
+
   static constexpr int SMEM = 232448;  // all of it; the rest is room for alignment
 };
 // Work split, in positions of a tile.  UNIT_COST: what a unit costs beyond its
@@ -133,6 +134,7 @@ struct Share {  // of a cluster, in shared memory
   long long start, end;  // the positions [start, end)
   int share;             // of all clusters, before cuts were moved
   int r, rt, pos, snap;  // of the start; how far cuts were moved
+  Seq seq;               // r's, so that nobody loads it again
 };
 
 // Piece of a unit: row tile rt of sequence r, key tiles [t0, t1).  Position v
@@ -148,7 +150,7 @@ struct Walk {
   __device__ __forceinline__ Walk(const LatentArgs &args, const Share &sh)
       : a(args), r(sh.r), rt(sh.rt), t0(0), t1(0), pos(sh.pos), left(sh.end - sh.start) {
     if (left > 0) {
-      s = load_seq<PAIR>(a, r);
+      s = sh.seq;
       if (rt >= s.nrt) next_seq();  // the share starts behind the sequence
     }
   }
@@ -194,11 +196,12 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
   constexpr long long MASK = (1LL << POS_BITS) - 1;
   int *most = reinterpret_cast<int *>(scratch + NW);  // [NW]
   int nrt, length;
+  Seq s;
   auto look = [&](int r) -> long long {
     nrt = 0;
     length = 1;
     if (r >= a.R) return 0;
-    const Seq s = load_seq<PAIR>(a, r);
+    s = load_seq<PAIR>(a, r);
     nrt = s.nrt;
     length = s.tiles + UNIT_COST<PAIR>;
     return ((long long)nrt << POS_BITS) | ((long long)nrt * length);
@@ -261,6 +264,7 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
         const int u = cluster - int((sum - mine) >> POS_BITS);  // of this sequence's
         if (u >= 0 && u < nrt) {
           out->end = out->share = length;
+          out->seq = s;
           out->r = r0 + threadIdx.x;
           out->rt = u;
         }
@@ -285,6 +289,7 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
           out->start = cut(start - lo);
           out->share = share;
           out->snap = snap;
+          out->seq = s;
           out->r = r0 + threadIdx.x;
           out->rt = rt;
           out->pos = pos;
@@ -425,9 +430,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                  p_full = k_full + 96, pv_done = k_full + 112, q_full = k_full + 128,
                  q_empty = k_full + 136, done = k_full + 144;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
-  volatile int *progress = reinterpret_cast<volatile int *>(bars + 43);  // tiles K was loaded of
-  Share *share = reinterpret_cast<Share *>(bars + 20);         // 40 bytes
-  long long *scan = reinterpret_cast<long long *>(bars + 25);  // [18]
+  volatile int *progress = reinterpret_cast<volatile int *>(bars + 46);  // tiles K was loaded of
+  Share *share = reinterpret_cast<Share *>(bars + 20);         // 64 bytes
+  long long *scan = reinterpret_cast<long long *>(bars + 28);  // [18]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;
@@ -790,9 +795,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int64_t srow = int64_t(slot) * C::UROWS + int(rank) * CROWS;
       if (half == 0 && part == 0) {
         const int64_t grow = grow0 + urow;
-        if (!whole)
+        if (urow >= rows) {
+        } else if (!whole)
           a.part_lse[srow + rl] = lse2;
-        else if (urow < rows && a.lse)
+        else if (a.lse)
           a.lse[int64_t(grow % a.H) * a.T + grow / a.H] = lse2 * LN2;
       }
       ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1));
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = inv == 0.f ? 0.f : __uint_as_float(o[e + k]) * inv;
-            dst[((dim0 + c + e) / 4) * CROWS] = make_float4(v[0], v[1], v[2], v[3]);
+            if (urow < rows) dst[((dim0 + c + e) / 4) * CROWS] = make_float4(v[0], v[1], v[2], v[3]);
           }
         }
         if (w.t0 == 0 && tid == 0 && rank == 0) {
@@ -985,20 +991,29 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
                                                             int T) {
   // cut units (cluster of the first piece) of many pieces, and of few with the
   // items before each
-  __shared__ int few[CT], many[CT], first[CT], warp_few[CW], warp_many[CW], warp_items[CW];
+  __shared__ int few[CT], many[CT], first[CT], first_m[CT];
+  __shared__ int warp_few[CW], warp_many[CW], warp_items[CW], warp_items_m[CW];
   __shared__ float4 sacc[CW][32];
   __shared__ float smax[CW][32], ssum[CW][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   chain_release();
   chain_wait();
-  const int n_here = int(threadIdx.x) < clusters ? desc[2 * threadIdx.x].x : 0;
+  int n_here = 0, groups = 0;  // pieces, groups of 32 rows
+  if (int(threadIdx.x) < clusters) {
+    const int4 d = desc[2 * threadIdx.x];
+    n_here = d.x;
+    groups = (d.y + 31) / 32;
+  }
   const bool is_few = n_here > 0 && n_here <= FEW;
-  const int items = is_few ? urows / 32 * (128 / few_columns(n_here)) : 0;
-  int inc = items;
+  const int items = is_few ? groups * (128 / few_columns(n_here)) : n_here > FEW ? groups * 128 : 0;
+  int inc = is_few ? items : 0, inc_m = is_few ? 0 : items;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += v;
+    const int v = __shfl_up_sync(0xffffffffu, inc, d), u = __shfl_up_sync(0xffffffffu, inc_m, d);
+    if (lane >= d) {
+      inc += v;
+      inc_m += u;
+    }
   }
   const uint32_t bf = __ballot_sync(0xffffffffu, is_few);
   const uint32_t bm = __ballot_sync(0xffffffffu, n_here > FEW);
@@ -1006,36 +1021,52 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
     warp_few[warp] = __popc(bf);
     warp_many[warp] = __popc(bm);
     warp_items[warp] = inc;
+    warp_items_m[warp] = inc_m;
   }
   __syncthreads();
-  int base_f = 0, base_m = 0, base_i = 0, num_f = 0, num_m = 0, num_i = 0;
+  int base_f = 0, base_m = 0, base_i = 0, base_im = 0, num_f = 0, num_m = 0, num_i = 0, num_im = 0;
 #pragma unroll
   for (int i = 0; i < CW; ++i) {
     if (i < warp) {
       base_f += warp_few[i];
       base_m += warp_many[i];
       base_i += warp_items[i];
+      base_im += warp_items_m[i];
     }
     num_f += warp_few[i];
     num_m += warp_many[i];
     num_i += warp_items[i];
+    num_im += warp_items_m[i];
   }
   const uint32_t below = (1u << lane) - 1;
   if (n_here > FEW) {
-    many[base_m + __popc(bm & below)] = threadIdx.x;
+    const int u = base_m + __popc(bm & below);
+    many[u] = threadIdx.x;
+    first_m[u] = base_im + inc_m - items;
   } else if (is_few) {
     const int u = base_f + __popc(bf & below);
     few[u] = threadIdx.x;
     first[u] = base_i + inc - items;
   }
   __syncthreads();
-  const int groups = urows / 32;
-  for (int it = blockIdx.x; it < num_m * groups * 128; it += gridDim.x) {
-    const int c0 = many[it / (groups * 128)], sub = it % (groups * 128);
+  auto unit_of = [](const int *start, int n, int it) {  // the last that starts at or before it
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (start[mid] <= it)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  };
+  for (int it = blockIdx.x; it < num_im; it += gridDim.x) {
+    const int u = unit_of(first_m, num_m, it), c0 = many[u], sub = it - first_m[u];
     const int row = (sub / 128) * 32 + lane, col4 = sub % 128;
     const int4 d = desc[2 * c0];
     const int64_t grow0 = *reinterpret_cast<const long long *>(desc + 2 * c0 + 1);
-    Joined<1> j = join_pieces<1, 16>(part_o, part_lse, c0, warp, CW, d.x, urows, row, col4);
+    Joined<1> j =
+        join_pieces<1, 16>(part_o, part_lse, c0, warp, CW, row < d.y ? d.x : 0, urows, row, col4);
     sacc[warp][lane] = j.acc[0];
     smax[warp][lane] = j.mx;
     ssum[warp][lane] = j.sum;
@@ -1061,23 +1092,16 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
     __syncthreads();
   }
   // (from the block after the last that had an item above)
-  const int turn = (blockIdx.x + gridDim.x - num_m * groups * 128 % gridDim.x) % gridDim.x;
+  const int turn = (blockIdx.x + gridDim.x - num_im % gridDim.x) % gridDim.x;
   for (int it = turn * CW + warp; it < num_i; it += gridDim.x * CW) {
-    int lo = 0, hi = num_f - 1;  // the unit of this item
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first[mid] <= it)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const int c0 = few[lo], sub = it - first[lo];
+    const int u = unit_of(first, num_f, it), c0 = few[u], sub = it - first[u];
     const int4 d = desc[2 * c0];
     const int64_t grow0 = *reinterpret_cast<const long long *>(desc + 2 * c0 + 1);
     const int w = few_columns(d.x), row = sub / (128 / w) * 32 + lane, col4 = sub % (128 / w) * w;
     auto one = [&](auto width, auto pieces) {
       constexpr int W = decltype(width)::value, U = decltype(pieces)::value;
-      const Joined<W> j = join_pieces<W, U>(part_o, part_lse, c0, 0, 1, d.x, urows, row, col4);
+      const Joined<W> j =
+          join_pieces<W, U>(part_o, part_lse, c0, 0, 1, row < d.y ? d.x : 0, urows, row, col4);
       if (row < d.y) join_store<W>(j, grow0 + row, col4, o, lse, H, T);
     };
     if (w == 8)
@@ -1122,6 +1146,9 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
   int rc = launch_chained(latent_attn_kernel<PAIR>, grid, THREADS, Cfg<PAIR>::SMEM, PAIR ? 2 : 1, s,
                           "latent_attn_kernel", maps, a);
   if (rc) return rc;
+  // sequences that the block table keeps short are never cut: nothing to join
+  const int64_t most_tiles = (int64_t(a.bt_stride) * a.bs + TILE - 1) / TILE;
+  if (most_tiles + UNIT_COST<PAIR> <= SHORT) return MLA_OK;
   return launch_chained(latent_combine_kernel, COMBINE_BLOCKS * num_sms(), CT, 0, 1, s, "latent_combine_kernel",
                         a.desc, PAIR ? grid / 2 : grid, Cfg<PAIR>::UROWS, a.part_o, a.part_lse, a.o,
                         a.lse, a.H, a.T);
