@@ -6,12 +6,13 @@
 //    absorption (B = W_uk[h], n contiguous) and the output expansion (B =
 //    W_uv[h]^T, k contiguous); 64x64 shared-memory tiles, 4x4 outputs a
 //    thread.
-//  * latent_attn_simt: one block per (new token, head).  Its warps take the
-//    keys in turn, KB at a time (the dot products' loads and reductions
-//    overlap, and the next ones' block ids are on their way), each with its
-//    own running maximum and sum; the warps' results are joined in shared
-//    memory.  Bound by the latency of that chain: 16 warps of 8 keys took 28.7
-//    to 14.4 us on 4 x 3 tokens, 16 heads, up to 700 keys of 80 floats.
+//  * latent_attn_simt: one block per (new token, head).  A group of G lanes
+//    takes a key at a time (U keys in flight), each lane NC 16-byte pieces of
+//    its row, so that a score costs log2 G shuffles and its weight needs none;
+//    each group has its own running maximum and sum, joined over the warp by
+//    shuffles and over the block in shared memory.  (A warp for a key, 32
+//    lanes over its columns, kept eight rows of 4-byte loads in flight and took
+//    20 us for 4 x 3 tokens, 16 heads, 700 keys of 80 floats; this 8.4.)
 #include "common.cuh"
 
 namespace mla {
@@ -33,6 +34,8 @@ __global__ void __launch_bounds__(256) head_gemm_simt(HeadGemm g) {
   __shared__ float As[GK][GT + 1];
   __shared__ float Bs[GK][GT + 1];
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  chain_release();
+  chain_wait();
   const int n0 = blockIdx.x * GT, m0 = blockIdx.y * GT, h = blockIdx.z;
   const T *A = static_cast<const T *>(g.a) + h * g.a_head;
   const T *B = static_cast<const T *>(g.b) + h * g.b_head;
@@ -91,118 +94,154 @@ struct LatentArgs {
   const int32_t *qsl, *seq_lens, *block_table;
   int32_t *status;
   int T, R, H, L, P, bs, num_blocks, bt_stride, causal;
+  Divider by_bs;
   float scale_log2;
 };
 
-// NV: 32-element slices of a row held by a warp (L + P <= 32 * NV); AW: warps of
-// a block; KB: keys a warp takes at once
-template <typename T, int NV, int AW, int KB>
+// 16 bytes of T
+template <typename T>
+struct Vec {
+  static constexpr int N = 16 / sizeof(T);
+  uint4 raw;
+  __device__ __forceinline__ float get(int i) const {
+    return to_f32(reinterpret_cast<const T *>(&raw)[i]);
+  }
+};
+
+// G lanes a key, NC pieces of 16 bytes a lane (rows of at most 16 G NC bytes),
+// AW warps a block, U keys of a group in flight
+template <typename T, int G, int NC, int AW, int U>
 __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
   extern __shared__ float sh[];  // [AW][L] partial outputs, [AW] maxima, [AW] sums
+  constexpr int N = Vec<T>::N, GROUPS = AW * 32 / G, STEP = GROUPS * U;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane % G, group = threadIdx.x / G;
   const int t = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  chain_release();
+  chain_wait();
   const int lo = max(__ldg(a.qsl), 0), hi = min(__ldg(a.qsl + a.R), a.T);
   if (t < lo || t >= hi) return;
   const int r = find_seq(a.qsl, a.R, t);
   const int q0 = max(__ldg(a.qsl + r), 0), q1 = min(__ldg(a.qsl + r + 1), a.T);
   if (t >= q1) return;
   const int len = max(__ldg(a.seq_lens + r), 0);
-  const int keys = int(min((long long)len, (long long)a.bt_stride * a.bs));
+  const int keys = keys_of(len, a.bt_stride, a.bs);
   const int nk = a.causal ? max(0, min(keys, len - (q1 - q0) + (t - q0) + 1)) : keys;
   const int LP = a.L + a.P;
   const T *q = static_cast<const T *>(a.q) + (int64_t(t) * a.H + h) * LP;
   const T *cache = static_cast<const T *>(a.cache);
   const int32_t *bt = a.block_table + int64_t(r) * a.bt_stride;
-  float qr[NV], acc[NV];
-#pragma unroll
-  for (int e = 0; e < NV; ++e) {
-    const int d = lane + 32 * e;
-    qr[e] = d < LP ? to_f32(q[d]) : 0.f;
-    acc[e] = 0.f;
-  }
-  float m = neg_inf(), l = 0.f;
   bool bad = keys < len;
-  // lane i < KB finds the cache row of key j0 + i; -1: past the end or bad
-  auto find = [&](int j0) -> int64_t {
-    const int j = j0 + lane;
-    if (lane >= KB || j >= nk) return -1;
-    const int b = j / a.bs;
-    const int blk = __ldg(bt + b);
-    if (blk < 0 || blk >= a.num_blocks) {
-      bad = true;
-      return -1;
+  // block ids of this group's next keys (key base + u * GROUPS + group)
+  int blk[U];
+  auto look_up = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = base + u * GROUPS + group;
+      blk[u] = j < nk ? __ldg(bt + a.by_bs.quotient(j)) : -2;
     }
-    return (int64_t(blk) * a.bs + j % a.bs) * LP;
   };
-  int64_t mine = find(warp * KB);
-  for (int j0 = warp * KB; j0 < nk; j0 += AW * KB) {
-    const T *row[KB];
-    float s[KB];
+  look_up(0);
+  float qr[NC][N], acc[NC][N];
 #pragma unroll
-    for (int i = 0; i < KB; ++i) {
-      const int64_t off = __shfl_sync(0xffffffffu, mine, i);
-      row[i] = off < 0 ? nullptr : cache + off;
-      s[i] = 0.f;
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int d = (c * G + sub) * N + e;
+      qr[c][e] = d < LP ? to_f32(q[d]) * a.scale_log2 : 0.f;
+      acc[c][e] = 0.f;
     }
-    mine = find(j0 + AW * KB);
-    float c[KB][NV];
+  float m = neg_inf(), l = 0.f;
+  for (int base = 0; base < nk; base += STEP) {
+    Vec<T> v[U][NC];
+    bool live[U];
 #pragma unroll
-    for (int i = 0; i < KB; ++i)
+    for (int u = 0; u < U; ++u) {
+      const int j = base + u * GROUPS + group;
+      live[u] = j < nk;
+      const bool good = blk[u] >= 0 && blk[u] < a.num_blocks;
+      if (live[u] && !good) bad = true;
+      const T *row = cache + (int64_t(blk[u]) * a.bs + (j - a.by_bs.quotient(j) * a.bs)) * LP;
 #pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        const int d = lane + 32 * e;
-        c[i][e] = (row[i] && d < LP) ? to_f32(row[i][d]) : 0.f;
-        s[i] = fmaf(qr[e], c[i][e], s[i]);
+      for (int c = 0; c < NC; ++c) {
+        const int d = (c * G + sub) * N;
+        v[u][c].raw = good && d < LP ? *reinterpret_cast<const uint4 *>(row + d)
+                                     : make_uint4(0, 0, 0, 0);
       }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-      for (int i = 0; i < KB; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
-    float mn = m;
-#pragma unroll
-    for (int i = 0; i < KB; ++i) {
-      s[i] = j0 + i < nk ? s[i] * a.scale_log2 : neg_inf();
-      mn = fmaxf(mn, s[i]);
     }
-    const float base = is_neg_inf(mn) ? 0.f : mn;  // every score so far is -inf
-    const float corr = exp2f(m - base);
-    float p[KB];
+    look_up(base + STEP);
+    float x[U], mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      x[u] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[u] = fmaf(qr[c][e], v[u][c].get(e), x[u]);
+    }
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1)
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] += __shfl_xor_sync(0xffffffffu, x[u], off);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!live[u]) x[u] = neg_inf();
+      mn = fmaxf(mn, x[u]);
+    }
+    const float ref = is_neg_inf(mn) ? 0.f : mn;  // every score so far is -inf
+    const float corr = exp2f(m - ref);
+    m = mn;
     l *= corr;
 #pragma unroll
-    for (int i = 0; i < KB; ++i) {
-      p[i] = exp2f(s[i] - base);
-      l += p[i];
-    }
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int e = 0; e < NV; ++e) {
-      acc[e] *= corr;
+      for (int e = 0; e < N; ++e) acc[c][e] *= corr;
 #pragma unroll
-      for (int i = 0; i < KB; ++i) acc[e] = fmaf(p[i], c[i][e], acc[e]);
+    for (int u = 0; u < U; ++u) {
+      const float p = exp2f(x[u] - ref);
+      l += p;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[c][e] = fmaf(p, v[u][c].get(e), acc[c][e]);
     }
-    m = mn;
   }
-  if (bad && a.status) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
+  if (bad && a.status && sub == 0) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
+  // the warp's groups
+  float mw = m;
+#pragma unroll
+  for (int off = 16; off >= G; off >>= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, off));
+  const float fw = exp2f(m - (is_neg_inf(mw) ? 0.f : mw));
+  l *= fw;
+#pragma unroll
+  for (int off = 16; off >= G; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      acc[c][e] *= fw;
+#pragma unroll
+      for (int off = 16; off >= G; off >>= 1)
+        acc[c][e] += __shfl_xor_sync(0xffffffffu, acc[c][e], off);
+      const int d = (c * G + sub) * N + e;
+      if (lane < G && d < a.L) sh[warp * a.L + d] = acc[c][e];
+    }
   float *sm = sh + AW * a.L, *sl = sm + AW;
-#pragma unroll
-  for (int e = 0; e < NV; ++e) {
-    const int d = lane + 32 * e;
-    if (d < a.L) sh[warp * a.L + d] = acc[e];
-  }
   if (lane == 0) {
-    sm[warp] = m;
+    sm[warp] = mw;
     sl[warp] = l;
   }
   __syncthreads();
   float mx = neg_inf(), tot = 0.f, w[AW];
 #pragma unroll
   for (int i = 0; i < AW; ++i) mx = fmaxf(mx, sm[i]);
-  const float base = is_neg_inf(mx) ? 0.f : mx;
+  const float ref = is_neg_inf(mx) ? 0.f : mx;
 #pragma unroll
   for (int i = 0; i < AW; ++i) {
-    w[i] = exp2f(sm[i] - base);
+    w[i] = exp2f(sm[i] - ref);
     tot = fmaf(w[i], sl[i], tot);
   }
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
   T *o = static_cast<T *>(a.o) + (int64_t(t) * a.H + h) * a.L;
   for (int d = threadIdx.x; d < a.L; d += 32 * AW) {
     float v = 0.f;
@@ -212,33 +251,31 @@ __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
   }
   if (threadIdx.x == 0 && a.lse)
     a.lse[int64_t(h) * a.T + t] =
-        tot > 0.f ? (mx + log2f(tot)) * 0.69314718055994531f : neg_inf();
+        tot == 0.f ? neg_inf() : (ref + log2f(tot)) * 0.69314718055994531f;
 }
 
-template <typename T, int NV, int AW, int KB>
-void launch_attn_n(const LatentArgs &a, int grid, cudaStream_t s) {
-  const size_t smem = (size_t(AW) * a.L + 2 * AW) * sizeof(float);  // at most 41 KB
-  latent_attn_simt<T, NV, AW, KB><<<grid, 32 * AW, smem, s>>>(a);
+template <typename T, int G, int NC, int AW, int U>
+int launch_attn_n(const LatentArgs &a, int grid, cudaStream_t s) {
+  const size_t smem = (size_t(AW) * a.L + 2 * AW) * sizeof(float);  // at most 33 KB
+  return launch_chained(latent_attn_simt<T, G, NC, AW, U>, grid, 32 * AW, smem, 1, s,
+                        "latent_attn_simt", a);
 }
 
+// By the 16-byte pieces of a row (at most 256: L + P <= 1024).
 template <typename T>
-void launch_attn_t(const LatentArgs &a, int grid, cudaStream_t s) {
-  const int LP = a.L + a.P;
-  if (LP <= 128)
-    launch_attn_n<T, 4, 16, 8>(a, grid, s);
-  else if (LP <= 320)
-    launch_attn_n<T, 10, 16, 4>(a, grid, s);
-  else if (LP <= 640)
-    launch_attn_n<T, 20, 16, 2>(a, grid, s);
-  else
-    launch_attn_n<T, 32, 8, 2>(a, grid, s);
+int launch_attn_t(const LatentArgs &a, int grid, cudaStream_t s) {
+  const int pieces = (a.L + a.P) * int(sizeof(T)) / 16;
+  if (pieces <= 20) return launch_attn_n<T, 4, 5, 8, 2>(a, grid, s);
+  if (pieces <= 40) return launch_attn_n<T, 8, 5, 8, 2>(a, grid, s);
+  if (pieces <= 80) return launch_attn_n<T, 16, 5, 8, 2>(a, grid, s);
+  if (pieces <= 160) return launch_attn_n<T, 32, 5, 8, 2>(a, grid, s);
+  return launch_attn_n<T, 32, 8, 8, 1>(a, grid, s);
 }
 
 template <typename T>
 int head_gemm(const HeadGemm &g, int H, cudaStream_t s) {
-  launch_begin(s);
-  head_gemm_simt<T><<<dim3((g.N + GT - 1) / GT, (g.M + GT - 1) / GT, H), 256, 0, s>>>(g);
-  return launch_status(s, "head_gemm_simt");
+  return launch_chained(head_gemm_simt<T>, dim3((g.N + GT - 1) / GT, (g.M + GT - 1) / GT, H), 256,
+                        0, 1, s, "head_gemm_simt", g);
 }
 
 }  // namespace
@@ -283,13 +320,9 @@ int launch_latent_attn_simt(const mla_dims_t &d, int causal, int R, const int32_
                             float *lse, int32_t *status, cudaStream_t s) {
   LatentArgs a{q, cache, o, lse, qsl, seq_lens, block_table, status, T, R, d.num_heads,
                d.kv_lora_rank, d.qk_rope_dim, d.block_size, num_blocks, bt_stride, causal,
-               d.softmax_scale * 1.4426950408889634f};
-  launch_begin(s);
-  if (d.dtype == MLA_DTYPE_BF16)
-    launch_attn_t<__nv_bfloat16>(a, T * d.num_heads, s);
-  else
-    launch_attn_t<float>(a, T * d.num_heads, s);
-  return launch_status(s, "latent_attn_simt");
+               Divider(d.block_size), d.softmax_scale * 1.4426950408889634f};
+  if (d.dtype == MLA_DTYPE_BF16) return launch_attn_t<__nv_bfloat16>(a, T * d.num_heads, s);
+  return launch_attn_t<float>(a, T * d.num_heads, s);
 }
 
 }  // namespace mla

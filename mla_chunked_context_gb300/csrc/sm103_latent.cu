@@ -108,7 +108,7 @@ struct LatentArgs {
   int4 *desc;
   int32_t *status;
   int T, R, H, bs, num_blocks, none, bt_stride, causal, box_log2;  // none: a row past the cache
-  uint32_t bs_mul, bs_shift;  // division by bs, see page_of
+  Divider by_bs;
   float scale_log2;
 };
 
@@ -123,7 +123,7 @@ __device__ __forceinline__ Seq load_seq(const LatentArgs &a, int r) {
   s.q0 = min(max(__ldg(a.qsl + r), 0), a.T);
   s.nq = max(min(__ldg(a.qsl + r + 1), a.T) - s.q0, 0);
   s.len = max(__ldg(a.seq_lens + r), 0);
-  s.keys = int(min((long long)s.len, (long long)a.bt_stride * a.bs));
+  s.keys = keys_of(s.len, a.bt_stride, a.bs);
   s.nrt = (s.nq * a.H + Cfg<PAIR>::UROWS - 1) / Cfg<PAIR>::UROWS;
   // a unit without keys still has its rows to write
   s.tiles = max(1, (s.keys + TILE - 1) / TILE);
@@ -303,20 +303,12 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
   }
 }
 
-// n / bs for 0 <= n < 2^31 without a division, which would take the loading
-// warps some 200 clocks a piece: with l = ceil(log2 bs) and m = floor(2^32 (2^l
-// - bs) / bs) + 1, n / bs = (n + floor(m n / 2^32)) >> l (Granlund and
-// Montgomery, Division by invariant integers using multiplication, 1994).
-__device__ __forceinline__ int page_of(const LatentArgs &a, int n) {
-  return int((__umulhi(a.bs_mul, uint32_t(n)) + uint32_t(n)) >> a.bs_shift);
-}
-
 // ---- cache loads --------------------------------------------------------------
 // Cache row of position j of a sequence (block table row bt): num_rows (which
 // the loads fill with zeros) past its length and for a bad block.
 __device__ __forceinline__ int cache_row(const LatentArgs &a, const int32_t *bt, int len, int j) {
   if (j >= len) return a.none;
-  const int b = page_of(a, j);
+  const int b = a.by_bs.quotient(j);
   const int blk = __ldg(bt + b);
   if (blk < 0 || blk >= a.num_blocks) {
     if (a.status) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
@@ -1183,14 +1175,10 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
                          WIDTH * 2, 64, 1u << i, true))
       return MLA_ERR_CUDA;
   for (int i = box_log2 + 1; i < MAPS; ++i) maps.c[i] = maps.c[box_log2];
-  uint32_t bs_shift = 0;
-  while ((uint64_t(1) << bs_shift) < uint64_t(d.block_size)) ++bs_shift;
-  const uint32_t bs_mul = uint32_t(
-      (uint64_t(1) << 32) * ((uint64_t(1) << bs_shift) - d.block_size) / d.block_size + 1);
   LatentArgs a{qsl, seq_lens, block_table, static_cast<const uint8_t *>(cache),
                static_cast<__nv_bfloat16 *>(o), lse, part_o, part_lse,
                static_cast<int4 *>(desc), status, T, R, d.num_heads, d.block_size, num_blocks,
-               int(cache_rows), bt_stride, causal, box_log2, bs_mul, bs_shift, d.softmax_scale * 1.4426950408889634f};
+               int(cache_rows), bt_stride, causal, box_log2, Divider(d.block_size), d.softmax_scale * 1.4426950408889634f};
   // rows of an average sequence beyond one CTA's 64: pairs
   const bool pair = int64_t(T) * d.num_heads > int64_t(64) * R;
   return pair ? launch_latent<true>(maps, a, max_ctas, s) : launch_latent<false>(maps, a, max_ctas, s);
