@@ -535,7 +535,8 @@ int mla_chunked_prefill_equal_window(
  * bit; it is not written, and is no key.
  * All four calls only enqueue kernels on `stream` and may be captured into a
  * graph.  Two calls that may run at the same time (two streams, two graphs)
- * need a workspace each.
+ * need a workspace each.  They take up to 65535 heads, 65535 * 64 tokens and
+ * 2^30 tokens x heads, beyond which they return MLA_ERR_UNSUPPORTED.
  *
  * mla_append_latent: per new token t of sequence r at position p
  *   row[0:L)   = kv_a[t][0:L) * norm_weight / sqrt(mean of squares + norm_eps)
@@ -561,6 +562,8 @@ int mla_chunked_prefill_equal_window(
  *   Arithmetic is float32, rounded once to dtype.  A token with a negative
  *   cache position (more new tokens than seq_lens) is skipped like a row of
  *   no sequence.  kv_cache must not overlap the inputs, new_latent not kv_a.
+ *   Of two tokens with the same cache slot (block tables that share it), either
+ *   one's values may end up in any part of it.
  *   Errors: MLA_ERR_UNSUPPORTED for an odd P with a rope table. */
 int mla_append_latent(const mla_dims_t *d, const void *kv_a, int64_t kv_a_ld,
                       const void *norm_weight, float norm_eps,

@@ -36,10 +36,11 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
 
 namespace {
 
-// Tokens x heads a call may have: grids and row indices stay within 31 bits.
+// Tokens x heads a call may have: grids (65535 tiles of 64 tokens) and row
+// indices (31 bits) hold them.
 int check_rows(const mla_dims_t &d, int T) {
   if (T < 0) return MLA_ERR_INVALID;
-  if (d.num_heads > 65535 || T > (1 << 22) || int64_t(T) * d.num_heads > (int64_t(1) << 30))
+  if (d.num_heads > 65535 || T > 65535 * 64 || int64_t(T) * d.num_heads > (int64_t(1) << 30))
     return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }

@@ -114,7 +114,6 @@ __device__ __forceinline__ void rotate_piece(Piece<T> &x, Piece<T> &y, const flo
   }
 }
 
-
 template <typename T, bool EARLY>
 __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
   constexpr int N = Piece<T>::N;
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
   const int r = find_seq_warp(a.qsl, a.R, t);
   const int q0 = max(__ldg(a.qsl + r), 0), q1 = min(__ldg(a.qsl + r + 1), a.T);
   if (t >= q1) return;  // locations that decrease
-  const int pos = __ldg(a.seq_lens + r) - (q1 - q0) + (t - q0);
+  const int pos = max(__ldg(a.seq_lens + r), 0) - (q1 - q0) + (t - q0);
   if (pos < 0) return;
   const int rpos = a.positions ? __ldg(a.positions + t) : pos;
   if (a.rope && (rpos < 0 || rpos >= a.max_pos)) {

@@ -132,6 +132,27 @@ def test_bindings_refuse_host_tensors():
         M.mla_append_latent(d, z(1, 80), z(2, **i), z(1, **i), None, z(4, 16, 80), z(1, 2, **i))
 
 
+def test_more_than_an_instance_has_room_for():
+    d = M.Dims(2, 64, 16, 32, 32, 16, 0.1, torch.float32)
+    dec, z = M.LatentDecode(d, 2, 2, device="cpu"), torch.zeros
+    i = dict(dtype=torch.int32)
+    for T, R in ((3, 2), (2, 3)):
+        with pytest.raises(ValueError, match="room"):
+            dec(z(T, 2, 48), z(T, 80), z(R + 1, **i), z(R, **i), None, z(4, 16, 80), z(R, 2, **i),
+                z(128, 64), z(T, 2, 32))
+
+
+def test_largest_calls_that_are_taken():
+    """One token more than the grids hold is refused, whatever the pointers."""
+    n = C.c_size_t(1)
+    f = lambda d, T: _lib.lib().mla_latent_attn_workspace_bytes(C.byref(d), T, 1, C.byref(n))
+    assert f(dims(H=1), 65535 * 64) == _lib.MLA_OK
+    assert f(dims(H=1), 65535 * 64 + 1) == UNSUPPORTED
+    assert f(dims(H=65535), 16384) == _lib.MLA_OK
+    assert f(dims(H=65535), 16385) == UNSUPPORTED
+    assert f(dims(H=65536), 1) == UNSUPPORTED
+
+
 # ------------------------------------------------------------------ oracle --
 def test_oracle_absorbed_equals_expanded():
     """Absorbed attention with the two head products is the expanded

@@ -519,3 +519,264 @@ def test_latent_attention_same_result_on_another_stream_and_again():
         M.mla_latent_attn(dims, True, a, b, gq, gc, gt, ws, o2, lse2, stream=s)
         torch.cuda.synchronize()
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# -------------------------------------------------- cut units and their joins --
+@pytest.mark.parametrize("H,lens,ql", [
+    (128, [20011], [1]),                            # dozens of pieces
+    (20, [20011], [1]),                             # the same, 44 of 64 rows dead
+    (33, [5000, 64, 7001], [4, 1, 3]),              # units of 128 and of a few rows
+    (128, [1500 - 17 * i for i in range(60)], [1] * 60),   # a few pieces each
+    (128, [900, 30, 901, 29], [9, 1, 2, 40]),
+    (16, [700 + i for i in range(200)], [1] * 200),
+    (64, [4000, 4000, 0, 4000], [1, 1, 1, 1]),
+])
+def test_latent_attention_cut_units(H, lens, ql):
+    rng = np.random.default_rng(H + len(lens))
+    dims, od = make_dims(LARGE, H, 64, "bf16")
+    qsl = loc(ql)
+    cache, table = make_cache(rng, lens, 64, 576, dims.dtype)
+    q = normal(rng, qsl[-1], H, 576, std=0.4, dtype=dims.dtype)
+    for causal in (True, False):
+        o, lse = run_attn(dims, causal, qsl, lens, q, cache, table)
+        check_attn(dims, od, causal, qsl, lens, q, cache, table, o, lse)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_latent_attention_thousand_requests(H):
+    """More sequences than a block has threads; sequences that share pages."""
+    rng = np.random.default_rng(H)
+    dims, od = make_dims(LARGE, H, 16, "bf16")
+    R = 1000
+    lens = [int(x) for x in rng.integers(0, 90, size=R)]
+    qsl = loc([int(x) for x in rng.integers(0, 3, size=R)])
+    cache, table = make_cache(rng, lens[:50], 16, 576, dims.dtype)
+    table = table[torch.arange(R) % 50]
+    lens = [min(n, lens[r % 50]) for r, n in enumerate(lens)]
+    q = normal(rng, qsl[-1], H, 576, std=0.4, dtype=dims.dtype)
+    o, lse = run_attn(dims, True, qsl, lens, q, cache, table)
+    check_attn(dims, od, True, qsl, lens, q, cache, table, o, lse)
+
+
+@pytest.mark.parametrize("blocks", [6, 7, 8, 9])
+@pytest.mark.parametrize("H", [64, 128])
+def test_latent_attention_short_tables(H, blocks):
+    """Block tables at and around the length up to which no unit is cut."""
+    rng = np.random.default_rng(blocks)
+    dims, od = make_dims(LARGE, H, 64, "bf16")
+    R = 170
+    lens = [int(x) for x in rng.integers(1, blocks * 64 + 1, size=R)]
+    lens[0] = blocks * 64
+    cache, table = make_cache(rng, lens, 64, 576, dims.dtype)
+    table = table[:, :blocks].contiguous()
+    q = normal(rng, R, H, 576, std=0.4, dtype=dims.dtype)
+    o, lse = run_attn(dims, True, list(range(R + 1)), lens, q, cache, table)
+    check_attn(dims, od, True, list(range(R + 1)), lens, q, cache, table, o, lse)
+
+
+def test_latent_attention_without_blocks():
+    """A cache of no blocks: every position is bad and read as zeros, so the
+    scores are 0, the output 0 and the log-sum ln n."""
+    import ctypes as C
+    dims, _ = make_dims(LARGE, 8, 16, "bf16")
+    d = dims.c()
+    cache = torch.ones(2, 16, 576, dtype=dims.dtype, device=DEV)
+    q = torch.ones(1, 8, 576, dtype=dims.dtype, device=DEV)
+    o = torch.full((1, 8, 512), 7.0, dtype=dims.dtype, device=DEV)
+    lse, table = torch.zeros(8, 1, device=DEV), torch.zeros(1, 8, dtype=torch.int32, device=DEV)
+    ws = torch.empty(M.mla_latent_attn_workspace_bytes(dims, 1, 1), dtype=torch.uint8, device=DEV)
+    status, qsl, lens = i32([0]), i32([0, 1]), i32([100])
+    rc = M.lib().mla_latent_attn(
+        C.byref(d), 1, 1, qsl.data_ptr(), lens.data_ptr(), 1, q.data_ptr(), cache.data_ptr(), 0,
+        table.data_ptr(), 8, ws.data_ptr(), ws.numel(), o.data_ptr(), lse.data_ptr(),
+        status.data_ptr(), None)
+    torch.cuda.synchronize()
+    assert rc == 0 and status.item() == M.MLA_STATUS_BAD_BLOCK and (o == 0).all()
+    # the sum 100 is exact; log2f of it (6.6) is within its last place 2^-21,
+    # times ln 2; the rounding of ln 2 (2^-25) times 6.6 and the product's 2^-22
+    within(f64(lse), np.full((8, 1), math.log(100)), 2.0 ** -21 * 0.7 + 6.7 * 2.0 ** -25 + 2.0 ** -22,
+           "lse")
+
+
+def test_append_and_attention_far_offsets_elsewhere():
+    """The append, and the CUDA-core attention, past 2^31 elements of a cache."""
+    dims, od = make_dims(SMALL, 2, 64, "f32")
+    blocks = 2 ** 31 // (64 * 80) + 100
+    cache = torch.empty(blocks, 64, 80, device=DEV)
+    rng = np.random.default_rng(9)
+    kv_a = normal(rng, 70, 80)
+    table = torch.tensor([[blocks - 1, blocks - 7]], dtype=torch.int32)
+    M.mla_append_latent(dims, kv_a.to(DEV), i32([0, 70]), i32([70]), None, cache, table.to(DEV))
+    assert torch.equal(cache[blocks - 1].cpu(), kv_a[:64])
+    assert torch.equal(cache[blocks - 7, :6].cpu(), kv_a[64:])
+    q = normal(rng, 1, 2, 80)
+    o, lse = run_attn(dims, True, [0, 1], [70], q, cache, table)
+    small = torch.full((2, 64, 80), float("nan"))
+    small[0], small[1, :6] = kv_a[:64], kv_a[64:]
+    del cache
+    check_attn(dims, od, True, [0, 1], [70], q, small, torch.tensor([[0, 1]], dtype=torch.int32), o, lse)
+
+
+# ------------------------------------------------- memory, streams, refusals --
+@pytest.mark.parametrize("shape,dtype,H", [(LARGE, "bf16", 128), (LARGE, "bf16", 20), (SMALL, "f32", 3),
+                                           (ODD, "bf16", 5)])
+def test_nothing_is_written_beside_the_outputs(shape, dtype, H):
+    """Outputs and workspace lie between guard bytes, which stay as they were."""
+    rng = np.random.default_rng(H)
+    dims, od = make_dims(shape, H, 16, dtype)
+    L, P, Dn, Dv = shape
+    T, lens, qsl = 5, [1200, 40], [0, 3, 4]                 # the last row: of no sequence
+    cache, table = make_cache(rng, lens, 16, L + P, dims.dtype)
+    guards = []
+
+    def guarded(*size, dtype):
+        n = math.prod(size) * dtype.itemsize
+        raw = torch.full((n + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+        guards.append((raw, n))
+        return raw[256:256 + n].view(dtype).view(*size)
+
+    q = normal(rng, T, H, Dn + P, dtype=dims.dtype).to(DEV)
+    w = normal(rng, H * (Dn + Dv), L, std=0.1, dtype=dims.dtype).to(DEV)
+    q_lat = guarded(T, H, L + P, dtype=dims.dtype)
+    o_lat = guarded(T, H, L, dtype=dims.dtype)
+    out = guarded(T, H, Dv, dtype=dims.dtype)
+    lse = guarded(H, T, dtype=torch.float32)
+    g_cache = guarded(*cache.shape, dtype=dims.dtype)
+    lat = guarded(T, L + P, dtype=dims.dtype)
+    ws = guarded(M.mla_latent_attn_workspace_bytes(dims, T, 2), dtype=torch.uint8)
+    g_cache.copy_(cache)
+    tab = torch.from_numpy(O.rope_table(1300, P).astype(np.float32)).to(DEV)
+    kv_a = normal(rng, T, L + P, dtype=dims.dtype).to(DEV)
+    a, b, t = i32(qsl), i32(lens), table.to(DEV)
+    M.mla_append_latent(dims, kv_a, a, b, tab, g_cache, t, new_latent=lat, q=q, q_pe_out=q_lat[..., L:])
+    M.mla_absorb_query(dims, q, w, q_lat, rope_columns=False)
+    M.mla_latent_attn(dims, True, a, b, q_lat, g_cache, t, ws, o_lat, lse)
+    M.mla_expand_output(dims, o_lat, w, out)
+    torch.cuda.synchronize()
+    for raw, n in guards:
+        assert (raw[:256] == 0x5A).all() and (raw[256 + n:] == 0x5A).all()
+    assert (lat[4].view(torch.uint8) == 0x5A).all() and (o_lat[4].view(torch.uint8) == 0x5A).all()
+    q_lat_ref = q_lat.clone()
+    q_lat_ref[4] = 0
+    _, rl, _, size = O.latent_attention(f64(q_lat_ref), f64(g_cache), table.numpy(), qsl, lens, od, True)
+    tol = (L + P + 8) * F * size + 2.0 ** -22 + (1200 / 8 + 16) * F + F * np.abs(rl)
+    within(f64(lse)[:, :4], rl[:, :4], tol[:, :4], "lse")
+
+
+def test_two_streams_at_once():
+    """Two attentions on two streams, a workspace each, give what each gives
+    alone; a side stream's inputs are made on it."""
+    rng = np.random.default_rng(21)
+    dims, od = make_dims(LARGE, 128, 64, "bf16")
+    sets = []
+    for lens in ([3000, 1200, 700], [64, 2500]):
+        cache, table = make_cache(rng, lens, 64, 576, dims.dtype)
+        q = normal(rng, len(lens), 128, 576, std=0.4, dtype=dims.dtype)
+        o, lse = run_attn(dims, True, list(range(len(lens) + 1)), lens, q, cache, table)
+        ws = torch.empty(M.mla_latent_attn_workspace_bytes(dims, len(lens), len(lens)),
+                         dtype=torch.uint8, device=DEV)
+        sets.append((i32(range(len(lens) + 1)), i32(lens), q.to(DEV), cache.to(DEV), table.to(DEV), ws,
+                     o, lse, torch.empty_like(o), torch.empty_like(lse), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for a, b, q, c, t, ws, _, _, o2, lse2, s in sets:
+            with torch.cuda.stream(s):
+                q2 = q * 1
+                M.mla_latent_attn(dims, True, a, b, q2, c, t, ws, o2, lse2)
+        torch.cuda.synchronize()
+        for *_, o, lse, o2, lse2, _ in sets:
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+            o2.fill_(0)
+            lse2.fill_(0)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("shape,dtype", [(LARGE, "bf16"), (SMALL, "f32")])
+def test_two_graphs_and_a_padded_batch(shape, dtype):
+    """Two captured steps that share an instance (its workspace too), replayed
+    in turn, the second for fewer tokens than its arrays have rows: what eager
+    calls of the tokens alone give, and the cache of the others untouched."""
+    rng = np.random.default_rng(6)
+    H = 16
+    dims, od = make_dims(shape, H, 16, dtype)
+    L, P, Dn, Dv = shape
+    lens = [600, 33, 1, 250]
+    cache, table = make_cache(rng, lens, 16, L + P, dims.dtype)
+    tab = torch.from_numpy(O.rope_table(700, P).astype(np.float32)).to(DEV)
+    w = normal(rng, H * (Dn + Dv), L, std=0.1, dtype=dims.dtype).to(DEV)
+    q = normal(rng, 8, H, Dn + P, dtype=dims.dtype).to(DEV)
+    kv_a = normal(rng, 8, L + P, dtype=dims.dtype).to(DEV)
+    table, dec = table.to(DEV), M.LatentDecode(dims, 8, 4, device=DEV)
+    eager = []
+    for n in (4, 2):
+        c, out = cache.to(DEV), torch.empty(n, H, Dv, dtype=dims.dtype, device=DEV)
+        dec(q[:n].contiguous(), kv_a[:n], i32(range(n + 1)), i32(lens[:n]), tab, c,
+            table[:n].contiguous(), w, out)
+        eager.append((c, out))
+    torch.cuda.synchronize()
+    graphs = []
+    for n, qsl in ((4, i32(range(5))), (2, i32([0, 1, 2, 2, 2]))):
+        c, ls = cache.to(DEV), i32(lens)
+        out = torch.empty(8, H, Dv, dtype=dims.dtype, device=DEV)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            dec(q, kv_a, qsl, ls, tab, c, table, w, out)
+        graphs.append((g, c, out, n, qsl, ls))
+    for _ in range(2):
+        for (g, c, out, n, _, _), (rc, ro) in zip(graphs, eager):
+            out.fill_(0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[:n], ro)
+            assert torch.equal(torch.nan_to_num(c.float(), 5.0), torch.nan_to_num(rc.float(), 5.0))
+
+
+def test_bindings_refuse():
+    """Wrong types, shapes and strides raise before anything is enqueued."""
+    dims, _ = make_dims(SMALL, 3, 16, "f32")
+    q = torch.zeros(2, 3, 48, device=DEV)
+    kv_a, ql, ol = torch.zeros(2, 80, device=DEV), torch.zeros(2, 3, 80, device=DEV), torch.zeros(2, 3, 64, device=DEV)
+    w, out = torch.zeros(3 * 64, 64, device=DEV), torch.zeros(2, 3, 32, device=DEV)
+    cache, table = torch.zeros(4, 16, 80, device=DEV), torch.zeros(2, 2, dtype=torch.int32, device=DEV)
+    a, b, tab = i32([0, 1, 2]), i32([5, 6]), torch.zeros(9, 16, device=DEV)
+    before = M.mla_kernel_launches()
+
+    def refuses(f, *args, **kw):
+        with pytest.raises((ValueError, M.MlaError)):
+            f(dims, *args, **kw)
+
+    wide = torch.zeros(2, 3, 160, device=DEV)
+    refuses(M.mla_absorb_query, q.bfloat16(), w, ql)
+    refuses(M.mla_absorb_query, q[:, :2], w, ql)
+    refuses(M.mla_absorb_query, q, w.t(), ql)
+    refuses(M.mla_absorb_query, q, w, wide[..., :80])
+    refuses(M.mla_absorb_query, q, w[:-1], ql)
+    refuses(M.mla_expand_output, ol, w, out[:1])
+    refuses(M.mla_expand_output, ol, w.cpu(), out)
+    refuses(M.mla_expand_output, ol[0], w, out)
+    refuses(M.mla_append_latent, kv_a[:, :79], a, b, tab, cache, table)
+    refuses(M.mla_append_latent, kv_a.t().contiguous().t(), a, b, tab, cache, table)
+    refuses(M.mla_append_latent, kv_a[:1].expand(2, 80), a, b, tab, cache, table)
+    refuses(M.mla_append_latent, kv_a, a.long(), b, tab, cache, table)
+    refuses(M.mla_append_latent, kv_a, a[:2], b, tab, cache, table)
+    refuses(M.mla_append_latent, kv_a, a, b, tab.double(), cache, table)
+    refuses(M.mla_append_latent, kv_a, a, b, tab, cache[:, :8], table)
+    refuses(M.mla_append_latent, kv_a, a, b, tab, cache, table, q=q)
+    refuses(M.mla_append_latent, kv_a, a, b, tab, cache, table, q=q, q_pe_out=ql[:, :2, 64:])
+    refuses(M.mla_append_latent, kv_a, a, b, tab, cache, table, q=q, q_pe_out=ql[..., ::5])
+    refuses(M.mla_append_latent, kv_a, a, b, tab, cache, table, q=q, q_pe_out=ql[..., 64:].flip(0)[:1])
+    refuses(M.mla_latent_attn, True, a, b, ql, cache.transpose(0, 1), table, None, ol)
+    refuses(M.mla_latent_attn, True, a, b, ql, cache, table[:1], None, ol)
+    refuses(M.mla_latent_attn, True, a, b, ql, cache, table, None, ol, torch.zeros(2, 3, device=DEV))
+    refuses(M.mla_latent_attn, True, a, b, ql[..., :64], cache, table, None, ol)
+    torch.cuda.synchronize()
+    assert M.mla_kernel_launches() == before
+    large, _ = make_dims(LARGE, 3, 16, "bf16")
+    need = M.mla_latent_attn_workspace_bytes(large, 2, 2)
+    h = {"dtype": torch.bfloat16, "device": DEV}
+    qb, cb, ob = torch.zeros(2, 3, 576, **h), torch.zeros(4, 16, 576, **h), torch.zeros(2, 3, 512, **h)
+    for ws in (None, torch.empty(need - 1, dtype=torch.uint8, device=DEV),
+               torch.empty(need + 16, dtype=torch.uint8, device=DEV)[1:]):
+        with pytest.raises((ValueError, M.MlaError)):
+            M.mla_latent_attn(large, True, a, b, qb, cb, table, ws, ob)
+    assert M.mla_kernel_launches() == before
