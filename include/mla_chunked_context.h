@@ -600,9 +600,8 @@ int mla_expand_output(const mla_dims_t *d, const void *o_latent,
  *   q_latent device [T, H, L+P], o_latent device [T, H, L], both in dtype;
  *   lse device float32 [H, T], nullable.  A row that sees no key gets 0 and
  *   -inf.  Cache rows past seq_lens are never used.  A cache row that is not
- *   finite makes the tokens that see it NaN, and on the tensor-core path (where
- *   its weight of 0 multiplies it) may make so the sequence's new tokens before
- *   it.  No output may overlap an input.
+ *   finite reaches only the tokens that see it: it makes them NaN (or weighs
+ *   nothing where its score is -inf).  No output may overlap an input.
  *   workspace: device, 16-byte aligned, mla_latent_attn_workspace_bytes bytes
  *   (partial results of key ranges: one size for the tensor-core shape,
  *   whatever the batch; 0 bytes and NULL otherwise); nothing in it has to be

@@ -108,7 +108,7 @@ struct LatentArgs {
   int4 *desc;
   int32_t *status;
   int T, R, H, bs, num_blocks, none, bt_stride, causal, box_log2;  // none: a row past the cache
-  Divider by_bs;
+  Divider by_bs, by_h;
   float scale_log2;
 };
 
@@ -176,6 +176,17 @@ struct Walk {
     t1 = max(0, pos - COST);
     left -= take;
     return t1 > t0;
+  }
+  // keys that row `row` of the unit sees
+  __device__ __forceinline__ int seen(int row) const {
+    if (!a.causal) return s.keys;
+    const int i = a.by_h.quotient(rt * Cfg<PAIR>::UROWS + row);  // token of the sequence
+    return max(0, min(s.keys, s.len - s.nq + i + 1));
+  }
+  // keys that all of the unit's rows see, and that any of them sees
+  __device__ __forceinline__ int seen_by_all() const { return seen(0); }
+  __device__ __forceinline__ int seen_by_any() const {
+    return seen(min(Cfg<PAIR>::UROWS, s.nq * a.H - rt * Cfg<PAIR>::UROWS) - 1);
   }
   // shares after this one that have a piece of this unit, which this one cuts
   __device__ __forceinline__ int others(const Share &sh) const {
@@ -391,6 +402,52 @@ __device__ __forceinline__ void mma_lo(uint32_t d, uint32_t alo, uint32_t blo, u
         : "memory");
 }
 
+// Any of 8 bf16 values infinite or NaN.
+__device__ __forceinline__ bool not_finite(uint4 v) {
+  auto bad = [](uint32_t x) {
+    return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+  };
+  return bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
+}
+
+// Keys that some rows of a unit see and others do not: where a value row is not
+// finite, zeros have to stand for it, as a weight of 0 would not hide it.  (The
+// rows that see it are NaN by their scores.)  Which of a tile's keys [from, to)
+// are not finite in the 256 columns from byte `col`; by a warp, whose lanes have
+// the cache rows of groups of 2^bl keys in row0, row1.  (Not inlined, like the
+// next: inlined, they cost every tile's loads a little, 1.5% of the whole.)
+__device__ __noinline__ uint64_t hidden_rows(const LatentArgs &a, int row0, int row1, int bl,
+                                             int from, int to, int col) {
+  uint64_t hidden = 0;
+  for (int j = from; j < to; ++j) {
+    const int i = j >> bl;
+    const int r = __shfl_sync(0xffffffffu, i < 32 ? row0 : row1, i & 31);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r != a.none)
+      v = __ldg(reinterpret_cast<const uint4 *>(
+              a.cache + int64_t(r + (j & ((1 << bl) - 1))) * (WIDTH * 2) + col) +
+          (threadIdx.x & 31));
+    if (__any_sync(0xffffffffu, not_finite(v))) hidden |= uint64_t(1) << j;
+  }
+  return hidden;
+}
+
+// A tile's V, row by row, without the hidden ones and those from `keys` on.
+template <bool PAIR>
+__device__ __noinline__ void load_unhidden(const Maps &m, int row0, int row1, int bl, int keys,
+                                           uint64_t hidden, uint32_t dst, int x, int none,
+                                           uint32_t bar) {
+  for (int j = 0; j < TILE; ++j) {
+    const int i = j >> bl;
+    const int r = __shfl_sync(0xffffffffu, i < 32 ? row0 : row1, i & 31);
+    const bool real = r != none && j < keys && !(hidden >> j & 1);
+    if (elect_one())
+      load_rows<PAIR>(m, 0, dst + (j >> 4) * V_GROUP + (j & 15) * 128, 16 * 128, 4, x,
+                      r + (j & ((1 << bl) - 1)), real, none, bar);
+    __syncwarp();
+  }
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -485,23 +542,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     while (ok && w.next()) {
       const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
+      const int all = w.seen_by_all(), any = w.seen_by_any();
       for (int t = w.t0; t < w.t1; ++t, ++g) {
         const int key0 = t * TILE + skip, st = g & 1;
         int row[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int off = (lane + 32 * i) << bl;
-          row[i] = off < nrows ? cache_row(a, bt, w.s.keys, key0 + off) : none;
+          row[i] = off < nrows ? cache_row(a, bt, any, key0 + off) : none;
         }
+        uint64_t hidden = 0;
+        if (is_v && all < any && key0 + TILE > all)
+          hidden = hidden_rows(a, row[0], row[1], bl, max(0, all - key0), min(TILE, any - key0),
+                               int(rank) * 512);
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((g >> 1) & 1) ^ 1));
         if (!ok) break;
         if (rank == 0 && lane == 0) mbar_expect_tx(full + 8 * st, (PAIR ? 2 : 1) * stage_bytes);
         __syncwarp();
+        if (hidden) {
+          load_unhidden<PAIR>(m, row[0], row[1], bl, any - key0, hidden, dst0 + st * stage_bytes,
+                              int(rank) * 256, none, full_lead + 8 * st);
+          continue;
+        }
         for (int i = 0; i < nrows >> bl; ++i) {
           const int r = __shfl_sync(0xffffffffu, i < 32 ? row[0] : row[1], i & 31);
           const int off = i << bl;
           // (a row past the length in K alone only makes scores that are masked)
-          const int valid = r == none ? 0 : PAIR && !is_v ? bx : min(bx, w.s.keys - key0 - off);
+          const int valid = r == none ? 0 : PAIR && !is_v ? bx : min(bx, any - key0 - off);
           if (elect_one()) {
             const uint32_t dst = dst0 + st * stage_bytes, bar = full_lead + 8 * st;
             if (!is_v)
@@ -531,6 +598,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t bar = lead(q_full);
     for (; ok && w.next(); ++n) {
       const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
+      const int any = w.seen_by_any();
       bool queries = false;
       auto load_queries = [&] {
         queries = true;
@@ -558,11 +626,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < C::KROWS >> bl; i += 32) {
           const int j = key0 + ((lane + i) << bl);
           int row = none;
-          if (((lane + i) << bl) < C::KROWS) row = cache_row(a, bt, w.s.keys, j);
+          if (((lane + i) << bl) < C::KROWS) row = cache_row(a, bt, any, j);
           if (row != none)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                              a.cache + int64_t(row) * (WIDTH * 2)),
-                         "r"(min(1 << bl, w.s.keys - j) * WIDTH * 2)
+                         "r"(min(1 << bl, any - j) * WIDTH * 2)
                          : "memory");
         }
         __syncwarp();
@@ -686,8 +754,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     while (ok && w.next()) {
       const int rows = w.s.nq * a.H - w.rt * C::UROWS;  // of the unit (may exceed it)
       const int urow = int(rank) * CROWS + rl;
-      const int i = (w.rt * C::UROWS + urow) / a.H;     // token of the sequence
-      const int vis = a.causal ? min(w.s.keys, w.s.len - w.s.nq + i + 1) : w.s.keys;
+      const int vis = w.seen(min(urow, rows - 1));
+      const int all = w.seen_by_all(), any = w.seen_by_any();
       if (w.s.keys < w.s.len && a.status && tid == 0) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
       float mref = neg_inf(), l = 0.f;
       for (int t = w.t0; t < w.t1; ++t, ++g) {
@@ -708,6 +776,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_arrive(s_empty + 8 * sb);
         }
         const int nvis = vis - t * TILE - half * SC - part * NC;
+        const bool mixed = all < any && t * TILE + TILE > all;  // rows may differ in what they see
         if (nvis < NC) {
 #pragma unroll
           for (int c = 0; c < NC; ++c)
@@ -766,6 +835,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 0; c < NC / 8; ++c)
           st_shared_v4(prow + (((c0 + c) ^ (rl & 7)) << 4),
                        make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]));
+        // Value rows that are not finite and that only some rows see are
+        // cleared: a weight of 0 would not hide them from the others.  The
+        // scores of the rows that see them are not finite either, and make them
+        // NaN (or, -inf, give a weight of 0; making NaN of those too costs every
+        // tile some 30 clocks).  The pair form's V loads do this.
+        if (!PAIR && mixed) {
+          ok = __all_sync(0xffffffffu, mbar_wait(k_full + 8 * sb, (g >> 1) & 1));
+          if (!ok) break;
+          const int from = max(0, all - t * TILE), n = min(TILE, any - t * TILE) - from;
+          for (int x = tid; x < n * 64; x += STHREADS) {  // row, column block, piece
+            const uint32_t v = sK + sb * C::K_STAGE + (x >> 3 & 7) * BLK_BYTES +
+                               (from + (x >> 6)) * 128 + (x & 7) * 16;
+            if (not_finite(ld_shared_v4(v))) st_shared_v4(v, make_uint4(0, 0, 0, 0));
+          }
+        }
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -1178,7 +1262,8 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
   LatentArgs a{qsl, seq_lens, block_table, static_cast<const uint8_t *>(cache),
                static_cast<__nv_bfloat16 *>(o), lse, part_o, part_lse,
                static_cast<int4 *>(desc), status, T, R, d.num_heads, d.block_size, num_blocks,
-               int(cache_rows), bt_stride, causal, box_log2, Divider(d.block_size), d.softmax_scale * 1.4426950408889634f};
+               int(cache_rows), bt_stride, causal, box_log2,
+               Divider(d.block_size), Divider(d.num_heads), d.softmax_scale * 1.4426950408889634f};
   // rows of an average sequence beyond one CTA's 64: pairs
   const bool pair = int64_t(T) * d.num_heads > int64_t(64) * R;
   return pair ? launch_latent<true>(maps, a, max_ctas, s) : launch_latent<false>(maps, a, max_ctas, s);

@@ -780,3 +780,38 @@ def test_bindings_refuse():
         with pytest.raises((ValueError, M.MlaError)):
             M.mla_latent_attn(large, True, a, b, qb, cb, table, ws, ob)
     assert M.mla_kernel_launches() == before
+
+
+@pytest.mark.parametrize("shape,dtype,H,bs", [
+    (LARGE, "bf16", 128, 64), (LARGE, "bf16", 32, 64), (LARGE, "bf16", 48, 16), (LARGE, "bf16", 32, 1),
+    (LARGE, "bf16", 16, 64), (LARGE, "bf16", 5, 4), (LARGE, "bf16", 40, 5), (SMALL, "f32", 4, 16)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_rows_that_are_not_finite_reach_only_tokens_that_see_them(shape, dtype, H, bs, value):
+    """Of four new tokens' cache rows the third's is not finite: the first two
+    tokens' results are bit for bit what they are without it, the others NaN
+    (but for heads that score the row -inf: it may weigh nothing there)."""
+    rng = np.random.default_rng(H + bs)
+    dims, od = make_dims(shape, H, bs, dtype)
+    L, LP = shape[0], shape[0] + shape[1]
+    lens, qsl = [700, 4, 66, 130], [0, 4, 8, 12, 13]
+    cache, table = make_cache(rng, lens, bs, LP, dims.dtype)
+    q = normal(rng, 13, H, LP, std=0.4, dtype=dims.dtype)
+    o, lse = run_attn(dims, True, qsl, lens, q, cache, table)
+    check_attn(dims, od, True, qsl, lens, q, cache, table, o, lse)
+    bad = cache.clone()
+    for r in range(3):
+        j = lens[r] - 2
+        for col in (L - 1, 0, L // 2, L + 1):
+            if r == 0 or col % 2:
+                bad[table[r, j // bs], j % bs, col] = value
+    o2, lse2 = run_attn(dims, True, qsl, lens, q, bad, table)
+    for t in range(13):
+        sees = t < 12 and t % 4 >= 2
+        if sees:
+            r = t // 4
+            row = f64(bad[table[r, (lens[r] - 2) // bs], (lens[r] - 2) % bs])
+            score = f64(q[t]) @ row
+            nan = torch.isnan(o2[t]).any(-1).cpu().numpy()
+            assert (nan | (score == -np.inf)).all() and nan.any()
+        else:
+            assert torch.equal(o2[t], o[t]) and torch.equal(lse2[:, t], lse[:, t]), t
