@@ -9,16 +9,21 @@
 // Every value is read once and written once (the row twice, when the dense
 // copy is asked for), so the kernel is bound by HBM when there are many
 // tokens and by the chain of dependent loads (sequence, length, block id)
-// when there are few.  So the row and the first pieces of the queries are read
-// before that chain is walked.  A block serves one token: warp 0 of its first
-// block the row, all other threads the heads of the queries, each the same
-// columns (and angles) of several heads.  Few tokens spread their heads over
-// several blocks.
+// when there are few.  (Reading the row and the first queries before that chain
+// is walked gains nothing for 16 tokens and makes 8192 take 60.5 us.)  A block
+// serves one token: warp 0 of its first block the row, all other threads the
+// heads of the queries, each the same columns (and angles) of several heads.
+// Few tokens spread their heads over several blocks.
+// Measured, 128 heads, bf16: 8192 tokens (299 MB) 54.6 us, 5.5 TB/s or 81% of
+// copy bandwidth, the queries' rope columns being 128 of every 384 bytes; 16
+// tokens 4.2 us in a graph.
 #include "common.cuh"
 
 namespace mla {
 namespace {
 
+// Of a block.  8192 tokens with 2, 3, 4, 5, 8, 16 warps: 61, 55.3, 54.6, 54.9,
+// 67, 113 us.
 constexpr int WARPS = 4;
 
 struct AppendArgs {
@@ -114,55 +119,14 @@ __device__ __forceinline__ void rotate_piece(Piece<T> &x, Piece<T> &y, const flo
   }
 }
 
-template <typename T, bool EARLY>
+template <typename T>
 __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
   constexpr int N = Piece<T>::N;
-  constexpr int ROW_PRE = EARLY ? 4 : 0;  // pieces of a row a lane reads ahead
-  constexpr int Q_PRE = EARLY ? 2 : 0;    // heads a thread reads ahead
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x;
   const bool row_warp = blockIdx.y == 0 && warp == 0;
   chain_release();
   chain_wait();
-
-  // ---- what does not depend on the token's sequence is read first
-  const T *x = static_cast<const T *>(a.kv_a) + t * a.kv_a_ld;
-  const T *w = static_cast<const T *>(a.norm_weight);
-  const int n_pieces = a.L / N;
-  Piece<T> row[EARLY ? ROW_PRE : 1];
-  // the queries: this block's share of the heads; a thread has columns k of
-  // heads qh, qh + q_step, ...
-  const int h0 = int(int64_t(a.H) * blockIdx.y / gridDim.y);
-  const int h1 = int(int64_t(a.H) * (blockIdx.y + 1) / gridDim.y);
-  const int q_tid = int(threadIdx.x) - (blockIdx.y == 0 ? 32 : 0);  // < 0: the row's warp
-  const int q_threads = int(blockDim.x) - (blockIdx.y == 0 ? 32 : 0);
-  const int units = a.P / (a.interleaved ? N : 2 * N);  // of a head, as pieces
-  const int qk = a.Dn + a.P;
-  const T *q = static_cast<const T *>(a.q) + int64_t(t) * a.H * qk + a.Dn;
-  T *qo = static_cast<T *>(a.q_pe) + int64_t(t) * a.H * a.q_pe_ld;
-  const int y_off = a.P / 2;
-  int k = 0, qh = h1, q_step = 1;
-  Piece<T> qx[EARLY ? Q_PRE : 1], qy[EARLY ? Q_PRE : 1];
-  if (row_warp) {
-    if (a.vec_row) {
-#pragma unroll
-      for (int i = 0; i < ROW_PRE; ++i)
-        if (lane + 32 * i < n_pieces) row[i].load(x + (lane + 32 * i) * N);
-    }
-  } else if (a.vec_q) {
-    q_step = q_threads / units;
-    if (q_tid < q_step * units) {
-      k = q_tid % units;
-      qh = h0 + q_tid / units;
-    }
-#pragma unroll
-    for (int i = 0; i < Q_PRE; ++i)
-      if (qh + i * q_step < h1) {
-        const T *src = q + int64_t(qh + i * q_step) * qk + k * N;
-        qx[i].load(src);
-        if (!a.interleaved) qy[i].load(src + y_off);
-      }
-  }
 
   // ---- the token's sequence and position
   const int first = max(__ldg(a.qsl), 0);
@@ -174,14 +138,19 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
   if (pos < 0) return;
   const int rpos = a.positions ? __ldg(a.positions + t) : pos;
   if (a.rope && (rpos < 0 || rpos >= a.max_pos)) {
-    if (a.status && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, MLA_STATUS_BAD_POSITION);
+    if (a.status && threadIdx.x == 0 && blockIdx.y == 0)
+      atomicOr(a.status, MLA_STATUS_BAD_POSITION);
     return;
   }
   const float *rope = a.rope ? a.rope + int64_t(rpos) * a.P : nullptr;
 
+  const T *x = static_cast<const T *>(a.kv_a) + t * a.kv_a_ld;
   if (row_warp) {
+    const T *w = static_cast<const T *>(a.norm_weight);
+    const int n_pieces = a.L / N;
     const int blk_i = pos / a.bs;
-    const int blk = blk_i < a.bt_stride ? __ldg(a.block_table + int64_t(r) * a.bt_stride + blk_i) : -1;
+    const int blk =
+        blk_i < a.bt_stride ? __ldg(a.block_table + int64_t(r) * a.bt_stride + blk_i) : -1;
     const bool good = blk >= 0 && blk < a.num_blocks;
     if (!good && lane == 0 && a.status) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
     const int LP = a.L + a.P;
@@ -195,10 +164,7 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
         for (int e = 0; e < N; ++e) ss = fmaf(p.v[e], p.v[e], ss);
       };
       if (a.vec_row) {
-#pragma unroll
-        for (int i = 0; i < ROW_PRE; ++i)
-          if (lane + 32 * i < n_pieces) square(row[i]);
-        for (int j = lane + 32 * ROW_PRE; j < n_pieces; j += 32) {
+        for (int j = lane; j < n_pieces; j += 32) {
           Piece<T> p;
           p.load(x + j * N);
           square(p);
@@ -214,7 +180,9 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
       inv = 1.f / sqrtf(ss / float(a.L) + a.eps);
     }
     if (a.vec_row) {
-      auto put = [&](Piece<T> p, int j) {
+      for (int j = lane; j < n_pieces; j += 32) {
+        Piece<T> p;
+        p.load(x + j * N);
         if (w) {
           Piece<T> g;
           g.load(w + j * N);
@@ -223,14 +191,6 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
         }
         if (d0) p.store(d0 + j * N);
         if (d1) p.store(d1 + j * N);
-      };
-#pragma unroll
-      for (int i = 0; i < ROW_PRE; ++i)
-        if (lane + 32 * i < n_pieces) put(row[i], lane + 32 * i);
-      for (int j = lane + 32 * ROW_PRE; j < n_pieces; j += 32) {
-        Piece<T> p;
-        p.load(x + j * N);
-        put(p, j);
       }
     } else {
       for (int j = lane; j < a.L; j += 32) {
@@ -255,8 +215,19 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
     return;
   }
   if (!a.q) return;
+  // the queries: this block's share of the heads
+  const int h0 = int(int64_t(a.H) * blockIdx.y / gridDim.y);
+  const int h1 = int(int64_t(a.H) * (blockIdx.y + 1) / gridDim.y);
+  const int q_tid = int(threadIdx.x) - (blockIdx.y == 0 ? 32 : 0);
+  const int q_threads = int(blockDim.x) - (blockIdx.y == 0 ? 32 : 0);
+  const int qk = a.Dn + a.P, y_off = a.P / 2;
+  const T *q = static_cast<const T *>(a.q) + int64_t(t) * a.H * qk + a.Dn;
+  T *qo = static_cast<T *>(a.q_pe) + int64_t(t) * a.H * a.q_pe_ld;
   if (a.vec_q) {
-    if (qh >= h1) return;
+    // a thread has columns k of heads qh, qh + q_step, ...
+    const int units = a.P / (a.interleaved ? N : 2 * N);  // of a head, as pieces
+    const int q_step = q_threads / units, k = q_tid % units, qh = h0 + q_tid / units;
+    if (q_tid >= q_step * units || qh >= h1) return;
     // the angles of this thread's columns, for all of its heads
     constexpr int NA = N;
     const int n_ang = a.interleaved ? N / 2 : N;
@@ -271,22 +242,16 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
         sn[e] = v.x;
         sn[e + 1] = v.y;
       }
-    auto put = [&](Piece<T> px, Piece<T> py, int h) {
-      rotate_piece<T>(px, py, c, sn, a.interleaved);
-      T *dst = qo + h * a.q_pe_ld + k * N;
-      px.store(dst);
-      if (!a.interleaved) py.store(dst + y_off);
-    };
-#pragma unroll
-    for (int i = 0; i < Q_PRE; ++i)
-      if (qh + i * q_step < h1) put(qx[i], qy[i], qh + i * q_step);
 #pragma unroll 1
-    for (int h = qh + Q_PRE * q_step; h < h1; h += q_step) {
+    for (int h = qh; h < h1; h += q_step) {
       const T *src = q + int64_t(h) * qk + k * N;
+      T *dst = qo + h * a.q_pe_ld + k * N;
       Piece<T> px, py;
       px.load(src);
       if (!a.interleaved) py.load(src + y_off);
-      put(px, py, h);
+      rotate_piece<T>(px, py, c, sn, a.interleaved);
+      px.store(dst);
+      if (!a.interleaved) py.store(dst + y_off);
     }
     return;
   }
@@ -319,8 +284,8 @@ int launch_append(const mla_dims_t &d, const void *kv_a, int64_t kv_a_ld, const 
   const int pair_bytes = interleaved ? P * es : P / 2 * es;  // a rotation's 16-byte pieces
   const int units = P * es / (interleaved ? 16 : 32);  // of a head
   a.vec_q = q && rope && (reinterpret_cast<uintptr_t>(rope) & 7) == 0 && units >= 1 &&
-            units <= 32 * (WARPS - 1) && pair_bytes % 16 == 0 && (d.qk_nope_dim * es) % 16 == 0 && (q_pe_ld * es) % 16 == 0 &&
-            al(q) && al(q_pe);
+            units <= 32 * (WARPS - 1) && pair_bytes % 16 == 0 && (d.qk_nope_dim * es) % 16 == 0 &&
+            (q_pe_ld * es) % 16 == 0 && al(q) && al(q_pe);
   // enough blocks for every SM where there are heads to share out
   const int want = 2 * num_sms();
   const int most = q ? (d.num_heads + 7) / 8 : 1;
@@ -328,12 +293,9 @@ int launch_append(const mla_dims_t &d, const void *kv_a, int64_t kv_a_ld, const 
   if (ys > most) ys = most;
   const dim3 grid(T, ys);
   const int threads = q ? 32 * WARPS : 32;
-  const bool early = T < want;
-  if (d.dtype == MLA_DTYPE_BF16)
-    return launch_chained(early ? append_kernel<__nv_bfloat16, true> : append_kernel<__nv_bfloat16, false>,
-                          grid, threads, 0, 1, s, "append_kernel", a);
-  return launch_chained(early ? append_kernel<float, true> : append_kernel<float, false>, grid,
-                        threads, 0, 1, s, "append_kernel", a);
+  auto *kernel =
+      d.dtype == MLA_DTYPE_BF16 ? append_kernel<__nv_bfloat16> : append_kernel<float>;
+  return launch_chained(kernel, grid, threads, 0, 1, s, "append_kernel", a);
 }
 
 }  // namespace mla

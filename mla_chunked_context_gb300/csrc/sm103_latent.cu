@@ -3,15 +3,15 @@
 //   s_j = scale * q . c_j (576 columns), o = sum_j softmax(s)_j c_j[0:512), lse
 // for every row (new token, head); the rows of a sequence share its cache rows.
 //
-// A row reads 1152 bytes and spends 2 * (576 + 512) FLOP per key: with 128
-// rows that is 242 FLOP/byte, just under the GPU's bf16 : HBM ratio of 289, so
-// both the tensor pipe and HBM have to be kept near their limits, and what
-// limits the tensor pipe is how its operands fit on chip:
+// A key is 1152 bytes and costs a row 2 * (576 + 512) FLOP: with 128 rows that
+// is 242 FLOP/byte, just under the GPU's bf16 : HBM ratio of 289, so both the
+// tensor pipe and HBM have to be kept near their limits, and what limits the
+// tensor pipe is how its operands fit on chip:
 //   * O (rows x 512 float32) lives in tensor memory.  128 rows would take all
 //     512 columns and leave none for S, so an SM holds 64 rows: 256 columns,
 //     in the layout where lanes 0-63 have the rows with one half of D's
-//     columns and lanes 64-127 the same rows with the other half.  Softmax
-//     threads of lanes l and l+64 share row l, each with half of the keys.
+//     columns and lanes 64-127 the same rows with the other half.  Four softmax
+//     threads share a row, each with a quarter of the keys.
 //   * an MMA takes a clock per 128 bytes that it reads from shared memory, when
 //     that is more than its products do (measured: M=64, N=64, K=16 of the
 //     single form 32 clocks, N=256 80; pair M=128 N=64 25, N=256 64), so S,
@@ -30,12 +30,17 @@
 // Work split: the units (sequence, 64 or 128 rows) are laid end to end, each
 // as long as its key tiles and a constant for its start and end, and dealt out
 // in equal contiguous shares, one per cluster, by the kernel itself from the
-// lengths on the device.  A unit that lies in one
-// share is written directly; the pieces of a cut one go to scratch as
-// normalised float32 with their log-sums, and latent_combine_kernel joins
-// them.
-// Warps: 0 K loads, 1 V loads (pair), 2 MMA issue, 3 query loads, 4-7 softmax
-// and epilogue (tensor-memory lanes 0-127).
+// lengths on the device.  A unit that lies in one share is written directly;
+// the pieces of a cut one go to scratch as normalised float32 with their
+// log-sums, and latent_combine_kernel joins them.
+// Measured, 64 keys at 1.6-1.95 GHz: single 3380 clocks, of which HBM's rate
+// takes 3200 (128 sequences of up to 8192 keys, 32 heads: 110 us, 83% of copy
+// bandwidth); pair about 2000, of which its shared-memory reads take 1860 and
+// its MMAs 1425 (24 sequences x 4 tokens x 128 heads: 82 us, 49% of the bf16
+// rate).  A launch has some 10000 clocks around its tiles: finding its share,
+// the first loads, the last rows out, and the joining kernel.
+// Warps: 0 K loads, 1 V loads (pair), 2 MMA issue, 3 query loads and prefetches
+// to L2, 4-11 softmax and epilogue (two a quarter of tensor memory's lanes).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -53,7 +58,7 @@ constexpr int Q_BYTES = NBLK * BLK_BYTES;
 constexpr int SWARPS = 8, STHREADS = 32 * SWARPS;  // softmax
 constexpr int THREADS = 128 + STHREADS;
 constexpr int MAPS = 7;  // cache boxes of 1, 2, 4 .. 64 rows
-constexpr uint32_t TMEM_COLS = 512, S_COL = 256;
+constexpr uint32_t TMEM_COLS = 512, S_COL = 256;  // O: columns 0-255, S: from 256
 constexpr float LN2 = 0.69314718055994531f;
 // O is rescaled only when a row's maximum has grown by more than this (log2):
 // until then p is at most 2^8, which float32 sums and bf16's exponent hold
@@ -91,7 +96,8 @@ constexpr int MIN_SHARE = 4;
 constexpr int SNAP = 1, SHORT = 10, WHOLE_SLACK = 8;
 
 // Tiles between asking for keys in L2 and copying them to shared memory, whose
-// two stages do not cover HBM's latency.
+// two stages do not cover HBM's latency: 128 ragged sequences took 118 us so,
+// 124 without, 126 with two tiles and 156 with four.
 constexpr int AHEAD = 1;
 
 struct Maps {
@@ -315,8 +321,8 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
 }
 
 // ---- cache loads --------------------------------------------------------------
-// Cache row of position j of a sequence (block table row bt): num_rows (which
-// the loads fill with zeros) past its length and for a bad block.
+// Cache row of position j of a sequence (block table row bt); a.none (which the
+// loads fill with zeros) from position len on and for a bad block.
 __device__ __forceinline__ int cache_row(const LatentArgs &a, const int32_t *bt, int len, int j) {
   if (j >= len) return a.none;
   const int b = a.by_bs.quotient(j);
@@ -689,9 +695,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           // S of this tile goes ahead of P V of the one before, so that the
           // softmax has the tensor pipe's time, unless its keys (or queries)
           // have yet to land.  Then the single form waits for that P V, which
-          // releases room for loads, its bottleneck (S always first: 6000
-          // clocks a tile, this: 3700); the pair form takes whichever is ready
-          // first (2810 to 2550).
+          // releases room for loads, its bottleneck (S always first took 1.6
+          // times as long a tile); the pair form takes whichever is ready first
+          // (that P V first: 1.1 times).
           auto ready = [&] {
             return mbar_test(k_full + 8 * st, parity) && (t > w.t0 || mbar_test(q_full, n & 1));
           };
@@ -901,11 +907,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float x = __uint_as_float(o[8 * e + 2 * k]), y = __uint_as_float(o[8 * e + 2 * k + 1]);
+              const float x = __uint_as_float(o[8 * e + 2 * k]);
+              const float y = __uint_as_float(o[8 * e + 2 * k + 1]);
               v[k] = inv == 0.f ? 0u : pack_bf16(x * inv, y * inv);
             }
             const int sw = PAIR ? (rl >> 1) & 3 : (rl >> 2) & 1;  // spreads the banks
-            st_shared_v4(stage + rl * (EC * 2) + ((e ^ sw) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+            st_shared_v4(stage + rl * (EC * 2) + ((e ^ sw) << 4),
+                         make_uint4(v[0], v[1], v[2], v[3]));
           }
           softmax_barrier();
 #pragma unroll
@@ -914,7 +922,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int qt = x / (64 * PIECES), r = x / PIECES % 64, e = x % PIECES;
             const int row = int(rank) * CROWS + r;
             const int sw = PAIR ? (r >> 1) & 3 : (r >> 2) & 1;
-            const int d = PAIR ? (qt & 1) * 256 + (qt >> 1) * 128 : (qt >> 1) * 256 + (qt & 1) * 128;
+            const int d =
+                PAIR ? (qt & 1) * 256 + (qt >> 1) * 128 : (qt >> 1) * 256 + (qt & 1) * 128;
             if (row < rows)
               *reinterpret_cast<uint4 *>(a.o + (grow0 + row) * LAT + d + c + e * 8) =
                   ld_shared_v4(sP + qt * (64 * EC * 2) + r * (EC * 2) + ((e ^ sw) << 4));
@@ -934,7 +943,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = inv == 0.f ? 0.f : __uint_as_float(o[e + k]) * inv;
-            if (urow < rows) dst[((dim0 + c + e) / 4) * CROWS] = make_float4(v[0], v[1], v[2], v[3]);
+            if (urow < rows)
+              dst[((dim0 + c + e) / 4) * CROWS] = make_float4(v[0], v[1], v[2], v[3]);
           }
         }
         if (w.t0 == 0 && tid == 0 && rank == 0) {
@@ -973,7 +983,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 constexpr int CT = 256, CW = CT / 32;  // threads, warps of a block; clusters <= CT
 constexpr int FEW = 8, COMBINE_BLOCKS = 2;
 
-__device__ __forceinline__ int few_columns(int pieces) { return pieces <= 2 ? 8 : pieces <= 4 ? 4 : 2; }
+__device__ __forceinline__ int few_columns(int pieces) {
+  return pieces <= 2 ? 8 : pieces <= 4 ? 4 : 2;
+}
 
 template <int W>
 struct Joined {
@@ -1225,9 +1237,9 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
   // sequences that the block table keeps short are never cut: nothing to join
   const int64_t most_tiles = (int64_t(a.bt_stride) * a.bs + TILE - 1) / TILE;
   if (most_tiles + UNIT_COST<PAIR> <= SHORT) return MLA_OK;
-  return launch_chained(latent_combine_kernel, COMBINE_BLOCKS * num_sms(), CT, 0, 1, s, "latent_combine_kernel",
-                        a.desc, PAIR ? grid / 2 : grid, Cfg<PAIR>::UROWS, a.part_o, a.part_lse, a.o,
-                        a.lse, a.H, a.T);
+  return launch_chained(latent_combine_kernel, COMBINE_BLOCKS * num_sms(), CT, 0, 1, s,
+                        "latent_combine_kernel", a.desc, PAIR ? grid / 2 : grid, Cfg<PAIR>::UROWS,
+                        a.part_o, a.part_lse, a.o, a.lse, a.H, a.T);
 }
 
 }  // namespace
@@ -1265,8 +1277,8 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
                int(cache_rows), bt_stride, causal, box_log2,
                Divider(d.block_size), Divider(d.num_heads), d.softmax_scale * 1.4426950408889634f};
   // rows of an average sequence beyond one CTA's 64: pairs
-  const bool pair = int64_t(T) * d.num_heads > int64_t(64) * R;
-  return pair ? launch_latent<true>(maps, a, max_ctas, s) : launch_latent<false>(maps, a, max_ctas, s);
+  if (int64_t(T) * d.num_heads > int64_t(64) * R) return launch_latent<true>(maps, a, max_ctas, s);
+  return launch_latent<false>(maps, a, max_ctas, s);
 }
 
 int latent_take_errors() { return sm103::take_error_flags_here(); }
