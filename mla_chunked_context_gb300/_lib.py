@@ -532,44 +532,22 @@ def mla_selftest_bounded_wait(limit_us: int, gave_up, stream=None) -> None:
 
 
 # ------------------------------------------------------------------ decode --
-# These calls are made once a layer and token, so their checks are kept to a
-# few comparisons a tensor.
-def _refuse(where, name, t, dtype, shape):
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        cur = f"cuda:{torch.cuda.current_device()}" if torch.cuda.is_available() else "none"
-        raise ValueError(f"{where}: {name} is on {t.device}, the current device is {cur}")
-    raise ValueError(f"{where}: {name} has to be contiguous {list(shape)} {dtype}, got "
-                     f"{list(t.shape)} {t.dtype}{'' if t.is_contiguous() else ', not contiguous'}")
+# These calls are made once a layer and token, so their tensors are checked in
+# a native module (csrc/py_decode.cpp).
+_decode = None
 
 
-def _take(where: str, *specs) -> None:
-    """Every (name, tensor or None, dtype, shape) is contiguous, of that type
-    and shape, and on the current device, where the C calls work."""
-    cur = None
-    for name, t, dtype, shape in specs:
-        if t is None:
-            continue
-        dev = t.get_device()
-        if cur is None and dev >= 0:
-            cur = torch.cuda.current_device()
-        if dev != cur or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-            _refuse(where, name, t, dtype, shape)
-
-
-def _p(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _raw_stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-
-
-def _dim(t: torch.Tensor, i: int, n: int, where: str, name: str) -> int:
-    if t.dim() != n:
-        raise ValueError(f"{where}: {name} has to have {n} dimensions, got {t.dim()}")
-    return t.shape[i]
+def _native():
+    global _decode
+    if _decode is None:
+        lib()
+        try:
+            from . import _decode as module
+        except ImportError as e:
+            raise ImportError("the decode calls' binding (_decode.so) is missing or not loadable: "
+                              "build it with mla_chunked_context_gb300.build.build()") from e
+        _decode = module
+    return _decode
 
 
 def mla_append_latent(dims: Dims, kv_a, query_start_loc, seq_lens, rope_table, kv_cache,
@@ -581,62 +559,27 @@ def mla_append_latent(dims: Dims, kv_a, query_start_loc, seq_lens, rope_table, k
     rope columns.  q_pe_out: a [T, H, P] view, e.g. ``q[..., Dn:]`` (in place)
     or ``q_latent[..., L:]``.  rope_table: float32 [positions, P], cos then
     sin, or None."""
-    w = "mla_append_latent"
-    dt, H, P, L = dims.dtype, dims.num_heads, dims.qk_rope_dim, dims.kv_lora_rank
-    T, R = _dim(kv_a, 0, 2, w, "kv_a"), _dim(seq_lens, 0, 1, w, "seq_lens")
-    blocks, stride = _dim(kv_cache, 0, 3, w, "kv_cache"), _dim(block_table, 1, 2, w, "block_table")
-    n_pos = 0 if rope_table is None else rope_table.shape[0]
-    i32 = torch.int32
-    ld = kv_a.stride(0) if T > 1 else L + P
-    if kv_a.dtype is not dt or kv_a.shape[1] != L + P or kv_a.stride(1) != 1 or ld < L + P:
-        raise ValueError(f"{w}: kv_a has to be [T, {L + P}] {dt} with contiguous rows")
-    _take(w, ("query_start_loc", query_start_loc, i32, (R + 1,)), ("seq_lens", seq_lens, i32, (R,)),
-          ("block_table", block_table, i32, (R, stride)),
-          ("kv_cache", kv_cache, dt, (blocks, dims.block_size, L + P)),
-          ("norm_weight", norm_weight, dt, (L,)), ("positions", positions, i32, (T,)),
-          ("rope_table", rope_table, torch.float32, (n_pos, P)),
-          ("new_latent", new_latent, dt, (T, L + P)),
-          ("q", q, dt, (T, H, dims.qk_nope_dim + P)), ("dev_status", dev_status, i32, (1,)))
-    if kv_a.get_device() != kv_cache.get_device():
-        _refuse(w, "kv_a", kv_a, dt, (T, L + P))
-    q_ld = P
-    if q_pe_out is not None:
-        st = q_pe_out.stride()
-        q_ld = st[1] if H > 1 else st[0] if T > 1 else P
-        if q_pe_out.dtype is not dt or q_pe_out.shape != (T, H, P) or (P > 1 and st[2] != 1) or \
-                (T > 1 and st[0] != H * q_ld) or q_pe_out.get_device() != kv_a.get_device():
-            raise ValueError(f"{w}: q_pe_out has to be a [{T}, {H}, {P}] {dt} view of evenly "
-                             "spaced rows on the same device")
-    _check(lib().mla_append_latent(
-        C.byref(dims.c()), kv_a.data_ptr(), ld, _p(norm_weight),
-        norm_eps, T, R, query_start_loc.data_ptr(), seq_lens.data_ptr(), _p(positions),
-        _p(rope_table), n_pos, 1 if interleaved else 0, kv_cache.data_ptr(), blocks,
-        block_table.data_ptr(), stride, _p(new_latent), _p(q), _p(q_pe_out), q_ld,
-        _p(dev_status), _raw_stream(stream)), w)
+    rc = (_decode or _native()).append(
+        dims, kv_a, query_start_loc, seq_lens, rope_table, kv_cache, block_table, norm_weight,
+        norm_eps, positions, interleaved, new_latent, q, q_pe_out, dev_status, stream)
+    if rc:
+        raise MlaError(rc, "mla_append_latent")
 
 
 def mla_absorb_query(dims: Dims, q, w_kv_b, q_latent, rope_columns: bool = True,
                      stream=None) -> None:
     """q [T, H, Dn+P] -> q_latent [T, H, L+P]; rope_columns False leaves the
     rope columns of q_latent as they are."""
-    w, dt, H = "mla_absorb_query", dims.dtype, dims.num_heads
-    T, L, P, Dn = _dim(q, 0, 3, w, "q"), dims.kv_lora_rank, dims.qk_rope_dim, dims.qk_nope_dim
-    _take(w, ("q", q, dt, (T, H, Dn + P)), ("w_kv_b", w_kv_b, dt, (H * (Dn + dims.v_dim), L)),
-          ("q_latent", q_latent, dt, (T, H, L + P)))
-    _check(lib().mla_absorb_query(C.byref(dims.c()), q.data_ptr(), T, w_kv_b.data_ptr(),
-                                  1 if rope_columns else 0, q_latent.data_ptr(),
-                                  _raw_stream(stream)), w)
+    rc = (_decode or _native()).absorb(dims, q, w_kv_b, q_latent, rope_columns, stream)
+    if rc:
+        raise MlaError(rc, "mla_absorb_query")
 
 
 def mla_expand_output(dims: Dims, o_latent, w_kv_b, out, stream=None) -> None:
     """o_latent [T, H, L] -> out [T, H, Dv]."""
-    w, dt, H = "mla_expand_output", dims.dtype, dims.num_heads
-    T, L = _dim(o_latent, 0, 3, w, "o_latent"), dims.kv_lora_rank
-    _take(w, ("o_latent", o_latent, dt, (T, H, L)),
-          ("w_kv_b", w_kv_b, dt, (H * (dims.qk_nope_dim + dims.v_dim), L)),
-          ("out", out, dt, (T, H, dims.v_dim)))
-    _check(lib().mla_expand_output(C.byref(dims.c()), o_latent.data_ptr(), T, w_kv_b.data_ptr(),
-                                   out.data_ptr(), _raw_stream(stream)), w)
+    rc = (_decode or _native()).expand(dims, o_latent, w_kv_b, out, stream)
+    if rc:
+        raise MlaError(rc, "mla_expand_output")
 
 
 def mla_latent_attn_workspace_bytes(dims: Dims, num_tokens: int, num_seqs: int) -> int:
@@ -653,19 +596,8 @@ def mla_latent_attn(dims: Dims, causal: bool, query_start_loc, seq_lens, q_laten
     """Absorbed attention over the paged latent cache: q_latent [T, H, L+P] ->
     o_latent [T, H, L], lse [H, T].  workspace: a uint8 device tensor of
     mla_latent_attn_workspace_bytes bytes."""
-    w, dt, H, L = "mla_latent_attn", dims.dtype, dims.num_heads, dims.kv_lora_rank
-    LP = L + dims.qk_rope_dim
-    T, R = _dim(q_latent, 0, 3, w, "q_latent"), _dim(seq_lens, 0, 1, w, "seq_lens")
-    blocks, stride = _dim(kv_cache, 0, 3, w, "kv_cache"), _dim(block_table, 1, 2, w, "block_table")
-    ws = 0 if workspace is None else workspace.numel()
-    i32 = torch.int32
-    _take(w, ("q_latent", q_latent, dt, (T, H, LP)),
-          ("query_start_loc", query_start_loc, i32, (R + 1,)), ("seq_lens", seq_lens, i32, (R,)),
-          ("block_table", block_table, i32, (R, stride)),
-          ("kv_cache", kv_cache, dt, (blocks, dims.block_size, LP)),
-          ("workspace", workspace, torch.uint8, (ws,)), ("o_latent", o_latent, dt, (T, H, L)),
-          ("lse", lse, torch.float32, (H, T)), ("dev_status", dev_status, i32, (1,)))
-    _check(lib().mla_latent_attn(
-        C.byref(dims.c()), 1 if causal else 0, R, query_start_loc.data_ptr(), seq_lens.data_ptr(),
-        T, q_latent.data_ptr(), kv_cache.data_ptr(), blocks, block_table.data_ptr(), stride,
-        _p(workspace), ws, o_latent.data_ptr(), _p(lse), _p(dev_status), _raw_stream(stream)), w)
+    rc = (_decode or _native()).attend(
+        dims, causal, query_start_loc, seq_lens, q_latent, kv_cache, block_table, workspace,
+        o_latent, lse, dev_status, stream)
+    if rc:
+        raise MlaError(rc, "mla_latent_attn")

@@ -3,7 +3,9 @@
 Every translation unit under ``csrc/`` is compiled in parallel to an object
 under ``_build/``; the objects are linked into
 ``mla_chunked_context_gb300/libmla_gb300.so`` (CUDA runtime linked statically,
-so the library loads on a machine without a GPU).
+so the library loads on a machine without a GPU).  ``csrc/py_decode.cpp``, the
+decode calls' Python binding, becomes the module ``_decode.so`` beside it, with
+the host compiler and the headers of Python and of the installed PyTorch.
 """
 
 from __future__ import annotations
@@ -13,11 +15,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla_gb300.so")
+MODULE = os.path.join(HERE, "_decode.so")
+MODULE_SRC = os.path.join(CSRC, "py_decode.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(HERE, "..", "include")]
@@ -31,7 +36,8 @@ def nvcc() -> str:
 
 
 def _sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
+    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
+                  if f.endswith((".cu", ".cpp")) and f != os.path.basename(MODULE_SRC))
 
 
 def _compile(src: str, extra) -> str:
@@ -45,17 +51,49 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _run(what: str, cmd) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_module() -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    obj = os.path.join(BUILD, os.path.basename(MODULE_SRC) + ".o")
+    _run(f"compiling {MODULE_SRC}", [
+        "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-I", os.path.join(HERE, "..", "include"), "-isystem", inc,
+        "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+        "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+        "-c", MODULE_SRC, "-o", obj])
+    return obj
+
+
+def _link_module(obj: str) -> None:
+    import torch
+    tmp = MODULE + ".tmp"
+    _run("linking the Python module", [
+        "g++", "-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN",
+        "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
+        "-lc10", "-lc10_cuda"])
+    os.replace(tmp, MODULE)
+
+
 def build(extra_flags=(), verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        module = ex.submit(_compile_module)
         objs = list(ex.map(lambda s: _compile(s, list(extra_flags)), srcs))
+        module = module.result()
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run("link", [nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp,
+                  *objs])
     os.replace(tmp, LIB)
+    _link_module(module)
     if verbose:
         print(f"built {LIB}")
     return LIB
