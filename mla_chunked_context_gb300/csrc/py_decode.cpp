@@ -231,6 +231,7 @@ int append(PyObject *const *a) {
     }
     pe = t.data_ptr();
   }
+  if (d.P == 0 && a[12] != Py_None && a[13] != Py_None) q = pe = nullptr;  // nothing to rotate
   const int32_t t32 = narrow(T, w, "kv_a"), r32 = narrow(R, w, "seq_lens"),
                 p32 = narrow(n_pos, w, "rope_table"), b32 = narrow(blocks, w, "kv_cache"),
                 s32 = narrow(stride, w, "block_table");

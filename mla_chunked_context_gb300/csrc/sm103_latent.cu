@@ -223,14 +223,82 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
     length = s.tiles + UNIT_COST<PAIR>;
     return ((long long)nrt << POS_BITS) | ((long long)nrt * length);
   };
-  // inclusive scan over the block's threads, the total, and the longest unit
-  int longest = 0;
-  auto scan = [&](long long v, int len, long long &all) {
+  // Gives a cluster whose share starts (or ends) in sequence r its part of it;
+  // called by the thread that has the sequence, the positions up to its end
+  // being sum.
+  auto deal = [&](int r, long long mine, long long sum, long long total, int longest) {
+    if (nrt == 0) return;
+    const long long positions = total & MASK;
+    const int units = int(total >> POS_BITS);
+    // (64-bit divisions only where 32 bits do not hold the numbers)
+    int share = positions <= 0x7fffffff
+                    ? int((unsigned(positions) + clusters - 1) / unsigned(clusters))
+                    : int(min((positions + clusters - 1) / clusters, 0x7fffffffLL));
+    const long long lo = (sum - mine) & MASK, hi = sum & MASK;
+    if (units <= clusters && longest <= share + WHOLE_SLACK) {
+      const int u = cluster - int((sum - mine) >> POS_BITS);  // of this sequence's
+      if (u >= 0 && u < nrt) {
+        out->end = out->share = length;
+        out->seq = s;
+        out->r = r;
+        out->rt = u;
+      }
+      return;
+    }
+    if (share < MIN_SHARE) share = MIN_SHARE;
+    const int snap = longest <= SHORT ? SHORT / 2 : SNAP;
+    const long long start = (long long)share * cluster, end = start + share;
+    // the cut nearest to position p of this sequence (from its start)
+    int rt, pos;
+    auto cut = [&](long long p) {
+      rt = p <= 0x7fffffff ? int(unsigned(p) / unsigned(length)) : int(p / length);
+      pos = int(p - (long long)rt * length);
+      if (pos <= snap) {
+        pos = 0;
+      } else if (length - pos <= snap) {
+        pos = 0;
+        ++rt;
+      }
+      return lo + (long long)rt * length + pos;
+    };
+    if (start >= lo && start < hi) {
+      out->start = cut(start - lo);
+      out->share = share;
+      out->snap = snap;
+      out->seq = s;
+      out->r = r;
+      out->rt = rt;
+      out->pos = pos;
+      if (end >= positions) out->end = positions;
+    }
+    if (end < positions && end >= lo && end < hi) out->end = cut(end - lo);
+  };
+  auto warp_scan = [&](long long v) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long u = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += u;
     }
+    return v;
+  };
+  if (threadIdx.x == 0) {  // no work, unless threads find some below
+    out->start = out->end = 0;
+    out->r = out->rt = out->pos = 0;
+  }
+  if (a.R <= 32) {  // one warp has them all: 0.3 us less than through shared memory
+    if (warp == 0) {
+      const long long mine = look(lane), sum = warp_scan(mine);
+      const int longest = __reduce_max_sync(0xffffffffu, nrt > 0 ? length : 0);
+      __syncwarp();
+      deal(lane, mine, sum, __shfl_sync(0xffffffffu, sum, 31), longest);
+    }
+    __syncthreads();
+    return;
+  }
+  // inclusive scan over the block's threads, the total, and the longest unit
+  int longest = 0;
+  auto scan = [&](long long v, int len, long long &all) {
+    v = warp_scan(v);
     len = __reduce_max_sync(0xffffffffu, len);
     if (lane == 31) {
       scratch[warp] = v;
@@ -246,10 +314,6 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
     }
     return v;
   };
-  if (threadIdx.x == 0) {  // no work, unless threads find some below
-    out->start = out->end = 0;
-    out->r = out->rt = out->pos = 0;
-  }
   // more sequences than threads: their totals first
   const bool many = a.R > THREADS;
   long long total = 0;
@@ -269,52 +333,7 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
     long long all;
     const long long sum = base + scan(mine, nrt > 0 ? length : 0, all);
     if (!many) total = all;
-    const long long positions = total & MASK;
-    const int units = int(total >> POS_BITS);
-    // (64-bit divisions only where 32 bits do not hold the numbers)
-    int share = positions <= 0x7fffffff
-                    ? int((unsigned(positions) + clusters - 1) / unsigned(clusters))
-                    : int(min((positions + clusters - 1) / clusters, 0x7fffffffLL));
-    if (nrt > 0) {
-      const long long lo = (sum - mine) & MASK, hi = sum & MASK;
-      if (units <= clusters && longest <= share + WHOLE_SLACK) {
-        const int u = cluster - int((sum - mine) >> POS_BITS);  // of this sequence's
-        if (u >= 0 && u < nrt) {
-          out->end = out->share = length;
-          out->seq = s;
-          out->r = r0 + threadIdx.x;
-          out->rt = u;
-        }
-      } else {
-        if (share < MIN_SHARE) share = MIN_SHARE;
-        const int snap = longest <= SHORT ? SHORT / 2 : SNAP;
-        const long long start = (long long)share * cluster, end = start + share;
-        // the cut nearest to position p of this sequence (from its start)
-        int rt, pos;
-        auto cut = [&](long long p) {
-          rt = p <= 0x7fffffff ? int(unsigned(p) / unsigned(length)) : int(p / length);
-          pos = int(p - (long long)rt * length);
-          if (pos <= snap) {
-            pos = 0;
-          } else if (length - pos <= snap) {
-            pos = 0;
-            ++rt;
-          }
-          return lo + (long long)rt * length + pos;
-        };
-        if (start >= lo && start < hi) {
-          out->start = cut(start - lo);
-          out->share = share;
-          out->snap = snap;
-          out->seq = s;
-          out->r = r0 + threadIdx.x;
-          out->rt = rt;
-          out->pos = pos;
-          if (end >= positions) out->end = positions;
-        }
-        if (end < positions && end >= lo && end < hi) out->end = cut(end - lo);
-      }
-    }
+    deal(r0 + threadIdx.x, mine, sum, total, longest);
     base += all;
     __syncthreads();
   }

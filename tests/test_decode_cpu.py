@@ -132,6 +132,23 @@ def test_bindings_refuse_host_tensors():
         M.mla_append_latent(d, z(1, 80), z(2, **i), z(1, **i), None, z(4, 16, 80), z(1, 2, **i))
 
 
+def test_bindings_refuse_what_is_no_tensor():
+    d = M.Dims(2, 64, 16, 32, 32, 16, 0.1, torch.float32)
+    z = torch.zeros
+    with pytest.raises(ValueError, match="q has to be a tensor"):
+        M.mla_absorb_query(d, None, z(128, 64), z(1, 2, 80))
+    with pytest.raises(ValueError, match="o_latent has to have 3 dimensions"):
+        M.mla_expand_output(d, z(2, 64), z(128, 64), z(1, 2, 32))
+    with pytest.raises(ValueError, match="kv_a has to be"):
+        M.mla_append_latent(d, z(1, 79), z(2), z(1), None, z(4, 16, 80), z(1, 2))
+    for dtype in (torch.int8, "float32"):
+        with pytest.raises(ValueError, match="unsupported dtype"):
+            M.mla_absorb_query(M.Dims(2, 64, 16, 32, 32, 16, 0.1, dtype), z(1, 2, 48), z(128, 64),
+                               z(1, 2, 80))
+    with pytest.raises(AttributeError):
+        M.mla_absorb_query(object(), z(1, 2, 48), z(128, 64), z(1, 2, 80))
+
+
 def test_more_than_an_instance_has_room_for():
     d = M.Dims(2, 64, 16, 32, 32, 16, 0.1, torch.float32)
     dec, z = M.LatentDecode(d, 2, 2, device="cpu"), torch.zeros

@@ -815,3 +815,33 @@ def test_rows_that_are_not_finite_reach_only_tokens_that_see_them(shape, dtype, 
             assert (nan | (score == -np.inf)).all() and nan.any()
         else:
             assert torch.equal(o2[t], o[t]) and torch.equal(lse2[:, t], lse[:, t]), t
+
+
+def test_decode_step_without_rope_columns_and_without_tokens():
+    rng = np.random.default_rng(2)
+    dims, od = make_dims((64, 0, 32, 32), 3, 16, "f32")
+    lens, qsl = [40, 7], [0, 1, 3]
+    cache, table = make_cache(rng, lens, 16, 64, dims.dtype)
+    q, kv_a = normal(rng, 3, 3, 32), normal(rng, 3, 64)
+    w = normal(rng, 3 * 64, 64, std=0.1)
+    g_cache, out, lse = cache.to(DEV), torch.empty(3, 3, 32, device=DEV), torch.empty(3, 3, device=DEV)
+    dec = M.LatentDecode(dims, 4, 2, device=DEV)
+    dec(q.to(DEV), kv_a.to(DEV), i32(qsl), i32(lens), None, g_cache, table.to(DEV), w.to(DEV), out, lse)
+    torch.cuda.synchronize()
+    for t, r, pos in O.token_positions(qsl, lens):
+        assert torch.equal(g_cache[table[r, pos // 16], pos % 16].cpu(), kv_a[t])
+    q_lat = f64(dec.q_latent[:3])
+    within(q_lat, O.absorb_query(f64(q), f64(w), od),
+           36 * F * O.absorb_query(np.abs(f64(q)), np.abs(f64(w)), od), "absorb")
+    _, rl, _, size = O.latent_attention(q_lat, f64(g_cache), table.numpy(), qsl, lens, od, True)
+    within(f64(lse), rl, 72 * F * size + 2.0 ** -22 + 21 * F + F * np.abs(rl), "lse")
+    o_lat = f64(dec.o_latent[:3])
+    within(f64(out), O.expand_output(o_lat, f64(w), od),
+           68 * F * O.expand_output(np.abs(o_lat), np.abs(f64(w)), od) + F * np.abs(f64(out)), "out")
+    before, n = out.clone(), M.mla_kernel_launches()
+    dec(q[:0].to(DEV), kv_a[:0].to(DEV), i32([0, 0, 0]), i32(lens), None, g_cache, table.to(DEV),
+        w.to(DEV), out[:0])
+    dec(q[:0].to(DEV), kv_a[:0].to(DEV), i32([0]), i32([]), None, g_cache, table[:0].to(DEV),
+        w.to(DEV), out[:0])
+    torch.cuda.synchronize()
+    assert torch.equal(out, before) and M.mla_kernel_launches() == n
