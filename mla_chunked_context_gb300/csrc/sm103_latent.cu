@@ -114,6 +114,7 @@ struct LatentArgs {
   int4 *desc;
   int32_t *status;
   int T, R, H, bs, num_blocks, none, bt_stride, causal, box_log2;  // none: a row past the cache
+  bool o_sectors;  // o is 32-byte aligned
   Divider by_bs, by_h;
   float scale_log2;
 };
@@ -425,6 +426,19 @@ __device__ __forceinline__ void mma_lo(uint32_t d, uint32_t alo, uint32_t blo, u
         " tcgen05.mma.ws.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
         "r"(alo), "r"(blo), "r"(DESC_HI), "r"(idesc), "r"(acc)
         : "memory");
+}
+
+// 32 bytes in one store where the address allows it, so that every sector is
+// written at once.
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t (&v)[8], bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 // Any of 8 bf16 values infinite or NaN.
@@ -891,16 +905,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const float lse2 = l > 0.f || l != l ? mref + log2f(l) : neg_inf();
-      const int64_t grow0 = int64_t(w.s.q0) * a.H + w.rt * C::UROWS;  // the unit's first row
+      const int grow0 = w.s.q0 * a.H + w.rt * C::UROWS;  // the unit's first row
       const int slot = 2 * cluster + (w.t0 == 0 ? 1 : 0);
       const int64_t srow = int64_t(slot) * C::UROWS + int(rank) * CROWS;
       if (half == 0 && part == 0) {
-        const int64_t grow = grow0 + urow;
+        const int token = a.by_h.quotient(grow0 + urow);
         if (urow >= rows) {
         } else if (!whole)
           a.part_lse[srow + rl] = lse2;
         else if (a.lse)
-          a.lse[int64_t(grow % a.H) * a.T + grow / a.H] = lse2 * LN2;
+          a.lse[int64_t(grow0 + urow - token * a.H) * a.T + token] = lse2 * LN2;
       }
       ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1));
       if (!ok) break;
@@ -908,44 +922,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       // D's columns: part 0 holds the first MMA's, part 1 the second's
       const int dim0 = PAIR ? half * 256 + part * 128 : part * 256 + half * 128;
       if (whole) {
-        // through shared memory (P's room), EC columns of all four quarters at
-        // a time, so that whole sectors are written
-        constexpr int EC = PAIR ? 32 : 16, PIECES = EC / 8;
-        const uint32_t stage = sP + (tid >> 6) * (64 * EC * 2);
+        __nv_bfloat16 *dst = a.o + int64_t(grow0 + urow) * LAT + dim0;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += EC) {
-          uint32_t o[EC];
-          if constexpr (PAIR)
-            tmem_ld32(t_lane + part * 128 + c, o);
-          else
-            tmem_ld16(t_lane + part * 128 + c, o);
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t o[2][32];
+          tmem_ld32(t_lane + part * 128 + c, o[0]);
+          tmem_ld32(t_lane + part * 128 + c + 32, o[1]);
           tmem_wait_ld();
-          if (c > 0) softmax_barrier();  // the stage has been read
 #pragma unroll
-          for (int e = 0; e < PIECES; ++e) {
-            uint32_t v[4];
+          for (int e = 0; e < 4; ++e) {  // 16 columns: a whole sector of the row
+            uint32_t v[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x = __uint_as_float(o[8 * e + 2 * k]);
-              const float y = __uint_as_float(o[8 * e + 2 * k + 1]);
+            for (int k = 0; k < 8; ++k) {
+              const float x = __uint_as_float(o[e >> 1][(e & 1) * 16 + 2 * k]);
+              const float y = __uint_as_float(o[e >> 1][(e & 1) * 16 + 2 * k + 1]);
               v[k] = inv == 0.f ? 0u : pack_bf16(x * inv, y * inv);
             }
-            const int sw = PAIR ? (rl >> 1) & 3 : (rl >> 2) & 1;  // spreads the banks
-            st_shared_v4(stage + rl * (EC * 2) + ((e ^ sw) << 4),
-                         make_uint4(v[0], v[1], v[2], v[3]));
-          }
-          softmax_barrier();
-#pragma unroll
-          for (int k = 0; k < PIECES; ++k) {
-            const int x = k * STHREADS + tid;  // quarter, row, piece
-            const int qt = x / (64 * PIECES), r = x / PIECES % 64, e = x % PIECES;
-            const int row = int(rank) * CROWS + r;
-            const int sw = PAIR ? (r >> 1) & 3 : (r >> 2) & 1;
-            const int d =
-                PAIR ? (qt & 1) * 256 + (qt >> 1) * 128 : (qt >> 1) * 256 + (qt & 1) * 128;
-            if (row < rows)
-              *reinterpret_cast<uint4 *>(a.o + (grow0 + row) * LAT + d + c + e * 8) =
-                  ld_shared_v4(sP + qt * (64 * EC * 2) + r * (EC * 2) + ((e ^ sw) << 4));
+            if (urow < rows) st_global_32(dst + c + e * 16, v, a.o_sectors);
           }
         }
       } else {
@@ -969,7 +962,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (w.t0 == 0 && tid == 0 && rank == 0) {
           // the unit's first piece: its others are in the shares that follow
           a.desc[2 * cluster] = make_int4(1 + w.others(*share), min(rows, C::UROWS), 0, 0);
-          *reinterpret_cast<long long *>(a.desc + 2 * cluster + 1) = grow0;
+          a.desc[2 * cluster + 1].x = grow0;
         }
       }
       tc_fence_before();  // the reads of O come before the next piece's P is handed over
@@ -1069,15 +1062,16 @@ __device__ __forceinline__ Joined<W> join_pieces(const float *part_o, const floa
 }
 
 template <int W>
-__device__ __forceinline__ void join_store(const Joined<W> &j, int64_t grow, int col4,
-                                           __nv_bfloat16 *o, float *lse, int H, int T) {
+__device__ __forceinline__ void join_store(const Joined<W> &j, int grow, int col4,
+                                           __nv_bfloat16 *o, float *lse, int H, Divider by_h,
+                                           int T) {
   const float inv = j.sum == 0.f ? 0.f : 1.f / j.sum;
   uint2 out[W];
 #pragma unroll
   for (int k = 0; k < W; ++k)
     out[k] = make_uint2(pack_bf16(j.acc[k].x * inv, j.acc[k].y * inv),
                         pack_bf16(j.acc[k].z * inv, j.acc[k].w * inv));
-  __nv_bfloat16 *dst = o + grow * LAT + col4 * 4;
+  __nv_bfloat16 *dst = o + int64_t(grow) * LAT + col4 * 4;
   if constexpr (W > 1) {
 #pragma unroll
     for (int k = 0; k < W; k += 2)
@@ -1086,16 +1080,18 @@ __device__ __forceinline__ void join_store(const Joined<W> &j, int64_t grow, int
   } else {
     *reinterpret_cast<uint2 *>(dst) = out[0];
   }
-  if (lse && col4 == 0)
-    lse[int64_t(grow % H) * T + grow / H] =
+  if (lse && col4 == 0) {
+    const int token = by_h.quotient(grow);
+    lse[int64_t(grow - token * H) * T + token] =
         j.sum == 0.f ? neg_inf() : ((is_neg_inf(j.mx) ? 0.f : j.mx) + log2f(j.sum)) * LN2;
+  }
 }
 
 __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, int clusters,
                                                             int urows, const float *part_o,
                                                             const float *part_lse,
                                                             __nv_bfloat16 *o, float *lse, int H,
-                                                            int T) {
+                                                            Divider by_h, int T) {
   // cut units (cluster of the first piece) of many pieces, and of few with the
   // items before each
   __shared__ int few[CT], many[CT], first[CT], first_m[CT];
@@ -1171,7 +1167,7 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
     const int u = unit_of(first_m, num_m, it), c0 = many[u], sub = it - first_m[u];
     const int row = (sub / 128) * 32 + lane, col4 = sub % 128;
     const int4 d = desc[2 * c0];
-    const int64_t grow0 = *reinterpret_cast<const long long *>(desc + 2 * c0 + 1);
+    const int grow0 = desc[2 * c0 + 1].x;
     Joined<1> j =
         join_pieces<1, 16>(part_o, part_lse, c0, warp, CW, row < d.y ? d.x : 0, urows, row, col4);
     sacc[warp][lane] = j.acc[0];
@@ -1194,7 +1190,7 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
         j.acc[0].z = fmaf(f, v.z, j.acc[0].z);
         j.acc[0].w = fmaf(f, v.w, j.acc[0].w);
       }
-      if (row < d.y) join_store<1>(j, grow0 + row, col4, o, lse, H, T);
+      if (row < d.y) join_store<1>(j, grow0 + row, col4, o, lse, H, by_h, T);
     }
     __syncthreads();
   }
@@ -1203,13 +1199,13 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
   for (int it = turn * CW + warp; it < num_i; it += gridDim.x * CW) {
     const int u = unit_of(first, num_f, it), c0 = few[u], sub = it - first[u];
     const int4 d = desc[2 * c0];
-    const int64_t grow0 = *reinterpret_cast<const long long *>(desc + 2 * c0 + 1);
+    const int grow0 = desc[2 * c0 + 1].x;
     const int w = few_columns(d.x), row = sub / (128 / w) * 32 + lane, col4 = sub % (128 / w) * w;
     auto one = [&](auto width, auto pieces) {
       constexpr int W = decltype(width)::value, U = decltype(pieces)::value;
       const Joined<W> j =
           join_pieces<W, U>(part_o, part_lse, c0, 0, 1, row < d.y ? d.x : 0, urows, row, col4);
-      if (row < d.y) join_store<W>(j, grow0 + row, col4, o, lse, H, T);
+      if (row < d.y) join_store<W>(j, grow0 + row, col4, o, lse, H, by_h, T);
     };
     if (w == 8)
       one(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
@@ -1258,7 +1254,7 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
   if (most_tiles + UNIT_COST<PAIR> <= SHORT) return MLA_OK;
   return launch_chained(latent_combine_kernel, COMBINE_BLOCKS * num_sms(), CT, 0, 1, s,
                         "latent_combine_kernel", a.desc, PAIR ? grid / 2 : grid, Cfg<PAIR>::UROWS,
-                        a.part_o, a.part_lse, a.o, a.lse, a.H, a.T);
+                        a.part_o, a.part_lse, a.o, a.lse, a.H, a.by_h, a.T);
 }
 
 }  // namespace
@@ -1294,7 +1290,7 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
                static_cast<__nv_bfloat16 *>(o), lse, part_o, part_lse,
                static_cast<int4 *>(desc), status, T, R, d.num_heads, d.block_size, num_blocks,
                int(cache_rows), bt_stride, causal, box_log2,
-               Divider(d.block_size), Divider(d.num_heads), d.softmax_scale * 1.4426950408889634f};
+               reinterpret_cast<uintptr_t>(o) % 32 == 0, Divider(d.block_size), Divider(d.num_heads), d.softmax_scale * 1.4426950408889634f};
   // rows of an average sequence beyond one CTA's 64: pairs
   if (int64_t(T) * d.num_heads > int64_t(64) * R) return launch_latent<true>(maps, a, max_ctas, s);
   return launch_latent<false>(maps, a, max_ctas, s);

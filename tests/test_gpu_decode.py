@@ -845,3 +845,21 @@ def test_decode_step_without_rope_columns_and_without_tokens():
         w.to(DEV), out[:0])
     torch.cuda.synchronize()
     assert torch.equal(out, before) and M.mla_kernel_launches() == n
+
+
+@pytest.mark.parametrize("H", [128, 40])
+def test_latent_attention_outputs_at_16_bytes(H):
+    """An output that starts 16 bytes into a sector gives the same bits."""
+    rng = np.random.default_rng(H)
+    dims, od = make_dims(LARGE, H, 64, "bf16")
+    lens, qsl = [70, 900, 2600], [0, 1, 3, 4]
+    cache, table = make_cache(rng, lens, 64, 576, dims.dtype)
+    q = normal(rng, 4, H, 576, std=0.4, dtype=dims.dtype)
+    o, lse = run_attn(dims, True, qsl, lens, q, cache, table)
+    raw = torch.full((4 * H * 512 + 24,), 7.0, dtype=dims.dtype, device=DEV)
+    o2 = raw[8:8 + 4 * H * 512].view(4, H, 512)
+    assert o2.data_ptr() % 32 == 16
+    ws = torch.empty(M.mla_latent_attn_workspace_bytes(dims, 4, 3), dtype=torch.uint8, device=DEV)
+    M.mla_latent_attn(dims, True, i32(qsl), i32(lens), q.to(DEV), cache.to(DEV), table.to(DEV), ws, o2)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and (raw[:8] == 7).all() and (raw[-16:] == 7).all()
