@@ -968,11 +968,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_before();  // the reads of O come before the next piece's P is handed over
     }
   }
+  // Every MMA has completed; and in the pair neither CTA leaves while the other
+  // may still arrive here.
+  if (warp == 2) mbar_wait(done, 0);
   tc_fence_before();
-  __syncthreads();
-  if (threadIdx.x == 0) mbar_wait(done, 0);
-  __syncthreads();
-  if (PAIR) cluster_sync();  // neither CTA leaves while the pair's MMAs or arrives may touch it
+  if (PAIR) {  // (a release would wait for the rows' way to L2)
+    cluster_arrive_relaxed();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   if (warp == 2) {
     __syncwarp();
