@@ -14,9 +14,9 @@
 // serves one token: warp 0 of its first block the row, all other threads the
 // heads of the queries, each the same columns (and angles) of several heads.
 // Few tokens spread their heads over several blocks.
-// Measured, 128 heads, bf16: 8192 tokens (299 MB) 54.6 us, 5.5 TB/s or 81% of
+// Measured, 128 heads, bf16: 8192 tokens (299 MB) 55.2 us, 5.4 TB/s or 80% of
 // copy bandwidth, the queries' rope columns being 128 of every 384 bytes; 16
-// tokens 4.2 us in a graph.
+// tokens 4.1 us in a graph.
 #include "common.cuh"
 
 namespace mla {

@@ -12,8 +12,8 @@
 // to spread the weights' loads over more SMs.  (Absorb with 256 columns, two
 // CTAs an SM: 27.0 us for 500 tokens and 128 heads, with 128 columns 26.0, with
 // 64 34.3; expand with 64: 21.7 against 19.6.)  Both move their bytes at 4.4
-// and 5.0 TB/s then, rows of 256 bytes of each token's 147 (131) KB; 16 tokens
-// take 6.6 us, the host's time for the call.
+// and 5.0 TB/s then, rows of 256 bytes of each token's 147 (131) KB; one
+// token takes 5.8 us (absorb), 16 take 5.0 (expand), most of it the weights.
 //   warp 0     TMA loads: per 64 columns of the contraction, the tokens' box
 //              (only as many rows as there are tokens: what the others' rows of
 //              the accumulator hold is never stored) and the weight's: absorb's
