@@ -35,6 +35,7 @@ namespace {
 constexpr int LAT = 512, ROPE = 64, HEAD = 128;   // L, P, Dn = Dv
 constexpr int TM = 128;                           // tokens of a tile
 constexpr int A_BYTES = TM * 128;                 // 128 tokens x 64 columns
+constexpr int MAX_STAGES = 8;
 constexpr int THREADS = 192;
 
 template <bool EXPAND>
@@ -42,16 +43,14 @@ struct Cfg {
   static constexpr int K = EXPAND ? LAT : HEAD, N = EXPAND ? HEAD : LAT;
   static constexpr int MAX_NC = 128;
   static constexpr int KBLOCKS = K / 64;
-  static constexpr int STAGES = EXPAND ? 3 : 2;
-  static constexpr int STAGE = A_BYTES + MAX_NC * 128;
-  static constexpr int CTAS = EXPAND ? 2 : 3;       // an SM
-  static constexpr int SMEM = 1024 + STAGES * STAGE + 128;
+  static constexpr int CTAS = EXPAND ? 2 : 4;       // an SM, at most
+  static constexpr int MAX_SMEM = (EXPAND ? 112 : 75) * 1024;  // of a CTA: 2 or 3 an SM fit
 };
 
 struct HeadArgs {
   const __nv_bfloat16 *q;  // absorb: rope columns to copy, or null
   __nv_bfloat16 *q_latent;
-  int T, H, nc, box_rows;
+  int T, H, nc, box_rows, stages, stage_bytes, bars;  // bars: offset of the barriers
 };
 
 template <bool EXPAND>
@@ -63,15 +62,17 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::STAGES * C::STAGE);
-  const uint32_t full = smem_u32(bars), empty = full + 8 * C::STAGES, acc_full = empty + 8 * C::STAGES;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * C::STAGES + 1);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + g.bars);
+  const uint32_t full = smem_u32(bars), empty = full + 8 * MAX_STAGES,
+                 acc_full = empty + 8 * MAX_STAGES;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * MAX_STAGES + 1);
+  const uint32_t stage0 = smem_u32(smem), a_bytes = uint32_t(g.box_rows) * 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * g.nc, t0 = blockIdx.y * TM, h = blockIdx.z;
   const uint32_t cols = uint32_t(g.nc);  // 64 or 128
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
+    for (int i = 0; i < g.stages; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
     }
@@ -101,10 +102,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t bytes = uint32_t(g.box_rows * 128 + g.nc * 128);
+      int st = 0;
+      uint32_t parity = 1;
       for (int kb = 0; kb < C::KBLOCKS; ++kb) {
-        const int st = kb % C::STAGES;
-        if (!mbar_wait(empty + 8 * st, ((kb / C::STAGES) & 1) ^ 1)) break;
-        const uint32_t a = smem_u32(smem + st * C::STAGE), w = a + A_BYTES, bar = full + 8 * st;
+        if (!mbar_wait(empty + 8 * st, parity)) break;
+        const uint32_t a = stage0 + st * g.stage_bytes, w = a + a_bytes, bar = full + 8 * st;
         mbar_expect_tx(bar, bytes);
         if (EXPAND) {
           tma_load_2d(w, &tm_w, bar, kb * 64, h * 2 * HEAD + HEAD + n0);  // NC rows
@@ -113,22 +115,32 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
             tma_load_2d(w + j * 8192, &tm_w, bar, n0 + j * 64, h * 2 * HEAD + kb * 64);
         }
         tma_load_2d(a, &tm_a, bar, (EXPAND ? h * LAT : h * (HEAD + ROPE)) + kb * 64, t0);
+        if (++st == g.stages) {
+          st = 0;
+          parity ^= 1;
+        }
       }
     }
   } else if (warp == 1) {
     if (elect_one()) {
       const uint32_t idesc = idesc_f16kind(TM, g.nc, false, !EXPAND, true);
+      int st = 0;
+      uint32_t parity = 0;
       for (int kb = 0; kb < C::KBLOCKS; ++kb) {
-        const int st = kb % C::STAGES;
-        if (!mbar_wait(full + 8 * st, (kb / C::STAGES) & 1)) break;
+        if (!mbar_wait(full + 8 * st, parity)) break;
         tc_fence_after();
-        const uint32_t a = smem_u32(smem + st * C::STAGE), w = a + A_BYTES;
+        // (rows of A from box_rows on are whatever follows it)
+        const uint32_t a = stage0 + st * g.stage_bytes, w = a + a_bytes;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           mma_bf16(tmem, desc_kmajor_sw128(a + ks * 32),
                    EXPAND ? desc_kmajor_sw128(w + ks * 32) : desc_mnmajor_sw128(w + ks * 2048, 8192),
                    idesc, (kb | ks) != 0);
         mma_commit(empty + 8 * st);
+        if (++st == g.stages) {
+          st = 0;
+          parity ^= 1;
+        }
       }
       mma_commit(acc_full);
     }
@@ -159,7 +171,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
     if (ok && t0 + quarter * 32 < g.T) {
       // every load has been consumed: the stages are free.  4 KB a piece of 32
       // rows x 64 columns, a warp's pieces behind each other.
-      const uint32_t stg = smem_u32(smem) + quarter * (C::MAX_NC / 64) * 4096;
+      const uint32_t stg = stage0 + quarter * (C::MAX_NC / 64) * 4096;
 #pragma unroll 1
       for (int j = 0; j < g.nc / 64; ++j) {
         uint32_t lo[32], hi[32];
@@ -196,8 +208,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
 }
 
 template <bool EXPAND>
-int launch_heads(const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to,
-                 const HeadArgs &g, cudaStream_t s) {
+int launch_heads(const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to, HeadArgs g,
+                 cudaStream_t s) {
   using C = Cfg<EXPAND>;
   constexpr int MAX_DEV = 64;
   static std::atomic<int> ready[MAX_DEV];
@@ -205,13 +217,22 @@ int launch_heads(const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEV) return MLA_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(head_gemm_kernel<EXPAND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM) != cudaSuccess)
+                             C::MAX_SMEM) != cudaSuccess)
       return MLA_ERR_CUDA;
     ready[dev].store(1, std::memory_order_release);
   }
+  // As many stages as there are blocks of the contraction, if they fit.  The
+  // rows behind a short box of A, which its MMAs read, and the epilogue's 32
+  // rows x 64 columns a warp stay within the stages or the room behind them.
+  constexpr int BARS = 8 * (2 * MAX_STAGES + 2);
+  g.stage_bytes = (g.box_rows + g.nc) * 128;
+  g.stages = std::min(C::KBLOCKS, (C::MAX_SMEM - 1024 - BARS) / g.stage_bytes);
+  const int warps = std::min(4, (g.box_rows + 31) / 32);  // of the epilogue, with rows to store
+  g.bars = std::max({g.stages * g.stage_bytes, (g.stages - 1) * g.stage_bytes + A_BYTES,
+                     warps * (C::MAX_NC / 64) * 4096});
   return launch_chained(head_gemm_kernel<EXPAND>, dim3(C::N / g.nc, (g.T + TM - 1) / TM, g.H),
-                        THREADS, C::SMEM, 1, s, EXPAND ? "expand_kernel" : "absorb_kernel", ta, tw,
-                        to, g);
+                        THREADS, 1024 + g.bars + BARS, 1, s,
+                        EXPAND ? "expand_kernel" : "absorb_kernel", ta, tw, to, g);
 }
 
 // Columns of a CTA.
