@@ -6,14 +6,17 @@
 // so the kernel is there to stream: the weight halves (16.8 MB each at 128
 // heads) once for few tokens, the activations once for many.
 //
-// A CTA computes 128 tokens x NC columns of one head; two (expand) or three
-// (absorb) CTAs an SM, so that one's loads run beside another's epilogue.  NC
-// is 128, and 64 where heads and tokens are too few to give every SM two CTAs,
-// to spread the weights' loads over more SMs.  (Absorb with 256 columns, two
-// CTAs an SM: 27.0 us for 500 tokens and 128 heads, with 128 columns 26.0, with
-// 64 34.3; expand with 64: 21.7 against 19.6.)  Both move their bytes at 4.4
-// and 5.0 TB/s then, rows of 256 bytes of each token's 147 (131) KB; one
-// token takes 5.8 us (absorb), 16 take 5.0 (expand), most of it the weights.
+// A CTA computes 128 tokens x NC columns of one head; two (expand) or three to
+// four (absorb) CTAs an SM, so that one's loads run beside another's epilogue.
+// NC is 128, and 64 where heads and tokens are too few to give every SM two
+// CTAs, to spread the weights' loads over more SMs.  A stage has room for the
+// tokens there are, so that for few of them all of the contraction is in flight
+// at once (with stages for 128: absorb of one token 5.9 us, expand of 16 5.2;
+// so 4.5 and 4.8, of which the weights' way takes most).
+// Many tokens (500, 128 heads) take 26.1 and 19.6 us, 4.4 and 5.0 TB/s: a CTA's
+// loads wait for L2.  Absorb with 256 columns a CTA: 27.0, with 64 34.3, as a
+// persistent kernel with two accumulators 32.2, with the four CTAs of a token
+// tile sharing its loads by multicast 32.9; expand with 64 columns 21.7.
 //   warp 0     TMA loads: per 64 columns of the contraction, the tokens' box
 //              (only as many rows as there are tokens: what the others' rows of
 //              the accumulator hold is never stored) and the weight's: absorb's

@@ -863,3 +863,26 @@ def test_latent_attention_outputs_at_16_bytes(H):
     M.mla_latent_attn(dims, True, i32(qsl), i32(lens), q.to(DEV), cache.to(DEV), table.to(DEV), ws, o2)
     torch.cuda.synchronize()
     assert torch.equal(o, o2) and (raw[:8] == 7).all() and (raw[-16:] == 7).all()
+
+
+@pytest.mark.parametrize("T,H", [(8, 128), (33, 80), (40, 128), (97, 128), (120, 9), (121, 128), (128, 40),
+                                 (500, 12), (257, 160)])
+def test_absorb_and_expand_tile_edges(T, H):
+    """Token counts at the edges of boxes, tiles, stages and of columns a CTA."""
+    rng = np.random.default_rng(T)
+    dims, od = make_dims(LARGE, H, 16, "bf16")
+    q = normal(rng, T, H, 192, dtype=dims.dtype)
+    w = normal(rng, H * 256, 512, std=0.1, dtype=dims.dtype)
+    ol = normal(rng, T, H, 512, dtype=dims.dtype)
+    got = torch.full((T, H, 576), 7.0, dtype=dims.dtype, device=DEV)
+    out = torch.full((T, H, 128), 7.0, dtype=dims.dtype, device=DEV)
+    M.mla_absorb_query(dims, q.to(DEV), w.to(DEV), got)
+    M.mla_expand_output(dims, ol.to(DEV), w.to(DEV), out)
+    for h in sorted({0, H // 2, H - 1}):
+        wh = f64(w[h * 256:(h + 1) * 256])
+        for a, b, g, K in ((f64(q[:, h, :128]), wh[:128], got[:, h, :512], 128),
+                           (f64(ol[:, h]), wh[128:].T, out[:, h], 512)):
+            ref = a @ b
+            within(f64(g), ref, unit(dims.dtype) * np.abs(ref) + (K + 4) * F * (np.abs(a) @ np.abs(b)),
+                   f"head {h}")
+    assert torch.equal(got[..., 512:].cpu(), q[..., 128:])
