@@ -13,7 +13,7 @@
 // tokens there are, so that for few of them all of the contraction is in flight
 // at once (with stages for 128: absorb of one token 5.9 us, expand of 16 5.2;
 // so 4.5 and 4.8, of which the weights' way takes most).
-// Many tokens (500, 128 heads) take 26.1 and 19.6 us, 4.4 and 5.0 TB/s: a CTA's
+// Many tokens (500, 128 heads) take 26.4 and 18.7 us, 4.4 and 5.3 TB/s: a CTA's
 // loads wait for L2.  Absorb with 256 columns a CTA: 27.0, with 64 34.3, as a
 // persistent kernel with two accumulators 32.2, with the four CTAs of a token
 // tile sharing its loads by multicast 32.9; expand with 64 columns 21.7.
@@ -53,10 +53,12 @@ struct Cfg {
 struct HeadArgs {
   const __nv_bfloat16 *q;  // absorb: rope columns to copy, or null
   __nv_bfloat16 *q_latent;
-  int T, H, nc, box_rows, stages, stage_bytes, bars;  // bars: offset of the barriers
+  int T, H, nc, box_rows;
+  int stages, stage_bytes, bars;          // bars: offset of the barriers
 };
 
-template <bool EXPAND>
+// MT: tiles of tokens of a CTA
+template <bool EXPAND, int MT>
 __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                      const __grid_constant__ CUtensorMap tm_w,
@@ -69,10 +71,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
   const uint32_t full = smem_u32(bars), empty = full + 8 * MAX_STAGES,
                  acc_full = empty + 8 * MAX_STAGES;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * MAX_STAGES + 1);
-  const uint32_t stage0 = smem_u32(smem), a_bytes = uint32_t(g.box_rows) * 128;
+  const uint32_t stage0 = smem_u32(smem), a_bytes = uint32_t(MT * g.box_rows) * 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * g.nc, t0 = blockIdx.y * TM, h = blockIdx.z;
-  const uint32_t cols = uint32_t(g.nc);  // 64 or 128
+  const int n0 = blockIdx.x * g.nc, t0 = blockIdx.y * TM * MT, h = blockIdx.z;
+  const uint32_t cols = uint32_t(MT * g.nc);  // 64, 128 or 256
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.stages; ++i) {
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
 
   if (warp == 0) {
     if (lane == 0) {
-      const uint32_t bytes = uint32_t(g.box_rows * 128 + g.nc * 128);
+      const uint32_t bytes = uint32_t((MT * g.box_rows + g.nc) * 128);
       int st = 0;
       uint32_t parity = 1;
       for (int kb = 0; kb < C::KBLOCKS; ++kb) {
@@ -117,7 +119,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
           for (int j = 0; j < g.nc / 64; ++j)  // 64 rows of the contraction, 64 columns
             tma_load_2d(w + j * 8192, &tm_w, bar, n0 + j * 64, h * 2 * HEAD + kb * 64);
         }
-        tma_load_2d(a, &tm_a, bar, (EXPAND ? h * LAT : h * (HEAD + ROPE)) + kb * 64, t0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          tma_load_2d(a + m * A_BYTES, &tm_a, bar,
+                      (EXPAND ? h * LAT : h * (HEAD + ROPE)) + kb * 64, t0 + m * TM);
         if (++st == g.stages) {
           st = 0;
           parity ^= 1;
@@ -135,10 +140,13 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
         // (rows of A from box_rows on are whatever follows it)
         const uint32_t a = stage0 + st * g.stage_bytes, w = a + a_bytes;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_bf16(tmem, desc_kmajor_sw128(a + ks * 32),
-                   EXPAND ? desc_kmajor_sw128(w + ks * 32) : desc_mnmajor_sw128(w + ks * 2048, 8192),
-                   idesc, (kb | ks) != 0);
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16(tmem + m * g.nc, desc_kmajor_sw128(a + m * A_BYTES + ks * 32),
+                     EXPAND ? desc_kmajor_sw128(w + ks * 32)
+                            : desc_mnmajor_sw128(w + ks * 2048, 8192),
+                     idesc, (kb | ks) != 0);
         mma_commit(empty + 8 * st);
         if (++st == g.stages) {
           st = 0;
@@ -171,14 +179,16 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
     }
     const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0));
     tc_fence_after();
-    if (ok && t0 + quarter * 32 < g.T) {
+    for (int m = 0; ok && m < MT; ++m) {
+      const int t = t0 + m * TM + quarter * 32;
+      if (t >= g.T) break;
       // every load has been consumed: the stages are free.  4 KB a piece of 32
       // rows x 64 columns, a warp's pieces behind each other.
-      const uint32_t stg = stage0 + quarter * (C::MAX_NC / 64) * 4096;
+      const uint32_t stg = stage0 + (m * 4 + quarter) * (C::MAX_NC / 64) * 4096;
 #pragma unroll 1
       for (int j = 0; j < g.nc / 64; ++j) {
         uint32_t lo[32], hi[32];
-        const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + j * 64;
+        const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + m * g.nc + j * 64;
         tmem_ld32(src, lo);
         tmem_ld32(src + 32, hi);
         tmem_wait_ld();
@@ -195,14 +205,14 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&tm_o, stg + j * 4096,
-                       (EXPAND ? h * HEAD : h * (LAT + ROPE)) + n0 + j * 64, t0 + quarter * 32);
+          tma_store_2d(&tm_o, stg + j * 4096, (EXPAND ? h * HEAD : h * (LAT + ROPE)) + n0 + j * 64,
+                       t);
           bulk_commit();
         }
       }
-      if (lane == 0) bulk_wait_all();
-      __syncwarp();
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -210,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
   if (warp == 1) tmem_dealloc(tmem, cols);
 }
 
-template <bool EXPAND>
+template <bool EXPAND, int MT>
 int launch_heads(const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to, HeadArgs g,
                  cudaStream_t s) {
   using C = Cfg<EXPAND>;
@@ -219,7 +229,7 @@ int launch_heads(const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEV) return MLA_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(head_gemm_kernel<EXPAND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(head_gemm_kernel<EXPAND, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::MAX_SMEM) != cudaSuccess)
       return MLA_ERR_CUDA;
     ready[dev].store(1, std::memory_order_release);
@@ -228,12 +238,12 @@ int launch_heads(const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap
   // rows behind a short box of A, which its MMAs read, and the epilogue's 32
   // rows x 64 columns a warp stay within the stages or the room behind them.
   constexpr int BARS = 8 * (2 * MAX_STAGES + 2);
-  g.stage_bytes = (g.box_rows + g.nc) * 128;
+  g.stage_bytes = (MT * g.box_rows + g.nc) * 128;
   g.stages = std::min(C::KBLOCKS, (C::MAX_SMEM - 1024 - BARS) / g.stage_bytes);
-  const int warps = std::min(4, (g.box_rows + 31) / 32);  // of the epilogue, with rows to store
+  const int warps = MT * std::min(4, (g.box_rows + 31) / 32);  // pieces of the epilogue
   g.bars = std::max({g.stages * g.stage_bytes, (g.stages - 1) * g.stage_bytes + A_BYTES,
                      warps * (C::MAX_NC / 64) * 4096});
-  return launch_chained(head_gemm_kernel<EXPAND>, dim3(C::N / g.nc, (g.T + TM - 1) / TM, g.H),
+  return launch_chained(head_gemm_kernel<EXPAND, MT>, dim3(C::N / g.nc, (g.T + MT * TM - 1) / (MT * TM), g.H),
                         THREADS, 1024 + g.bars + BARS, 1, s,
                         EXPAND ? "expand_kernel" : "absorb_kernel", ta, tw, to, g);
 }
@@ -261,14 +271,20 @@ int launch_absorb_tc(const mla_dims_t &d, const void *q, int T, const void *w, i
       !make_tmap_2d_16(&to, false, q_latent, uint64_t(H) * LP, T, uint64_t(H) * LP * 2, 64, 32,
                        true))
     return MLA_ERR_CUDA;
-  return launch_heads<false>(ta, tw, to, g, s);
+  return launch_heads<false, 1>(ta, tw, to, g, s);
 }
 
 int launch_expand_tc(const mla_dims_t &d, const void *o_latent, int T, const void *w, void *out,
                      cudaStream_t s) {
   using namespace sm103;
   const int H = d.num_heads;
-  HeadArgs g{nullptr, nullptr, T, H, pick_nc(T, H, HEAD), std::min(TM, (T + 7) / 8 * 8)};
+  // two tiles of tokens a CTA where one each would not fit the GPU at once: the
+  // weights come once for both (500 tokens 20.2 -> 18.7 us, 1000 36.0 -> 32.8;
+  // absorb, whose contraction is short, gains nothing: 26.4 -> 27.4)
+  const int nc = pick_nc(T, H, HEAD);
+  const int64_t tiles = int64_t((T + TM - 1) / TM) * H;
+  const bool two = nc == 128 && T > TM && tiles > Cfg<true>::CTAS * num_sms();
+  HeadArgs g{nullptr, nullptr, T, H, nc, std::min(TM, (T + 7) / 8 * 8)};
   CUtensorMap ta, tw, to;
   if (!make_tmap_2d_16(&ta, false, o_latent, uint64_t(H) * LAT, T, uint64_t(H) * LAT * 2, 64,
                        g.box_rows, true) ||
@@ -276,7 +292,7 @@ int launch_expand_tc(const mla_dims_t &d, const void *o_latent, int T, const voi
       !make_tmap_2d_16(&to, false, out, uint64_t(H) * HEAD, T, uint64_t(H) * HEAD * 2, 64, 32,
                        true))
     return MLA_ERR_CUDA;
-  return launch_heads<true>(ta, tw, to, g, s);
+  return two ? launch_heads<true, 2>(ta, tw, to, g, s) : launch_heads<true, 1>(ta, tw, to, g, s);
 }
 
 int heads_take_errors() { return sm103::take_error_flags_here(); }
