@@ -9,12 +9,14 @@
 // Every value is read once and written once (the row twice, when the dense
 // copy is asked for), so the kernel is bound by HBM when there are many
 // tokens and by the chain of dependent loads (sequence, length, block id)
-// when there are few.  (Reading the row and the first queries before that chain
-// is walked gains nothing for 16 tokens and makes 8192 take 60.5 us.)  A block
-// serves one token: warp 0 of its first block the row, all other threads the
-// heads of the queries, each the same columns (and angles) of several heads.
-// Few tokens spread their heads over several blocks.
-// Measured, 128 heads, bf16: 8192 tokens (299 MB) 55.2 us, 5.4 TB/s or 80% of
+// when there are few.  Many tokens live on warps in flight, that is on few
+// registers: reading two heads at once takes 62 us where this takes 53.6, rows
+// and queries before the sequence is known 60.5, one kernel for both orders of
+// the rotation 55.0; nothing of it changes 16 tokens' time.  A block serves one
+// token: warp 0 of its first block the row, all other threads the heads of the
+// queries, each the same columns (and angles) of several heads.  Few tokens
+// spread their heads over several blocks.
+// Measured, 128 heads, bf16: 8192 tokens (299 MB) 53.6 us, 5.6 TB/s or 82% of
 // copy bandwidth, the queries' rope columns being 128 of every 384 bytes; 16
 // tokens 4.1 us in a graph.
 #include "common.cuh"
@@ -22,8 +24,8 @@
 namespace mla {
 namespace {
 
-// Of a block.  8192 tokens with 2, 3, 4, 5, 8, 16 warps: 61, 55.3, 54.6, 54.9,
-// 67, 113 us.
+// Of a block.  8192 tokens with 2, 3, 5, 8, 16 warps took 12, 1, 1, 23 and 107%
+// longer.
 constexpr int WARPS = 4;
 
 struct AppendArgs {
@@ -119,7 +121,7 @@ __device__ __forceinline__ void rotate_piece(Piece<T> &x, Piece<T> &y, const flo
   }
 }
 
-template <typename T>
+template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
   constexpr int N = Piece<T>::N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
       }
     } else {
       for (int j = lane; j < a.P / 2; j += 32)
-        rotate_pair<T>(x + a.L, p0, p1, rope, a.P, j, a.interleaved);
+        rotate_pair<T>(x + a.L, p0, p1, rope, a.P, j, INTERLEAVED);
     }
     return;
   }
@@ -225,12 +227,12 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
   T *qo = static_cast<T *>(a.q_pe) + int64_t(t) * a.H * a.q_pe_ld;
   if (a.vec_q) {
     // a thread has columns k of heads qh, qh + q_step, ...
-    const int units = a.P / (a.interleaved ? N : 2 * N);  // of a head, as pieces
+    const int units = a.P / (INTERLEAVED ? N : 2 * N);  // of a head, as pieces
     const int q_step = q_threads / units, k = q_tid % units, qh = h0 + q_tid / units;
     if (q_tid >= q_step * units || qh >= h1) return;
     // the angles of this thread's columns, for all of its heads
     constexpr int NA = N;
-    const int n_ang = a.interleaved ? N / 2 : N;
+    const int n_ang = INTERLEAVED ? N / 2 : N;
     float c[NA], sn[NA];
 #pragma unroll
     for (int e = 0; e < NA; e += 2)  // (the table's rows are 8-byte aligned here)
@@ -248,10 +250,10 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
       T *dst = qo + h * a.q_pe_ld + k * N;
       Piece<T> px, py;
       px.load(src);
-      if (!a.interleaved) py.load(src + y_off);
-      rotate_piece<T>(px, py, c, sn, a.interleaved);
+      if (!INTERLEAVED) py.load(src + y_off);
+      rotate_piece<T>(px, py, c, sn, INTERLEAVED);
       px.store(dst);
-      if (!a.interleaved) py.store(dst + y_off);
+      if (!INTERLEAVED) py.store(dst + y_off);
     }
     return;
   }
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(32 * WARPS) append_kernel(AppendArgs a) {
   for (int u = q_tid; u < (h1 - h0) * per_head; u += q_threads) {
     const int h = h0 + u / per_head, j = u % per_head;
     if (rope)
-      rotate_pair<T>(q + int64_t(h) * qk, qo + h * a.q_pe_ld, nullptr, rope, a.P, j, a.interleaved);
+      rotate_pair<T>(q + int64_t(h) * qk, qo + h * a.q_pe_ld, nullptr, rope, a.P, j, INTERLEAVED);
     else
       qo[h * a.q_pe_ld + j] = q[int64_t(h) * qk + j];
   }
@@ -293,8 +295,10 @@ int launch_append(const mla_dims_t &d, const void *kv_a, int64_t kv_a_ld, const 
   if (ys > most) ys = most;
   const dim3 grid(T, ys);
   const int threads = q ? 32 * WARPS : 32;
-  auto *kernel =
-      d.dtype == MLA_DTYPE_BF16 ? append_kernel<__nv_bfloat16> : append_kernel<float>;
+  auto *kernel = d.dtype == MLA_DTYPE_BF16
+                     ? (interleaved ? append_kernel<__nv_bfloat16, true>
+                                    : append_kernel<__nv_bfloat16, false>)
+                     : (interleaved ? append_kernel<float, true> : append_kernel<float, false>);
   return launch_chained(kernel, grid, threads, 0, 1, s, "append_kernel", a);
 }
 
