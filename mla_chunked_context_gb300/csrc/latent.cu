@@ -5,7 +5,10 @@
 //  * head_gemm_simt: per head h, C[t, n] = sum_k A[t, k] B(k, n): the query
 //    absorption (B = W_uk[h], n contiguous) and the output expansion (B =
 //    W_uv[h]^T, k contiguous); 64x64 shared-memory tiles, 4x4 outputs a
-//    thread.
+//    thread, 32 of the contraction a step, the next step's loads in flight
+//    meanwhile; the first column block copies the rope columns.  (16 a step,
+//    loaded when needed: expansion of 500 tokens, 40 heads of 64 -> 32 14.4 us,
+//    so 10.0; of one token 5.9 and 4.1.)
 //  * latent_attn_simt: one block per (new token, head).  A group of G lanes
 //    takes a key at a time (U keys in flight), each lane NC 16-byte pieces of
 //    its row, so that a score costs log2 G shuffles and its weight needs none;
@@ -18,7 +21,7 @@
 namespace mla {
 namespace {
 
-constexpr int GT = 64, GK = 16;
+constexpr int GT = 64, GK = 32;
 
 struct HeadGemm {
   const void *a, *b;
@@ -27,6 +30,7 @@ struct HeadGemm {
   int64_t b_k, b_n, b_head;    // strides of B
   int64_t c_row, c_head;
   int M, N, K;
+  int rope;  // columns of A behind its K that go to C behind its N
 };
 
 template <typename T>
@@ -41,17 +45,30 @@ __global__ void __launch_bounds__(256) head_gemm_simt(HeadGemm g) {
   const T *B = static_cast<const T *>(g.b) + h * g.b_head;
   T *C = static_cast<T *>(g.c) + h * g.c_head;
   float acc[4][4] = {};
-  for (int k0 = 0; k0 < g.K; k0 += GK) {
-    for (int e = threadIdx.x; e < GT * GK; e += 256) {
-      const int r = e / GK, k = e % GK;
-      As[k][r] = (m0 + r < g.M && k0 + k < g.K) ? to_f32(A[(m0 + r) * g.a_row + k0 + k]) : 0.f;
+  // the next step's elements come while this one is multiplied
+  constexpr int NE = GT * GK / 256;
+  float va[NE], vb[NE];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = i * 256 + threadIdx.x, r = e / GK, k = e % GK;
+      va[i] = (m0 + r < g.M && k0 + k < g.K) ? to_f32(A[(m0 + r) * g.a_row + k0 + k]) : 0.f;
       // walk B along its contiguous dimension
       const int rb = g.b_n == 1 ? e % GT : r, kb = g.b_n == 1 ? e / GT : k;
-      Bs[kb][rb] = (n0 + rb < g.N && k0 + kb < g.K)
-                       ? to_f32(B[(k0 + kb) * g.b_k + (n0 + rb) * g.b_n])
-                       : 0.f;
+      vb[i] = (n0 + rb < g.N && k0 + kb < g.K) ? to_f32(B[(k0 + kb) * g.b_k + (n0 + rb) * g.b_n])
+                                               : 0.f;
+    }
+  };
+  load(0);
+  for (int k0 = 0; k0 < g.K; k0 += GK) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = i * 256 + threadIdx.x, r = e / GK, k = e % GK;
+      As[k][r] = va[i];
+      Bs[g.b_n == 1 ? e / GT : k][g.b_n == 1 ? e % GT : r] = vb[i];
     }
     __syncthreads();
+    if (k0 + GK < g.K) load(k0 + GK);
 #pragma unroll
     for (int k = 0; k < GK; ++k) {
       float a[4], b[4];
@@ -67,6 +84,11 @@ __global__ void __launch_bounds__(256) head_gemm_simt(HeadGemm g) {
     }
     __syncthreads();
   }
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e < GT * g.rope; e += 256) {
+      const int m = m0 + e / g.rope, k = e % g.rope;
+      if (m < g.M) C[m * g.c_row + g.N + k] = A[m * g.a_row + g.K + k];
+    }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -74,17 +96,6 @@ __global__ void __launch_bounds__(256) head_gemm_simt(HeadGemm g) {
       const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
       if (m < g.M && n < g.N) C[m * g.c_row + n] = from_f32<T>(acc[i][j]);
     }
-}
-
-// q_latent[row, L:L+P) = q[row, Dn:Dn+P) over rows (token, head)
-template <typename T>
-__global__ void __launch_bounds__(256) copy_rope_columns(const T *q, T *o, int64_t rows, int q_ld,
-                                                         int q_off, int o_ld, int o_off, int P) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= rows * P) return;
-  const int64_t row = i / P;
-  const int k = int(i % P);
-  o[row * o_ld + o_off + k] = q[row * q_ld + q_off + k];
 }
 
 struct LatentArgs {
@@ -285,22 +296,8 @@ int launch_absorb_simt(const mla_dims_t &d, const void *q, int T, const void *w,
   const int L = d.kv_lora_rank, P = d.qk_rope_dim, Dn = d.qk_nope_dim, H = d.num_heads;
   const int QK = Dn + P, LP = L + P;
   HeadGemm g{q, w, q_latent, int64_t(H) * QK, QK, L, 1, int64_t(Dn + d.v_dim) * L,
-             int64_t(H) * LP, LP, T, L, Dn};
-  const bool bf = d.dtype == MLA_DTYPE_BF16;
-  int rc = bf ? head_gemm<__nv_bfloat16>(g, H, s) : head_gemm<float>(g, H, s);
-  if (rc || !rope_columns || P == 0) return rc;
-  const int64_t rows = int64_t(T) * H;
-  const unsigned blocks = unsigned((rows * P + 255) / 256);
-  launch_begin(s);
-  if (bf)
-    copy_rope_columns<<<blocks, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(q),
-                                             static_cast<__nv_bfloat16 *>(q_latent), rows, QK, Dn,
-                                             LP, L, P);
-  else
-    copy_rope_columns<<<blocks, 256, 0, s>>>(static_cast<const float *>(q),
-                                             static_cast<float *>(q_latent), rows, QK, Dn, LP, L,
-                                             P);
-  return launch_status(s, "copy_rope_columns");
+             int64_t(H) * LP, LP, T, L, Dn, rope_columns ? P : 0};
+  return d.dtype == MLA_DTYPE_BF16 ? head_gemm<__nv_bfloat16>(g, H, s) : head_gemm<float>(g, H, s);
 }
 
 int launch_expand_simt(const mla_dims_t &d, const void *o_latent, int T, const void *w, void *out,
@@ -308,7 +305,7 @@ int launch_expand_simt(const mla_dims_t &d, const void *o_latent, int T, const v
   const int L = d.kv_lora_rank, Dn = d.qk_nope_dim, Dv = d.v_dim, H = d.num_heads;
   const int64_t off = int64_t(Dn) * L * elem_bytes(d.dtype);
   HeadGemm g{o_latent, static_cast<const char *>(w) + off, out, int64_t(H) * L, L, 1, L,
-             int64_t(Dn + Dv) * L, int64_t(H) * Dv, Dv, T, Dv, L};
+             int64_t(Dn + Dv) * L, int64_t(H) * Dv, Dv, T, Dv, L, 0};
   return d.dtype == MLA_DTYPE_BF16 ? head_gemm<__nv_bfloat16>(g, H, s) : head_gemm<float>(g, H, s);
 }
 
