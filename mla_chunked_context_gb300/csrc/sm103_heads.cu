@@ -87,8 +87,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<EXPAND>::CTAS)
     prefetch_map(&tm_w);
     prefetch_map(&tm_o);
   }
-  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), cols);
-  chain_release();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), cols);
+    chain_release();  // (not before: a later kernel's CTA could take the columns and wait for us)
+  }
   if (warp == 0 && lane == 0) {
     // the weights on their way to L2 while the kernels before this one finish
     for (int k = 0; k < C::K; k += 64) {

@@ -552,10 +552,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
     else
       tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    chain_release();  // (not before: a later kernel's CTA could take the columns and wait for us)
   }
   tc_fence_before();
   if (PAIR) cluster_arrive();  // both CTAs' barriers exist before any load or arrive
-  chain_release();
   chain_wait();
   find_share<PAIR>(a, cluster, clusters, share, scan);  // (ends with a barrier)
   if (PAIR) cluster_wait();

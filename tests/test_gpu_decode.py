@@ -886,3 +886,39 @@ def test_absorb_and_expand_tile_edges(T, H):
             within(f64(g), ref, unit(dims.dtype) * np.abs(ref) + (K + 4) * F * (np.abs(a) @ np.abs(b)),
                    f"head {h}")
     assert torch.equal(got[..., 512:].cpu(), q[..., 128:])
+
+
+@pytest.mark.parametrize("T", [1, 16, 300, 500])
+def test_chained_calls_back_to_back(T):
+    """Absorptions, expansions and attentions enqueued one after another, whose
+    blocks may be resident beside each other's, give what each gives alone."""
+    rng = np.random.default_rng(T)
+    H = 128
+    dims, od = make_dims(LARGE, H, 64, "bf16")
+    q = normal(rng, T, H, 192, dtype=dims.dtype).to(DEV)
+    w = normal(rng, H * 256, 512, std=0.1, dtype=dims.dtype).to(DEV)
+    q_small = q[:1].contiguous()
+    cache, table = make_cache(rng, [200] * T if T < 20 else [64] * T, 64, 576, dims.dtype)
+    cache, table = torch.nan_to_num(cache).to(DEV), table.to(DEV)
+    lens, qsl = i32([200] * T if T < 20 else [64] * T), i32(range(T + 1))
+    ws = torch.empty(M.mla_latent_attn_workspace_bytes(dims, T, T), dtype=torch.uint8, device=DEV)
+
+    def step(sync):
+        ql, small = torch.zeros(T, H, 576, dtype=dims.dtype, device=DEV), torch.zeros(1, H, 576, dtype=dims.dtype, device=DEV)
+        ol, out = torch.zeros(T, H, 512, dtype=dims.dtype, device=DEV), torch.zeros(T, H, 128, dtype=dims.dtype, device=DEV)
+        torch.cuda.synchronize()
+        for _ in range(1 if sync else 5):
+            for f in (lambda: M.mla_absorb_query(dims, q, w, ql),
+                      lambda: M.mla_latent_attn(dims, True, qsl, lens, ql, cache, table, ws, ol),
+                      lambda: M.mla_expand_output(dims, ol, w, out),
+                      lambda: M.mla_absorb_query(dims, q_small, w, small)):
+                f()
+                if sync:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return ql, ol, out, small
+
+    alone = step(True)
+    for _ in range(4):
+        for x, y in zip(step(False), alone):
+            assert torch.equal(x, y)
