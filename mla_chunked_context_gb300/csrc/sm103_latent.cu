@@ -82,11 +82,13 @@ struct Cfg {
   static constexpr int SMEM = 232448;  // all of it; the rest is room for alignment
 };
 // Work split, in positions of a tile.  UNIT_COST: what a unit costs beyond its
-// tiles (queries in, rows out: about 5000 clocks, a tile taking 1700 to 3400).
+// tiles (queries in, first scores, rows out: 5000 to 8000 clocks, a tile taking
+// 2000 to 3400).  31 short sequences beside one of 131072 keys took 55.3, 48.3,
+// 47.4 and 47.6 us with 2, 3, 4 and 5 in the pair form.
 // MIN_SHARE: the least that a share is worth; shorter ones cost more in scratch
 // traffic and joining than they save.
 template <bool PAIR>
-constexpr int UNIT_COST = PAIR ? 3 : 2;
+constexpr int UNIT_COST = PAIR ? 4 : 2;
 constexpr int MIN_SHARE = 4;
 // A cut costs another UNIT_COST and the joining, some 10 tiles' time of the
 // whole GPU when it is the only one.  So: no cut nearer than SNAP to a unit's
