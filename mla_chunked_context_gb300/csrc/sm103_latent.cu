@@ -1297,7 +1297,8 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
                static_cast<__nv_bfloat16 *>(o), lse, part_o, part_lse,
                static_cast<int4 *>(desc), status, T, R, d.num_heads, d.block_size, num_blocks,
                int(cache_rows), bt_stride, causal, box_log2,
-               reinterpret_cast<uintptr_t>(o) % 32 == 0, Divider(d.block_size), Divider(d.num_heads), d.softmax_scale * 1.4426950408889634f};
+               reinterpret_cast<uintptr_t>(o) % 32 == 0, Divider(d.block_size),
+               Divider(d.num_heads), d.softmax_scale * 1.4426950408889634f};
   // rows of an average sequence beyond one CTA's 64: pairs
   if (int64_t(T) * d.num_heads > int64_t(64) * R) return launch_latent<true>(maps, a, max_ctas, s);
   return launch_latent<false>(maps, a, max_ctas, s);
