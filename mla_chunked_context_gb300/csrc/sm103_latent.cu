@@ -45,6 +45,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "row_join.h"
 #include "sm103.cuh"
 
 namespace mla {
@@ -783,12 +784,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t s_empty_lead = lead(s_empty), p_full_lead = lead(p_full);
     if (tid == 0 && rank == 0) a.desc[2 * cluster] = make_int4(0, 0, 0, 0);
-    // the value of the four threads of a row, by f
-    auto row_join = [&](float *x, float v, auto f) {
-      x[tid] = v;
-      softmax_barrier();
-      return f(f(v, x[tid ^ 64]), f(x[tid ^ 128], x[tid ^ 192]));
-    };
+    // the tiles' maxima and the pieces' sums, over the four threads of a row
+    RowJoin<STHREADS> row_join(xmax, tid);
+    auto barrier = [] { softmax_barrier(); };
     Walk<PAIR> w(a, *share);
     int g = 0;
     bool ok = true;
@@ -826,7 +824,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
         for (int c = 0; c < NC; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-        const float mt = row_join(xmax + sb * 256, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+        const float mt = row_join(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), barrier,
                                   [](float x, float y) { return fmaxf(x, y); }) *
                          a.scale_log2;
         // the threads of a row see the same maxima and decide alike
@@ -903,7 +901,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!ok) break;
       // ---- the piece's rows
-      l = row_join(xmax + (g & 1) * 256, l, [](float x, float y) { return x + y; });
+      l = row_join(l, barrier, [](float x, float y) { return x + y; });
       const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const float lse2 = l > 0.f || l != l ? mref + log2f(l) : neg_inf();
