@@ -511,8 +511,9 @@ int mla_chunked_prefill_equal_window(
  * it in the absorbed form (the queries are taken into the latent space, keys
  * and values are the cache rows themselves, nothing is up-projected).  One
  * decode step of a layer is, in order,
- *   mla_append_latent    new rows -> cache (norm, rotation), q_pe rotated
- *   mla_absorb_query     q -> q_latent
+ *   mla_absorb_query     q -> q_latent, rope columns as they are
+ *   mla_append_latent    new rows -> cache (norm, rotation), q_latent's rope
+ *                        columns rotated
  *   mla_latent_attn      q_latent x cache -> o_latent, LSE
  *   mla_expand_output    o_latent -> O
  * mla_append_latent also prepares a prefill: it fills the cache, and its
@@ -558,7 +559,8 @@ int mla_chunked_prefill_equal_window(
  *              the result starts at q_pe_out + (t*H + h) * q_pe_ld elements,
  *              q_pe_ld >= P.  q_pe_out = q + Dn with q_pe_ld = Dn+P rotates in
  *              place; q_pe_out = q_latent + L with q_pe_ld = L+P writes the
- *              rope columns of the absorbed queries.
+ *              rope columns of the absorbed queries (those of a skipped
+ *              token stay what mla_absorb_query copied there before).
  *   Arithmetic is float32, rounded once to dtype.  A token with a negative
  *   cache position (more new tokens than seq_lens) is skipped like a row of
  *   no sequence.  kv_cache must not overlap the inputs, new_latent not kv_a.
@@ -579,7 +581,7 @@ int mla_append_latent(const mla_dims_t *d, const void *kv_a, int64_t kv_a_ld,
 
 /* mla_absorb_query: q_latent[t, h, 0:L) = sum_d q[t, h, d] w_kv_b[h*(Dn+Dv)+d]
  *   over the Dn nope columns; with rope_columns = 1 also q_latent[t, h, L:L+P)
- *   = q[t, h, Dn:Dn+P) (0: left as they are, for mla_append_latent to write).
+ *   = q[t, h, Dn:Dn+P) (0: left as they are).
  *   q device [T, H, Dn+P], w_kv_b device [H*(Dn+Dv), L], q_latent device
  *   [T, H, L+P], all in dtype; float32 sums, rounded once.
  * mla_expand_output: out[t, h, v] = sum_l o_latent[t, h, l] w_kv_b[h*(Dn+Dv)

@@ -73,7 +73,7 @@ class ChunkedPrefill:
 class LatentDecode:
     """Holds the absorbed queries, latent outputs and workspace for decode
     steps of up to max_tokens new tokens and max_seqs sequences, and runs a
-    layer's step on them: append to the cache, absorb the queries, attend,
+    layer's step on them: absorb the queries, append to the cache, attend,
     expand.  The lengths are read on the device, so one captured step can be
     replayed as they grow.  One instance serves one step at a time."""
 
@@ -92,17 +92,23 @@ class LatentDecode:
                  interleaved=False, causal=True, dev_status=None, stream=None):
         """q [T, H, Dn+P] before rotation, kv_a [T, L+P] before norm and
         rotation; out [T, H, Dv], lse [H, T].  Rows of no sequence are left
-        out of the cache; what out holds for them is not specified."""
+        out of the cache; what out holds for them is not specified.  A token
+        that the append skips (a rope position outside the table, more new
+        tokens than seq_lens says) attends with its rope columns unrotated,
+        and its cache slot keeps what it held: pass dev_status to learn of
+        positions outside the table."""
         T, dims = q.shape[0], self.dims
         if T > self.max_tokens or seq_lens.shape[0] > self.max_seqs:
             raise ValueError(f"LatentDecode: {T} tokens of {seq_lens.shape[0]} sequences, room "
                              f"for {self.max_tokens} of {self.max_seqs}")
         q_lat, o_lat = self.q_latent[:T], self.o_latent[:T]
+        # The rope columns come with the absorption first, so that a token that
+        # the append skips has its own there and not an earlier step's.
+        mla_absorb_query(dims, q, w_kv_b, q_lat, stream=stream)
         mla_append_latent(dims, kv_a, query_start_loc, seq_lens, rope_table, kv_cache,
                           block_table, norm_weight, norm_eps, positions, interleaved, q=q,
                           q_pe_out=q_lat[..., dims.kv_lora_rank:], dev_status=dev_status,
                           stream=stream)
-        mla_absorb_query(dims, q, w_kv_b, q_lat, rope_columns=False, stream=stream)
         mla_latent_attn(dims, causal, query_start_loc, seq_lens, q_lat, kv_cache, block_table,
                         self.workspace, o_lat, lse, dev_status, stream)
         mla_expand_output(dims, o_lat, w_kv_b, out, stream)
