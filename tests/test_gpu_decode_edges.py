@@ -65,3 +65,89 @@ def test_step_with_tokens_that_are_not_appended(shape, dtype, H):
         assert torch.equal(out, other[0]) and torch.equal(lse, other[1])
     _, rl, _, size = O.latent_attention(f64(q_lat), f64(c), table.numpy(), qsl, lens, od, False)
     within(f64(lse), rl, (L + P + 8) * F * size + 2.0 ** -22 + (70 / 8 + 16) * F + F * np.abs(rl), "lse")
+
+
+# ------------------------------------------ invalid blocks, in both forms --
+@pytest.mark.parametrize("bs", [1, 8, 16, 32, 64])
+@pytest.mark.parametrize("H", [128, 40, 8])
+def test_bad_blocks_beside_rows_that_are_not_finite(H, bs):
+    """Bad block ids in the middle of sequences, in a tile of which the new
+    tokens see different parts, and among those parts; in the same tiles rows
+    that are not finite and that only some tokens see.  (128 and 40 heads of
+    these tokens are more than 64 rows a sequence, the form of two blocks.)"""
+    rng = np.random.default_rng(H + bs)
+    dims, od = make_dims(LARGE, H, bs, "bf16")
+    lens, ql = [300, 130, 700, 90], [4, 4, 1, 2]
+    qsl = loc(ql)
+    cache, table = make_cache(rng, lens, bs, 576, dims.dtype)
+    q = normal(rng, qsl[-1], H, 576, std=0.4, dtype=dims.dtype)
+    bad = table.clone()
+    bad[0, (272 if bs <= 16 else 192) // bs] = cache.shape[0]      # beside the first's new tokens
+    bad[1, 128 // bs] = -1                                         # two of the second's are in it
+    for j in (130, 131, 400):
+        bad[2, j // bs] = 2 ** 31 - 1
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o, lse = run_attn(dims, True, qsl, lens, q, cache, bad, status=status)
+    assert status.item() == M.MLA_STATUS_BAD_BLOCK
+    zero = torch.cat([cache, torch.zeros_like(cache[:1])])
+    ztab = bad.clone()
+    ztab[(ztab < 0) | (ztab > len(cache))] = len(cache)
+    check_attn(dims, od, True, qsl, lens, q, zero, ztab, o, lse)
+    wild = cache.clone()
+    for r, j in ((0, 298), (1, 127), (3, 89)):                     # the third or the last new token's
+        wild[table[r, j // bs], j % bs] = math.nan
+    o2, lse2 = run_attn(dims, True, qsl, lens, q, wild, bad, status=status)
+    for t in range(qsl[-1]):
+        if t in (0, 1, 4, 8, 9):                                   # those that do not see them
+            assert torch.equal(o2[t], o[t]) and torch.equal(lse2[:, t], lse[:, t]), t
+        else:
+            assert torch.isnan(o2[t]).all() and torch.isnan(lse2[:, t]).all(), t
+
+
+@pytest.mark.parametrize("H,T", [(128, 1), (128, 3), (40, 2)])
+def test_no_blocks_in_the_form_of_two_blocks(H, T):
+    """A cache of no blocks: scores 0, output 0, the log-sum ln n."""
+    import ctypes as C
+    dims, _ = make_dims(LARGE, H, 16, "bf16")
+    d = dims.c()
+    cache = torch.ones(2, 16, 576, dtype=dims.dtype, device=DEV)
+    q = torch.ones(T, H, 576, dtype=dims.dtype, device=DEV)
+    o = torch.full((T, H, 512), 7.0, dtype=dims.dtype, device=DEV)
+    lse, table = torch.zeros(H, T, device=DEV), torch.zeros(1, 8, dtype=torch.int32, device=DEV)
+    ws = torch.empty(M.mla_latent_attn_workspace_bytes(dims, T, 1), dtype=torch.uint8, device=DEV)
+    status, qsl, lens = i32([0]), i32([0, T]), i32([100])
+    rc = M.lib().mla_latent_attn(
+        C.byref(d), 0, 1, qsl.data_ptr(), lens.data_ptr(), T, q.data_ptr(), cache.data_ptr(), 0,
+        table.data_ptr(), 8, ws.data_ptr(), ws.numel(), o.data_ptr(), lse.data_ptr(),
+        status.data_ptr(), None)
+    torch.cuda.synchronize()
+    assert rc == 0 and status.item() == M.MLA_STATUS_BAD_BLOCK and (o == 0).all()
+    # as in test_gpu_decode.py: the sum is exact, log2f and ln 2 are rounded
+    within(f64(lse), np.full((H, T), math.log(100)), 2.0 ** -21 * 0.7 + 6.7 * 2.0 ** -25 + 2.0 ** -22,
+           "lse")
+
+
+@pytest.mark.parametrize("bs", [64, 8])
+def test_far_offsets_in_the_form_of_two_blocks(bs):
+    """Cache rows beyond 2^31 elements and 2^32 bytes, of two new tokens, the
+    second's not finite."""
+    dims, od = make_dims(LARGE, 128, bs, "bf16")
+    blocks = 64000 * 64 // bs
+    cache = torch.zeros(blocks, bs, 576, dtype=torch.bfloat16, device=DEV)
+    rng = np.random.default_rng(bs)
+    lens, qsl = [200], [0, 2]
+    small, table = make_cache(rng, lens, bs, 576, dims.dtype, spare=0)
+    far = blocks - 1 - torch.arange(len(small))
+    cache[far.to(DEV)] = small.to(DEV)
+    q = normal(rng, 2, 128, 576, std=0.4, dtype=dims.dtype)
+    need = -(-200 // bs)
+    ftab = table.clone()
+    ftab[0, :need] = far[table[0, :need].long()].int()
+    o, lse = run_attn(dims, True, qsl, lens, q, cache, ftab)
+    cache[int(ftab[0, 199 // bs]), 199 % bs] = math.inf
+    o2, lse2 = run_attn(dims, True, qsl, lens, q, cache, ftab)
+    del cache
+    check_attn(dims, od, True, qsl, lens, q, small, table, o, lse)
+    assert torch.equal(o2[0], o[0]) and torch.equal(lse2[:, 0], lse[:, 0])
+    score = f64(q[1]) @ np.full(576, np.inf)                       # inf - inf: NaN
+    assert np.isnan(score).all() and torch.isnan(o2[1]).all()
