@@ -969,7 +969,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
   // Every MMA has completed; and in the pair neither CTA leaves while the other
-  // may still arrive here.
+  // may still arrive here.  (The odd CTA's warp 2 has issued nothing: its wait,
+  // limited as all are, begins when the others' work ends, not the kernel.)
+  if (rank != 0) __syncthreads();
   if (warp == 2) mbar_wait(done, 0);
   tc_fence_before();
   if (PAIR) {  // (a release would wait for the rows' way to L2)

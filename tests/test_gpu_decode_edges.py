@@ -151,3 +151,27 @@ def test_far_offsets_in_the_form_of_two_blocks(bs):
     assert torch.equal(o2[0], o[0]) and torch.equal(lse2[:, 0], lse[:, 0])
     score = f64(q[1]) @ np.full(576, np.inf)                       # inf - inf: NaN
     assert np.isnan(score).all() and torch.isnan(o2[1]).all()
+
+
+# ------------------------------------------------------------ long calls --
+def test_seconds_of_work_are_no_timeout():
+    """A call of some three seconds (4096 tokens over 3.2 million keys, a few
+    pages again and again) is right, and no wait of it counts as given up: what
+    a barrier's wait is limited by is one step of the pipeline, not the call."""
+    rng = np.random.default_rng(31)
+    H, T, blocks, times = 128, 4096, 5, 10000
+    dims, od = make_dims(LARGE, H, 64, "bf16")
+    n = 64 * blocks * times
+    cache = normal(rng, blocks, 64, 576, dtype=dims.dtype)
+    table = torch.arange(blocks, dtype=torch.int32).repeat(times)[None]
+    q = (0.4 * torch.randn(T, H, 576, device=DEV)).to(dims.dtype)
+    o, lse = run_attn(dims, False, [0, T], [n], q, cache, table)
+    assert M.mla_device_error_flags() == 0
+    for t in (0, 1777, T - 1):
+        ro, rl, mass, size = O.latent_attention(f64(q[t:t + 1]), f64(cache), np.arange(blocks)[None],
+                                                [0, 1], [64 * blocks], od, False)
+        E = (512 + 64 + 8) * F * size + 2.0 ** -22
+        rl = rl + math.log(times)
+        within(f64(lse[:, t:t + 1]), rl, E + (n / 8 + 16) * F + F * np.abs(rl), "lse")
+        u = torch.finfo(dims.dtype).eps / 2
+        within(f64(o[t:t + 1]), ro, u * np.abs(ro) + (2 * E.T[:, :, None] + (n / 8 + 64) * F + u) * mass, "o")
