@@ -544,8 +544,12 @@ def _native():
         try:
             from . import _decode as module
         except ImportError as e:
-            raise ImportError("the decode calls' binding (_decode.so) is missing or not loadable: "
+            raise ImportError("the decode calls' binding (_decode) is missing or not loadable: "
                               "build it with mla_chunked_context_gb300.build.build()") from e
+        if module.built_for != torch.__version__:
+            raise ImportError(f"the decode calls' binding is built for PyTorch {module.built_for}, "
+                              f"this is {torch.__version__}: build it again with "
+                              "mla_chunked_context_gb300.build.build()")
         _decode = module
     return _decode
 

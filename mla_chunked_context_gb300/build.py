@@ -4,8 +4,11 @@ Every translation unit under ``csrc/`` is compiled in parallel to an object
 under ``_build/``; the objects are linked into
 ``mla_chunked_context_gb300/libmla_gb300.so`` (CUDA runtime linked statically,
 so the library loads on a machine without a GPU).  ``csrc/py_decode.cpp``, the
-decode calls' Python binding, becomes the module ``_decode.so`` beside it, with
-the host compiler and the headers of Python and of the installed PyTorch.
+decode calls' Python binding, becomes the module ``_decode`` beside it (its file
+name says for which Python, its ``built_for`` for which PyTorch), with the host
+compiler and the headers of Python and of the installed PyTorch.  The library
+needs neither: ``build_library()`` makes it alone, and ``build()`` leaves it
+built where the module fails.
 """
 
 from __future__ import annotations
@@ -21,7 +24,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla_gb300.so")
-MODULE = os.path.join(HERE, "_decode.so")
+MODULE = os.path.join(HERE, "_decode" + sysconfig.get_config_var("EXT_SUFFIX"))
+HEADER = os.path.join(HERE, "..", "include", "mla_chunked_context.h")
 MODULE_SRC = os.path.join(CSRC, "py_decode.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -64,6 +68,7 @@ def _compile_module() -> str:
     obj = os.path.join(BUILD, os.path.basename(MODULE_SRC) + ".o")
     _run(f"compiling {MODULE_SRC}", [
         "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+        f'-DMLA_BUILT_FOR="{torch.__version__}"',
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
         "-I", os.path.join(HERE, "..", "include"), "-isystem", inc,
         "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
@@ -82,18 +87,36 @@ def _link_module(obj: str) -> None:
     os.replace(tmp, MODULE)
 
 
-def build(extra_flags=(), verbose: bool = False) -> str:
+def stale() -> bool:
+    """The library or the module is missing, or older than a source."""
+    srcs = [HEADER, *(os.path.join(CSRC, f) for f in os.listdir(CSRC))]
+    newest = max(os.path.getmtime(p) for p in srcs)
+    return any(not os.path.exists(p) or os.path.getmtime(p) < newest for p in (LIB, MODULE))
+
+
+def build_library(extra_flags=()) -> str:
+    """The C library alone."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        module = ex.submit(_compile_module)
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, list(extra_flags)), srcs))
-        module = module.result()
     tmp = LIB + ".tmp"
     _run("link", [nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp,
                   *objs])
     os.replace(tmp, LIB)
-    _link_module(module)
+    return LIB
+
+
+def build(extra_flags=(), verbose: bool = False) -> str:
+    """The library and the module, compiled side by side."""
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        module = ex.submit(_compile_module)
+        build_library(extra_flags)
+        _link_module(module.result())
+    untagged = os.path.join(HERE, "_decode.so")  # of a build before the name said for which Python
+    if os.path.exists(untagged):
+        os.remove(untagged)
     if verbose:
         print(f"built {LIB}")
     return LIB

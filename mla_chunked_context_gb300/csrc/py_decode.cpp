@@ -339,5 +339,7 @@ PyMODINIT_FUNC PyInit__decode() {
   for (int i = 0; i < 8; ++i)
     if (!(names.field[i] = PyUnicode_InternFromString(fields[i]))) return nullptr;
   if (!(names.cuda_stream = PyUnicode_InternFromString("cuda_stream"))) return nullptr;
-  return PyModule_Create(&module);
+  PyObject *m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", MLA_BUILT_FOR)) Py_CLEAR(m);
+  return m;
 }

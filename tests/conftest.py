@@ -13,6 +13,14 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: full-size parity case")
 
 
+@pytest.fixture(scope="session", autouse=True)
+def built():
+    """The library and the binding's module, neither older than a source."""
+    from mla_chunked_context_gb300 import build
+    if build.stale():
+        build.build()
+
+
 @pytest.fixture(scope="session")
 def golden_dir():
     return os.path.join(ROOT, "tests", "golden")
