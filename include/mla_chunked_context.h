@@ -608,7 +608,13 @@ int mla_expand_output(const mla_dims_t *d, const void *o_latent,
  *   (partial results of key ranges: one size for the tensor-core shape,
  *   whatever the batch; 0 bytes and NULL otherwise); nothing in it has to be
  *   initialised, and nothing in it is kept from call to call.
- *   Errors: MLA_ERR_UNSUPPORTED for L+P > 1024 off the tensor-core shape. */
+ *   Arithmetic is float32, rounded once to dtype, but for one more rounding on
+ *   the tensor-core shape: the weights e^(s_j - m) are rounded to bf16 for the
+ *   sum over c_j (not for the LSE or the sum that divides it), which adds at
+ *   most 2^-8 sum_j softmax(s)_j |c_j| to an output's error.
+ *   Errors: MLA_ERR_UNSUPPORTED for L+P > 1024 off the tensor-core shape, and
+ *   on it for a cache of 2^31 - 64 rows or more.  A call may hold 2^39 pieces of
+ *   64 keys x 64 rows (hours of work) and no more; that is not checked. */
 int mla_latent_attn_workspace_bytes(const mla_dims_t *d, int32_t num_tokens,
                                     int32_t num_seqs, size_t *bytes);
 int mla_latent_attn(const mla_dims_t *d, int32_t causal, int32_t num_seqs,

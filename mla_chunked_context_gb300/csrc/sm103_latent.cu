@@ -47,6 +47,7 @@
 
 #include "row_join.h"
 #include "sm103.cuh"
+#include "unit_sum.h"
 
 namespace mla {
 namespace sm103 {
@@ -206,41 +207,38 @@ struct Walk {
 
 // All threads: this cluster's share of the positions of all units.  Cluster c
 // of n starts at position c * share, moved to the end of a unit where one is
-// near.  (Sequences' units and positions are summed in one 64-bit scan, 24 and
-// 40 bits: there are at most 2^24 units, and 2^40 positions would take years.)
-constexpr int POS_BITS = 40;
+// near.  (Sequences' units and positions are summed in one 64-bit scan.)
 template <bool PAIR>
 __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int clusters,
-                                           Share *out, long long *scratch) {
+                                           Share *out, uint64_t *scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int NW = THREADS / 32;
-  constexpr long long MASK = (1LL << POS_BITS) - 1;
   int *most = reinterpret_cast<int *>(scratch + NW);  // [NW]
   int nrt, length;
   Seq s;
-  auto look = [&](int r) -> long long {
+  auto look = [&](int r) -> uint64_t {
     nrt = 0;
     length = 1;
     if (r >= a.R) return 0;
     s = load_seq<PAIR>(a, r);
     nrt = s.nrt;
     length = s.tiles + UNIT_COST<PAIR>;
-    return ((long long)nrt << POS_BITS) | ((long long)nrt * length);
+    return UnitSum::of(nrt, length);
   };
   // Gives a cluster whose share starts (or ends) in sequence r its part of it;
   // called by the thread that has the sequence, the positions up to its end
   // being sum.
-  auto deal = [&](int r, long long mine, long long sum, long long total, int longest) {
+  auto deal = [&](int r, uint64_t mine, uint64_t sum, uint64_t total, int longest) {
     if (nrt == 0) return;
-    const long long positions = total & MASK;
-    const int units = int(total >> POS_BITS);
+    const long long positions = UnitSum::positions(total);
+    const int units = UnitSum::units(total);
     // (64-bit divisions only where 32 bits do not hold the numbers)
     int share = positions <= 0x7fffffff
                     ? int((unsigned(positions) + clusters - 1) / unsigned(clusters))
                     : int(min((positions + clusters - 1) / clusters, 0x7fffffffLL));
-    const long long lo = (sum - mine) & MASK, hi = sum & MASK;
+    const long long lo = UnitSum::positions(sum - mine), hi = UnitSum::positions(sum);
     if (units <= clusters && longest <= share + WHOLE_SLACK) {
-      const int u = cluster - int((sum - mine) >> POS_BITS);  // of this sequence's
+      const int u = cluster - UnitSum::units(sum - mine);  // of this sequence's
       if (u >= 0 && u < nrt) {
         out->end = out->share = length;
         out->seq = s;
@@ -277,10 +275,10 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
     }
     if (end < positions && end >= lo && end < hi) out->end = cut(end - lo);
   };
-  auto warp_scan = [&](long long v) {  // inclusive
+  auto warp_scan = [&](uint64_t v) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += u;
     }
     return v;
@@ -291,7 +289,7 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
   }
   if (a.R <= 32) {  // one warp has them all: 0.3 us less than through shared memory
     if (warp == 0) {
-      const long long mine = look(lane), sum = warp_scan(mine);
+      const uint64_t mine = look(lane), sum = warp_scan(mine);
       const int longest = __reduce_max_sync(0xffffffffu, nrt > 0 ? length : 0);
       __syncwarp();
       deal(lane, mine, sum, __shfl_sync(0xffffffffu, sum, 31), longest);
@@ -301,7 +299,7 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
   }
   // inclusive scan over the block's threads, the total, and the longest unit
   int longest = 0;
-  auto scan = [&](long long v, int len, long long &all) {
+  auto scan = [&](uint64_t v, int len, uint64_t &all) {
     v = warp_scan(v);
     len = __reduce_max_sync(0xffffffffu, len);
     if (lane == 31) {
@@ -320,9 +318,9 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
   };
   // more sequences than threads: their totals first
   const bool many = a.R > THREADS;
-  long long total = 0;
+  uint64_t total = 0;
   if (many) {
-    long long sum = 0;
+    uint64_t sum = 0;
     int len = 0;
     for (int r = threadIdx.x; r < a.R; r += THREADS) {
       sum += look(r);
@@ -331,11 +329,11 @@ __device__ __forceinline__ void find_share(const LatentArgs &a, int cluster, int
     scan(sum, len, total);
     __syncthreads();
   }
-  long long base = 0;
+  uint64_t base = 0;
   for (int r0 = 0; r0 < a.R; r0 += THREADS) {
-    const long long mine = look(r0 + threadIdx.x);
-    long long all;
-    const long long sum = base + scan(mine, nrt > 0 ? length : 0, all);
+    const uint64_t mine = look(r0 + threadIdx.x);
+    uint64_t all;
+    const uint64_t sum = base + scan(mine, nrt > 0 ? length : 0, all);
     if (!many) total = all;
     deal(r0 + threadIdx.x, mine, sum, total, longest);
     base += all;
@@ -523,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
   volatile int *progress = reinterpret_cast<volatile int *>(bars + 46);  // tiles K was loaded of
   Share *share = reinterpret_cast<Share *>(bars + 20);         // 64 bytes
-  long long *scan = reinterpret_cast<long long *>(bars + 28);  // [18]
+  uint64_t *scan = bars + 28;  // [18]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;
@@ -961,7 +959,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (w.t0 == 0 && tid == 0 && rank == 0) {
           // the unit's first piece: its others are in the shares that follow
-          a.desc[2 * cluster] = make_int4(1 + w.others(*share), min(rows, C::UROWS), 0, 0);
+          // (never more than there are clusters, whatever the locations were)
+          a.desc[2 * cluster] =
+              make_int4(min(1 + w.others(*share), clusters - cluster), min(rows, C::UROWS), 0, 0);
           a.desc[2 * cluster + 1].x = grow0;
         }
       }
