@@ -35,7 +35,7 @@ struct AppendArgs {
   const float *rope;
   int32_t *status;
   int64_t kv_a_ld, q_pe_ld;
-  int T, R, H, L, P, Dn, bs, num_blocks, bt_stride, max_pos, interleaved;
+  int T, R, H, L, P, Dn, bs, num_blocks, bt_stride, max_pos;
   float eps;
   int vec_row, vec_q;  // rows / queries move as 16-byte pieces
 };
@@ -279,7 +279,7 @@ int launch_append(const mla_dims_t &d, const void *kv_a, int64_t kv_a_ld, const 
   auto al = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   AppendArgs a{kv_a, norm_weight, q, kv_cache, new_latent, q_pe, qsl, seq_lens, positions,
                block_table, rope, status, kv_a_ld, q_pe_ld, T, R, d.num_heads, L, P,
-               d.qk_nope_dim, d.block_size, num_blocks, bt_stride, max_pos, interleaved, eps, 0, 0};
+               d.qk_nope_dim, d.block_size, num_blocks, bt_stride, max_pos, eps, 0, 0};
   // cache rows are multiples of 16 bytes from an aligned base; the rest is checked here
   a.vec_row = (L * es) % 16 == 0 && (kv_a_ld * es) % 16 == 0 && al(kv_a) && al(norm_weight) &&
               al(kv_cache) && al(new_latent);

@@ -149,11 +149,13 @@ inline int launch_status(cudaStream_t s, const char *name) {
 // Programmatic dependent launch, for the chains of short decode kernels: a
 // kernel launched with launch_chained may start while the one before it on the
 // stream is still running (once all of that one's blocks have called
-// chain_release or exited), and calls chain_wait before it touches any global
-// memory: there it waits until the kernels before it have completed and their
-// writes are visible.  A kernel that allocates tensor memory calls chain_release
-// (one call counts for its block) only once it has: else a block of a kernel
-// behind it, resident beside it, could hold the columns that it still needs.
+// chain_release or exited), and calls chain_wait before it reads or writes any
+// global memory: there it waits until the kernels before it have completed and
+// their writes are visible.  (Before it the head products only ask for their
+// weights in L2, where a write of the kernel before would find them.)  A kernel
+// that allocates tensor memory calls chain_release (one call counts for its
+// block) only once it has: else a block of a kernel behind it, resident beside
+// it, could hold the columns that it still needs.
 __device__ __forceinline__ void chain_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

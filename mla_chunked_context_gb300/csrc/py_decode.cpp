@@ -30,12 +30,6 @@ PyObject *attr(PyObject *o, PyObject *name) {
   return v;  // a new reference
 }
 
-int64_t integer(PyObject *o) {
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw PythonError();
-  return v;
-}
-
 bool truth(PyObject *o) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) throw PythonError();
