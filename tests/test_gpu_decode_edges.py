@@ -175,3 +175,183 @@ def test_seconds_of_work_are_no_timeout():
         within(f64(lse[:, t:t + 1]), rl, E + (n / 8 + 16) * F + F * np.abs(rl), "lse")
         u = torch.finfo(dims.dtype).eps / 2
         within(f64(o[t:t + 1]), ro, u * np.abs(ro) + (2 * E.T[:, :, None] + (n / 8 + 64) * F + u) * mass, "o")
+
+
+# ------------------------------------------------- batches, streams, graphs --
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("bs", [64, 16])
+def test_more_slots_than_tokens(bs, causal):
+    """Many sequence slots of which few have new tokens: the form of one block
+    with several units a sequence, whose rows see different keys; lengths below
+    zero count as none."""
+    rng = np.random.default_rng(bs)
+    H, R = 128, 60
+    dims, od = make_dims(LARGE, H, bs, "bf16")
+    ql, lens = [0] * R, [5] * R
+    for r, (n, k) in {3: (3, 300), 17: (1, 1000), 40: (5, 129), 41: (2, 0), 59: (4, 66)}.items():
+        ql[r], lens[r] = n, k
+    qsl = loc(ql)
+    cache, table = make_cache(rng, lens, bs, 576, dims.dtype)
+    q = normal(rng, qsl[-1] + 2, H, 576, std=0.4, dtype=dims.dtype)
+    assert (qsl[-1] + 2) * H <= 64 * R
+    device_lens = [-7 if r == 41 else n for r, n in enumerate(lens)]
+    o, lse = run_attn(dims, causal, qsl, device_lens, q, cache, table)
+    check_attn(dims, od, causal, qsl, lens, q, cache, table, o, lse)
+    wild = cache.clone()                      # seen by two of the third's three, one of the last's four
+    for r, j in ((3, 298), (59, 65)):
+        wild[table[r, j // bs], j % bs] = math.inf
+    o2, lse2 = run_attn(dims, causal, qsl, device_lens, q, wild, table)
+    for t in range(qsl[-1]):
+        sees = t in ((1, 2, qsl[-1] - 1) if causal else (0, 1, 2, *range(qsl[-1] - 4, qsl[-1])))
+        if not sees:
+            assert torch.equal(o2[t], o[t]) and torch.equal(lse2[:, t], lse[:, t]), t
+        else:
+            assert torch.isnan(o2[t]).all(), t
+
+
+def step_inputs(rng, shape, dtype, H, lens, bs=16):
+    dims, od = make_dims(shape, H, bs, dtype)
+    L, P, Dn, Dv = shape
+    R = len(lens)
+    cache, table = make_cache(rng, [n + 4 for n in lens], bs, L + P, dims.dtype)
+    return dims, od, dict(
+        q=normal(rng, R, H, Dn + P, dtype=dims.dtype).to(DEV), kv_a=normal(rng, R, L + P, dtype=dims.dtype).to(DEV),
+        qsl=i32(range(R + 1)), lens=i32(lens), cache=cache.to(DEV), table=table.to(DEV),
+        tab=torch.from_numpy(O.rope_table(max(lens) + 8, P).astype(np.float32)).to(DEV),
+        w=normal(rng, H * (Dn + Dv), L, std=0.1, dtype=dims.dtype).to(DEV),
+        out=torch.empty(R, H, Dv, dtype=dims.dtype, device=DEV), lse=torch.empty(H, R, device=DEV))
+
+
+def run_step(dec, x, **kw):
+    return dec(x["q"], x["kv_a"], x["qsl"], x["lens"], x["tab"], x["cache"], x["table"], x["w"], x["out"],
+               x["lse"], **kw)
+
+
+@pytest.mark.parametrize("shape,dtype", [(LARGE, "bf16"), (SMALL, "f32")])
+def test_captured_between_other_work(shape, dtype):
+    """Steps captured between memory sets, copies, other kernels and work of a
+    second stream that forks and joins give what eager calls give."""
+    rng = np.random.default_rng(50)
+    H = 32
+    dims, od, x = step_inputs(rng, shape, dtype, H, [100, 40, 700])
+    start = x["cache"].clone()
+    dec = M.LatentDecode(dims, 3, 3, device=DEV)
+    run_step(dec, x)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (x["out"], x["lse"], x["cache"])]
+    src = {k: x[k].clone() for k in ("q", "kv_a", "cache", "w")}
+    src["cache"].copy_(start)
+    other, side = torch.zeros_like(x["out"]), torch.cuda.Stream()
+    host = torch.zeros_like(x["lens"]).cpu().pin_memory()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        x["lse"].zero_()                              # a memory set before the first call
+        x["cache"].copy_(src["cache"])
+        x["q"].copy_(src["q"])                        # a copy
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x["w"].copy_(src["w"])                    # on the second stream, joined before the first call
+            x["kv_a"].copy_(src["kv_a"] * 1)
+        main.wait_stream(side)
+        run_step(dec, x)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):                 # the expansion once more, behind the join
+            M.mla_expand_output(dims, dec.o_latent[:3], x["w"], other)
+        host.copy_(x["lens"], non_blocking=True)
+        main.wait_stream(side)
+    for _ in range(3):
+        for t in (x["out"], x["lse"], x["q"], x["kv_a"], x["w"], other):
+            t.fill_(5.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x["out"], want[0]) and torch.equal(x["lse"], want[1]) and torch.equal(other, want[0])
+        assert torch.equal(torch.nan_to_num(x["cache"].float(), 5.0), torch.nan_to_num(want[2].float(), 5.0))
+
+
+def test_two_threads_a_stream_and_an_instance_each():
+    import threading
+    rng = np.random.default_rng(51)
+    sets = []
+    for lens in ([900, 30], [64, 2000, 5]):
+        dims, od, x = step_inputs(rng, LARGE, "bf16", 128, lens, bs=64)
+        dec = M.LatentDecode(dims, len(lens), len(lens), device=DEV)
+        run_step(dec, x)
+        torch.cuda.synchronize()
+        sets.append((dec, x, x["out"].clone(), x["lse"].clone(), torch.cuda.Stream()))
+    failed = []
+
+    def work(dec, x, out, lse, stream):
+        try:
+            torch.cuda.set_device(0)
+            for _ in range(40):
+                with torch.cuda.stream(stream):
+                    x["out"].fill_(0)
+                    run_step(dec, x)
+                    stream.synchronize()
+                    if not (torch.equal(x["out"], out) and torch.equal(x["lse"], lse)):
+                        failed.append("result")
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=s) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+
+
+@pytest.mark.parametrize("shape,dtype,H", [(LARGE, "bf16", 16), (SMALL, "f32", 4)])
+def test_append_prepares_a_prefill(shape, dtype, H):
+    """The append's dense rows and rotated queries are a prefill's inputs; its
+    cache rows then serve a decode step.  Tolerance: the framework's for
+    attention output (O: 2e-2 + 2e-2 |ref|, LSE 1e-3), in bf16 with the step's
+    rounding of the absorbed query as in test_gpu_decode.py."""
+    rng = np.random.default_rng(H)
+    bs, ctx, new = 16, [200, 0, 37], [70, 33, 1]
+    dims, od = make_dims(shape, H, bs, dtype)
+    L, P, Dn, Dv = shape
+    R, T = len(ctx), sum(new)
+    total = [c + n for c, n in zip(ctx, new)]
+    cache, table = make_cache(rng, [n + 1 for n in total], bs, L + P, dims.dtype)
+    g_cache, g_table = cache.to(DEV), table.to(DEV)
+    tab = torch.from_numpy(O.rope_table(400, P).astype(np.float32)).to(DEV)
+    gw = (1 + 0.1 * normal(rng, L)).to(dims.dtype).to(DEV)
+    w = normal(rng, H * (Dn + Dv), L, std=0.5 / math.sqrt(L), dtype=dims.dtype).to(DEV)
+    q, kv_a = normal(rng, T, H, Dn + P, dtype=dims.dtype), normal(rng, T, L + P, dtype=dims.dtype)
+    g_q, lat = q.to(DEV), torch.empty(T, L + P, dtype=dims.dtype, device=DEV)
+    M.mla_append_latent(dims, kv_a.to(DEV), i32(loc(new)), i32(total), tab, g_cache, g_table,
+                        norm_weight=gw, new_latent=lat, q=g_q, q_pe_out=g_q[..., Dn:])
+    out, lse = torch.empty(T, H, Dv, dtype=dims.dtype, device=DEV), torch.empty(H, T, device=DEV)
+    pf = M.ChunkedPrefill(dims, ctx, new, 128, 128, 16, device=DEV)
+    pf(g_q, lat, g_cache, g_table, w, out, lse)
+    # the same tokens as one decode step of many new tokens, on a cache of its own
+    c2 = cache.to(DEV)
+    out2, lse2 = torch.empty_like(out), torch.empty_like(lse)
+    M.LatentDecode(dims, T, R, device=DEV)(q.to(DEV), kv_a.to(DEV), i32(loc(new)), i32(total), tab, c2,
+                                           g_table, w, out2, lse2, norm_weight=gw)
+    torch.cuda.synchronize()
+    assert torch.equal(torch.nan_to_num(g_cache.float(), 5.0), torch.nan_to_num(c2.float(), 5.0))
+    c, wn = f64(g_cache), f64(w)
+    for r in range(R):
+        sl = slice(loc(new)[r], loc(new)[r + 1])
+        rows = np.stack([O.context_row(c, table.numpy(), r, j, bs) for j in range(total[r])])
+        kn, v = O.up_project(rows, wn, od)
+        qr = f64(q[sl])
+        for i in range(new[r]):
+            qr[i, :, Dn:] = O.rotate(qr[i, :, Dn:], f64(tab)[ctx[r] + i], False)
+        vis = np.arange(total[r])[None, :] <= (ctx[r] + np.arange(new[r]))[:, None]
+        ro, rl = O.attention_with_lse(qr, kn, rows[:, L:], v, od.softmax_scale, vis)
+        slack, turned = 0.0, 0.0
+        if dtype == "bf16":
+            u = torch.finfo(dims.dtype).eps / 2
+            ql = np.abs(O.absorb_query(qr, wn, od))
+            slack = u * od.softmax_scale * np.einsum("thl,nl->thn", ql, np.abs(rows), optimize=True).max()
+            # the prefill's rotated query is rounded to bf16 before its scores
+            turned = u * od.softmax_scale * np.einsum("thp,np->thn", np.abs(qr[..., Dn:]),
+                                                      np.abs(rows[:, L:]), optimize=True).max()
+        within(f64(lse)[:, sl], rl, 1e-3 + turned, "prefill lse")
+        within(f64(lse2)[:, sl], rl, 1e-3 + slack, "step lse")
+        within(f64(out)[sl], ro, 2e-2 + 2e-2 * np.abs(ro), "prefill out")
+        within(f64(out2)[sl], ro, 2e-2 + 2e-2 * np.abs(ro), "step out")
