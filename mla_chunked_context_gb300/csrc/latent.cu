@@ -15,7 +15,10 @@
 //    each group has its own running maximum and sum, joined over the warp by
 //    shuffles and over the block in shared memory.  (A warp for a key, 32
 //    lanes over its columns, kept eight rows of 4-byte loads in flight and took
-//    20 us for 4 x 3 tokens, 16 heads, 700 keys of 80 floats; this 8.4.)
+//    20 us for 4 x 3 tokens, 16 heads, 700 keys of 80 floats; this 8.4.)  Every
+//    head of a token reads the token's keys, all but the first from L2: 8 x 2000
+//    keys of 576 floats, 16 heads 115 us (590 MB, 5.1 TB/s; the keys once would
+//    take 5.5), 16 x 4096 of 288 bf16 144 us.
 #include "common.cuh"
 
 namespace mla {

@@ -13,8 +13,8 @@
 // tokens there are, so that for few of them all of the contraction is in flight
 // at once (with stages for 128: absorb of one token 5.9 us, expand of 16 5.2;
 // so 4.5 and 4.8, of which the weights' way takes most).
-// Many tokens (500, 128 heads) take 26.4 and 18.7 us, 4.4 and 5.3 TB/s: a CTA's
-// loads wait for L2.  Absorb with 256 columns a CTA: 27.0, with 64 34.3, as a
+// Many tokens (500, 128 heads) take 25.9 and 18.9 us, 4.4 and 5.2 TB/s: a CTA's
+// loads wait for L2, and absorb's 2048 CTAs, three an SM, are 4.5 waves run as 5.  Absorb with 256 columns a CTA: 27.0, with 64 34.3, as a
 // persistent kernel with two accumulators 32.2, with the four CTAs of a token
 // tile sharing its loads by multicast 32.9; expand with 64 columns 21.7.
 //   warp 0     TMA loads: per 64 columns of the contraction, the tokens' box

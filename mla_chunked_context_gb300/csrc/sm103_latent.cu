@@ -37,8 +37,10 @@
 // takes 3200 (128 sequences of up to 8192 keys, 32 heads: 110 us, 83% of copy
 // bandwidth); pair about 2000, of which its shared-memory reads take 1860 and
 // its MMAs 1425 (24 sequences x 4 tokens x 128 heads: 82 us, 49% of the bf16
-// rate).  A launch has some 10000 clocks around its tiles: finding its share,
-// the first loads, the last rows out, and the joining kernel.
+// rate).  With one token a sequence and 128 heads these reads, not HBM, hold the
+// pair form too: 128 sequences of 4096 keys take 130 us, their bytes 94.  A
+// launch has some 10000 clocks around its tiles: finding its share, the first
+// loads, the last rows out, and the joining kernel.
 // Warps: 0 K loads, 1 V loads (pair), 2 MMA issue, 3 query loads and prefetches
 // to L2, 4-11 softmax and epilogue (two a quarter of tensor memory's lanes).
 #include <algorithm>
@@ -86,9 +88,14 @@ struct Cfg {
 // Work split, in positions of a tile.  UNIT_COST: what a unit costs beyond its
 // tiles (queries in, first scores, rows out: 5000 to 8000 clocks, a tile taking
 // 2000 to 3400).  31 short sequences beside one of 131072 keys took 55.3, 48.3,
-// 47.4 and 47.6 us with 2, 3, 4 and 5 in the pair form.
+// 47.4 and 47.6 us with 2, 3, 4 and 5 in the pair form.  One less or more in both
+// forms moves long and ragged batches by 2% at most; 128 heads, 1 x 2048 keys
+// 15.6 and 14.6 us (so 14.0), 100 x 500 36.5 and 33.9 (32.5), 200 x 400 38.5 and
+// 45.1 (45.4).
 // MIN_SHARE: the least that a share is worth; shorter ones cost more in scratch
-// traffic and joining than they save.
+// traffic and joining than they save (2 and 8: 128 heads, 4 x 2048 keys 25.9 and
+// 19.1 us, so 16.7; 1 x 6000 16.7 and 19.8, so 16.9; 16 heads, 1 x 2048 10.6 and
+// 17.7, so 13.0).
 template <bool PAIR>
 constexpr int UNIT_COST = PAIR ? 4 : 2;
 constexpr int MIN_SHARE = 4;
@@ -96,7 +103,12 @@ constexpr int MIN_SHARE = 4;
 // whole GPU when it is the only one.  So: no cut nearer than SNAP to a unit's
 // end; none at all through units of up to SHORT positions; and where there are
 // no more units than clusters, one each, unless the longest is more than
-// WHOLE_SLACK beyond an equal share.
+// WHOLE_SLACK beyond an equal share.  Measured, 128 heads, us: SNAP 0 and 2,
+// 16 x 4096 keys 31.0 and 31.5 (so 30.7), 200 x 400 49.0 and 45.4 (45.4).  SHORT 6
+// and 16, 40 x 600 20.2 and 18.1 (20.2), 200 x 400 45.3 and 38.8 (45.4), 300 ragged
+// of up to 700 56.1 and 53.1 (56.2).  WHOLE_SLACK 0 and 16, 40 x 600 27.6 and 20.2
+// (20.2), 64 x 4096 76.5 and 69.3 (76.5), 64 heads 100 x 900 42.9 and 35.7 (35.6).
+// Longer ragged batches and single long sequences move by less than 2%.
 constexpr int SNAP = 1, SHORT = 10, WHOLE_SLACK = 8;
 
 // Tiles between asking for keys in L2 and copying them to shared memory, whose
@@ -1299,7 +1311,14 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
                int(cache_rows), bt_stride, causal, box_log2,
                reinterpret_cast<uintptr_t>(o) % 32 == 0, Divider(d.block_size),
                Divider(d.num_heads), d.softmax_scale * 1.4426950408889634f};
-  // rows of an average sequence beyond one CTA's 64: pairs
+  // Rows of an average sequence beyond one CTA's 64: pairs, which read the keys
+  // once for 128 rows (16 x 4096 keys, 65 to 128 heads: 30 us, single 40; 64 x
+  // 4096, 80 heads: 74.5, 115.7).  Up to 64 the single form streams better where
+  // there are sequences enough for all SMs (128 x 4096, 32 heads: 109, pairs 119;
+  // 128 x 512, 64 heads: 25.0, 35.7); of few long ones it makes more pieces to join
+  // (16 x 4096, 64 heads: 52.5, 28.3).  The average is over the slots, of which
+  // those without tokens count (their lengths are on the device): 8 of 32 slots x
+  // 4096, 128 heads, run single in 51.6 us, pairs 34.8.
   if (int64_t(T) * d.num_heads > int64_t(64) * R) return launch_latent<true>(maps, a, max_ctas, s);
   return launch_latent<false>(maps, a, max_ctas, s);
 }
