@@ -63,6 +63,9 @@
  *       MLA_STATUS_BAD_POSITION  a rope position outside the rope table was
  *                              met (mla_append_latent): nothing was written
  *                              for that token.
+ *       MLA_STATUS_BAD_TREE    a tree of drafted tokens that is none (a parent
+ *                              that is not an earlier node, a node or token out
+ *                              of range): see the calls.
  */
 #ifndef MLA_CHUNKED_CONTEXT_H
 #define MLA_CHUNKED_CONTEXT_H
@@ -98,7 +101,8 @@ enum { MLA_DTYPE_F32 = 0, MLA_DTYPE_BF16 = 1, MLA_DTYPE_F16 = 2 };
 enum {
   MLA_STATUS_BAD_BLOCK = 1,
   MLA_STATUS_FP16_RANGE = 2,
-  MLA_STATUS_BAD_POSITION = 4
+  MLA_STATUS_BAD_POSITION = 4,
+  MLA_STATUS_BAD_TREE = 8
 };
 
 /* Bits of mla_device_error_flags(). */
@@ -624,6 +628,121 @@ int mla_latent_attn(const mla_dims_t *d, int32_t causal, int32_t num_seqs,
                     const int32_t *block_table, int32_t block_table_stride,
                     void *workspace, size_t workspace_bytes, void *o_latent,
                     float *lse, int32_t *dev_status, mla_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Drafted trees: decode steps whose new tokens are the nodes of a tree, the
+ * last sampled token (the root) and drafts that may follow it.  A step is, in
+ * order,
+ *   mla_tree_layout      parents -> masks, rope positions       once a step
+ *   mla_absorb_query, mla_append_latent (with those positions), mla_tree_attn,
+ *   mla_expand_output                                           every layer
+ *   mla_verify_tree      target rows -> the kept path, the next token
+ *   mla_commit_tree      the kept path's cache rows moved behind the cached
+ *                        tokens, in all layers; new lengths
+ * The batch is described on the device as above.  Node i of sequence r is its
+ * new token i, row qsl[r] + i of the token arrays, at cache position
+ * seq_lens[r] - n + i whatever its depth.
+ *   parents   device int32 [T]: a node's parent as an index within its
+ *             sequence, smaller than its own; -1: none (it follows the cached
+ *             tokens).  Any other value counts as -1 and sets
+ *             MLA_STATUS_BAD_TREE.
+ * All calls only enqueue kernels on `stream` and may be captured into a graph.
+ *
+ * mla_tree_layout: per node t, node i of sequence r,
+ *   tree_mask[t]: bit j % 64 of word j / 64 set when node j is i or an ancestor
+ *             of i; device uint64 [T, mask_words], 8-byte aligned.  Nodes from
+ *             64 * mask_words on have no bit and set MLA_STATUS_BAD_TREE.
+ *   positions[t] = seq_lens[r] - n + depth of i, device int32 [T], nullable
+ *             (and seq_lens with it). */
+int mla_tree_layout(int32_t num_tokens, int32_t num_seqs,
+                    const int32_t *query_start_loc, const int32_t *seq_lens,
+                    const int32_t *parents, int32_t mask_words,
+                    uint64_t *tree_mask, int32_t *positions,
+                    int32_t *dev_status, mla_stream_t stream);
+
+/* mla_tree_attn: mla_latent_attn with another rule for what a token sees: all
+ *   of its sequence's positions before the new tokens (j < seq_lens[r] - n),
+ *   and new token i of the sequence where bit i of its tree_mask row is set (its
+ *   own one too only then; bits past the mask's words count as 0).  Any bits
+ *   will do, also such as are no tree's.  Everything else, the workspace
+ *   (mla_latent_attn_workspace_bytes) among it, as there; a cache row that is
+ *   not finite reaches only the tokens that see it. */
+int mla_tree_attn(const mla_dims_t *d, int32_t num_seqs,
+                  const int32_t *query_start_loc, const int32_t *seq_lens,
+                  const uint64_t *tree_mask, int32_t mask_words,
+                  int32_t num_tokens, const void *q_latent,
+                  const void *kv_cache, int32_t num_blocks,
+                  const int32_t *block_table, int32_t block_table_stride,
+                  void *workspace, size_t workspace_bytes, void *o_latent,
+                  float *lse, int32_t *dev_status, mla_stream_t stream);
+
+/* mla_verify_tree: which nodes the target keeps, and the token after them.
+ *   target    device [T, vocab] in dtype (F32 or BF16), rows target_ld >= vocab
+ *             elements apart: row t holds the target's probabilities of the
+ *             token after node t (greedy: any scores, such as logits).
+ *   draft     device [T, vocab] in dtype, rows draft_ld apart: the
+ *             probabilities that node t's children were drawn from,
+ *             independently of each other.  NULL: the children were not drawn
+ *             but chosen (the likeliest tokens, a lookup).
+ *   tokens    device int32 [T]; the first node's is not looked at.
+ *   uniform   device float32 [T]: the random number in [0, 1) of node t's test
+ *   uniform_next  device float32 [num_seqs]: that of the next token
+ *   The walk starts at the sequence's first node, which is kept always, and
+ *   tests the children of a node in index order:
+ *     with draft     a child with token x is kept when u q(x) < r(x), r being
+ *                    the node's target row p at first; else r becomes
+ *                    max(r - q, 0) divided by its sum, for the next child
+ *     without        kept when u S < r(x), r = p and S = 1 at first; else r(x)
+ *                    becomes 0 and S the sum of r
+ *     greedy (uniform and uniform_next NULL; draft not looked at)  kept when x
+ *                    is the row's largest value, the lowest index among equals
+ *   and goes on at the one that is kept.  Then
+ *     next_tokens[r] = the first v with r(0) + .. + r(v) > uniform_next[r] S, S
+ *                    the sum of r (r = p where nothing is left); greedy: the
+ *                    row's largest value.
+ *   So the tokens follow the target's probabilities whatever the draft.
+ *   path      device int32 [num_seqs, path_ld]: the kept nodes, as indices
+ *             within the sequence, rising, the first one 0; then -1.  At most
+ *             path_ld nodes are kept: the path_ld-th is taken for a leaf.
+ *   num_kept  device int32 [num_seqs].  A sequence without new tokens has 0 and
+ *             next_tokens -1.
+ *   Sums are held in 48 bits: the results are those of exact sums but for
+ *   borders nearer than some 2^-40 of the sum.  Values that are negative or NaN
+ *   count as 0 (greedy: NaN as -infinity; a row of nothing else gives token 0).
+ *   A sequence's first 1024 nodes are looked at; more set MLA_STATUS_BAD_TREE,
+ *   as does a child whose token is outside [0, vocab) (it is passed over).
+ *   Errors: MLA_ERR_UNSUPPORTED for a vocabulary beyond 2^24 or more than 2^24
+ *   tokens or sequences. */
+int mla_verify_tree(int32_t dtype, int32_t num_tokens, int32_t num_seqs,
+                    int32_t vocab, const void *target, int64_t target_ld,
+                    const void *draft, int64_t draft_ld, const int32_t *tokens,
+                    const int32_t *parents, const int32_t *query_start_loc,
+                    const float *uniform, const float *uniform_next,
+                    int32_t *path, int32_t path_ld, int32_t *num_kept,
+                    int32_t *next_tokens, int32_t *dev_status,
+                    mla_stream_t stream);
+
+/* mla_commit_tree: per sequence r with n new tokens, for d < num_kept[r], the
+ *   cache row of position base + path[r][d] goes to position base + d, base =
+ *   seq_lens[r] - n, in every layer; new_seq_lens[r] = base + num_kept[r]
+ *   (device int32 [num_seqs], nullable; not seq_lens itself).  All rows are
+ *   taken before any is overwritten.
+ *   kv_caches  host array of num_layers device pointers, each [num_blocks,
+ *              block_size, L+P] in dtype, 16-byte aligned, no two the same.
+ *   path       device int32 [num_seqs, path_ld], as mla_verify_tree leaves it:
+ *              an entry has to be at least its place d and less than n, else
+ *              nothing moves for it and MLA_STATUS_BAD_TREE is set; so it is
+ *              for num_kept outside [0, min(n, path_ld)], which is clamped.
+ *   Positions below 0 and bad blocks (MLA_STATUS_BAD_BLOCK) are neither read
+ *   nor written. */
+int mla_commit_tree(const mla_dims_t *d, int32_t num_seqs, int32_t num_tokens,
+                    const int32_t *path, int32_t path_ld,
+                    const int32_t *num_kept, const int32_t *query_start_loc,
+                    const int32_t *seq_lens, void *const *kv_caches,
+                    int32_t num_layers, int32_t num_blocks,
+                    const int32_t *block_table, int32_t block_table_stride,
+                    int32_t *new_seq_lens, int32_t *dev_status,
+                    mla_stream_t stream);
 
 /* 1 when the current device runs the tcgen05 (sm_103a) kernels of this
  * library. */

@@ -19,7 +19,9 @@ from ._lib import (Chunk, Dims, MlaError, lib, merge_attn_states, mla_chunk_kv_d
                    mla_fused_attn_plan, mla_prefill_pinned_bytes, mla_profile_begin,
                    mla_profile_end, mla_set_pipeline_overlap, MLA_STATUS_FP16_RANGE,
                    MLA_STATUS_BAD_POSITION, mla_append_latent, mla_absorb_query,
-                   mla_expand_output, mla_latent_attn, mla_latent_attn_workspace_bytes)
+                   mla_expand_output, mla_latent_attn, mla_latent_attn_workspace_bytes,
+                   MLA_STATUS_BAD_TREE, mla_tree_layout, mla_tree_attn, mla_verify_tree,
+                   mla_commit_tree)
 
 __all__ = ["Chunk", "Dims", "MlaError", "lib", "merge_attn_states", "mla_chunk_kv_dtype",
            "mla_chunk_workspace_bytes", "mla_device_error_flags",
@@ -34,7 +36,8 @@ __all__ = ["Chunk", "Dims", "MlaError", "lib", "merge_attn_states", "mla_chunk_k
            "mla_profile_begin", "mla_profile_end", "mla_set_pipeline_overlap",
            "MLA_STATUS_FP16_RANGE", "ChunkedPrefill", "MLA_STATUS_BAD_POSITION",
            "mla_append_latent", "mla_absorb_query", "mla_expand_output", "mla_latent_attn",
-           "mla_latent_attn_workspace_bytes", "LatentDecode"]
+           "mla_latent_attn_workspace_bytes", "LatentDecode", "MLA_STATUS_BAD_TREE",
+           "mla_tree_layout", "mla_tree_attn", "mla_verify_tree", "mla_commit_tree", "TreeDecode"]
 
 
 class ChunkedPrefill:
@@ -109,7 +112,84 @@ class LatentDecode:
                           block_table, norm_weight, norm_eps, positions, interleaved, q=q,
                           q_pe_out=q_lat[..., dims.kv_lora_rank:], dev_status=dev_status,
                           stream=stream)
-        mla_latent_attn(dims, causal, query_start_loc, seq_lens, q_lat, kv_cache, block_table,
-                        self.workspace, o_lat, lse, dev_status, stream)
+        self._attend(causal, query_start_loc, seq_lens, q_lat, kv_cache, block_table, o_lat, lse,
+                     dev_status, stream)
         mla_expand_output(dims, o_lat, w_kv_b, out, stream)
         return out
+
+    def _attend(self, causal, query_start_loc, seq_lens, q_lat, kv_cache, block_table, o_lat, lse,
+                dev_status, stream):
+        mla_latent_attn(self.dims, causal, query_start_loc, seq_lens, q_lat, kv_cache, block_table,
+                        self.workspace, o_lat, lse, dev_status, stream)
+
+
+class TreeDecode(LatentDecode):
+    """LatentDecode for steps whose new tokens are trees of drafts: ``plan``
+    once a step, then the call for each layer, ``verify`` with the target's
+    rows, ``commit``.  It holds what these hand on: the trees' masks and rope
+    positions (nodes up to 64 * mask_words a sequence), the kept paths of up to
+    max_path nodes, num_kept and next_tokens.  All of it is on the device, and a
+    captured step can be replayed with other trees of the same numbers of tokens."""
+
+    def __init__(self, dims: Dims, max_tokens: int, max_seqs: int, mask_words: int = 1,
+                 max_path: int = 16, device="cuda"):
+        import torch
+        super().__init__(dims, max_tokens, max_seqs, device)
+
+        def i32(*shape):
+            return torch.zeros(*shape, dtype=torch.int32, device=device)
+
+        self.tree_mask = torch.zeros(self.max_tokens, int(mask_words), dtype=torch.int64,
+                                     device=device)
+        self.positions = i32(self.max_tokens)
+        self.path, self.num_kept = i32(self.max_seqs, int(max_path)), i32(self.max_seqs)
+        self.next_tokens = i32(self.max_seqs)
+        self._step = None
+
+    def plan(self, parents, query_start_loc, seq_lens, dev_status=None, stream=None):
+        """The step's trees (mla_tree_layout); the layers' calls and verify use
+        these parents, query_start_loc and seq_lens."""
+        T, R = parents.shape[0], seq_lens.shape[0]
+        if T > self.max_tokens or R > self.max_seqs:
+            raise ValueError(f"TreeDecode: {T} tokens of {R} sequences, room for "
+                             f"{self.max_tokens} of {self.max_seqs}")
+        mla_tree_layout(parents, query_start_loc, seq_lens, self.tree_mask[:T],
+                        self.positions[:T], dev_status, stream)
+        self._step = (T, R, parents, query_start_loc, seq_lens)
+
+    def _planned(self):
+        if self._step is None:
+            raise ValueError("TreeDecode: plan comes first")
+        return self._step
+
+    def __call__(self, q, kv_a, rope_table, kv_cache, block_table, w_kv_b, out, lse=None,
+                 norm_weight=None, norm_eps=1e-6, interleaved=False, dev_status=None, stream=None):
+        """A layer of the step: arguments as LatentDecode's."""
+        T, _, _, query_start_loc, seq_lens = self._planned()
+        if q.shape[0] != T:
+            raise ValueError(f"TreeDecode: {q.shape[0]} tokens, planned for {T}")
+        return super().__call__(q, kv_a, query_start_loc, seq_lens, rope_table, kv_cache,
+                                block_table, w_kv_b, out, lse, norm_weight, norm_eps,
+                                self.positions[:T], interleaved, dev_status=dev_status,
+                                stream=stream)
+
+    def _attend(self, causal, query_start_loc, seq_lens, q_lat, kv_cache, block_table, o_lat, lse,
+                dev_status, stream):
+        mla_tree_attn(self.dims, query_start_loc, seq_lens, self.tree_mask[:q_lat.shape[0]], q_lat,
+                      kv_cache, block_table, self.workspace, o_lat, lse, dev_status, stream)
+
+    def verify(self, target, tokens, uniform=None, uniform_next=None, draft=None, dev_status=None,
+               stream=None):
+        """mla_verify_tree on the planned trees: (path [R, max_path], num_kept
+        [R], next_tokens [R]), this object's own buffers."""
+        _, R, parents, query_start_loc, _ = self._planned()
+        out = self.path[:R], self.num_kept[:R], self.next_tokens[:R]
+        mla_verify_tree(target, draft, tokens, parents, query_start_loc, uniform, uniform_next,
+                        *out, dev_status, stream)
+        return out
+
+    def commit(self, kv_caches, block_table, new_seq_lens=None, dev_status=None, stream=None):
+        """mla_commit_tree of what verify kept, in all layers' caches."""
+        T, R, _, query_start_loc, seq_lens = self._planned()
+        mla_commit_tree(self.dims, self.path[:R], self.num_kept[:R], query_start_loc, seq_lens,
+                        kv_caches, block_table, new_seq_lens, T, dev_status, stream)

@@ -23,7 +23,7 @@ HEADER = os.path.join(HERE, "..", "include", "mla_chunked_context.h")
 MLA_OK, MLA_ERR_INVALID, MLA_ERR_TOO_SMALL, MLA_ERR_PLANNER_STUCK, MLA_ERR_CUDA, \
     MLA_ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5
 MLA_DTYPE_F32, MLA_DTYPE_BF16, MLA_DTYPE_F16 = 0, 1, 2
-MLA_STATUS_BAD_BLOCK, MLA_STATUS_FP16_RANGE, MLA_STATUS_BAD_POSITION = 1, 2, 4
+MLA_STATUS_BAD_BLOCK, MLA_STATUS_FP16_RANGE, MLA_STATUS_BAD_POSITION, MLA_STATUS_BAD_TREE = 1, 2, 4, 8
 
 _ERRORS = {MLA_ERR_INVALID: "invalid argument", MLA_ERR_TOO_SMALL: "buffer too small",
            MLA_ERR_PLANNER_STUCK: "planner cannot progress (budget below one aligned split)",
@@ -40,7 +40,8 @@ EXPORTED = ("mla_plan_context_chunks", "merge_attn_states", "mla_gather_context_
             "mla_fused_context_attn", "mla_fused_attn_plan", "mla_prefill_pinned_bytes",
             "mla_profile_begin", "mla_profile_end", "mla_set_pipeline_overlap",
             "mla_append_latent", "mla_absorb_query", "mla_expand_output",
-            "mla_latent_attn_workspace_bytes", "mla_latent_attn")
+            "mla_latent_attn_workspace_bytes", "mla_latent_attn", "mla_tree_layout",
+            "mla_tree_attn", "mla_verify_tree", "mla_commit_tree")
 MLA_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 
@@ -121,6 +122,11 @@ def lib() -> C.CDLL:
             "mla_expand_output": [P, P, I32, P, P, P],
             "mla_latent_attn_workspace_bytes": [P, I32, I32, P],
             "mla_latent_attn": [P, I32, I32, P, P, I32, P, P, I32, P, I32, P, SZ, P, P, P, P],
+            "mla_tree_layout": [I32, I32, P, P, P, I32, P, P, P, P],
+            "mla_tree_attn": [P, I32, P, P, P, I32, I32, P, P, I32, P, I32, P, SZ, P, P, P, P],
+            "mla_verify_tree": [I32, I32, I32, I32, P, I64, P, I64, P, P, P, P, P, P, I32, P, P, P,
+                                P],
+            "mla_commit_tree": [P, I32, I32, P, I32, P, P, P, P, I32, I32, P, I32, P, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -605,3 +611,56 @@ def mla_latent_attn(dims: Dims, causal: bool, query_start_loc, seq_lens, q_laten
         o_latent, lse, dev_status, stream)
     if rc:
         raise MlaError(rc, "mla_latent_attn")
+
+
+# ----------------------------------------------------------- drafted trees --
+def mla_tree_layout(parents, query_start_loc, seq_lens, tree_mask, positions=None, dev_status=None,
+                    stream=None) -> None:
+    """Masks and rope positions of trees of new tokens.  parents: int32 [T],
+    indices within the sequence, -1 for a root; tree_mask: int64 [T, words] of
+    64 nodes each, positions: int32 [T], both written."""
+    rc = (_decode or _native()).layout(parents, query_start_loc, seq_lens, tree_mask, positions,
+                                       dev_status, stream)
+    if rc:
+        raise MlaError(rc, "mla_tree_layout")
+
+
+def mla_tree_attn(dims: Dims, query_start_loc, seq_lens, tree_mask, q_latent, kv_cache,
+                  block_table, workspace, o_latent, lse=None, dev_status=None,
+                  stream=None) -> None:
+    """mla_latent_attn where a new token sees the tokens before the new ones and
+    those of its sequence's new tokens whose bit is set in its row of tree_mask
+    (int64 [T, words]); workspace as there."""
+    rc = (_decode or _native()).tree_attend(
+        dims, query_start_loc, seq_lens, tree_mask, q_latent, kv_cache, block_table, workspace,
+        o_latent, lse, dev_status, stream)
+    if rc:
+        raise MlaError(rc, "mla_tree_attn")
+
+
+def mla_verify_tree(target, draft, tokens, parents, query_start_loc, uniform, uniform_next, path,
+                    num_kept, next_tokens, dev_status=None, stream=None) -> None:
+    """Which drafted tokens the target keeps.  target [T, vocab] (float32 or
+    bfloat16, rows may be padded): row t holds the probabilities of the token
+    after node t; draft: those that its children were drawn from, or None for
+    children that were chosen.  uniform [T], uniform_next [R]: random numbers in
+    [0, 1); both None: greedy, and target may hold logits.  Written: path int32
+    [R, most], the kept nodes and then -1, num_kept and next_tokens int32 [R]."""
+    rc = (_decode or _native()).verify(target, draft, tokens, parents, query_start_loc, uniform,
+                                       uniform_next, path, num_kept, next_tokens, dev_status,
+                                       stream)
+    if rc:
+        raise MlaError(rc, "mla_verify_tree")
+
+
+def mla_commit_tree(dims: Dims, path, num_kept, query_start_loc, seq_lens, kv_caches, block_table,
+                    new_seq_lens=None, num_tokens: Optional[int] = None, dev_status=None,
+                    stream=None) -> None:
+    """Moves the cache rows of the kept nodes (mla_verify_tree's path and
+    num_kept) behind the cached tokens, and writes the new lengths.  kv_caches:
+    the layers' caches as a list, or one; num_tokens: what query_start_loc is
+    clamped to, as the other calls do (None: not clamped)."""
+    rc = (_decode or _native()).commit(dims, path, num_kept, query_start_loc, seq_lens, kv_caches,
+                                       block_table, new_seq_lens, num_tokens, dev_status, stream)
+    if rc:
+        raise MlaError(rc, "mla_commit_tree")

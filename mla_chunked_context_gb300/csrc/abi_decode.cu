@@ -7,7 +7,7 @@
 
 namespace mla {
 
-// kernels (append.cu, latent.cu)
+// kernels (append.cu, latent.cu, tree.cu, verify.cu)
 int launch_append(const mla_dims_t &d, const void *kv_a, int64_t kv_a_ld, const void *norm_weight,
                   float eps, int T, int R, const int32_t *qsl, const int32_t *seq_lens,
                   const int32_t *positions, const float *rope, int max_pos, int interleaved,
@@ -19,8 +19,9 @@ int launch_absorb_simt(const mla_dims_t &d, const void *q, int T, const void *w,
 int launch_expand_simt(const mla_dims_t &d, const void *o_latent, int T, const void *w, void *out,
                        cudaStream_t s);
 bool latent_simt_ok(const mla_dims_t &d);
-int launch_latent_attn_simt(const mla_dims_t &d, int causal, int R, const int32_t *qsl,
-                            const int32_t *seq_lens, int T, const void *q, const void *cache,
+int launch_latent_attn_simt(const mla_dims_t &d, int causal, const TreeMask &tree, int R,
+                            const int32_t *qsl, const int32_t *seq_lens, int T, const void *q,
+                            const void *cache,
                             int num_blocks, const int32_t *block_table, int bt_stride, void *o,
                             float *lse, int32_t *status, cudaStream_t s);
 // sm103_heads.cu, sm103_latent.cu
@@ -28,11 +29,22 @@ int launch_absorb_tc(const mla_dims_t &d, const void *q, int T, const void *w, i
                      void *q_latent, cudaStream_t s);
 int launch_expand_tc(const mla_dims_t &d, const void *o_latent, int T, const void *w, void *out,
                      cudaStream_t s);
-int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t *qsl,
-                          const int32_t *seq_lens, int T, const void *q, const void *cache,
-                          int num_blocks, const int32_t *block_table, int bt_stride, float *part_o,
-                          float *part_lse, void *desc, int max_ctas, void *o, float *lse,
-                          int32_t *status, cudaStream_t s);
+int launch_latent_attn_tc(const mla_dims_t &d, int causal, const TreeMask &tree, int R,
+                          const int32_t *qsl, const int32_t *seq_lens, int T, const void *q,
+                          const void *cache, int num_blocks, const int32_t *block_table,
+                          int bt_stride, float *part_o, float *part_lse, void *desc, int max_ctas,
+                          void *o, float *lse, int32_t *status, cudaStream_t s);
+int launch_tree_layout(const int32_t *parents, const int32_t *qsl, const int32_t *seq_lens, int T,
+                       int R, int words, uint64_t *mask, int32_t *positions, int32_t *status,
+                       cudaStream_t s);
+int launch_commit(const mla_dims_t &d, const int32_t *path, int path_ld, const int32_t *kept, int T,
+                  int R, const int32_t *qsl, const int32_t *seq_lens, void *const *caches,
+                  int layers, int num_blocks, const int32_t *block_table, int bt_stride,
+                  int32_t *new_lens, int32_t *status, cudaStream_t s);
+int launch_verify(const void *p, int64_t p_ld, const void *q, int64_t q_ld, int dtype, int V,
+                  const int32_t *tokens, const int32_t *parents, int T, int R, const int32_t *qsl,
+                  const float *u, const float *u_next, int32_t *path, int path_ld, int32_t *kept,
+                  int32_t *next, int32_t *status, cudaStream_t s);
 
 namespace {
 
@@ -65,6 +77,37 @@ size_t latent_workspace(const mla_dims_t &d, void *base, LatentWorkspace &w) {
 
 bool aligned_to(const void *p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & uintptr_t(bytes - 1)) == 0;
+}
+
+// mla_latent_attn, and with a mask mla_tree_attn
+int attend(const mla_dims_t *d, int causal, const TreeMask &tree, int num_seqs,
+           const int32_t *query_start_loc, const int32_t *seq_lens, int num_tokens,
+           const void *q_latent, const void *kv_cache, int num_blocks, const int32_t *block_table,
+           int block_table_stride, void *workspace, size_t workspace_bytes, void *o_latent,
+           float *lse, int32_t *dev_status, mla_stream_t stream) {
+  if (!query_start_loc || !seq_lens || !q_latent || !kv_cache || !block_table || !o_latent)
+    return MLA_ERR_INVALID;
+  const int es = elem_bytes(d->dtype);
+  if (!aligned_to(q_latent, es) || !aligned_to(o_latent, es) || !aligned4(lse) ||
+      !aligned16(kv_cache))
+    return MLA_ERR_INVALID;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (tc_shape(*d)) {
+    LatentWorkspace w;
+    const size_t need = latent_workspace(*d, workspace, w);
+    if (!workspace || !aligned16(workspace)) return MLA_ERR_INVALID;
+    if (workspace_bytes < need) return MLA_ERR_TOO_SMALL;
+    if (!aligned16(q_latent) || !aligned16(o_latent) || !tc_available())
+      return MLA_ERR_UNSUPPORTED;
+    return launch_latent_attn_tc(*d, causal, tree, num_seqs, query_start_loc, seq_lens, num_tokens,
+                                 q_latent, kv_cache, num_blocks, block_table, block_table_stride,
+                                 w.part_o, w.part_lse, w.desc, kMaxCtas, o_latent, lse, dev_status,
+                                 s);
+  }
+  if (!latent_simt_ok(*d)) return MLA_ERR_UNSUPPORTED;
+  return launch_latent_attn_simt(*d, causal, tree, num_seqs, query_start_loc, seq_lens, num_tokens,
+                                 q_latent, kv_cache, num_blocks, block_table, block_table_stride,
+                                 o_latent, lse, dev_status, s);
 }
 
 }  // namespace
@@ -178,27 +221,91 @@ extern "C" int mla_latent_attn(const mla_dims_t *d, int32_t causal, int32_t num_
   if ((causal != 0 && causal != 1) || num_seqs < 0 || num_blocks < 0 || block_table_stride < 1)
     return MLA_ERR_INVALID;
   if (num_tokens == 0 || num_seqs == 0) return MLA_OK;
-  if (!query_start_loc || !seq_lens || !q_latent || !kv_cache || !block_table || !o_latent)
+  return attend(d, causal, TreeMask(), num_seqs, query_start_loc, seq_lens, num_tokens, q_latent,
+                kv_cache, num_blocks, block_table, block_table_stride, workspace, workspace_bytes,
+                o_latent, lse, dev_status, stream);
+}
+
+extern "C" int mla_tree_layout(int32_t num_tokens, int32_t num_seqs,
+                               const int32_t *query_start_loc, const int32_t *seq_lens,
+                               const int32_t *parents, int32_t mask_words, uint64_t *tree_mask,
+                               int32_t *positions, int32_t *dev_status, mla_stream_t stream) {
+  if (num_tokens < 0 || num_seqs < 0 || mask_words < 1) return MLA_ERR_INVALID;
+  if (num_tokens == 0 || num_seqs == 0) return MLA_OK;
+  if (!query_start_loc || !parents || !tree_mask || (positions && !seq_lens) ||
+      !aligned_to(tree_mask, 8) || !aligned4(parents) || !aligned4(positions))
     return MLA_ERR_INVALID;
-  const int es = elem_bytes(d->dtype);
-  if (!aligned_to(q_latent, es) || !aligned_to(o_latent, es) || !aligned4(lse) ||
-      !aligned16(kv_cache))
+  return launch_tree_layout(parents, query_start_loc, positions ? seq_lens : nullptr, num_tokens,
+                            num_seqs, mask_words, tree_mask, positions, dev_status,
+                            static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int mla_tree_attn(const mla_dims_t *d, int32_t num_seqs, const int32_t *query_start_loc,
+                             const int32_t *seq_lens, const uint64_t *tree_mask,
+                             int32_t mask_words, int32_t num_tokens, const void *q_latent,
+                             const void *kv_cache, int32_t num_blocks, const int32_t *block_table,
+                             int32_t block_table_stride, void *workspace, size_t workspace_bytes,
+                             void *o_latent, float *lse, int32_t *dev_status,
+                             mla_stream_t stream) {
+  int rc = check_dims(d);
+  if (rc) return rc;
+  rc = check_rows(*d, num_tokens);
+  if (rc) return rc;
+  if (num_seqs < 0 || num_blocks < 0 || block_table_stride < 1 || mask_words < 1)
     return MLA_ERR_INVALID;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (tc_shape(*d)) {
-    LatentWorkspace w;
-    const size_t need = latent_workspace(*d, workspace, w);
-    if (!workspace || !aligned16(workspace)) return MLA_ERR_INVALID;
-    if (workspace_bytes < need) return MLA_ERR_TOO_SMALL;
-    if (!aligned16(q_latent) || !aligned16(o_latent) || !tc_available())
-      return MLA_ERR_UNSUPPORTED;
-    return launch_latent_attn_tc(*d, causal, num_seqs, query_start_loc, seq_lens, num_tokens,
-                                 q_latent, kv_cache, num_blocks, block_table, block_table_stride,
-                                 w.part_o, w.part_lse, w.desc, kMaxCtas, o_latent, lse, dev_status,
-                                 s);
-  }
-  if (!latent_simt_ok(*d)) return MLA_ERR_UNSUPPORTED;
-  return launch_latent_attn_simt(*d, causal, num_seqs, query_start_loc, seq_lens, num_tokens,
-                                 q_latent, kv_cache, num_blocks, block_table, block_table_stride,
-                                 o_latent, lse, dev_status, s);
+  if (num_tokens == 0 || num_seqs == 0) return MLA_OK;
+  if (!tree_mask || !aligned_to(tree_mask, 8)) return MLA_ERR_INVALID;
+  return attend(d, 0, TreeMask{tree_mask, mask_words}, num_seqs, query_start_loc, seq_lens,
+                num_tokens, q_latent, kv_cache, num_blocks, block_table, block_table_stride,
+                workspace, workspace_bytes, o_latent, lse, dev_status, stream);
+}
+
+extern "C" int mla_verify_tree(int32_t dtype, int32_t num_tokens, int32_t num_seqs, int32_t vocab,
+                               const void *target, int64_t target_ld, const void *draft,
+                               int64_t draft_ld, const int32_t *tokens, const int32_t *parents,
+                               const int32_t *query_start_loc, const float *uniform,
+                               const float *uniform_next, int32_t *path, int32_t path_ld,
+                               int32_t *num_kept, int32_t *next_tokens, int32_t *dev_status,
+                               mla_stream_t stream) {
+  if (!valid_dtype(dtype) || num_tokens < 0 || num_seqs < 0 || vocab < 1 || path_ld < 1 ||
+      target_ld < vocab || (draft && draft_ld < vocab))
+    return MLA_ERR_INVALID;
+  constexpr int kMost = 1 << 24;
+  if (vocab > kMost || num_tokens > kMost || num_seqs > kMost) return MLA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return MLA_OK;
+  const int es = elem_bytes(dtype);
+  if (!query_start_loc || !path || !num_kept || !next_tokens ||
+      (uniform == nullptr) != (uniform_next == nullptr) || !aligned4(path) ||
+      !aligned4(num_kept) || !aligned4(next_tokens) || !aligned4(query_start_loc))
+    return MLA_ERR_INVALID;
+  if (num_tokens > 0 && (!target || !tokens || !parents || !aligned_to(target, es) ||
+                         !aligned_to(draft, es) || !aligned4(tokens) || !aligned4(parents) ||
+                         !aligned4(uniform) || !aligned4(uniform_next)))
+    return MLA_ERR_INVALID;
+  return launch_verify(target, target_ld, uniform ? draft : nullptr, draft_ld, dtype, vocab, tokens,
+                       parents, num_tokens, num_seqs, query_start_loc, uniform, uniform_next, path,
+                       path_ld, num_kept, next_tokens, dev_status,
+                       static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int mla_commit_tree(const mla_dims_t *d, int32_t num_seqs, int32_t num_tokens,
+                               const int32_t *path, int32_t path_ld, const int32_t *num_kept,
+                               const int32_t *query_start_loc, const int32_t *seq_lens,
+                               void *const *kv_caches, int32_t num_layers, int32_t num_blocks,
+                               const int32_t *block_table, int32_t block_table_stride,
+                               int32_t *new_seq_lens, int32_t *dev_status, mla_stream_t stream) {
+  int rc = check_dims(d);
+  if (rc) return rc;
+  if (num_seqs < 0 || num_tokens < 0 || path_ld < 1 || num_layers < 0 || num_blocks < 0 ||
+      block_table_stride < 1)
+    return MLA_ERR_INVALID;
+  if (num_seqs == 0) return MLA_OK;
+  if (!path || !num_kept || !query_start_loc || !seq_lens || !block_table ||
+      (num_layers > 0 && !kv_caches) || new_seq_lens == seq_lens)
+    return MLA_ERR_INVALID;
+  for (int32_t l = 0; l < num_layers; ++l)
+    if (!kv_caches[l] || !aligned16(kv_caches[l])) return MLA_ERR_INVALID;
+  return launch_commit(*d, path, path_ld, num_kept, num_tokens, num_seqs, query_start_loc, seq_lens,
+                       kv_caches, num_layers, num_blocks, block_table, block_table_stride,
+                       new_seq_lens, dev_status, static_cast<cudaStream_t>(stream));
 }

@@ -87,6 +87,27 @@ __device__ __forceinline__ int keys_of(int len, int stride, int bs) {
   return int(min((long long)len, row < most ? row : most));
 }
 
+// Which of its sequence's new tokens each new token sees, as bits: [T][words],
+// new token j of the sequence in bit j % 64 of word j / 64.  Without bits the
+// attention is causal or full.
+struct TreeMask {
+  const uint64_t *bits = nullptr;
+  int words = 0;
+};
+__device__ __forceinline__ bool tree_bit(const uint64_t *row, int words, int j) {
+  return (j >> 6) < words && (__ldg(row + (j >> 6)) >> (j & 63) & 1) != 0;
+}
+// 32 bits of a row from new token `from` on (in bit 0); tokens before the
+// first (from < 0) are cached ones, which all see.
+__device__ __forceinline__ uint32_t tree_bits(const uint64_t *row, int words, int from) {
+  if (from <= -32) return ~0u;
+  const int w = from >> 6, sh = from & 63;  // (from < 0: word -1, which is all ones)
+  uint64_t v = w < 0 ? ~uint64_t(0) : w < words ? __ldg(row + w) : 0;
+  v >>= sh;
+  if (sh > 32 && w + 1 < words) v |= __ldg(row + w + 1) << (64 - sh);
+  return uint32_t(v);
+}
+
 // Kernels this library has enqueued since it was loaded (every launcher
 // calls launch_status() once, right after its launch).
 inline std::atomic<unsigned long long> g_kernel_launches{0};

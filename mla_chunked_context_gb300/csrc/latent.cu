@@ -110,6 +110,7 @@ struct LatentArgs {
   int T, R, H, L, P, bs, num_blocks, bt_stride, causal;
   Divider by_bs;
   float scale_log2;
+  TreeMask tree;
 };
 
 // 16 bytes of T
@@ -123,8 +124,9 @@ struct Vec {
 };
 
 // G lanes a key, NC pieces of 16 bytes a lane (rows of at most 16 G NC bytes),
-// AW warps a block, U keys of a group in flight
-template <typename T, int G, int NC, int AW, int U>
+// AW warps a block, U keys of a group in flight.  TREE: the token's mask says
+// which of the new tokens it sees; a key that it does not see is not loaded.
+template <typename T, int G, int NC, int AW, int U, bool TREE>
 __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
   extern __shared__ float sh[];  // [AW][L] partial outputs, [AW] maxima, [AW] sums
   constexpr int N = Vec<T>::N, GROUPS = AW * 32 / G, STEP = GROUPS * U;
@@ -140,7 +142,12 @@ __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
   if (t >= q1) return;
   const int len = max(__ldg(a.seq_lens + r), 0);
   const int keys = keys_of(len, a.bt_stride, a.bs);
-  const int nk = a.causal ? max(0, min(keys, len - (q1 - q0) + (t - q0) + 1)) : keys;
+  const int base_len = len - (q1 - q0);  // the first new token's position
+  const int nk = !TREE && a.causal ? max(0, min(keys, base_len + (t - q0) + 1)) : keys;
+  const uint64_t *bits = TREE ? a.tree.bits + int64_t(t) * a.tree.words : nullptr;
+  auto sees = [&](int j) {
+    return j < nk && (!TREE || j < base_len || tree_bit(bits, a.tree.words, j - base_len));
+  };
   const int LP = a.L + a.P;
   const T *q = static_cast<const T *>(a.q) + (int64_t(t) * a.H + h) * LP;
   const T *cache = static_cast<const T *>(a.cache);
@@ -148,11 +155,13 @@ __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
   bool bad = keys < len;
   // block ids of this group's next keys (key base + u * GROUPS + group)
   int blk[U];
+  bool seen[U];
   auto look_up = [&](int base) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = base + u * GROUPS + group;
-      blk[u] = j < nk ? __ldg(bt + a.by_bs.quotient(j)) : -2;
+      seen[u] = sees(j);
+      blk[u] = seen[u] ? __ldg(bt + a.by_bs.quotient(j)) : -1;
     }
   };
   look_up(0);
@@ -172,7 +181,7 @@ __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = base + u * GROUPS + group;
-      live[u] = j < nk;
+      live[u] = seen[u];
       const bool good = blk[u] >= 0 && blk[u] < a.num_blocks;
       if (live[u] && !good) bad = true;
       const T *row = cache + (int64_t(blk[u]) * a.bs + (j - a.by_bs.quotient(j) * a.bs)) * LP;
@@ -271,7 +280,10 @@ __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
 template <typename T, int G, int NC, int AW, int U>
 int launch_attn_n(const LatentArgs &a, int grid, cudaStream_t s) {
   const size_t smem = (size_t(AW) * a.L + 2 * AW) * sizeof(float);  // at most 33 KB
-  return launch_chained(latent_attn_simt<T, G, NC, AW, U>, grid, 32 * AW, smem, 1, s,
+  if (a.tree.bits)
+    return launch_chained(latent_attn_simt<T, G, NC, AW, U, true>, grid, 32 * AW, smem, 1, s,
+                          "tree_attn_simt", a);
+  return launch_chained(latent_attn_simt<T, G, NC, AW, U, false>, grid, 32 * AW, smem, 1, s,
                         "latent_attn_simt", a);
 }
 
@@ -314,13 +326,14 @@ int launch_expand_simt(const mla_dims_t &d, const void *o_latent, int T, const v
 
 bool latent_simt_ok(const mla_dims_t &d) { return d.kv_lora_rank + d.qk_rope_dim <= 1024; }
 
-int launch_latent_attn_simt(const mla_dims_t &d, int causal, int R, const int32_t *qsl,
-                            const int32_t *seq_lens, int T, const void *q, const void *cache,
+int launch_latent_attn_simt(const mla_dims_t &d, int causal, const TreeMask &tree, int R,
+                            const int32_t *qsl, const int32_t *seq_lens, int T, const void *q,
+                            const void *cache,
                             int num_blocks, const int32_t *block_table, int bt_stride, void *o,
                             float *lse, int32_t *status, cudaStream_t s) {
   LatentArgs a{q, cache, o, lse, qsl, seq_lens, block_table, status, T, R, d.num_heads,
                d.kv_lora_rank, d.qk_rope_dim, d.block_size, num_blocks, bt_stride, causal,
-               Divider(d.block_size), d.softmax_scale * 1.4426950408889634f};
+               Divider(d.block_size), d.softmax_scale * 1.4426950408889634f, tree};
   if (d.dtype == MLA_DTYPE_BF16) return launch_attn_t<__nv_bfloat16>(a, T * d.num_heads, s);
   return launch_attn_t<float>(a, T * d.num_heads, s);
 }

@@ -13,6 +13,7 @@
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "mla_chunked_context.h"
 
@@ -174,7 +175,7 @@ std::string type_name(ScalarType t) {
   return s.str();
 }
 
-constexpr ScalarType I32 = ScalarType::Int, F32 = ScalarType::Float;
+constexpr ScalarType I32 = ScalarType::Int, F32 = ScalarType::Float, I64 = ScalarType::Long;
 
 // dims, kv_a, query_start_loc, seq_lens, rope_table, kv_cache, block_table,
 // norm_weight, norm_eps, positions, interleaved, new_latent, q, q_pe_out,
@@ -295,6 +296,150 @@ int attend(PyObject *const *a) {
   });
 }
 
+// parents, query_start_loc, seq_lens, tree_mask, positions, dev_status, stream
+int layout(PyObject *const *a) {
+  const char *w = "mla_tree_layout";
+  Call c(w);
+  const int64_t T = c.size("parents", a[0], 0, 1), R = c.size("seq_lens", a[2], 0, 1);
+  const int64_t words = c.size("tree_mask", a[3], 1, 2);
+  const auto *parents = c.take<int32_t>("parents", a[0], I32, {T});
+  const auto *qsl = c.take<int32_t>("query_start_loc", a[1], I32, {R + 1});
+  const auto *lens = c.take<int32_t>("seq_lens", a[2], I32, {R});
+  auto *mask = c.take<uint64_t>("tree_mask", a[3], I64, {T, words});
+  auto *positions = c.take<int32_t>("positions", a[4], I32, {T});
+  auto *status = c.take<int32_t>("dev_status", a[5], I32, {1});
+  const int32_t t32 = narrow(T, w, "parents"), r32 = narrow(R, w, "seq_lens"),
+                w32 = narrow(words, w, "tree_mask");
+  void *s = c.stream(a[6]);
+  return unlocked([&] {
+    return mla_tree_layout(t32, r32, qsl, lens, parents, w32, mask, positions, status, s);
+  });
+}
+
+// dims, query_start_loc, seq_lens, tree_mask, q_latent, kv_cache, block_table,
+// workspace, o_latent, lse, dev_status, stream
+int tree_attend(PyObject *const *a) {
+  const char *w = "mla_tree_attn";
+  const Dims d(a[0]);
+  Call c(w);
+  const int64_t T = c.size("q_latent", a[4], 0, 3), R = c.size("seq_lens", a[2], 0, 1);
+  const int64_t blocks = c.size("kv_cache", a[5], 0, 3), stride = c.size("block_table", a[6], 1, 2);
+  const int64_t words = c.size("tree_mask", a[3], 1, 2);
+  const int64_t LP = d.L + d.P;
+  const int64_t ws_bytes = a[7] == Py_None ? 0 : c.tensor("workspace", a[7]).numel();
+  const void *q = c.take("q_latent", a[4], d.type, {T, d.H, LP});
+  const auto *qsl = c.take<int32_t>("query_start_loc", a[1], I32, {R + 1});
+  const auto *lens = c.take<int32_t>("seq_lens", a[2], I32, {R});
+  const auto *mask = c.take<uint64_t>("tree_mask", a[3], I64, {T, words});
+  const auto *table = c.take<int32_t>("block_table", a[6], I32, {R, stride});
+  const void *cache = c.take("kv_cache", a[5], d.type, {blocks, d.bs, LP});
+  void *ws = c.take("workspace", a[7], ScalarType::Byte, {ws_bytes});
+  void *o = c.take("o_latent", a[8], d.type, {T, d.H, d.L});
+  auto *lse = c.take<float>("lse", a[9], F32, {d.H, T});
+  auto *status = c.take<int32_t>("dev_status", a[10], I32, {1});
+  const int32_t t32 = narrow(T, w, "q_latent"), r32 = narrow(R, w, "seq_lens"),
+                b32 = narrow(blocks, w, "kv_cache"), s32 = narrow(stride, w, "block_table"),
+                w32 = narrow(words, w, "tree_mask");
+  void *s = c.stream(a[11]);
+  return unlocked([&] {
+    return mla_tree_attn(&d.c, r32, qsl, lens, mask, w32, t32, q, cache, b32, table, s32, ws,
+                         size_t(ws_bytes), o, lse, status, s);
+  });
+}
+
+// target, draft, tokens, parents, query_start_loc, uniform, uniform_next, path,
+// num_kept, next_tokens, dev_status, stream
+int verify(PyObject *const *a) {
+  const char *w = "mla_verify_tree";
+  Call c(w);
+  const int64_t T = c.size("target", a[0], 0, 2), V = c.size("target", a[0], 1, 2);
+  const int64_t R = c.size("path", a[7], 0, 2), deep = c.size("path", a[7], 1, 2);
+  const at::Tensor &target = c.tensor("target", a[0]);
+  const ScalarType type = target.scalar_type();
+  int32_t dtype = MLA_DTYPE_F32;
+  if (type == ScalarType::BFloat16)
+    dtype = MLA_DTYPE_BF16;
+  else if (type != F32)
+    c.refuse("target has to be float32 or bfloat16, got " + type_name(type));
+  int64_t ld[2] = {V, V};
+  const void *rows[2] = {nullptr, nullptr};
+  for (int i = 0; i < 2; ++i) {
+    if (i == 1 && a[1] == Py_None) break;
+    const char *name = i ? "draft" : "target";
+    const at::Tensor &t = c.tensor(name, a[i]);
+    c.on_device(name, t);
+    if (T > 1 && t.dim() == 2) ld[i] = t.stride(0);
+    if (t.scalar_type() != type || t.dim() != 2 || t.size(0) != T || t.size(1) != V ||
+        (V > 1 && t.stride(1) != 1) || ld[i] < V)
+      c.refuse(std::string(name) + " has to be [" + std::to_string(T) + ", " + std::to_string(V) +
+               "] " + type_name(type) + " with contiguous rows");
+    rows[i] = t.data_ptr();
+  }
+  const auto *tokens = c.take<int32_t>("tokens", a[2], I32, {T});
+  const auto *parents = c.take<int32_t>("parents", a[3], I32, {T});
+  const auto *qsl = c.take<int32_t>("query_start_loc", a[4], I32, {R + 1});
+  const auto *u = c.take<float>("uniform", a[5], F32, {T});
+  const auto *u_next = c.take<float>("uniform_next", a[6], F32, {R});
+  if ((a[5] == Py_None) != (a[6] == Py_None)) c.refuse("uniform and uniform_next go together");
+  auto *path = c.take<int32_t>("path", a[7], I32, {R, deep});
+  auto *kept = c.take<int32_t>("num_kept", a[8], I32, {R});
+  auto *next = c.take<int32_t>("next_tokens", a[9], I32, {R});
+  auto *status = c.take<int32_t>("dev_status", a[10], I32, {1});
+  const int32_t t32 = narrow(T, w, "target"), v32 = narrow(V, w, "target"),
+                r32 = narrow(R, w, "path"), p32 = narrow(deep, w, "path");
+  void *s = c.stream(a[11]);
+  return unlocked([&] {
+    return mla_verify_tree(dtype, t32, r32, v32, rows[0], ld[0], rows[1], ld[1], tokens, parents,
+                           qsl, u, u_next, path, p32, kept, next, status, s);
+  });
+}
+
+// dims, path, num_kept, query_start_loc, seq_lens, kv_caches, block_table,
+// new_seq_lens, num_tokens, dev_status, stream
+int commit(PyObject *const *a) {
+  const char *w = "mla_commit_tree";
+  const Dims d(a[0]);
+  Call c(w);
+  const int64_t R = c.size("path", a[1], 0, 2), deep = c.size("path", a[1], 1, 2);
+  const int64_t stride = c.size("block_table", a[6], 1, 2), LP = d.L + d.P;
+  const auto *path = c.take<int32_t>("path", a[1], I32, {R, deep});
+  const auto *kept = c.take<int32_t>("num_kept", a[2], I32, {R});
+  const auto *qsl = c.take<int32_t>("query_start_loc", a[3], I32, {R + 1});
+  const auto *lens = c.take<int32_t>("seq_lens", a[4], I32, {R});
+  const auto *table = c.take<int32_t>("block_table", a[6], I32, {R, stride});
+  std::vector<void *> caches;
+  int64_t blocks = 0;
+  auto layer = [&](PyObject *o) {
+    if (caches.empty()) blocks = c.size("kv_caches", o, 0, 3);
+    void *p = c.take("kv_caches", o, d.type, {blocks, d.bs, LP});
+    if (!p && blocks > 0) c.refuse("kv_caches has to be tensors");
+    caches.push_back(p);
+  };
+  if (PyList_Check(a[5]) || PyTuple_Check(a[5])) {
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(a[5]);
+    for (Py_ssize_t i = 0; i < n; ++i) layer(PySequence_Fast_GET_ITEM(a[5], i));
+  } else {
+    layer(a[5]);
+  }
+  if (blocks == 0) caches.clear();  // nothing to move
+  auto *new_lens = c.take<int32_t>("new_seq_lens", a[7], I32, {R});
+  int64_t T = INT32_MAX;
+  if (a[8] != Py_None) {
+    T = PyLong_AsLongLong(a[8]);
+    if (T == -1 && PyErr_Occurred()) throw PythonError();
+  }
+  auto *status = c.take<int32_t>("dev_status", a[9], I32, {1});
+  const int32_t t32 = narrow(T, w, "num_tokens"), r32 = narrow(R, w, "path"),
+                p32 = narrow(deep, w, "path"), b32 = narrow(blocks, w, "kv_caches"),
+                s32 = narrow(stride, w, "block_table"),
+                l32 = narrow(int64_t(caches.size()), w, "kv_caches");
+  void *s = c.stream(a[10]);
+  return unlocked([&] {
+    return mla_commit_tree(&d.c, r32, t32, path, p32, kept, qsl, lens, caches.data(), l32, b32,
+                           table, s32, new_lens, status, s);
+  });
+}
+
 // No C++ exception leaves the module.
 template <int (*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -320,6 +465,10 @@ PyMethodDef methods[] = {
     {"absorb", fast(entry<absorb, 6>), METH_FASTCALL, nullptr},
     {"expand", fast(entry<expand, 5>), METH_FASTCALL, nullptr},
     {"attend", fast(entry<attend, 12>), METH_FASTCALL, nullptr},
+    {"layout", fast(entry<layout, 7>), METH_FASTCALL, nullptr},
+    {"tree_attend", fast(entry<tree_attend, 12>), METH_FASTCALL, nullptr},
+    {"verify", fast(entry<verify, 12>), METH_FASTCALL, nullptr},
+    {"commit", fast(entry<commit, 11>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode", nullptr, -1, methods,

@@ -133,6 +133,7 @@ struct LatentArgs {
   bool o_sectors;  // o is 32-byte aligned
   Divider by_bs, by_h;
   float scale_log2;
+  TreeMask tree;
 };
 
 // ---- the work split ---------------------------------------------------------
@@ -163,7 +164,7 @@ struct Share {  // of a cluster, in shared memory
 // Piece of a unit: row tile rt of sequence r, key tiles [t0, t1).  Position v
 // of a unit is its tile v - UNIT_COST: a share that ends (or starts) in the
 // first UNIT_COST positions has none (or all) of the unit's tiles.
-template <bool PAIR>
+template <bool PAIR, bool TREE>
 struct Walk {
   static constexpr int COST = UNIT_COST<PAIR>;
   const LatentArgs &a;
@@ -200,15 +201,21 @@ struct Walk {
     left -= take;
     return t1 > t0;
   }
-  // keys that row `row` of the unit sees
-  __device__ __forceinline__ int seen(int row) const {
-    if (!a.causal) return s.keys;
-    const int i = a.by_h.quotient(rt * Cfg<PAIR>::UROWS + row);  // token of the sequence
-    return max(0, min(s.keys, s.len - s.nq + i + 1));
+  // token of the sequence that row `row` of the unit belongs to
+  __device__ __forceinline__ int token(int row) const {
+    return a.by_h.quotient(rt * Cfg<PAIR>::UROWS + row);
   }
-  // keys that all of the unit's rows see, and that any of them sees
-  __device__ __forceinline__ int seen_by_all() const { return seen(0); }
+  // keys that row `row` of the unit sees (tree: some of them, by its mask)
+  __device__ __forceinline__ int seen(int row) const {
+    if (TREE || !a.causal) return s.keys;
+    return max(0, min(s.keys, s.len - s.nq + token(row) + 1));
+  }
+  // keys that all of the unit's rows see, and that any of them may see
+  __device__ __forceinline__ int seen_by_all() const {
+    return TREE ? max(0, min(s.keys, s.len - s.nq)) : seen(0);
+  }
   __device__ __forceinline__ int seen_by_any() const {
+    if (TREE) return s.keys;
     return seen(min(Cfg<PAIR>::UROWS, s.nq * a.H - rt * Cfg<PAIR>::UROWS) - 1);
   }
   // shares after this one that have a piece of this unit, which this one cuts
@@ -510,7 +517,7 @@ __device__ __forceinline__ void softmax_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(STHREADS) : "memory");
 }
 
-template <bool PAIR>
+template <bool PAIR, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ Maps m, const LatentArgs a) {
   using C = Cfg<PAIR>;
@@ -529,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t k_full = smem_u32(bars), k_empty = k_full + 16, v_full = k_full + 32,
                  v_empty = k_full + 48, s_full = k_full + 64, s_empty = k_full + 80,
                  p_full = k_full + 96, pv_done = k_full + 112, q_full = k_full + 128,
-                 q_empty = k_full + 136, done = k_full + 144;
+                 q_empty = k_full + 136, done = k_full + 144, v_own = k_full + 376;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
   volatile int *progress = reinterpret_cast<volatile int *>(bars + 46);  // tiles K was loaded of
   Share *share = reinterpret_cast<Share *>(bars + 20);         // 64 bytes
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_empty + 8 * i, 1);
-      mbar_init(v_full + 8 * i, 1);
+      mbar_init(v_full + 8 * i, TREE && PAIR ? 2 : 1);
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(s_empty + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
@@ -556,6 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(done, 1);
+    if (TREE && PAIR) mbar_init(v_own, 1);
     fence_mbar_init();
     prefetch_map(&m.q);
     prefetch_map(&m.c[a.box_log2]);
@@ -589,14 +597,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int nrows = is_v ? 64 : C::KROWS, blocks = is_v ? 4 : NBLK;
     const int bl = min(a.box_log2, is_v ? 4 : PAIR ? 5 : 6), bx = 1 << bl;  // rows at once
     const int skip = PAIR && !is_v ? int(rank) * C::KROWS : 0;  // first key of the tile here
-    Walk<PAIR> w(a, *share);
-    int g = 0;
+    Walk<PAIR, TREE> w(a, *share);
+    int g = 0, checked = 0;
     bool ok = true;
     while (ok && w.next()) {
       const int32_t *bt = a.block_table + int64_t(w.r) * a.bt_stride;
       const int all = w.seen_by_all(), any = w.seen_by_any();
       for (int t = w.t0; t < w.t1; ++t, ++g) {
         const int key0 = t * TILE + skip, st = g & 1;
+        const bool mixed = is_v && all < any && key0 + TILE > all;
         int row[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -604,12 +613,21 @@ __global__ void __launch_bounds__(THREADS, 1)
           row[i] = off < nrows ? cache_row(a, bt, any, key0 + off) : none;
         }
         uint64_t hidden = 0;
-        if (is_v && all < any && key0 + TILE > all)
+        if (!TREE && mixed)
           hidden = hidden_rows(a, row[0], row[1], bl, max(0, all - key0), min(TILE, any - key0),
                                int(rank) * 512);
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((g >> 1) & 1) ^ 1));
         if (!ok) break;
-        if (rank == 0 && lane == 0) mbar_expect_tx(full + 8 * st, (PAIR ? 2 : 1) * stage_bytes);
+        // (a tree's mixed tile comes here on a barrier of this CTA's own)
+        const bool own = TREE && mixed;
+        if (lane == 0) {
+          if (own)
+            mbar_expect_tx(v_own, stage_bytes);
+          else if (rank == 0)
+            mbar_expect_tx(full + 8 * st, (PAIR ? 2 : 1) * stage_bytes);
+          else if (TREE && is_v)
+            mbar_arrive_remote(full_lead + 8 * st);
+        }
         __syncwarp();
         if (hidden) {
           load_unhidden<PAIR>(m, row[0], row[1], bl, any - key0, hidden, dst0 + st * stage_bytes,
@@ -622,7 +640,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // (a row past the length in K alone only makes scores that are masked)
           const int valid = r == none ? 0 : PAIR && !is_v ? bx : min(bx, any - key0 - off);
           if (elect_one()) {
-            const uint32_t dst = dst0 + st * stage_bytes, bar = full_lead + 8 * st;
+            const uint32_t dst = dst0 + st * stage_bytes, bar = own ? v_own : full_lead + 8 * st;
             if (!is_v)
               load_rows<PAIR>(m, bl, dst + off * 128, nrows * 128, blocks, 0, r, valid, none, bar);
             else if (bl == 4 && (valid == 0 || valid == 16))
@@ -632,6 +650,24 @@ __global__ void __launch_bounds__(THREADS, 1)
                               int(rank) * 256, r, valid, none, bar);
           }
           __syncwarp();
+        }
+        if (own) {
+          // A tree's rows differ in most of the new tokens that they see, so
+          // these are looked at where they have landed: a row takes one load of
+          // the warp.  (Read from memory beforehand, as where a few rows are
+          // hidden, one takes some 600 clocks.)
+          ok = __all_sync(0xffffffffu, mbar_wait(v_own, checked++ & 1));
+          if (!ok) break;
+          const uint32_t v = dst0 + st * stage_bytes + (lane >> 3) * (16 * 128) + (lane & 7) * 16;
+          const int to = min(TILE, any - key0);
+#pragma unroll 4
+          for (int j = max(0, all - key0); j < to; ++j) {
+            const uint32_t at = v + (j >> 4) * V_GROUP + (j & 15) * 128;
+            if (not_finite(ld_shared_v4(at))) st_shared_v4(at, make_uint4(0, 0, 0, 0));
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(full_lead + 8 * st);
         }
         if (!is_v && lane == 0) *progress = g + 1;
       }
@@ -644,7 +680,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // AHEAD tiles before the K loads come to them, whose progress paces this
     // warp (nothing waits for it but the queries)
     const int bl = min(a.box_log2, PAIR ? 5 : 6);
-    Walk<PAIR> w(a, *share);
+    Walk<PAIR, TREE> w(a, *share);
     int g = 0, n = 0;
     bool ok = true;
     const uint32_t bar = lead(q_full);
@@ -731,7 +767,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         commit(pv_done + 8 * st);
         return true;
       };
-      Walk<PAIR> w(a, *share);
+      Walk<PAIR, TREE> w(a, *share);
       int g = 0, n = 0;
       bool ok = true, first = false;  // first: the pending P V starts a unit's O
       for (; ok && w.next(); ++n) {
@@ -797,18 +833,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     // the tiles' maxima and the pieces' sums, over the four threads of a row
     RowJoin<STHREADS> row_join(xmax, tid);
     auto barrier = [] { softmax_barrier(); };
-    Walk<PAIR> w(a, *share);
+    Walk<PAIR, TREE> w(a, *share);
     int g = 0;
     bool ok = true;
     while (ok && w.next()) {
       const int rows = w.s.nq * a.H - w.rt * C::UROWS;  // of the unit (may exceed it)
       const int urow = int(rank) * CROWS + rl;
       const int vis = w.seen(min(urow, rows - 1));
+      const uint64_t *tree = nullptr;  // this row's mask
+      if (TREE)
+        tree = a.tree.bits + int64_t(w.s.q0 + w.token(min(urow, rows - 1))) * a.tree.words;
       const int all = w.seen_by_all(), any = w.seen_by_any();
       if (w.s.keys < w.s.len && a.status && tid == 0) atomicOr(a.status, MLA_STATUS_BAD_BLOCK);
       float mref = neg_inf(), l = 0.f;
       for (int t = w.t0; t < w.t1; ++t, ++g) {
-        const int sb = g & 1;
+        const int sb = g & 1, key = t * TILE + half * SC + part * NC;  // this thread's first
+        const int nvis = vis - key;
+        const bool mixed = all < any && t * TILE + TILE > all;  // rows may differ in what they see
+        uint32_t sees = nvis >= NC ? ~0u : nvis > 0 ? (1u << nvis) - 1 : 0;
+        if (TREE && mixed) sees &= tree_bits(tree, a.tree.words, key - (w.s.len - w.s.nq));
         ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * sb, (g >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
@@ -824,12 +867,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           else
             mbar_arrive(s_empty + 8 * sb);
         }
-        const int nvis = vis - t * TILE - half * SC - part * NC;
-        const bool mixed = all < any && t * TILE + TILE > all;  // rows may differ in what they see
-        if (nvis < NC) {
+        if (TREE ? mixed || nvis < NC : nvis < NC) {
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            if (c >= nvis) s[c] = __float_as_uint(neg_inf());
+            if (TREE ? !(sees >> c & 1) : c >= nvis) s[c] = __float_as_uint(neg_inf());
         }
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
@@ -1235,7 +1276,7 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
   }
 }
 
-template <bool PAIR>
+template <bool PAIR, bool TREE>
 int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaStream_t s) {
   constexpr int MAX_DEV = 64;
   static std::atomic<int> grid_of[MAX_DEV];  // CTAs that fit the device, 0: not asked yet
@@ -1254,19 +1295,22 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
   cfg.numAttrs = 1;
   int grid = grid_of[dev].load(std::memory_order_acquire);
   if (grid == 0) {
-    if (cudaFuncSetAttribute(latent_attn_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(latent_attn_kernel<PAIR, TREE>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Cfg<PAIR>::SMEM) != cudaSuccess)
       return MLA_ERR_CUDA;
     const int cs = PAIR ? 2 : 1;
     cfg.gridDim = dim3(cs * (num_sms() / cs));
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<PAIR>, &cfg) != cudaSuccess || n < 1)
+    if (cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<PAIR, TREE>, &cfg) != cudaSuccess ||
+        n < 1)
       n = num_sms() / cs;
     grid = std::min(cs * n, urows_limit);
     grid_of[dev].store(grid, std::memory_order_release);
   }
-  int rc = launch_chained(latent_attn_kernel<PAIR>, grid, THREADS, Cfg<PAIR>::SMEM, PAIR ? 2 : 1, s,
-                          "latent_attn_kernel", maps, a);
+  int rc = launch_chained(latent_attn_kernel<PAIR, TREE>, grid, THREADS, Cfg<PAIR>::SMEM,
+                          PAIR ? 2 : 1, s, TREE ? "tree_attn_kernel" : "latent_attn_kernel", maps,
+                          a);
   if (rc) return rc;
   // sequences that the block table keeps short are never cut: nothing to join
   const int64_t most_tiles = (int64_t(a.bt_stride) * a.bs + TILE - 1) / TILE;
@@ -1281,8 +1325,9 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
 
 // part_o [2 * max_ctas * 64 * 512], part_lse [2 * max_ctas * 64], desc
 // [2 * max_ctas] int4.
-int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t *qsl,
-                          const int32_t *seq_lens, int T, const void *q, const void *cache,
+int launch_latent_attn_tc(const mla_dims_t &d, int causal, const TreeMask &tree, int R,
+                          const int32_t *qsl, const int32_t *seq_lens, int T, const void *q,
+                          const void *cache,
                           int num_blocks, const int32_t *block_table, int bt_stride, float *part_o,
                           float *part_lse, void *desc, int max_ctas, void *o, float *lse,
                           int32_t *status, cudaStream_t s) {
@@ -1310,7 +1355,7 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
                static_cast<int4 *>(desc), status, T, R, d.num_heads, d.block_size, num_blocks,
                int(cache_rows), bt_stride, causal, box_log2,
                reinterpret_cast<uintptr_t>(o) % 32 == 0, Divider(d.block_size),
-               Divider(d.num_heads), d.softmax_scale * 1.4426950408889634f};
+               Divider(d.num_heads), d.softmax_scale * 1.4426950408889634f, tree};
   // Rows of an average sequence beyond one CTA's 64: pairs, which read the keys
   // once for 128 rows (16 x 4096 keys, 65 to 128 heads: 30 us, single 40; 64 x
   // 4096, 80 heads: 74.5, 115.7).  Up to 64 the single form streams better where
@@ -1319,8 +1364,12 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, int R, const int32_t 
   // (16 x 4096, 64 heads: 52.5, 28.3).  The average is over the slots, of which
   // those without tokens count (their lengths are on the device): 8 of 32 slots x
   // 4096, 128 heads, run single in 51.6 us, pairs 34.8.
-  if (int64_t(T) * d.num_heads > int64_t(64) * R) return launch_latent<true>(maps, a, max_ctas, s);
-  return launch_latent<false>(maps, a, max_ctas, s);
+  const bool pair = int64_t(T) * d.num_heads > int64_t(64) * R;
+  if (tree.bits)
+    return pair ? launch_latent<true, true>(maps, a, max_ctas, s)
+                : launch_latent<false, true>(maps, a, max_ctas, s);
+  return pair ? launch_latent<true, false>(maps, a, max_ctas, s)
+              : launch_latent<false, false>(maps, a, max_ctas, s);
 }
 
 int latent_take_errors() { return sm103::take_error_flags_here(); }
