@@ -342,8 +342,8 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(const VerifyArgs a) {
             if (out && taken(x.first((s + k) * 32 + lane) + i)) hi = lo = 0.f;
             sum.add(hi, lo);
           }
+        sum.renormalise();
       }
-      sum.renormalise();
       return sum;
     };
     auto sum_row = [&](const Left &l, const Pieces<T> &x, int s0, int s1) {

@@ -20,11 +20,13 @@ mla      -- gather, W_kv_b up-projection, varlen softmax attention with LSE,
             partial (PR #49294 report, test_mask_empty_context; PR #50613
             report, item 3), the chunked prefill loop and an unchunked
             reference over the full context.
+tree     -- trees of drafted tokens: masks, attention by mask, verification,
+            commit (pinned by ``tests/test_tree_cpu.py``).
 
-Every function is pinned by ``tests/test_oracle_pins.py`` against values the
+Every other function is pinned by ``tests/test_oracle_pins.py`` against values the
 pages print, closed forms, brute force on tiny inputs, or a library routine
 computing the same quantity by another route.  No function here is
 "parity unpinned".
 """
 
-from . import planner, mla  # noqa: F401
+from . import planner, mla, tree  # noqa: F401
