@@ -72,6 +72,7 @@ int fused_take_errors();
 int gather_take_errors();
 int latent_take_errors();
 int heads_take_errors();
+int verify_take_errors();
 
 namespace {
 
@@ -987,9 +988,9 @@ extern "C" int mla_device_error_flags(int32_t *flags) {
   if (cudaDeviceSynchronize() != cudaSuccess) return MLA_ERR_CUDA;
   const int a = gemm_take_errors(), b = attn_take_errors(), c = fused_take_errors(),
             e = gather_take_errors(), f = latent_take_errors(),
-            g = heads_take_errors();
-  if (a < 0 || b < 0 || c < 0 || e < 0 || f < 0 || g < 0) return MLA_ERR_CUDA;
-  *flags = a | b | c | e | f | g;
+            g = heads_take_errors(), h = verify_take_errors();
+  if (a < 0 || b < 0 || c < 0 || e < 0 || f < 0 || g < 0 || h < 0) return MLA_ERR_CUDA;
+  *flags = a | b | c | e | f | g | h;
   return MLA_OK;
 }
 

@@ -16,18 +16,27 @@
 //
 // The results are whole numbers that have to be the same whatever the order of
 // sums, and a vocabulary's cumulated float32 sum is off by more than a token's
-// share.  So sums are pairs of float32 (48 bits; Dekker 1971, Knuth's two-sum),
-// and the few scalars 64-bit.  (64-bit sums of all values would be bound by
-// their rate, a 64th of float32's.)
+// share.  So a value is rounded to units of 2^-45, as two integers (what adding
+// 2, and then 1.5 * 2^-22, leaves in a float32's low bits), and sums are sums of
+// integers: exact, in any order, and the same at every level of the search for
+// the next token.  (Pairs of float32 with 64-bit floating point for the walk,
+// which has a 64th of float32's rate here, took 22 us for a chain of 5 over
+// 32000 tokens, 149 for 64 trees of 16 over 131072 and 58 for 24 of up to 21 over
+// 100003 in bf16; this 6.5, 54 and 14.)
 //
 // Only the rows where a child was rejected and the last node's row are read,
 // one row at a time as each depends on the walk: a call of few sequences is
-// bound by latency, one of many by HBM.  A cluster of up to 8 CTAs takes a
-// sequence; each walks the tree by itself (the same numbers, the same steps)
-// over values gathered at the start, sums its part of a row, and tells the
-// others through distributed shared memory.  For the next token the sums of
-// CTAs, of warps, then of 32 lanes' 16-byte pieces are searched; only the last
-// warp reads its part of the row again.
+// bound by latency (of 12000 clocks for a chain: 2800 to the gathered values,
+// 2300 for the walk, 3300 for the row, 1400 for the cluster's sums, 2500 for the
+// next token), one of many by its sequence with the most rejections: 64 trees
+// read 119 rows, but one of them 11, a row at 13000 clocks once the others are
+// done.  A cluster of up to 8 CTAs takes a sequence; each walks the tree by
+// itself (the same numbers, the same steps) over values gathered at the start,
+// sums its part of a row, and tells the others through distributed shared
+// memory.  For the next token the sums of CTAs, of warps, then of 32 lanes'
+// 16-byte pieces are searched by one warp of one CTA.  Where a warp's part of a
+// row is four pieces a lane or less it stays in registers for the sums that
+// follow at the same node.
 #include <type_traits>
 
 #include "sm103.cuh"
@@ -35,9 +44,10 @@
 namespace mla {
 namespace {
 
-constexpr int VT = 512, VW = VT / 32;  // threads, warps
-constexpr int NODES = 1024;            // of a sequence
+constexpr int MAX_WARPS = 32;
+constexpr int NODES = 1024;  // of a sequence
 constexpr int MAX_CLUSTER = 8;
+constexpr int U = 4;         // pieces a lane has in flight
 enum Mode { kDraft, kPoint, kGreedy };
 
 struct VerifyArgs {
@@ -46,69 +56,92 @@ struct VerifyArgs {
   const int32_t *tokens, *parents, *qsl;
   const float *u, *u_next;
   int32_t *path, *kept, *next, *status;
-  int T, V, path_ld, cluster;
+  int T, V, path_ld, cluster_log2, warps_log2;
 };
 
-// A sum in two floats, |lo| <= half a step of hi (once renormalised).
-struct Sum2 {
-  float hi = 0.f, lo = 0.f;
-  __device__ __forceinline__ void add(float x, float x_lo) {
-    const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
-    const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
-    hi = s;
-    lo = __fadd_rn(lo, __fadd_rn(e, x_lo));
-  }
-  __device__ __forceinline__ void renormalise() {
-    const float s = __fadd_rn(hi, lo);
-    lo = __fsub_rn(lo, __fsub_rn(s, hi));
-    hi = s;
-  }
+// A number in two floats (some 46 bits): |lo| is at most half a step of hi.
+struct Two {
+  float hi, lo;
 };
-
-__device__ __forceinline__ Sum2 warp_sum(Sum2 s) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float h = __shfl_xor_sync(0xffffffffu, s.hi, o), l = __shfl_xor_sync(0xffffffffu, s.lo, o);
-    s.add(h, l);
-    s.renormalise();
-  }
-  return s;
+__device__ __forceinline__ Two two(float hi, float lo) {  // |hi| >= |lo|
+  const float s = __fadd_rn(hi, lo);
+  return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  const float h = __fmul_rn(a.hi, b.hi);
+  return two(h, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -h))));
+}
+__device__ __forceinline__ Two plus_one(Two a) {
+  const float s = __fadd_rn(a.hi, 1.f), b = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, b)), __fsub_rn(1.f, b));
+  return two(s, __fadd_rn(e, a.lo));
+}
+__device__ __forceinline__ Two reciprocal(Two a) {  // one step of Newton's from float32's
+  const float r = 1.f / a.hi;
+  const float e = __fmaf_rn(-a.lo, r, __fmaf_rn(-a.hi, r, 1.f));
+  return two(r, __fmul_rn(r, e));
 }
 
-// What is left of a row: max(a p - b q, 0), a and b in two floats each.
+// What is left of a row: max(a p - b q, 0).
 struct Left {
-  float ah, al, bh, bl;
-  int kind;  // 0: p; 1: p - q; 2: any
-  __device__ __forceinline__ static Left of(double a, double b) {
-    Left l;
-    l.ah = float(a);
-    l.al = float(a - double(l.ah));
-    l.bh = float(b);
-    l.bl = float(b - double(l.bh));
-    l.kind = b == 0.0 ? 0 : a == 1.0 && b == 1.0 ? 1 : 2;
-    return l;
-  }
+  Two a, b;
 };
+
+// Values in units of 2^-45 (0 <= w < 2): w = hi * 2^-22 + lo * 2^-45.
+constexpr float GRID = 2.f, FINE = 1.5f / 4194304.f;
+constexpr uint32_t GRID_BITS = 0x40000000u, FINE_BITS = 0x34C00000u;
+__device__ __forceinline__ int64_t units(uint32_t hi, uint32_t lo) {
+  return (int64_t(int32_t(hi)) << 23) + int32_t(lo);
+}
+// A sum of units as a number; x times a sum, rounded down (0 <= x <= 1).
+__device__ __forceinline__ Two number(int64_t v) {
+  const float hi = float(v);
+  return {hi * (1.f / 35184372088832.f), float(v - int64_t(hi)) * (1.f / 35184372088832.f)};
+}
+__device__ __forceinline__ int64_t part(float x, int64_t v) {
+  if (x >= 1.f) return v;
+  return int64_t(__umul64hi(__float2ull_rz(x * 18446744073709551616.f), uint64_t(v)));
+}
+
+// hi and lo of one value; KIND 0: p, 1: p - q, 2: a p - b q.  What the grid
+// leaves of w is computed from the parts of w, without its rounding.  (Integer
+// instructions and minima have half the rate of float32 sums, hence no more of
+// them than this.)
 template <int KIND>
-__device__ __forceinline__ void left_of(const Left &l, float p, float q, float &hi, float &lo) {
-  lo = 0.f;
-  if (KIND == 0) {
-    hi = fmaxf(p, 0.f);  // (0 for a NaN)
-    return;
-  }
-  float x = p, y = q, e = 0.f;
+__device__ __forceinline__ void left_of(const Left &l, float p, float q, uint32_t &hi,
+                                        uint32_t &lo) {
+  float x = p, y = 0.f, e = 0.f;
+  if (KIND == 1) y = fminf(q, x);
   if (KIND == 2) {
-    x = __fmul_rn(l.ah, p);
-    y = __fmul_rn(l.bh, q);
-    const float ex = __fmaf_rn(l.al, p, __fmaf_rn(l.ah, p, -x));
-    const float ey = __fmaf_rn(l.bl, q, __fmaf_rn(l.bh, q, -y));
-    e = __fsub_rn(ex, ey);
+    x = __fmul_rn(l.a.hi, p);
+    y = __fmul_rn(l.b.hi, q);
+    e = __fsub_rn(__fmaf_rn(l.a.hi, p, -x), __fmaf_rn(l.b.hi, q, -y));
+    e = __fmaf_rn(l.a.lo, p, e);
+    e = __fmaf_rn(-l.b.lo, q, e);
+    e = y < x ? e : 0.f;
+    y = fminf(y, x);
   }
-  const float d = __fsub_rn(x, y), b = __fsub_rn(d, x);
-  e = __fadd_rn(e, __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(y, b)));
-  const bool some = __fadd_rn(d, e) > 0.f;
-  hi = some ? d : 0.f;
-  lo = some ? e : 0.f;
+  const float t = __fadd_rn(KIND == 0 ? x : __fsub_rn(x, y), GRID);
+  float rest = __fsub_rn(x, __fsub_rn(t, GRID));
+  if (KIND != 0) rest = __fsub_rn(rest, y);
+  if (KIND == 2) rest = __fadd_rn(rest, e);
+  hi = __float_as_uint(t) - GRID_BITS;
+  lo = __float_as_uint(__fadd_rn(rest, FINE)) - FINE_BITS;
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {  // |v| < 2^70
+  const uint32_t a = __reduce_add_sync(0xffffffffu, uint32_t(v) & 0x3fffff);
+  const uint32_t b = __reduce_add_sync(0xffffffffu, uint32_t(v >> 22) & 0x3fffff);
+  const int c = __reduce_add_sync(0xffffffffu, int(v >> 44));
+  return int64_t(a) + (int64_t(b) << 22) + (int64_t(c) << 44);
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (int(threadIdx.x & 31) >= o) v += y;
+  }
+  return v;
 }
 
 // A row's 16-byte pieces, counted from the aligned address at or before its
@@ -126,19 +159,39 @@ struct Pieces {
   }
   __device__ __forceinline__ int first(int piece) const { return piece * N - head; }
   // elements outside the row are zeros
-  __device__ __forceinline__ static uint4 one(const T *row, bool vector, int at, int V) {
-    if (vector) return __ldg(reinterpret_cast<const uint4 *>(row + at));
+  __device__ __forceinline__ static uint4 one(const T *row, int at, int V) {
     alignas(16) T e[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) e[i] = at + i >= 0 && at + i < V ? row[at + i] : from_f32<T>(0.f);
     return *reinterpret_cast<const uint4 *>(e);
   }
-  template <bool Q>
-  __device__ __forceinline__ void load(int piece, uint4 &vp, uint4 &vq) const {
-    const int at = first(piece);
-    const bool whole = piece < count && at >= 0 && at + N <= V;
-    vp = one(p, whole, at, V);
-    if (Q) vq = one(q, whole && same, at, V);
+  // steps s .. s + U - 1 of 32 pieces, zeros from step s1 on
+  template <bool Q, int U>
+  __device__ __forceinline__ void load(int s, int s1, uint4 (&vp)[U], uint4 (&vq)[U]) const {
+    const int at = first(s * 32 + int(threadIdx.x & 31));
+    bool edges = Q && !same;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int e = at + k * 32 * N;
+      vp[k] = make_uint4(0, 0, 0, 0);
+      if (Q) vq[k] = make_uint4(0, 0, 0, 0);
+      if (s + k < s1) {
+        const bool whole = e >= 0 && e + N <= V;
+        if (whole) vp[k] = __ldg(reinterpret_cast<const uint4 *>(p + e));
+        if (Q && whole && same) vq[k] = __ldg(reinterpret_cast<const uint4 *>(q + e));
+        edges = edges || (!whole && e < V);
+      }
+    }
+    if (edges) {  // a row's ends, and a q that lies otherwise than p
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int e = at + k * 32 * N;
+        if (s + k < s1 && e < V) {
+          vp[k] = one(p, e, V);
+          if (Q) vq[k] = one(q, e, V);
+        }
+      }
+    }
   }
   __device__ __forceinline__ static float get(const uint4 &v, int i) {
     return to_f32(reinterpret_cast<const T *>(&v)[i]);
@@ -148,32 +201,50 @@ struct Pieces {
 struct Shared {
   int parent[NODES], token[NODES], path[NODES];
   float p[NODES], q[NODES], u[NODES];  // p and q of a node's token in its parent's rows
-  float hi[VW], lo[VW];                // sums of warps
-  float all_hi[2][MAX_CLUSTER], all_lo[2][MAX_CLUSTER];  // of the cluster's CTAs
-  int all_at[2][MAX_CLUSTER];                            // greedy: where the largest value is
-  // what the walk asks of the row
-  int cur, kept, finish, gone;  // gone: tokens taken out, in `out`
-  double a, b;
-  int out[NODES];
-  int next;
+  int out[NODES];                      // nodes whose tokens are taken out of the row
+  int64_t warp[MAX_WARPS];             // sums of warps
+  int64_t cta[2][MAX_CLUSTER];         // of the cluster's CTAs; greedy: largest value and place
+  uint64_t bar[2];                     // their arrival
+  // what the walk asks of the row, and then of the search
+  Left left;
+  int cur, kept, finish, gone, kind;
+  int64_t border;
+  int owner;
 };
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// Stores 8 bytes in a CTA of the cluster and counts them on an mbarrier there.
+__device__ __forceinline__ void st_async(uint32_t addr, int64_t v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(addr),
+               "l"(v), "r"(bar)
+               : "memory");
+}
+
+// A float's order as an unsigned integer's; 0 for NaN and -infinity.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  if (!(v > neg_inf())) return 0;
+  const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(VT, 2) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
   using sm103::cluster_arrive;
   using sm103::cluster_wait;
   using sm103::mapa_shared;
+  using sm103::mbar_wait;
   using sm103::smem_u32;
   constexpr int N = Pieces<T>::N;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = a.cluster;
-  const int rank = int(blockIdx.x) % C, r = int(blockIdx.x) / C;
-  cluster_arrive();  // (nobody writes to a CTA that has not started)
+  const int threads = blockDim.x, warps = threads >> 5;
+  const int C = 1 << a.cluster_log2, rank = int(blockIdx.x) & (C - 1);
+  const int r = int(blockIdx.x >> a.cluster_log2);
+  if (tid == 0) {
+    sm103::mbar_init(smem_u32(&sh.bar[0]), 1);
+    sm103::mbar_init(smem_u32(&sh.bar[1]), 1);
+    sm103::fence_mbar_init();
+  }
+  cluster_arrive();  // (its wait is before the first write to another CTA)
   chain_release();
   chain_wait();
   const int q0 = min(max(__ldg(a.qsl + r), 0), a.T), q1 = min(__ldg(a.qsl + r + 1), a.T);
@@ -181,9 +252,10 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(const VerifyArgs a) {
   const T *P = static_cast<const T *>(a.p) + int64_t(q0) * a.p_ld;
   const T *Q = MODE == kDraft ? static_cast<const T *>(a.q) + int64_t(q0) * a.q_ld : nullptr;
   bool bad = n > nodes;
-  for (int i = tid; i < nodes; i += VT) {
+  for (int i = tid; i < nodes; i += threads) {
     int up = __ldg(a.parents + q0 + i);
     const int x = __ldg(a.tokens + q0 + i);
+    if (MODE != kGreedy) sh.u[i] = __ldg(a.u + q0 + i);
     if (up < -1 || up >= i) {
       bad = true;
       up = -1;
@@ -195,7 +267,6 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(const VerifyArgs a) {
     sh.parent[i] = up;
     sh.token[i] = x;
     if (MODE != kGreedy && i > 0 && up >= 0) {
-      sh.u[i] = __ldg(a.u + q0 + i);
       sh.p[i] = to_f32(P[up * a.p_ld + x]);
       if (MODE == kDraft) sh.q[i] = to_f32(Q[up * a.q_ld + x]);
     }
@@ -203,7 +274,6 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(const VerifyArgs a) {
   if (bad && rank == 0 && a.status) atomicOr(a.status, MLA_STATUS_BAD_TREE);
   if (tid == 0) sh.path[0] = 0;
   __syncthreads();
-  cluster_wait();
 
   // the first child of cur behind node `after`, or -1 (by a whole warp)
   auto next_child = [&](int cur, int after) {
@@ -215,87 +285,83 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(const VerifyArgs a) {
     }
     return -1;
   };
+  // Warp 0: tells every CTA of the cluster this one's value, and returns CTA
+  // `lane`'s (none: for the lanes without one).  Two barriers take turns: a CTA
+  // that is a pass ahead writes to the other one, and cannot be two ahead, as it
+  // needs this one's value.  (A wait that gave up is the last: what follows
+  // is not valid, and short.)
   int pass = 0;
-  // tells every CTA of the cluster this one's sum (and place)
-  auto tell = [&](float hi, float lo, int at) {
-    if (warp == 0 && lane < C) {
-      const int b = pass & 1;
-      st_cluster(mapa_shared(smem_u32(&sh.all_hi[b][rank]), lane), __float_as_uint(hi));
-      st_cluster(mapa_shared(smem_u32(&sh.all_lo[b][rank]), lane), __float_as_uint(lo));
-      if (MODE == kGreedy) st_cluster(mapa_shared(smem_u32(&sh.all_at[b][rank]), lane), at);
-    }
-    cluster_arrive();
-    cluster_wait();
+  bool lost = false;
+  auto exchange = [&](int64_t v, int64_t none) {
+    if (lost) return none;
+    const int b = pass & 1;
+    const uint32_t bar = smem_u32(&sh.bar[b]);
+    if (lane == 0) sm103::mbar_expect_tx(bar, uint32_t(C) * 8);
+    __syncwarp();
+    if (lane < C)
+      st_async(mapa_shared(smem_u32(&sh.cta[b][rank]), lane), v, mapa_shared(bar, lane));
+    lost = !__all_sync(0xffffffffu, mbar_wait(bar, (pass >> 1) & 1));
+    ++pass;
+    return !lost && lane < C ? *const_cast<volatile int64_t *>(&sh.cta[b][lane]) : none;
   };
   // this CTA's and this warp's steps of 32 pieces
   auto steps_of = [&](const Pieces<T> &x, int &s0, int &s1) {
-    const int steps = (x.count + 31) / 32, per_cta = (steps + C - 1) / C;
+    const int steps = (x.count + 31) / 32, per_cta = (steps + C - 1) >> a.cluster_log2;
     const int c0 = min(rank * per_cta, steps), c1 = min(c0 + per_cta, steps);
-    const int per_warp = (c1 - c0 + VW - 1) / VW;
+    const int per_warp = (c1 - c0 + warps - 1) >> a.warps_log2;
     s0 = min(c0 + warp * per_warp, c1);
     s1 = min(s0 + per_warp, c1);
   };
-  // Is token v among those taken out?
-  auto taken = [&](int v) {
-    for (int i = 0; i < sh.gone; ++i)
-      if (sh.out[i] == v) return true;
-    return false;
+  auto store_path = [&](int kept) {
+    for (int d = tid; d < a.path_ld; d += threads)
+      a.path[int64_t(r) * a.path_ld + d] = d < kept ? sh.path[d] : -1;
+    if (tid == 0) a.kept[r] = kept;
   };
 
   if constexpr (MODE == kGreedy) {
-    int cur = 0, kept = nodes > 0;
-    int best = -1;
+    int cur = 0, kept = nodes > 0, best = -1;
+    cluster_wait();
     while (kept > 0) {
       const Pieces<T> x(P + cur * a.p_ld, nullptr, a.V);
       int s0, s1;
       steps_of(x, s0, s1);
-      float top = neg_inf();
-      int at = a.V;
-      constexpr int U = 4;
+      uint32_t top = 0;
+      int at = 0x7fffffff;
       for (int s = s0; s < s1; s += U) {
-        uint4 v[U], none;
+        uint4 v[U], none[U];
+        x.template load<false>(s, s1, v, none);
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-          if (s + k < s1) x.template load<false>((s + k) * 32 + lane, v[k], none);
+        for (int k = 0; k < U; ++k) {
+          const int e = x.first((s + k) * 32 + lane);
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-          if (s + k < s1) {
-            const int e = x.first((s + k) * 32 + lane);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              if (x.get(v[k], i) > top && e + i >= 0 && e + i < a.V) {  // (rising: ties stay)
-                top = x.get(v[k], i);
-                at = e + i;
-              }
+          for (int i = 0; i < N; ++i) {
+            const uint32_t o = s + k < s1 ? order_of(x.get(v[k], i)) : 0;
+            if (o > top && e + i >= 0 && e + i < a.V) {  // (rising indices: ties stay)
+              top = o;
+              at = e + i;
+            }
           }
-      }
-      auto better = [&](float t, int i) {
-        if (t > top || (t == top && i < at)) {
-          top = t;
-          at = i;
         }
-      };
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        better(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, at, o));
-      if (lane == 0) {
-        sh.hi[warp] = top;
-        sh.out[warp] = at;
       }
+      // the largest value and the lowest of its places
+      auto join = [&](uint32_t t, int i) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, t);
+        const uint32_t f = __reduce_min_sync(0xffffffffu, t == m ? uint32_t(i) : 0x7fffffffu);
+        return int64_t(uint64_t(m) << 32 | f);
+      };
+      int64_t v = join(top, at);
+      if (lane == 0) sh.warp[warp] = v;
       __syncthreads();
       if (warp == 0) {
-        top = lane < VW ? sh.hi[lane] : neg_inf();
-        at = lane < VW ? sh.out[lane] : a.V;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          better(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, at, o));
+        v = lane < warps ? sh.warp[lane] : 0x7fffffff;
+        v = join(uint32_t(uint64_t(v) >> 32), int(v));
+        v = exchange(v, 0x7fffffff);
+        v = join(uint32_t(uint64_t(v) >> 32), int(v));
+        if (lane == 0) sh.border = v;
       }
-      tell(top, 0.f, at);
-      top = neg_inf();
-      at = a.V;
-      for (int c = 0; c < C; ++c) better(sh.all_hi[pass & 1][c], sh.all_at[pass & 1][c]);
-      best = at < a.V ? at : 0;  // (a row of nothing but -inf and NaN)
-      ++pass;
+      __syncthreads();
+      v = sh.border;
+      best = v >> 32 ? int(v) : 0;  // (a row of nothing but -inf and NaN)
       int child = -1;
       if (kept < depth) {
         child = next_child(cur, cur);
@@ -308,136 +374,92 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(const VerifyArgs a) {
     }
     if (rank == 0) {
       __syncthreads();
-      for (int d = tid; d < a.path_ld; d += VT)
-        a.path[int64_t(r) * a.path_ld + d] = d < kept ? sh.path[d] : -1;
-      if (tid == 0) {
-        a.kept[r] = kept;
-        a.next[r] = best;
-      }
+      store_path(kept);
+      if (tid == 0) a.next[r] = best;
     }
     return;
   } else {
-    // the walk's state, the same in all lanes of warp 0
-    int cur = 0, after = 0, kept = nodes > 0, tried = 0;
-    double ca = 1.0, cb = 0.0, mass = 1.0;
-    bool summed = false, told = true;  // told: `mass` is of what is left now
-    // Sums what is left of the row of sh.cur: this warp's sum goes to sh.hi,
-    // sh.lo, the CTAs' to sh.all_hi, sh.all_lo.
-    auto row_pass = [&](auto kind, const Left &l, const Pieces<T> &x, int s0, int s1, bool out) {
-      constexpr int K = decltype(kind)::value, U = 16 / N;  // (16 elements a thread in flight)
-      Sum2 sum;
-      for (int s = s0; s < s1; s += U) {
-        uint4 vp[U], vq[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          vp[k] = vq[k] = make_uint4(0, 0, 0, 0);
-          if (s + k < s1) x.template load<K != 0>((s + k) * 32 + lane, vp[k], vq[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            float hi, lo;
-            left_of<K>(l, x.get(vp[k], i), x.get(vq[k], i), hi, lo);
-            if (out && taken(x.first((s + k) * 32 + lane) + i)) hi = lo = 0.f;
-            sum.add(hi, lo);
-          }
-        sum.renormalise();
-      }
-      return sum;
-    };
-    auto sum_row = [&](const Left &l, const Pieces<T> &x, int s0, int s1) {
-      bool out = false;  // a token that was taken out is in this warp's part
-      if (MODE == kPoint) {
-        const int e0 = x.first(s0 * 32), e1 = x.first(s1 * 32);
-        for (int i = 0; i < sh.gone; ++i) out = out || (sh.out[i] >= e0 && sh.out[i] < e1);
-      }
-      Sum2 s;
-      if (MODE == kPoint || l.kind == 0)
-        s = row_pass(std::integral_constant<int, 0>(), l, x, s0, s1, out);
-      else if (l.kind == 1)
-        s = row_pass(std::integral_constant<int, 1>(), l, x, s0, s1, false);
-      else
-        s = row_pass(std::integral_constant<int, 2>(), l, x, s0, s1, false);
-      s = warp_sum(s);
-      if (lane == 0) {
-        sh.hi[warp] = s.hi;
-        sh.lo[warp] = s.lo;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        s.hi = lane < VW ? sh.hi[lane] : 0.f;
-        s.lo = lane < VW ? sh.lo[lane] : 0.f;
-        s = warp_sum(s);
-      }
-      tell(s.hi, s.lo, 0);
-      double total = 0.0;
-      if (warp == 0 || sh.finish)
-        for (int c = 0; c < C; ++c)
-          total += double(sh.all_hi[pass & 1][c]) + double(sh.all_lo[pass & 1][c]);
-      ++pass;
-      return total;
-    };
     if (nodes == 0) {
+      cluster_wait();
       if (rank == 0) {
-        for (int d = tid; d < a.path_ld; d += VT) a.path[int64_t(r) * a.path_ld + d] = -1;
-        if (tid == 0) {
-          a.kept[r] = 0;
-          a.next[r] = -1;
-        }
+        store_path(0);
+        if (tid == 0) a.next[r] = -1;
       }
       return;
     }
+    // Which of a lane's values of steps s .. s + U - 1 are tokens taken out: N
+    // bits a step.
+    auto taken = [&](const Pieces<T> &x, int s) {
+      uint32_t m = 0;
+      for (int i = 0; i < sh.gone; ++i) {
+        const int e = sh.token[sh.out[i]] + x.head, at = e / (32 * N) - s;
+        if (at >= 0 && at < U && (e / N & 31) == lane) m |= 1u << (at * N + e % N);
+      }
+      return m;
+    };
+    // the walk's state, the same in all lanes of warp 0
+    int cur = 0, after = 0, kept = 1, tried = 0;
+    Left left{{1.f, 0.f}, {0.f, 0.f}};
+    int64_t mass = 0;  // of what is left, from the first rejection on
+    bool told = true;  // it is of what is left now
+    uint4 vp[U], vq[U];
+    int held = -1;  // the node whose values vp, vq hold
     for (;;) {
       if (warp == 0) {
-        bool finish = false;
+        int finish = 0;
         for (;;) {
           const int c = kept < depth ? next_child(cur, after) : -1;
           if (c < 0) {
-            finish = true;
+            finish = 1;
             break;
           }
-          if (!told) {  // the children behind a rejected one need the sum
-            if (MODE == kDraft || !summed) break;
-            told = true;
-          }
+          if (!told) break;  // the children behind a rejected one need the sum
+          const float p = sh.p[c], u = sh.u[c];
           const int x = sh.token[c];
-          double w = fmax(double(sh.p[c]), 0.0), q = 1.0;
-          if (MODE == kDraft) {
-            q = double(sh.q[c]);
-            if (cb != 0.0) w = fmax(ca * double(sh.p[c]) - cb * q, 0.0);
+          bool keep;
+          int64_t w = 0;
+          uint32_t hi, lo;
+          if (tried == 0) {  // S = 1, r = p: u q < p, exactly
+            const float q = MODE == kDraft ? sh.q[c] : 1.f;
+            const float y = __fmul_rn(u, q);
+            keep = y < p || (y == p && __fmaf_rn(u, q, -y) < 0.f);
+          } else if (MODE == kDraft) {
+            const float q = sh.q[c];
+            left_of<2>(left, p, q, hi, lo);
+            keep = part(q, part(u, mass)) < units(hi, lo);
           } else {
-            for (int i = lane; i < tried; i += 32)
-              if (sh.out[i] == x) w = -1.0;
-            if (__any_sync(0xffffffffu, w < 0.0)) w = 0.0;
+            bool again = false;
+            for (int i = lane; i < tried; i += 32) again = again || sh.token[sh.out[i]] == x;
+            left_of<0>(left, p, 0.f, hi, lo);
+            w = __any_sync(0xffffffffu, again) ? 0 : units(hi, lo);
+            keep = part(u, mass) < w;
           }
-          if (double(sh.u[c]) * q * mass < w) {
+          if (keep) {
             if (lane == 0) sh.path[kept] = c;
             ++kept;
             cur = after = c;
             tried = 0;
-            ca = mass = 1.0;
-            cb = 0.0;
-            summed = false;
-            told = true;
+            left = Left{{1.f, 0.f}, {0.f, 0.f}};
             continue;
           }
           after = c;
           if (MODE == kDraft) {
-            if (mass > 0.0) {
-              ca /= mass;
-              cb = cb / mass + 1.0;
+            if (tried == 0) {
+              left.b = Two{1.f, 0.f};
+            } else if (mass > 0) {
+              const Two inv = reciprocal(number(mass));
+              left.a = left.a * inv;
+              left.b = plus_one(left.b * inv);
             }
+            ++tried;
             told = false;
-          } else {
-            if (w > 0.0 || tried == 0) {
-              if (lane == 0) sh.out[tried] = x;
-              ++tried;
-              if (summed)
-                mass -= w;
-              else
-                told = false;
-            }
+          } else if (tried == 0 || w > 0) {
+            if (lane == 0) sh.out[tried] = c;
+            if (tried == 0)
+              told = false;
+            else
+              mass -= w;
+            ++tried;
             __syncwarp();
           }
         }
@@ -446,119 +468,145 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(const VerifyArgs a) {
           sh.kept = kept;
           sh.finish = finish;
           sh.gone = MODE == kPoint ? tried : 0;
-          sh.a = ca;
-          sh.b = cb;
+          sh.kind = MODE == kPoint || tried == 0 ? 0 : tried == 1 ? 1 : 2;
+          if (MODE == kDraft) sh.left = left;
         }
       }
       __syncthreads();
-      const int64_t at = sh.cur;
-      const Pieces<T> x(P + at * a.p_ld, MODE == kDraft ? Q + at * a.q_ld : nullptr, a.V);
+      // ---- the sum of what is left of the row of sh.cur
+      const int node = sh.cur, kind = sh.kind, finish = sh.finish, gone = sh.gone;
+      const Left l = sh.left;
+      const Pieces<T> x(P + node * a.p_ld, MODE == kDraft ? Q + node * a.q_ld : nullptr, a.V);
       int s0, s1;
       steps_of(x, s0, s1);
-      Left l = Left::of(sh.a, sh.b);
-      double total = sum_row(l, x, s0, s1);
-      if (!sh.finish) {
-        if (warp == 0) {
-          mass = total;
-          told = summed = true;
+      const bool fits = s1 - s0 <= U;
+      bool out = false;  // a token that was taken out is in this warp's part
+      int64_t sum = 0;
+      if (MODE == kPoint) {
+        const int e0 = x.first(s0 * 32), e1 = x.first(s1 * 32);
+        for (int i = 0; i < gone; ++i) {
+          const int c = sh.out[i], t = sh.token[c];
+          if (t >= e0 && t < e1) {
+            uint32_t hi, lo;
+            left_of<0>(l, sh.p[c], 0.f, hi, lo);
+            if (lane == 0) sum -= units(hi, lo);
+            out = true;
+          }
         }
-        __syncthreads();  // sh.cur .. are read
-        continue;
       }
-      if (!(total > 0.0)) {  // nothing left (rounded rows): the row itself
-        __syncthreads();
-        l = Left::of(1.0, 0.0);
-        if (tid == 0) sh.gone = 0;
-        __syncthreads();
-        total = sum_row(l, x, s0, s1);
-      }
-      // ---- the next token: the CTA, the warp, the lane, the element
-      const int last = (pass - 1) & 1;
-      const double border = double(__ldg(a.u_next + r)) * total;
-      int owner = -1, some = 0;
-      double before = 0.0, mine = 0.0;
-      for (int c = 0; c < C; ++c) {
-        const double v = double(sh.all_hi[last][c]) + double(sh.all_lo[last][c]);
-        if (v > 0.0) some = c;
-        if (c == rank) mine = before;
-        before += v;
-        if (owner < 0 && before > border) owner = c;
-      }
-      if (owner < 0) owner = some;  // the border is the sum: the last token with mass
-      if (rank == owner) {
-        if (warp == 0) {
-          const double v = lane < VW ? double(sh.hi[lane]) + double(sh.lo[lane]) : 0.0;
-          double inc = v;
+      auto sum_row = [&](auto k_) {
+        constexpr int K = decltype(k_)::value;
+        for (int s = s0; s < s1; s += U) {
+          if (!fits || held != node) x.template load<K != 0>(s, s1, vp, vq);
+          uint32_t hi = 0, lo = 0;  // (at most 32 values of 23 bits)
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-          }
-          const uint32_t over = __ballot_sync(0xffffffffu, lane < VW && mine + inc > border);
-          const uint32_t has = __ballot_sync(0xffffffffu, v > 0.0);
-          const int w = over ? __ffs(int(over)) - 1 : has ? 31 - __clz(int(has)) : 0;
-          const double up_to = __shfl_sync(0xffffffffu, mine + (inc - v), w);
-          if (lane == 0) {
-            sh.cur = w;
-            sh.a = up_to;
-          }
-        }
-        __syncthreads();
-        if (warp == sh.cur) {
-          double base = sh.a;
-          int found = -1, final_some = -1;
-          for (int s = s0; s < s1 && found < 0; ++s) {
-            uint4 vp, vq = make_uint4(0, 0, 0, 0);
-            const int piece = s * 32 + lane, e = x.first(piece);
-            double v[N], sum = 0.0;
-            if (MODE == kDraft && l.kind != 0)
-              x.template load<true>(piece, vp, vq);
-            else
-              x.template load<false>(piece, vp, vq);
+          for (int k = 0; k < U; ++k)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-              float hi, lo;
-              if (MODE == kPoint || l.kind == 0)
-                left_of<0>(l, x.get(vp, i), 0.f, hi, lo);
-              else if (l.kind == 1)
-                left_of<1>(l, x.get(vp, i), x.get(vq, i), hi, lo);
-              else
-                left_of<2>(l, x.get(vp, i), x.get(vq, i), hi, lo);
-              if (MODE == kPoint && taken(e + i)) hi = lo = 0.f;
-              v[i] = double(hi) + double(lo);
-              sum += v[i];
+              uint32_t h, o;
+              left_of<K>(l, x.get(vp[k], i), x.get(vq[k], i), h, o);
+              hi += h;
+              lo += o;
             }
-            double inc = sum;
+          sum += units(hi, lo);
+        }
+      };
+      if (kind == 0)
+        sum_row(std::integral_constant<int, 0>());
+      else if (kind == 1)
+        sum_row(std::integral_constant<int, 1>());
+      else
+        sum_row(std::integral_constant<int, 2>());
+      held = node;
+      sum = warp_sum(sum);
+      if (lane == 0) sh.warp[warp] = sum;
+      __syncthreads();
+      if (warp == 0) {
+        const int64_t of_warp = lane < warps ? sh.warp[lane] : 0;
+        if (pass == 0) cluster_wait();
+        const int64_t of_cta = exchange(warp_sum(of_warp), 0), total = warp_sum(of_cta);
+        if (!finish) {
+          mass = total;
+          told = true;
+          continue;
+        }
+        if (total <= 0 && kind + gone > 0) {
+          if (lane == 0) sh.owner = -2;  // nothing left (rounded rows): the row itself
+        } else {
+          // the border, and whose part it is in: the CTA, then the warp
+          const int64_t border =
+              total > 0 ? min(part(__ldg(a.u_next + r), total), total - 1) : 0;
+          const int64_t up_to = warp_scan(of_cta);
+          const uint32_t over = __ballot_sync(0xffffffffu, up_to > border);
+          const int owner = over ? __ffs(int(over)) - 1 : -1;
+          int of = -1;
+          if (owner == rank) {
+            const int64_t before = __shfl_sync(0xffffffffu, up_to - of_cta, rank);
+            const int64_t inc = before + warp_scan(of_warp);
+            const uint32_t m = __ballot_sync(0xffffffffu, inc > border);
+            of = m ? __ffs(int(m)) - 1 : warps - 1;
+            const int64_t rest = border - __shfl_sync(0xffffffffu, inc - of_warp, of);
+            if (lane == 0) sh.border = rest;
+          } else if (owner < 0 && rank == 0 && lane == 0) {
+            a.next[r] = a.V - 1;  // a row without mass
+          }
+          if (lane == 0) sh.owner = of;
+        }
+      } else if (!finish) {
+        continue;
+      }
+      __syncthreads();
+      if (sh.owner == -2) {
+        if (warp == 0) {
+          tried = 0;  // (no children are left: the walk comes back with the row)
+          left = Left{{1.f, 0.f}, {0.f, 0.f}};
+        }
+        __syncthreads();
+        continue;
+      }
+      // ---- the next token, by the warp that has it: the step, the lane, the value
+      if (warp == sh.owner) {
+        int64_t border = sh.border;
+        int found = -1;
+        // (One step at a time, in little code that runs once: the general form
+        // gives the same units as the others where a or b is 1, b 0.)
+#pragma unroll 1
+        for (int s = s0; s < s1 && found < 0; ++s) {
+          uint4 wp[1], wq[1] = {make_uint4(0, 0, 0, 0)};
+          if (MODE == kDraft && kind != 0)
+            x.template load<true>(s, s1, wp, wq);
+          else
+            x.template load<false>(s, s1, wp, wq);
+          const uint32_t gone_bits = MODE == kPoint && out ? taken(x, s) : 0;
+          int64_t v[N], mine = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const double y = __shfl_up_sync(0xffffffffu, inc, o);
-              if (lane >= o) inc += y;
-            }
-            double run = base + (inc - sum);
-            int here = -1, last_some = -1;
+          for (int i = 0; i < N; ++i) {
+            uint32_t h, o;
+            if (MODE == kPoint)
+              left_of<0>(l, x.get(wp[0], i), 0.f, h, o);
+            else
+              left_of<2>(l, x.get(wp[0], i), x.get(wq[0], i), h, o);
+            v[i] = gone_bits >> i & 1 ? 0 : units(h, o);
+            mine += v[i];
+          }
+          const int64_t inc = warp_scan(mine);
+          const uint32_t hit = __ballot_sync(0xffffffffu, inc > border);
+          if (hit) {
+            const int e = x.first(s * 32 + lane);
+            int64_t run = inc - mine;
+            int here = e + N - 1;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
               run += v[i];
-              if (v[i] > 0.0) {
-                last_some = e + i;
-                if (here < 0 && run > border) here = e + i;
-              }
+              if (run > border) here = min(here, e + i);
             }
-            const uint32_t hit = __ballot_sync(0xffffffffu, here >= 0);
-            const uint32_t has = __ballot_sync(0xffffffffu, last_some >= 0);
-            if (has) final_some = __shfl_sync(0xffffffffu, last_some, 31 - __clz(int(has)));
-            if (hit) found = __shfl_sync(0xffffffffu, here, __ffs(int(hit)) - 1);
-            base += __shfl_sync(0xffffffffu, inc, 31);
+            found = __shfl_sync(0xffffffffu, here, __ffs(int(hit)) - 1);
           }
-          if (found < 0) found = final_some >= 0 ? final_some : a.V - 1;
-          if (lane == 0) a.next[r] = found;
+          border -= __shfl_sync(0xffffffffu, inc, 31);
         }
+        if (lane == 0) a.next[r] = found < 0 || found >= a.V ? a.V - 1 : found;
       }
-      if (rank == 0) {
-        for (int d = tid; d < a.path_ld; d += VT)
-          a.path[int64_t(r) * a.path_ld + d] = d < sh.kept ? sh.path[d] : -1;
-        if (tid == 0) a.kept[r] = sh.kept;
-      }
+      if (rank == 0) store_path(sh.kept);
       return;
     }
   }
@@ -571,16 +619,24 @@ int launch_verify(const void *p, int64_t p_ld, const void *q, int64_t q_ld, int 
                   const float *u, const float *u_next, int32_t *path, int path_ld, int32_t *kept,
                   int32_t *next, int32_t *status, cudaStream_t s) {
   VerifyArgs a{p, q, p_ld, q_ld, tokens, parents, qsl, u, u_next, path, kept, next, status,
-               T, V, path_ld, 1};
-  // two CTAs an SM
-  while (a.cluster < MAX_CLUSTER && int64_t(R) * a.cluster * 2 <= 2 * num_sms()) a.cluster *= 2;
+               T, V, path_ld, 0, 5};
+  // Clusters of 8 while four CTAs of 256 threads an SM hold them all; 1024
+  // threads an SM.
+  const int sms = num_sms();
+  while (2 << a.cluster_log2 <= MAX_CLUSTER && (int64_t(R) * 2 << a.cluster_log2) <= 4 * sms)
+    ++a.cluster_log2;
+  while (a.warps_log2 > 3 && (int64_t(R) << a.cluster_log2) > (int64_t(sms) << (5 - a.warps_log2)))
+    --a.warps_log2;
+  const int threads = 32 << a.warps_log2;
   auto pick = [&](auto t) {
     using E = decltype(t);
     return !u ? verify_kernel<E, kGreedy> : q ? verify_kernel<E, kDraft> : verify_kernel<E, kPoint>;
   };
   auto *kernel = dtype == MLA_DTYPE_BF16 ? pick(__nv_bfloat16()) : pick(float());
-  return launch_chained(kernel, dim3(unsigned(R) * unsigned(a.cluster)), VT, 0, a.cluster, s,
-                        "verify_kernel", a);
+  return launch_chained(kernel, dim3(unsigned(R) << a.cluster_log2), threads, 0,
+                        1 << a.cluster_log2, s, "verify_kernel", a);
 }
+
+int verify_take_errors() { return sm103::take_error_flags_here(); }
 
 }  // namespace mla

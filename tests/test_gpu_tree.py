@@ -1,7 +1,7 @@
 """Parity of the calls on trees of drafted tokens with the float64 oracle.
 Attention tolerances as in test_gpu_decode.py (the same arithmetic); layout,
 verification and commit are whole numbers and moved rows, which have to be
-equal but where a random number is next to a border (SLACK below)."""
+equal but where a random number is next to a border (slack below)."""
 
 import math
 
@@ -295,15 +295,15 @@ def run_verify(p, q, tokens, parents, qsl, u, un, most, status=None):
     return path.cpu().numpy(), kept.cpu().numpy(), nxt.cpu().numpy()
 
 
-# How near the next token's border decides otherwise than exact sums.  A thread
-# adds at most n = 16 * ceil(V / 8192) values here (512 threads a CTA, pieces of
-# 16 bytes, 16 values between renormalisations); between these |lo| <= 17 * 2^-24
-# hi, so that a rounding of lo is at most 2^-24 * 2^-19.9 hi, and all of them
-# n 2^-43.9 of the sum: 2^-35.9 for the largest n, 256.  The joins of 32 lanes,
-# 16 warps and 8 CTAs add 2^-44, the oracle's own sums V 2^-53.  (A row of equal
-# shares whose border is exactly the end of one, as in test_verify_borders, is
-# decided by the oracle's own rounding.)
-SLACK = 2.0 ** -35
+# How near the next token's border decides otherwise than exact sums, as a part
+# of the sum: a value is rounded to units of 2^-45, by at most 2^-46, and before
+# that a p - b q is off by some 2^-47 (a and b have 48 bits); sums of units are
+# exact.  Over V values 2^-45 V of a sum of 1, and a row's sum is about 1 here
+# (or more).  The oracle's own sums are off by 2^-53 V.  (A row of equal shares
+# whose border is exactly the end of one, as in test_verify_borders, is decided
+# by the oracle's own rounding.)
+def slack(V):
+    return V * 2.0 ** -45
 
 
 def check_verify(got, p, q, tokens, parents, qsl, u, un, most):
@@ -313,7 +313,7 @@ def check_verify(got, p, q, tokens, parents, qsl, u, un, most):
         lo, hi = qsl[r], qsl[r + 1]
         f = lambda x: None if x is None else np.asarray(x, np.float32)[lo:hi]  # noqa: E731
         rp, rn, near = TR.verify(p[lo:hi], None if q is None else q[lo:hi], tokens[lo:hi], parents[lo:hi], f(u),
-                                 None if un is None else np.float32(un[r]), most, SLACK)
+                                 None if un is None else np.float32(un[r]), most, slack(p.shape[1]))
         assert kept[r] == len(rp) and nxt[r] in near, (r, kept[r], rp, nxt[r], rn)
         assert path[r].tolist() == rp + [-1] * (most - len(rp))
 
