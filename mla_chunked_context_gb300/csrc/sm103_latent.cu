@@ -383,10 +383,18 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
     tma_load_2d(dst, m, bar, x, y);
 }
 
-// V of the pair form lies in groups of 16 keys (an MMA's K): [4 column blocks][16
-// keys][64 columns], so that one copy brings a group whatever the page size
-// (a multiple of 16).
-constexpr int V_GROUP = 4 * 16 * 128;
+// V of the pair form lies in groups of 2^vb keys: [4 column blocks][2^vb keys]
+// [64 columns].  Pages of 64 and 32 keys (and their multiples) make groups of
+// that many, a copy for each column block; others groups of 16 (an MMA's K),
+// which one copy of three dimensions brings.
+struct VLayout {
+  int vb;
+  __device__ __forceinline__ explicit VLayout(int box_log2) : vb(min(max(box_log2, 4), 6)) {}
+  __device__ __forceinline__ uint32_t block() const { return 128u << vb; }  // bytes to the next
+  __device__ __forceinline__ uint32_t row(int j) const {  // of key j's first column block
+    return (uint32_t(j >> vb) << (vb + 9)) + (uint32_t(j & ((1 << vb) - 1)) << 7);
+  }
+};
 
 // A box of cache rows from `row`, the first `valid` of them real and the others
 // zeros, to dst and, `count` times, on to the next column block `step` bytes
@@ -494,15 +502,15 @@ __device__ __noinline__ uint64_t hidden_rows(const LatentArgs &a, int row0, int 
 // A tile's V, row by row, without the hidden ones and those from `keys` on.
 template <bool PAIR>
 __device__ __noinline__ void load_unhidden(const Maps &m, int row0, int row1, int bl, int keys,
-                                           uint64_t hidden, uint32_t dst, int x, int none,
-                                           uint32_t bar) {
+                                           uint64_t hidden, uint32_t dst, VLayout lay, int x,
+                                           int none, uint32_t bar) {
   for (int j = 0; j < TILE; ++j) {
     const int i = j >> bl;
     const int r = __shfl_sync(0xffffffffu, i < 32 ? row0 : row1, i & 31);
     const bool real = r != none && j < keys && !(hidden >> j & 1);
     if (elect_one())
-      load_rows<PAIR>(m, 0, dst + (j >> 4) * V_GROUP + (j & 15) * 128, 16 * 128, 4, x,
-                      r + (j & ((1 << bl) - 1)), real, none, bar);
+      load_rows<PAIR>(m, 0, dst + lay.row(j), lay.block(), 4, x, r + (j & ((1 << bl) - 1)), real,
+                      none, bar);
     __syncwarp();
   }
 }
@@ -595,7 +603,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t full_lead = lead(full);
     const uint32_t dst0 = is_v ? sV : sK, stage_bytes = is_v ? C::V_STAGE : C::K_STAGE;
     const int nrows = is_v ? 64 : C::KROWS, blocks = is_v ? 4 : NBLK;
-    const int bl = min(a.box_log2, is_v ? 4 : PAIR ? 5 : 6), bx = 1 << bl;  // rows at once
+    const VLayout lay(a.box_log2);
+    const int bl = min(a.box_log2, is_v ? lay.vb : PAIR ? 5 : 6), bx = 1 << bl;  // rows at once
     const int skip = PAIR && !is_v ? int(rank) * C::KROWS : 0;  // first key of the tile here
     Walk<PAIR, TREE> w(a, *share);
     int g = 0, checked = 0;
@@ -631,7 +640,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (hidden) {
           load_unhidden<PAIR>(m, row[0], row[1], bl, any - key0, hidden, dst0 + st * stage_bytes,
-                              int(rank) * 256, none, full_lead + 8 * st);
+                              lay, int(rank) * 256, none, full_lead + 8 * st);
           continue;
         }
         for (int i = 0; i < nrows >> bl; ++i) {
@@ -644,10 +653,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!is_v)
               load_rows<PAIR>(m, bl, dst + off * 128, nrows * 128, blocks, 0, r, valid, none, bar);
             else if (bl == 4 && (valid == 0 || valid == 16))
-              tma_load_3d_pair(dst + (off >> 4) * V_GROUP, &m.v, bar, 0, r, int(rank) * 4);
+              tma_load_3d_pair(dst + lay.row(off), &m.v, bar, 0, r, int(rank) * 4);
             else
-              load_rows<PAIR>(m, bl, dst + (off >> 4) * V_GROUP + (off & 15) * 128, 16 * 128, 4,
-                              int(rank) * 256, r, valid, none, bar);
+              load_rows<PAIR>(m, bl, dst + lay.row(off), lay.block(), 4, int(rank) * 256, r, valid,
+                              none, bar);
           }
           __syncwarp();
         }
@@ -658,11 +667,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           // hidden, one takes some 600 clocks.)
           ok = __all_sync(0xffffffffu, mbar_wait(v_own, checked++ & 1));
           if (!ok) break;
-          const uint32_t v = dst0 + st * stage_bytes + (lane >> 3) * (16 * 128) + (lane & 7) * 16;
+          const uint32_t v = dst0 + st * stage_bytes + (lane >> 3) * lay.block() + (lane & 7) * 16;
           const int to = min(TILE, any - key0);
 #pragma unroll 4
           for (int j = max(0, all - key0); j < to; ++j) {
-            const uint32_t at = v + (j >> 4) * V_GROUP + (j & 15) * 128;
+            const uint32_t at = v + lay.row(j);
             if (not_finite(ld_shared_v4(at))) st_shared_v4(at, make_uint4(0, 0, 0, 0));
           }
           fence_async_smem();
@@ -742,10 +751,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           mma_commit(bar);
       };
       const uint32_t q_lo = desc_lo_k(sQ), k_lo = desc_lo_k(sK), p_lo = desc_lo_k(sP);
-      // V, MN-major: blocks of 64 columns BLK_BYTES (pair: 16 rows) apart
-      const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, PAIR ? 16 * 128 : BLK_BYTES);
-      constexpr uint32_t V_KS = (PAIR ? V_GROUP : 2048) >> 4;  // 16 keys
-      constexpr uint32_t V_J = PAIR ? 2 * 16 * 128 >> 4 : 4 * BLK;  // second MMA's columns
+      // V, MN-major: blocks of 64 columns BLK_BYTES (pair: a group's rows) apart
+      const VLayout lay(a.box_log2);
+      const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, PAIR ? lay.block() : BLK_BYTES);
+      const uint32_t v_ks = (PAIR && lay.vb == 4 ? 4 * 16 * 128 : 2048) >> 4;  // 16 keys
+      const uint32_t v_ks2 = (PAIR ? lay.row(32) : 4096) >> 4;                 // 32
+      const uint32_t v_j = PAIR ? 2 * lay.block() >> 4 : 4 * BLK;  // second MMA's columns
       constexpr uint32_t K_STEP = C::K_STAGE >> 4, V_STEP = (PAIR ? C::V_STAGE : C::K_STAGE) >> 4;
       constexpr uint32_t KBLK = C::KROWS * 128 >> 4;
       // O (+)= P V of tile g
@@ -761,7 +772,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            mma_lo<PAIR>(tmem + j * 128, p + ks * 2, v + j * V_J + ks * V_KS, id_o,
+            mma_lo<PAIR>(tmem + j * 128, p + ks * 2,
+                         v + j * v_j + (ks & 1) * v_ks + (ks >> 1) * v_ks2, id_o,
                          ks == 0 ? acc0 : 1);
         commit((PAIR ? v_empty : k_empty) + 8 * st);
         commit(pv_done + 8 * st);
