@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = base + u * GROUPS + group;
-      seen[u] = sees(j);
-      blk[u] = seen[u] ? __ldg(bt + a.by_bs.quotient(j)) : -1;
+      if (TREE) seen[u] = sees(j);
+      blk[u] = (TREE ? seen[u] : j < nk) ? __ldg(bt + a.by_bs.quotient(j)) : -2;
     }
   };
   look_up(0);
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(32 * AW) latent_attn_simt(LatentArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = base + u * GROUPS + group;
-      live[u] = seen[u];
+      live[u] = TREE ? seen[u] : j < nk;
       const bool good = blk[u] >= 0 && blk[u] < a.num_blocks;
       if (live[u] && !good) bad = true;
       const T *row = cache + (int64_t(blk[u]) * a.bs + (j - a.by_bs.quotient(j) * a.bs)) * LP;

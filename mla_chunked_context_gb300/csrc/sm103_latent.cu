@@ -383,16 +383,20 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
     tma_load_2d(dst, m, bar, x, y);
 }
 
-// V of the pair form lies in groups of 2^vb keys: [4 column blocks][2^vb keys]
-// [64 columns].  Pages of 64 and 32 keys (and their multiples) make groups of
-// that many, a copy for each column block; others groups of 16 (an MMA's K),
-// which one copy of three dimensions brings.
+// V of the pair form lies in groups of 2^VB keys: [4 column blocks][2^VB keys][64
+// columns].  Pages of 64 keys and their multiples make groups of 64, a copy for
+// each column block; others groups of 16 (an MMA's K), which one copy of three
+// dimensions brings whatever the page size (a multiple of 16).  Such a copy
+// takes 330 clocks to issue, one of two dimensions with as many bytes 190 (pages
+// of 64, 16 x 32 tokens x 4096 keys: 460 us with groups of 16, 437 with 64); but
+// 16 copies of 16 rows take longer than four of them (pages of 16, 24 ragged
+// trees: 117, so 105).
+template <int VB>
 struct VLayout {
-  int vb;
-  __device__ __forceinline__ explicit VLayout(int box_log2) : vb(min(max(box_log2, 4), 6)) {}
-  __device__ __forceinline__ uint32_t block() const { return 128u << vb; }  // bytes to the next
-  __device__ __forceinline__ uint32_t row(int j) const {  // of key j's first column block
-    return (uint32_t(j >> vb) << (vb + 9)) + (uint32_t(j & ((1 << vb) - 1)) << 7);
+  static constexpr uint32_t BLOCK = 128u << VB;  // bytes to the next column block
+  // of key j's row in the first column block
+  __device__ __forceinline__ static uint32_t row(int j) {
+    return (uint32_t(j >> VB) << (VB + 9)) + (uint32_t(j & ((1 << VB) - 1)) << 7);
   }
 };
 
@@ -437,10 +441,24 @@ __device__ __forceinline__ uint32_t desc_lo_k(uint32_t saddr) {
 __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t mn_block_bytes) {
   return ((saddr >> 4) & 0x3FFF) | ((mn_block_bytes >> 4) << 16);
 }
-template <bool PAIR>
+template <bool PAIR, int A = 0>
 __device__ __forceinline__ void mma_lo(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc,
                                        uint32_t acc) {
-  if (PAIR)
+  if (PAIR && A == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n"
+        " mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::2.kind::f16.collector::a::fill [%0], x, y, %4, p;\n}\n" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(DESC_HI), "r"(idesc), "r"(acc)
+        : "memory");
+  else if (PAIR && A == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n"
+        " mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [%0], x, y, %4, p;\n}\n" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(DESC_HI), "r"(idesc), "r"(acc)
+        : "memory");
+  else if (PAIR)
     asm volatile(
         "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n"
         " mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
@@ -500,17 +518,17 @@ __device__ __noinline__ uint64_t hidden_rows(const LatentArgs &a, int row0, int 
 }
 
 // A tile's V, row by row, without the hidden ones and those from `keys` on.
-template <bool PAIR>
+template <bool PAIR, int VB>
 __device__ __noinline__ void load_unhidden(const Maps &m, int row0, int row1, int bl, int keys,
-                                           uint64_t hidden, uint32_t dst, VLayout lay, int x,
-                                           int none, uint32_t bar) {
+                                           uint64_t hidden, uint32_t dst, int x, int none,
+                                           uint32_t bar) {
   for (int j = 0; j < TILE; ++j) {
     const int i = j >> bl;
     const int r = __shfl_sync(0xffffffffu, i < 32 ? row0 : row1, i & 31);
     const bool real = r != none && j < keys && !(hidden >> j & 1);
     if (elect_one())
-      load_rows<PAIR>(m, 0, dst + lay.row(j), lay.block(), 4, x, r + (j & ((1 << bl) - 1)), real,
-                      none, bar);
+      load_rows<PAIR>(m, 0, dst + VLayout<VB>::row(j), VLayout<VB>::BLOCK, 4, x,
+                      r + (j & ((1 << bl) - 1)), real, none, bar);
     __syncwarp();
   }
 }
@@ -525,10 +543,11 @@ __device__ __forceinline__ void softmax_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(STHREADS) : "memory");
 }
 
-template <bool PAIR, bool TREE>
+template <bool PAIR, bool TREE, int VB>
 __global__ void __launch_bounds__(THREADS, 1)
     latent_attn_kernel(const __grid_constant__ Maps m, const LatentArgs a) {
   using C = Cfg<PAIR>;
+  using Lay = VLayout<VB>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -603,8 +622,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t full_lead = lead(full);
     const uint32_t dst0 = is_v ? sV : sK, stage_bytes = is_v ? C::V_STAGE : C::K_STAGE;
     const int nrows = is_v ? 64 : C::KROWS, blocks = is_v ? 4 : NBLK;
-    const VLayout lay(a.box_log2);
-    const int bl = min(a.box_log2, is_v ? lay.vb : PAIR ? 5 : 6), bx = 1 << bl;  // rows at once
+    const int bl = min(a.box_log2, is_v ? VB : PAIR ? 5 : 6), bx = 1 << bl;  // rows at once
     const int skip = PAIR && !is_v ? int(rank) * C::KROWS : 0;  // first key of the tile here
     Walk<PAIR, TREE> w(a, *share);
     int g = 0, checked = 0;
@@ -639,8 +657,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
         if (hidden) {
-          load_unhidden<PAIR>(m, row[0], row[1], bl, any - key0, hidden, dst0 + st * stage_bytes,
-                              lay, int(rank) * 256, none, full_lead + 8 * st);
+          load_unhidden<PAIR, VB>(m, row[0], row[1], bl, any - key0, hidden,
+                                  dst0 + st * stage_bytes, int(rank) * 256, none,
+                                  full_lead + 8 * st);
           continue;
         }
         for (int i = 0; i < nrows >> bl; ++i) {
@@ -650,12 +669,21 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int valid = r == none ? 0 : PAIR && !is_v ? bx : min(bx, any - key0 - off);
           if (elect_one()) {
             const uint32_t dst = dst0 + st * stage_bytes, bar = own ? v_own : full_lead + 8 * st;
-            if (!is_v)
+            if (VB == 6 && !is_v) {  // one box of 32 keys: straight through
+              const int y = valid > 0 ? r : none;
+#pragma unroll
+              for (int b = 0; b < NBLK; ++b)
+                tma_load_2d_pair(dst + b * (C::KROWS * 128), &m.c[5], bar, b * 64, y);
+            } else if (VB == 6 && valid == TILE) {  // one of 64
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                tma_load_2d_pair(dst + b * Lay::BLOCK, &m.c[6], bar, int(rank) * 256 + b * 64, r);
+            } else if (!is_v)
               load_rows<PAIR>(m, bl, dst + off * 128, nrows * 128, blocks, 0, r, valid, none, bar);
-            else if (bl == 4 && (valid == 0 || valid == 16))
-              tma_load_3d_pair(dst + lay.row(off), &m.v, bar, 0, r, int(rank) * 4);
+            else if (VB == 4 && bl == 4 && (valid == 0 || valid == 16))
+              tma_load_3d_pair(dst + Lay::row(off), &m.v, bar, 0, r, int(rank) * 4);
             else
-              load_rows<PAIR>(m, bl, dst + lay.row(off), lay.block(), 4, int(rank) * 256, r, valid,
+              load_rows<PAIR>(m, bl, dst + Lay::row(off), Lay::BLOCK, 4, int(rank) * 256, r, valid,
                               none, bar);
           }
           __syncwarp();
@@ -667,11 +695,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           // hidden, one takes some 600 clocks.)
           ok = __all_sync(0xffffffffu, mbar_wait(v_own, checked++ & 1));
           if (!ok) break;
-          const uint32_t v = dst0 + st * stage_bytes + (lane >> 3) * lay.block() + (lane & 7) * 16;
+          const uint32_t v = dst0 + st * stage_bytes + (lane >> 3) * Lay::BLOCK + (lane & 7) * 16;
           const int to = min(TILE, any - key0);
 #pragma unroll 4
           for (int j = max(0, all - key0); j < to; ++j) {
-            const uint32_t at = v + lay.row(j);
+            const uint32_t at = v + Lay::row(j);
             if (not_finite(ld_shared_v4(at))) st_shared_v4(at, make_uint4(0, 0, 0, 0));
           }
           fence_async_smem();
@@ -752,11 +780,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       const uint32_t q_lo = desc_lo_k(sQ), k_lo = desc_lo_k(sK), p_lo = desc_lo_k(sP);
       // V, MN-major: blocks of 64 columns BLK_BYTES (pair: a group's rows) apart
-      const VLayout lay(a.box_log2);
-      const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, PAIR ? lay.block() : BLK_BYTES);
-      const uint32_t v_ks = (PAIR && lay.vb == 4 ? 4 * 16 * 128 : 2048) >> 4;  // 16 keys
-      const uint32_t v_ks2 = (PAIR ? lay.row(32) : 4096) >> 4;                 // 32
-      const uint32_t v_j = PAIR ? 2 * lay.block() >> 4 : 4 * BLK;  // second MMA's columns
+      const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, PAIR ? Lay::BLOCK : BLK_BYTES);
+      constexpr uint32_t V_KS = (PAIR && VB == 4 ? 4 * 16 * 128 : 2048) >> 4;  // 16 keys
+      constexpr uint32_t V_J = PAIR ? 2 * Lay::BLOCK >> 4 : 4 * BLK;  // second MMA's columns
       constexpr uint32_t K_STEP = C::K_STAGE >> 4, V_STEP = (PAIR ? C::V_STAGE : C::K_STAGE) >> 4;
       constexpr uint32_t KBLK = C::KROWS * 128 >> 4;
       // O (+)= P V of tile g
@@ -770,11 +796,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t v = v_lo + st * V_STEP, p = p_lo + (PAIR ? st * BLK : 0);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            mma_lo<PAIR>(tmem + j * 128, p + ks * 2,
-                         v + j * v_j + (ks & 1) * v_ks + (ks >> 1) * v_ks2, id_o,
-                         ks == 0 ? acc0 : 1);
+          {
+            const uint32_t vk = v + ks * V_KS, acc = ks == 0 ? acc0 : 1;
+            // (P's rows are read for the first MMA and kept for the second)
+            mma_lo<PAIR, 1>(tmem, p + ks * 2, vk, id_o, acc);
+            mma_lo<PAIR, 2>(tmem + 128, p + ks * 2, vk + V_J, id_o, acc);
+          }
         commit((PAIR ? v_empty : k_empty) + 8 * st);
         commit(pv_done + 8 * st);
         return true;
@@ -1288,7 +1315,7 @@ __global__ void __launch_bounds__(CT) latent_combine_kernel(const int4 *desc, in
   }
 }
 
-template <bool PAIR, bool TREE>
+template <bool PAIR, bool TREE, int VB>
 int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaStream_t s) {
   constexpr int MAX_DEV = 64;
   static std::atomic<int> grid_of[MAX_DEV];  // CTAs that fit the device, 0: not asked yet
@@ -1307,20 +1334,20 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
   cfg.numAttrs = 1;
   int grid = grid_of[dev].load(std::memory_order_acquire);
   if (grid == 0) {
-    if (cudaFuncSetAttribute(latent_attn_kernel<PAIR, TREE>,
+    if (cudaFuncSetAttribute(latent_attn_kernel<PAIR, TREE, VB>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Cfg<PAIR>::SMEM) != cudaSuccess)
       return MLA_ERR_CUDA;
     const int cs = PAIR ? 2 : 1;
     cfg.gridDim = dim3(cs * (num_sms() / cs));
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<PAIR, TREE>, &cfg) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<PAIR, TREE, VB>, &cfg) != cudaSuccess ||
         n < 1)
       n = num_sms() / cs;
     grid = std::min(cs * n, urows_limit);
     grid_of[dev].store(grid, std::memory_order_release);
   }
-  int rc = launch_chained(latent_attn_kernel<PAIR, TREE>, grid, THREADS, Cfg<PAIR>::SMEM,
+  int rc = launch_chained(latent_attn_kernel<PAIR, TREE, VB>, grid, THREADS, Cfg<PAIR>::SMEM,
                           PAIR ? 2 : 1, s, TREE ? "tree_attn_kernel" : "latent_attn_kernel", maps,
                           a);
   if (rc) return rc;
@@ -1376,12 +1403,14 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, const TreeMask &tree,
   // (16 x 4096, 64 heads: 52.5, 28.3).  The average is over the slots, of which
   // those without tokens count (their lengths are on the device): 8 of 32 slots x
   // 4096, 128 heads, run single in 51.6 us, pairs 34.8.
-  const bool pair = int64_t(T) * d.num_heads > int64_t(64) * R;
-  if (tree.bits)
-    return pair ? launch_latent<true, true>(maps, a, max_ctas, s)
-                : launch_latent<false, true>(maps, a, max_ctas, s);
-  return pair ? launch_latent<true, false>(maps, a, max_ctas, s)
-              : launch_latent<false, false>(maps, a, max_ctas, s);
+  auto launch = [&](auto tree_mask) {
+    constexpr bool TREE = decltype(tree_mask)::value;
+    if (int64_t(T) * d.num_heads <= int64_t(64) * R)
+      return launch_latent<false, TREE, 4>(maps, a, max_ctas, s);
+    return box_log2 == 6 ? launch_latent<true, TREE, 6>(maps, a, max_ctas, s)
+                         : launch_latent<true, TREE, 4>(maps, a, max_ctas, s);
+  };
+  return tree.bits ? launch(std::true_type()) : launch(std::false_type());
 }
 
 int latent_take_errors() { return sm103::take_error_flags_here(); }
