@@ -706,8 +706,8 @@ int mla_tree_attn(const mla_dims_t *d, int32_t num_seqs,
  *             path_ld nodes are kept: the path_ld-th is taken for a leaf.
  *   num_kept  device int32 [num_seqs].  A sequence without new tokens has 0 and
  *             next_tokens -1.
- *   Values are held in units of 2^-45: the results are those of exact sums but
- *   for borders nearer than vocab * 2^-45.  They have to be at least 0 and less
+ *   Values are held in units of 2^-45 (before r is divided by its sum): the
+ *   results are those of exact sums but for borders nearer than vocab * 2^-45.  They have to be at least 0 and less
  *   than 2, a row's sum less than 512 (probabilities' is 1); what a row that is
  *   not gives is not specified, but its tokens are below vocab.  Greedy: NaN
  *   counts as -infinity, and a row of nothing else gives token 0.

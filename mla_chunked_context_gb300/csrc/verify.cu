@@ -3,10 +3,11 @@
 //
 // From the root on, at a node with target row p, its children c in index order:
 //   with draft rows   r = p at first; kept when u_c q(x_c) < r(x_c); else
-//                     r <- max(r - q, 0) / S, S the sum of max(r - q, 0).  So r
-//                     = max(a p - b q, 0) always, with a = b = 1 after the first
-//                     rejection and then a <- a / S, b <- b / S + 1: a rejection
-//                     costs one sum over the row and nothing is stored.
+//                     r <- max(r - q, 0) / (its sum).  So r is always
+//                     max(p - t q, 0) / S, S the sum of max(p - t q, 0), with t =
+//                     0, S = 1 at first, t = 1 after a rejection and t <- t + S
+//                     after each further one: a rejection costs one sum over the
+//                     row, and nothing is stored or divided.
 //   without           kept when u_c S < p(x_c), S = 1 at first and then the sum
 //                     of p without the tokens rejected before.
 //   greedy            kept when x_c is the row's largest value.
@@ -63,70 +64,51 @@ struct VerifyArgs {
 struct Two {
   float hi, lo;
 };
-__device__ __forceinline__ Two two(float hi, float lo) {  // |hi| >= |lo|
-  const float s = __fadd_rn(hi, lo);
-  return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
-}
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-  const float h = __fmul_rn(a.hi, b.hi);
-  return two(h, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -h))));
-}
-__device__ __forceinline__ Two plus_one(Two a) {
-  const float s = __fadd_rn(a.hi, 1.f), b = __fsub_rn(s, a.hi);
-  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, b)), __fsub_rn(1.f, b));
-  return two(s, __fadd_rn(e, a.lo));
-}
-__device__ __forceinline__ Two reciprocal(Two a) {  // one step of Newton's from float32's
-  const float r = 1.f / a.hi;
-  const float e = __fmaf_rn(-a.lo, r, __fmaf_rn(-a.hi, r, 1.f));
-  return two(r, __fmul_rn(r, e));
-}
-
-// What is left of a row: max(a p - b q, 0).
-struct Left {
-  Two a, b;
-};
 
 // Values in units of 2^-45 (0 <= w < 2): w = hi * 2^-22 + lo * 2^-45.
 constexpr float GRID = 2.f, FINE = 1.5f / 4194304.f;
 constexpr uint32_t GRID_BITS = 0x40000000u, FINE_BITS = 0x34C00000u;
+constexpr int64_t ONE = int64_t(1) << 45;
 __device__ __forceinline__ int64_t units(uint32_t hi, uint32_t lo) {
   return (int64_t(int32_t(hi)) << 23) + int32_t(lo);
 }
-// A sum of units as a number; x times a sum, rounded down (0 <= x <= 1).
-__device__ __forceinline__ Two number(int64_t v) {
-  const float hi = float(v);
-  return {hi * (1.f / 35184372088832.f), float(v - int64_t(hi)) * (1.f / 35184372088832.f)};
+// A sum of units as a number; x times a sum, rounded down (0 <= x <= 1).  By
+// conversions of 32 bits, as those of 64 are slow.
+__device__ __forceinline__ Two number(int64_t v) {  // 0 <= v < 2^54
+  const int a = int(v >> 24);
+  const float hi = float(a);
+  const float lo = float(a - int(hi)) * 16777216.f + float(int(v & 0xffffff));
+  return {hi * (1.f / 2097152.f), lo * (1.f / 35184372088832.f)};
 }
 __device__ __forceinline__ int64_t part(float x, int64_t v) {
-  if (x >= 1.f) return v;
-  return int64_t(__umul64hi(__float2ull_rz(x * 18446744073709551616.f), uint64_t(v)));
+  if (!(x < 1.f)) return v;
+  const float y = x * 4294967296.f;
+  const uint32_t hi = __float2uint_rz(y);
+  const uint32_t lo = __float2uint_rz(__fsub_rn(y, truncf(y)) * 4294967296.f);
+  return int64_t(__umul64hi(uint64_t(hi) << 32 | lo, uint64_t(v)));
 }
 
-// hi and lo of one value; KIND 0: p, 1: p - q, 2: a p - b q.  What the grid
-// leaves of w is computed from the parts of w, without its rounding.  (Integer
-// instructions and minima have half the rate of float32 sums, hence no more of
-// them than this.)
-template <int KIND>
-__device__ __forceinline__ void left_of(const Left &l, float p, float q, uint32_t &hi,
-                                        uint32_t &lo) {
-  float x = p, y = 0.f, e = 0.f;
-  if (KIND == 1) y = fminf(q, x);
-  if (KIND == 2) {
-    x = __fmul_rn(l.a.hi, p);
-    y = __fmul_rn(l.b.hi, q);
-    e = __fsub_rn(__fmaf_rn(l.a.hi, p, -x), __fmaf_rn(l.b.hi, q, -y));
-    e = __fmaf_rn(l.a.lo, p, e);
-    e = __fmaf_rn(-l.b.lo, q, e);
-    e = y < x ? e : 0.f;
-    y = fminf(y, x);
+// Adds one value, max(p - t q, 0) or (without Q) p, to hi and lo.  What the grid
+// leaves of it, p - i - t q, has one rounding, of 2^-24 of that little.  (Integer
+// instructions, minima and choices have half the rate of float32 sums, hence no
+// more of them than this.)
+template <bool Q>
+__device__ __forceinline__ void add_left(Two t, float p, float q, uint32_t &hi, uint32_t &lo) {
+  const float d = Q ? __fmaf_rn(-t.hi, q, p) : p;
+  const float g = __fadd_rn(d, GRID);
+  float rest = __fsub_rn(p, __fsub_rn(g, GRID));
+  if (Q) rest = __fmaf_rn(-t.lo, q, __fmaf_rn(-t.hi, q, rest));
+  const float f = __fadd_rn(rest, FINE);
+  if (!Q || d > 0.f) {
+    hi += __float_as_uint(g) - GRID_BITS;
+    lo += __float_as_uint(f) - FINE_BITS;
   }
-  const float t = __fadd_rn(KIND == 0 ? x : __fsub_rn(x, y), GRID);
-  float rest = __fsub_rn(x, __fsub_rn(t, GRID));
-  if (KIND != 0) rest = __fsub_rn(rest, y);
-  if (KIND == 2) rest = __fadd_rn(rest, e);
-  hi = __float_as_uint(t) - GRID_BITS;
-  lo = __float_as_uint(__fadd_rn(rest, FINE)) - FINE_BITS;
+}
+template <bool Q>
+__device__ __forceinline__ int64_t left_of(Two t, float p, float q) {
+  uint32_t hi = 0, lo = 0;
+  add_left<Q>(t, p, q, hi, lo);
+  return units(hi, lo);
 }
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {  // |v| < 2^70
@@ -154,7 +136,8 @@ struct Pieces {
   bool same;  // q's pieces are aligned with p's
   __device__ __forceinline__ Pieces(const T *row, const T *row_q, int v) : p(row), q(row_q), V(v) {
     head = int((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-    same = ((reinterpret_cast<uintptr_t>(row_q) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0;
+    same = !row_q ||
+           ((reinterpret_cast<uintptr_t>(row_q) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0;
     count = (V + head + N - 1) / N;
   }
   __device__ __forceinline__ int first(int piece) const { return piece * N - head; }
@@ -165,32 +148,22 @@ struct Pieces {
     for (int i = 0; i < N; ++i) e[i] = at + i >= 0 && at + i < V ? row[at + i] : from_f32<T>(0.f);
     return *reinterpret_cast<const uint4 *>(e);
   }
-  // steps s .. s + U - 1 of 32 pieces, zeros from step s1 on
-  template <bool Q, int U>
-  __device__ __forceinline__ void load(int s, int s1, uint4 (&vp)[U], uint4 (&vq)[U]) const {
-    const int at = first(s * 32 + int(threadIdx.x & 31));
-    bool edges = Q && !same;
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int e = at + k * 32 * N;
-      vp[k] = make_uint4(0, 0, 0, 0);
-      if (Q) vq[k] = make_uint4(0, 0, 0, 0);
-      if (s + k < s1) {
-        const bool whole = e >= 0 && e + N <= V;
-        if (whole) vp[k] = __ldg(reinterpret_cast<const uint4 *>(p + e));
-        if (Q && whole && same) vq[k] = __ldg(reinterpret_cast<const uint4 *>(q + e));
-        edges = edges || (!whole && e < V);
-      }
-    }
-    if (edges) {  // a row's ends, and a q that lies otherwise than p
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int e = at + k * 32 * N;
-        if (s + k < s1 && e < V) {
-          vp[k] = one(p, e, V);
-          if (Q) vq[k] = one(q, e, V);
-        }
-      }
+  // Do steps s0 .. s1 - 1 reach over a row's ends, or does q lie otherwise than p?
+  __device__ __forceinline__ bool odd(int s0, int s1) const {
+    return first(s0 * 32) < 0 || first(s1 * 32) > V || !same;
+  }
+  // this lane's piece of step s
+  template <bool Q>
+  __device__ __forceinline__ void load(int s, bool odd, uint4 &vp, uint4 &vq) const {
+    const int e = first(s * 32 + int(threadIdx.x & 31));
+    const bool whole = unsigned(e) < unsigned(max(V - N + 1, 0));
+    vp = make_uint4(0, 0, 0, 0);
+    if (Q) vq = make_uint4(0, 0, 0, 0);
+    if (whole) vp = __ldg(reinterpret_cast<const uint4 *>(p + e));
+    if (Q && whole && !odd) vq = __ldg(reinterpret_cast<const uint4 *>(q + e));
+    if (odd && e < V) {
+      if (!whole) vp = one(p, e, V);
+      if (Q) vq = one(q, e, V);
     }
   }
   __device__ __forceinline__ static float get(const uint4 &v, int i) {
@@ -206,8 +179,8 @@ struct Shared {
   int64_t cta[2][MAX_CLUSTER];         // of the cluster's CTAs; greedy: largest value and place
   uint64_t bar[2];                     // their arrival
   // what the walk asks of the row, and then of the search
-  Left left;
-  int cur, kept, finish, gone, kind;
+  Two t;
+  int cur, kept, finish, gone, minus_q;
   int64_t border;
   int owner;
 };
@@ -327,21 +300,25 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
       steps_of(x, s0, s1);
       uint32_t top = 0;
       int at = 0x7fffffff;
+      const bool odd = x.odd(s0, s1);
       for (int s = s0; s < s1; s += U) {
-        uint4 v[U], none[U];
-        x.template load<false>(s, s1, v, none);
+        uint4 v[U], none;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const int e = x.first((s + k) * 32 + lane);
+        for (int k = 0; k < U; ++k)
+          if (s + k < s1) x.template load<false>(s + k, odd, v[k], none);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const uint32_t o = s + k < s1 ? order_of(x.get(v[k], i)) : 0;
-            if (o > top && e + i >= 0 && e + i < a.V) {  // (rising indices: ties stay)
-              top = o;
-              at = e + i;
+        for (int k = 0; k < U; ++k)
+          if (s + k < s1) {
+            const int e = x.first((s + k) * 32 + lane);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const uint32_t o = order_of(x.get(v[k], i));
+              if (o > top && e + i >= 0 && e + i < a.V) {  // (rising indices: ties stay)
+                top = o;
+                at = e + i;
+              }
             }
           }
-        }
       }
       // the largest value and the lowest of its places
       auto join = [&](uint32_t t, int i) {
@@ -399,7 +376,8 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
     };
     // the walk's state, the same in all lanes of warp 0
     int cur = 0, after = 0, kept = 1, tried = 0;
-    Left left{{1.f, 0.f}, {0.f, 0.f}};
+    int64_t t = 0;     // in units
+    Two t_two{0.f, 0.f};
     int64_t mass = 0;  // of what is left, from the first rejection on
     bool told = true;  // it is of what is left now
     uint4 vp[U], vq[U];
@@ -418,20 +396,17 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
           const int x = sh.token[c];
           bool keep;
           int64_t w = 0;
-          uint32_t hi, lo;
           if (tried == 0) {  // S = 1, r = p: u q < p, exactly
             const float q = MODE == kDraft ? sh.q[c] : 1.f;
             const float y = __fmul_rn(u, q);
             keep = y < p || (y == p && __fmaf_rn(u, q, -y) < 0.f);
           } else if (MODE == kDraft) {
             const float q = sh.q[c];
-            left_of<2>(left, p, q, hi, lo);
-            keep = part(q, part(u, mass)) < units(hi, lo);
+            keep = part(q, part(u, mass)) < left_of<true>(t_two, p, q);
           } else {
             bool again = false;
             for (int i = lane; i < tried; i += 32) again = again || sh.token[sh.out[i]] == x;
-            left_of<0>(left, p, 0.f, hi, lo);
-            w = __any_sync(0xffffffffu, again) ? 0 : units(hi, lo);
+            w = __any_sync(0xffffffffu, again) ? 0 : left_of<false>(Two(), p, 0.f);
             keep = part(u, mass) < w;
           }
           if (keep) {
@@ -439,18 +414,14 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
             ++kept;
             cur = after = c;
             tried = 0;
-            left = Left{{1.f, 0.f}, {0.f, 0.f}};
+            t = 0;
+            t_two = Two{0.f, 0.f};
             continue;
           }
           after = c;
           if (MODE == kDraft) {
-            if (tried == 0) {
-              left.b = Two{1.f, 0.f};
-            } else if (mass > 0) {
-              const Two inv = reciprocal(number(mass));
-              left.a = left.a * inv;
-              left.b = plus_one(left.b * inv);
-            }
+            t = tried == 0 ? ONE : t + mass;
+            t_two = number(t);
             ++tried;
             told = false;
           } else if (tried == 0 || w > 0) {
@@ -468,14 +439,14 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
           sh.kept = kept;
           sh.finish = finish;
           sh.gone = MODE == kPoint ? tried : 0;
-          sh.kind = MODE == kPoint || tried == 0 ? 0 : tried == 1 ? 1 : 2;
-          if (MODE == kDraft) sh.left = left;
+          sh.minus_q = MODE == kDraft && tried > 0;
+          if (MODE == kDraft) sh.t = t_two;
         }
       }
       __syncthreads();
       // ---- the sum of what is left of the row of sh.cur
-      const int node = sh.cur, kind = sh.kind, finish = sh.finish, gone = sh.gone;
-      const Left l = sh.left;
+      const int node = sh.cur, minus_q = sh.minus_q, finish = sh.finish, gone = sh.gone;
+      const Two t2 = sh.t;
       const Pieces<T> x(P + node * a.p_ld, MODE == kDraft ? Q + node * a.q_ld : nullptr, a.V);
       int s0, s1;
       steps_of(x, s0, s1);
@@ -487,36 +458,35 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
         for (int i = 0; i < gone; ++i) {
           const int c = sh.out[i], t = sh.token[c];
           if (t >= e0 && t < e1) {
-            uint32_t hi, lo;
-            left_of<0>(l, sh.p[c], 0.f, hi, lo);
-            if (lane == 0) sum -= units(hi, lo);
+            if (lane == 0) sum -= left_of<false>(t2, sh.p[c], 0.f);
             out = true;
           }
         }
       }
-      auto sum_row = [&](auto k_) {
-        constexpr int K = decltype(k_)::value;
+      auto sum_row = [&](auto with_q) {
+        constexpr bool Q = decltype(with_q)::value;
+        const bool odd = x.odd(s0, s1);
         for (int s = s0; s < s1; s += U) {
-          if (!fits || held != node) x.template load<K != 0>(s, s1, vp, vq);
+          if (!fits || held != node) {
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+              if (s + k < s1) x.template load<Q>(s + k, odd, vp[k], vq[k]);
+          }
           uint32_t hi = 0, lo = 0;  // (at most 32 values of 23 bits)
 #pragma unroll
           for (int k = 0; k < U; ++k)
+            if (s + k < s1) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              uint32_t h, o;
-              left_of<K>(l, x.get(vp[k], i), x.get(vq[k], i), h, o);
-              hi += h;
-              lo += o;
+              for (int i = 0; i < N; ++i)
+                add_left<Q>(t2, x.get(vp[k], i), x.get(vq[k], i), hi, lo);
             }
           sum += units(hi, lo);
         }
       };
-      if (kind == 0)
-        sum_row(std::integral_constant<int, 0>());
-      else if (kind == 1)
-        sum_row(std::integral_constant<int, 1>());
+      if (MODE == kDraft && minus_q)
+        sum_row(std::true_type());
       else
-        sum_row(std::integral_constant<int, 2>());
+        sum_row(std::false_type());
       held = node;
       sum = warp_sum(sum);
       if (lane == 0) sh.warp[warp] = sum;
@@ -530,7 +500,7 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
           told = true;
           continue;
         }
-        if (total <= 0 && kind + gone > 0) {
+        if (total <= 0 && minus_q + gone > 0) {
           if (lane == 0) sh.owner = -2;  // nothing left (rounded rows): the row itself
         } else {
           // the border, and whose part it is in: the CTA, then the warp
@@ -559,7 +529,7 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
       if (sh.owner == -2) {
         if (warp == 0) {
           tried = 0;  // (no children are left: the walk comes back with the row)
-          left = Left{{1.f, 0.f}, {0.f, 0.f}};
+          t_two = Two{0.f, 0.f};
         }
         __syncthreads();
         continue;
@@ -568,25 +538,20 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
       if (warp == sh.owner) {
         int64_t border = sh.border;
         int found = -1;
-        // (One step at a time, in little code that runs once: the general form
-        // gives the same units as the others where a or b is 1, b 0.)
+        // (one step at a time, in little code, which runs once)
 #pragma unroll 1
         for (int s = s0; s < s1 && found < 0; ++s) {
-          uint4 wp[1], wq[1] = {make_uint4(0, 0, 0, 0)};
-          if (MODE == kDraft && kind != 0)
-            x.template load<true>(s, s1, wp, wq);
+          uint4 wp, wq = make_uint4(0, 0, 0, 0);
+          if (MODE == kDraft && minus_q)
+            x.template load<true>(s, x.odd(s0, s1), wp, wq);
           else
-            x.template load<false>(s, s1, wp, wq);
+            x.template load<false>(s, x.odd(s0, s1), wp, wq);
           const uint32_t gone_bits = MODE == kPoint && out ? taken(x, s) : 0;
           int64_t v[N], mine = 0;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            uint32_t h, o;
-            if (MODE == kPoint)
-              left_of<0>(l, x.get(wp[0], i), 0.f, h, o);
-            else
-              left_of<2>(l, x.get(wp[0], i), x.get(wq[0], i), h, o);
-            v[i] = gone_bits >> i & 1 ? 0 : units(h, o);
+            v[i] = left_of<MODE == kDraft>(t2, x.get(wp, i), x.get(wq, i));
+            if (gone_bits >> i & 1) v[i] = 0;
             mine += v[i];
           }
           const int64_t inc = warp_scan(mine);

@@ -67,8 +67,9 @@ def tree_attention(q_latent, cache, block_table, query_start_loc, seq_lens, mask
 def verify(target, draft, tokens, parents, uniform, u_next, most: int, slack=None):
     """One sequence: (kept nodes, next token).  target, draft [n, V]; draft None:
     chosen children; uniform None: greedy.  With slack, a third value: the
-    tokens with mass whose share of the sum comes within slack * sum of the next
-    token's border."""
+    tokens with mass whose share of the sum comes within slack of the next
+    token's border, slack being a part of the row before anything was taken out
+    and divided by its sum."""
     n, V = target.shape
     if n == 0:
         return ([], -1) if slack is None else ([], -1, [-1])
@@ -89,7 +90,7 @@ def verify(target, draft, tokens, parents, uniform, u_next, most: int, slack=Non
             path.append(cur)
             continue
         p = np.maximum(np.nan_to_num(p64[cur], nan=0.0), 0.0)
-        left, mass, kept = p, 1.0, None
+        left, mass, kept, scale = p, 1.0, None, 1.0
         for i in kids:
             x = tokens[i]
             q = 1.0 if draft is None else float(draft[cur][x])
@@ -100,6 +101,7 @@ def verify(target, draft, tokens, parents, uniform, u_next, most: int, slack=Non
                 left = left.copy()
                 left[x] = 0.0
             elif mass > 0:
+                scale *= mass
                 left = np.maximum(left / mass - np.asarray(draft[cur], dtype=np.float64), 0.0)
             mass = left.sum()
         if kept is None:
@@ -108,7 +110,7 @@ def verify(target, draft, tokens, parents, uniform, u_next, most: int, slack=Non
             v = min(int(np.searchsorted(total, border, side="right")), V - 1)
             if slack is None:
                 return path, v
-            e, own = slack * total[-1], np.diff(total, prepend=0.0)
+            e, own = slack / scale, np.diff(total, prepend=0.0)
             near = (own > 0) & (total > border - e) & (total - own <= border + e)
             return path, v, sorted({v, *(int(x) for x in np.flatnonzero(near))})
         cur = kept

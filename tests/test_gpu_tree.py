@@ -295,13 +295,13 @@ def run_verify(p, q, tokens, parents, qsl, u, un, most, status=None):
     return path.cpu().numpy(), kept.cpu().numpy(), nxt.cpu().numpy()
 
 
-# How near the next token's border decides otherwise than exact sums, as a part
-# of the sum: a value is rounded to units of 2^-45, by at most 2^-46, and before
-# that a p - b q is off by some 2^-47 (a and b have 48 bits); sums of units are
-# exact.  Over V values 2^-45 V of a sum of 1, and a row's sum is about 1 here
-# (or more).  The oracle's own sums are off by 2^-53 V.  (A row of equal shares
-# whose border is exactly the end of one, as in test_verify_borders, is decided
-# by the oracle's own rounding.)
+# How near the next token's border decides otherwise than exact sums: a value p -
+# t q is rounded to units of 2^-45, by at most 2^-46, and before that it is off by
+# some 2^-47 (t has 48 bits, and t q at most the row's largest value, 1); sums of
+# units are exact.  So cumulated values are off by at most 2^-45 V (before they
+# are divided by their sum, which the oracle does).  The oracle's own sums are
+# off by 2^-53 V.  (A row of equal shares whose border is exactly the end of one,
+# as in test_verify_borders, is decided by the oracle's own rounding.)
 def slack(V):
     return V * 2.0 ** -45
 
