@@ -167,7 +167,12 @@ int launch_commit(const mla_dims_t &d, const int32_t *path, int path_ld, const i
   for (int l0 = 0; l0 == 0 || l0 < layers; l0 += COMMIT_LAYERS) {  // (lengths without layers too)
     a.layers = layers - l0 < COMMIT_LAYERS ? layers - l0 : COMMIT_LAYERS;
     for (int l = 0; l < a.layers; ++l) a.cache[l] = static_cast<uint4 *>(caches[l0 + l]);
-    a.group = 1;
+    // Layers of a block: one while the blocks of all sequences and layers fit the
+    // SMs at once, then as many as keep them there.
+    const int64_t fit = 4 * num_sms();
+    a.group = int((int64_t(R) * a.layers + fit - 1) / fit);
+    if (a.group > a.layers) a.group = a.layers;
+    if (a.group < 1) a.group = 1;
     const dim3 grid(R, a.layers ? (a.layers + a.group - 1) / a.group : 1);
     const int rc = launch_chained(commit_kernel, grid, COMMIT_THREADS, 0, 1, s, "commit_kernel", a);
     if (rc) return rc;

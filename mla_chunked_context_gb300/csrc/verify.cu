@@ -23,18 +23,20 @@
 // the next token.  (Pairs of float32 with 64-bit floating point for the walk,
 // which has a 64th of float32's rate here, took 22 us for a chain of 5 over
 // 32000 tokens, 149 for 64 trees of 16 over 131072 and 58 for 24 of up to 21 over
-// 100003 in bf16; this 6.5, 54 and 14.)
+// 100003 in bf16; this 5.7, 50 and 12.)
 //
 // Only the rows where a child was rejected and the last node's row are read,
 // one row at a time as each depends on the walk: a call of few sequences is
-// bound by latency (of 12000 clocks for a chain: 2800 to the gathered values,
-// 2300 for the walk, 3300 for the row, 1400 for the cluster's sums, 2500 for the
-// next token), one of many by its sequence with the most rejections: 64 trees
-// read 119 rows, but one of them 11, a row at 13000 clocks once the others are
-// done.  A cluster of up to 8 CTAs takes a sequence; each walks the tree by
-// itself (the same numbers, the same steps) over values gathered at the start,
-// sums its part of a row, and tells the others through distributed shared
-// memory.  For the next token the sums of CTAs, of warps, then of 32 lanes'
+// bound by latency (of 10500 clocks for a chain: 2900 to the gathered values,
+// 2200 for the walk, 2600 for the row, 1400 for the cluster's sums, 1400 for the
+// next token; much of each is code fetched for the first time), one of many by
+// its sequence with the most rejections: 64 trees read 119 rows, 20 us of HBM,
+// but one of them 11, a row at some 7000 clocks once the others are done.  (More
+// bytes on their way, by a ring in shared memory or by prefetches, did not
+// shorten that: 54 and 52 us.)  A cluster of up to 8 CTAs takes a sequence; each
+// walks the tree by itself (the same numbers, the same steps) over values
+// gathered at the start, sums its part of a row, and tells the others through
+// distributed shared memory.  For the next token the sums of CTAs, of warps, then of 32 lanes'
 // 16-byte pieces are searched by one warp of one CTA.  Where a warp's part of a
 // row is four pieces a lane or less it stays in registers for the sums that
 // follow at the same node.
@@ -72,20 +74,22 @@ constexpr int64_t ONE = int64_t(1) << 45;
 __device__ __forceinline__ int64_t units(uint32_t hi, uint32_t lo) {
   return (int64_t(int32_t(hi)) << 23) + int32_t(lo);
 }
-// A sum of units as a number; x times a sum, rounded down (0 <= x <= 1).  By
-// conversions of 32 bits, as those of 64 are slow.
+// A sum of units as a number; a fraction and its part of a sum, rounded down.
+// (By conversions of 32 bits: those of 64 are slow.)
 __device__ __forceinline__ Two number(int64_t v) {  // 0 <= v < 2^54
   const int a = int(v >> 24);
   const float hi = float(a);
   const float lo = float(a - int(hi)) * 16777216.f + float(int(v & 0xffffff));
   return {hi * (1.f / 2097152.f), lo * (1.f / 35184372088832.f)};
 }
-__device__ __forceinline__ int64_t part(float x, int64_t v) {
-  if (!(x < 1.f)) return v;
+__device__ __forceinline__ uint64_t fraction(float x) {  // 0 <= x < 1, in 2^-64
   const float y = x * 4294967296.f;
   const uint32_t hi = __float2uint_rz(y);
   const uint32_t lo = __float2uint_rz(__fsub_rn(y, truncf(y)) * 4294967296.f);
-  return int64_t(__umul64hi(uint64_t(hi) << 32 | lo, uint64_t(v)));
+  return uint64_t(hi) << 32 | lo;
+}
+__device__ __forceinline__ int64_t part(uint64_t x, int64_t v) {
+  return int64_t(__umul64hi(x, uint64_t(v)));
 }
 
 // Adds one value, max(p - t q, 0) or (without Q) p, to hi and lo.  What the grid
@@ -172,9 +176,13 @@ struct Pieces {
 };
 
 struct Shared {
-  int parent[NODES], token[NODES], path[NODES];
-  float p[NODES], q[NODES], u[NODES];  // p and q of a node's token in its parent's rows
-  int out[NODES];                      // nodes whose tokens are taken out of the row
+  // of a node: u q (or u) as a fraction; p and q of its token in its parent's rows
+  uint64_t uq[NODES];
+  float p[NODES], q[NODES];
+  int token[NODES];
+  int16_t parent[NODES], path[NODES];
+  int16_t out[NODES];  // nodes whose tokens are taken out of the row
+  uint8_t first[NODES];  // whether it is kept as its parent's first child
   int64_t warp[MAX_WARPS];             // sums of warps
   int64_t cta[2][MAX_CLUSTER];         // of the cluster's CTAs; greedy: largest value and place
   uint64_t bar[2];                     // their arrival
@@ -224,11 +232,12 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
   const int n = max(q1 - q0, 0), nodes = min(n, NODES), depth = min(a.path_ld, nodes);
   const T *P = static_cast<const T *>(a.p) + int64_t(q0) * a.p_ld;
   const T *Q = MODE == kDraft ? static_cast<const T *>(a.q) + int64_t(q0) * a.q_ld : nullptr;
+  const float u_next = MODE != kGreedy ? __ldg(a.u_next + r) : 0.f;
   bool bad = n > nodes;
   for (int i = tid; i < nodes; i += threads) {
     int up = __ldg(a.parents + q0 + i);
     const int x = __ldg(a.tokens + q0 + i);
-    if (MODE != kGreedy) sh.u[i] = __ldg(a.u + q0 + i);
+    const float u = MODE != kGreedy ? __ldg(a.u + q0 + i) : 0.f;
     if (up < -1 || up >= i) {
       bad = true;
       up = -1;
@@ -237,11 +246,17 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
       bad = true;
       up = -1;  // nobody's child
     }
-    sh.parent[i] = up;
+    sh.parent[i] = int16_t(up);
     sh.token[i] = x;
     if (MODE != kGreedy && i > 0 && up >= 0) {
-      sh.p[i] = to_f32(P[up * a.p_ld + x]);
-      if (MODE == kDraft) sh.q[i] = to_f32(Q[up * a.q_ld + x]);
+      const float p = to_f32(P[up * a.p_ld + x]);
+      const float q = MODE == kDraft ? to_f32(Q[up * a.q_ld + x]) : 1.f;
+      const float y = __fmul_rn(u, q), rest = __fmaf_rn(u, q, -y);
+      sh.p[i] = p;
+      sh.q[i] = q;
+      sh.first[i] = y < p || (y == p && rest < 0.f);  // u q < p, exactly
+      sh.uq[i] = y < 1.f ? fraction(y) + uint64_t(__float2ll_rn(rest * 18446744073709551616.f))
+                         : ~uint64_t(0);
     }
   }
   if (bad && rank == 0 && a.status) atomicOr(a.status, MLA_STATUS_BAD_TREE);
@@ -345,7 +360,7 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
         while (child >= 0 && sh.token[child] != best) child = next_child(cur, child);
       }
       if (child < 0) break;
-      if (tid == 0) sh.path[kept] = child;
+      if (tid == 0) sh.path[kept] = int16_t(child);
       ++kept;
       cur = child;
     }
@@ -392,25 +407,23 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
             break;
           }
           if (!told) break;  // the children behind a rejected one need the sum
-          const float p = sh.p[c], u = sh.u[c];
-          const int x = sh.token[c];
           bool keep;
           int64_t w = 0;
-          if (tried == 0) {  // S = 1, r = p: u q < p, exactly
-            const float q = MODE == kDraft ? sh.q[c] : 1.f;
-            const float y = __fmul_rn(u, q);
-            keep = y < p || (y == p && __fmaf_rn(u, q, -y) < 0.f);
-          } else if (MODE == kDraft) {
-            const float q = sh.q[c];
-            keep = part(q, part(u, mass)) < left_of<true>(t_two, p, q);
+          if (tried == 0) {  // S = 1, r = p
+            keep = sh.first[c];
           } else {
-            bool again = false;
-            for (int i = lane; i < tried; i += 32) again = again || sh.token[sh.out[i]] == x;
-            w = __any_sync(0xffffffffu, again) ? 0 : left_of<false>(Two(), p, 0.f);
-            keep = part(u, mass) < w;
+            if (MODE == kDraft) {
+              w = left_of<true>(t_two, sh.p[c], sh.q[c]);
+            } else {
+              const int x = sh.token[c];
+              bool again = false;
+              for (int i = lane; i < tried; i += 32) again = again || sh.token[sh.out[i]] == x;
+              w = __any_sync(0xffffffffu, again) ? 0 : left_of<false>(Two(), sh.p[c], 0.f);
+            }
+            keep = part(sh.uq[c], mass) < w;
           }
           if (keep) {
-            if (lane == 0) sh.path[kept] = c;
+            if (lane == 0) sh.path[kept] = int16_t(c);
             ++kept;
             cur = after = c;
             tried = 0;
@@ -425,7 +438,7 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
             ++tried;
             told = false;
           } else if (tried == 0 || w > 0) {
-            if (lane == 0) sh.out[tried] = c;
+            if (lane == 0) sh.out[tried] = int16_t(c);
             if (tried == 0)
               told = false;
             else
@@ -505,7 +518,7 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
         } else {
           // the border, and whose part it is in: the CTA, then the warp
           const int64_t border =
-              total > 0 ? min(part(__ldg(a.u_next + r), total), total - 1) : 0;
+              total > 0 ? min(part(fraction(u_next), total), total - 1) : 0;
           const int64_t up_to = warp_scan(of_cta);
           const uint32_t over = __ballot_sync(0xffffffffu, up_to > border);
           const int owner = over ? __ffs(int(over)) - 1 : -1;
