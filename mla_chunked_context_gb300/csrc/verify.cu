@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
     sm103::mbar_init(smem_u32(&sh.bar[1]), 1);
     sm103::fence_mbar_init();
   }
-  cluster_arrive();  // (its wait is before the first write to another CTA)
+  cluster_arrive();  // (its wait comes before any write to another CTA)
   chain_release();
   chain_wait();
   const int q0 = min(max(__ldg(a.qsl + r), 0), a.T), q1 = min(__ldg(a.qsl + r + 1), a.T);
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
   if (bad && rank == 0 && a.status) atomicOr(a.status, MLA_STATUS_BAD_TREE);
   if (tid == 0) sh.path[0] = 0;
   __syncthreads();
+  cluster_wait();
 
   // the first child of cur behind node `after`, or -1 (by a whole warp)
   auto next_child = [&](int cur, int after) {
@@ -308,7 +309,6 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
 
   if constexpr (MODE == kGreedy) {
     int cur = 0, kept = nodes > 0, best = -1;
-    cluster_wait();
     while (kept > 0) {
       const Pieces<T> x(P + cur * a.p_ld, nullptr, a.V);
       int s0, s1;
@@ -372,7 +372,6 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
     return;
   } else {
     if (nodes == 0) {
-      cluster_wait();
       if (rank == 0) {
         store_path(0);
         if (tid == 0) a.next[r] = -1;
@@ -506,7 +505,6 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
       __syncthreads();
       if (warp == 0) {
         const int64_t of_warp = lane < warps ? sh.warp[lane] : 0;
-        if (pass == 0) cluster_wait();
         const int64_t of_cta = exchange(warp_sum(of_warp), 0), total = warp_sum(of_cta);
         if (!finish) {
           mass = total;
