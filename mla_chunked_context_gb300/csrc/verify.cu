@@ -23,7 +23,7 @@
 // the next token.  (Pairs of float32 with 64-bit floating point for the walk,
 // which has a 64th of float32's rate here, took 22 us for a chain of 5 over
 // 32000 tokens, 149 for 64 trees of 16 over 131072 and 58 for 24 of up to 21 over
-// 100003 in bf16; this 5.7, 50 and 12.)
+// 100003 in bf16; this 5.7, 45 and 12.)
 //
 // Only the rows where a child was rejected and the last node's row are read,
 // one row at a time as each depends on the walk: a call of few sequences is
@@ -33,7 +33,7 @@
 // its sequence with the most rejections: 64 trees read 119 rows, 20 us of HBM,
 // but one of them 11, a row at some 7000 clocks once the others are done.  (More
 // bytes on their way, by a ring in shared memory or by prefetches, did not
-// shorten that: 54 and 52 us.)  A cluster of up to 8 CTAs takes a sequence; each
+// shorten that.)  A cluster of up to 8 CTAs takes a sequence; each
 // walks the tree by itself (the same numbers, the same steps) over values
 // gathered at the start, sums its part of a row, and tells the others through
 // distributed shared memory.  For the next token the sums of CTAs, of warps, then of 32 lanes'
@@ -596,12 +596,18 @@ int launch_verify(const void *p, int64_t p_ld, const void *q, int64_t q_ld, int 
                   int32_t *next, int32_t *status, cudaStream_t s) {
   VerifyArgs a{p, q, p_ld, q_ld, tokens, parents, qsl, u, u_next, path, kept, next, status,
                T, V, path_ld, 0, 5};
-  // Clusters of 8 while four CTAs of 256 threads an SM hold them all; 1024
-  // threads an SM.
+  // Clusters of 8 while four CTAs an SM are no fewer than them all.  1024 threads
+  // an SM: a CTA has 32 to 8 warps, or 16 at least where 8 would have more than U
+  // pieces a lane each (8 and 16: 64 trees, V 131072 50 and 45 us, 109 chains of 9,
+  // greedy, 98294 49 and 43; 126 trees, 2066 in bf16 14 and 19, 58 single nodes,
+  // 57225 in bf16 5.5 and 8.1).
   const int sms = num_sms();
   while (2 << a.cluster_log2 <= MAX_CLUSTER && (int64_t(R) * 2 << a.cluster_log2) <= 4 * sms)
     ++a.cluster_log2;
-  while (a.warps_log2 > 3 && (int64_t(R) << a.cluster_log2) > (int64_t(sms) << (5 - a.warps_log2)))
+  const int step = 32 * 16 / elem_bytes(dtype), steps = (V + step - 1) / step;
+  const int fewest = steps > (8 * U << a.cluster_log2) ? 4 : 3;
+  while (a.warps_log2 > fewest &&
+         (int64_t(R) << a.cluster_log2) > (int64_t(sms) << (5 - a.warps_log2)))
     --a.warps_log2;
   const int threads = 32 << a.warps_log2;
   auto pick = [&](auto t) {
