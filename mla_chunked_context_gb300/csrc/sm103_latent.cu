@@ -33,14 +33,23 @@
 // lengths on the device.  A unit that lies in one share is written directly;
 // the pieces of a cut one go to scratch as normalised float32 with their
 // log-sums, and latent_combine_kernel joins them.
+// With a mask (template parameter TREE, mla_tree_attn) a token sees the keys
+// before its sequence's new tokens, and of these the ones in its mask: where a
+// tile has any, a softmax thread takes its 16 keys' bits from the mask row, which
+// it asks for before it waits for the scores.
 // Measured, 64 keys at 1.6-1.95 GHz: single 3380 clocks, of which HBM's rate
 // takes 3200 (128 sequences of up to 8192 keys, 32 heads: 110 us, 83% of copy
-// bandwidth); pair about 2000, of which its shared-memory reads take 1860 and
-// its MMAs 1425 (24 sequences x 4 tokens x 128 heads: 82 us, 49% of the bf16
-// rate).  With one token a sequence and 128 heads these reads, not HBM, hold the
-// pair form too: 128 sequences of 4096 keys take 130 us, their bytes 94.  A
-// launch has some 10000 clocks around its tiles: finding its share, the first
-// loads, the last rows out, and the joining kernel.
+// bandwidth); pair 1700 with pages of 64 (16 x 4096 keys, trees of 32 nodes, 128
+// heads: 445 us, 1300 TFLOP/s, 69% of the bf16 rate, 77% of what the power limit
+// lets it keep up) and about 2000 with pages of 16 (24 sequences x 4 tokens x 128
+// heads: 80 us, 52%).  The pair's MMAs take 1425 of that.  They, the copies into
+// shared memory (545 lines of 128 bytes a tile) and the softmax (290) want 2080 of
+// its cycles, so these hold the pair form, with one token a sequence too: 128
+// sequences of 4096 keys take 130 us, their bytes 94.  Not faster: K in three
+// column groups with barriers of their own (550 us for 437); S and P V with one
+// commit each for all that waits for them; new tokens' rows looked at a tile
+// later (463 for 445).  A launch has some 10000 clocks around its tiles: finding
+// its share, the first loads, the last rows out, and the joining kernel.
 // Warps: 0 K loads, 1 V loads (pair), 2 MMA issue, 3 query loads and prefetches
 // to L2, 4-11 softmax and epilogue (two a quarter of tensor memory's lanes).
 #include <algorithm>
@@ -384,13 +393,14 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
 }
 
 // V of the pair form lies in groups of 2^VB keys: [4 column blocks][2^VB keys][64
-// columns].  Pages of 64 keys and their multiples make groups of 64, a copy for
-// each column block; others groups of 16 (an MMA's K), which one copy of three
-// dimensions brings whatever the page size (a multiple of 16).  Such a copy
-// takes 330 clocks to issue, one of two dimensions with as many bytes 190 (pages
-// of 64, 16 x 32 tokens x 4096 keys: 460 us with groups of 16, 437 with 64); but
-// 16 copies of 16 rows take longer than four of them (pages of 16, 24 ragged
-// trees: 117, so 105).
+// columns].  Pages of 64 or 32 keys and their multiples make groups of that many,
+// a copy for each column block; others groups of 16 (an MMA's K), which one copy
+// of three dimensions brings whatever the page size (a multiple of 16).  Such a
+// copy takes 330 clocks to issue, one of two dimensions with as many bytes 190
+// (groups of 16 and as many as the page: pages of 64, 16 trees of 32 nodes on
+// 2048 keys 265 and 240 us, 128 x 4096 keys 132 and 129.5; pages of 32, 265 and
+// 243, 133 and 130); but 16 copies of 16 rows take longer than four of them (pages
+// of 16, 24 ragged trees: 117, so 105).
 template <int VB>
 struct VLayout {
   static constexpr uint32_t BLOCK = 128u << VB;  // bytes to the next column block
@@ -455,7 +465,8 @@ __device__ __forceinline__ void mma_lo(uint32_t d, uint32_t alo, uint32_t blo, u
     asm volatile(
         "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n"
         " mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
-        " tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [%0], x, y, %4, p;\n}\n" ::"r"(d),
+        " tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [%0], x, y, %4, p;\n}\n" ::"r"(
+            d),
         "r"(alo), "r"(blo), "r"(DESC_HI), "r"(idesc), "r"(acc)
         : "memory");
   else if (PAIR)
@@ -781,7 +792,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t q_lo = desc_lo_k(sQ), k_lo = desc_lo_k(sK), p_lo = desc_lo_k(sP);
       // V, MN-major: blocks of 64 columns BLK_BYTES (pair: a group's rows) apart
       const uint32_t v_lo = desc_lo_mn(PAIR ? sV : sK, PAIR ? Lay::BLOCK : BLK_BYTES);
-      constexpr uint32_t V_KS = (PAIR && VB == 4 ? 4 * 16 * 128 : 2048) >> 4;  // 16 keys
+      // of 16 keys more (single: 64 rows in a block)
+      auto v_ks = [](int ks) { return (PAIR ? Lay::row(16 * ks) : 2048u * ks) >> 4; };
       constexpr uint32_t V_J = PAIR ? 2 * Lay::BLOCK >> 4 : 4 * BLK;  // second MMA's columns
       constexpr uint32_t K_STEP = C::K_STAGE >> 4, V_STEP = (PAIR ? C::V_STAGE : C::K_STAGE) >> 4;
       constexpr uint32_t KBLK = C::KROWS * 128 >> 4;
@@ -797,7 +809,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           {
-            const uint32_t vk = v + ks * V_KS, acc = ks == 0 ? acc0 : 1;
+            const uint32_t vk = v + v_ks(ks), acc = ks == 0 ? acc0 : 1;
             // (P's rows are read for the first MMA and kept for the second)
             mma_lo<PAIR, 1>(tmem, p + ks * 2, vk, id_o, acc);
             mma_lo<PAIR, 2>(tmem + 128, p + ks * 2, vk + V_J, id_o, acc);
@@ -1341,7 +1353,8 @@ int launch_latent(const Maps &maps, const LatentArgs &a, int urows_limit, cudaSt
     const int cs = PAIR ? 2 : 1;
     cfg.gridDim = dim3(cs * (num_sms() / cs));
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<PAIR, TREE, VB>, &cfg) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<PAIR, TREE, VB>, &cfg) !=
+            cudaSuccess ||
         n < 1)
       n = num_sms() / cs;
     grid = std::min(cs * n, urows_limit);
@@ -1407,8 +1420,9 @@ int launch_latent_attn_tc(const mla_dims_t &d, int causal, const TreeMask &tree,
     constexpr bool TREE = decltype(tree_mask)::value;
     if (int64_t(T) * d.num_heads <= int64_t(64) * R)
       return launch_latent<false, TREE, 4>(maps, a, max_ctas, s);
-    return box_log2 == 6 ? launch_latent<true, TREE, 6>(maps, a, max_ctas, s)
-                         : launch_latent<true, TREE, 4>(maps, a, max_ctas, s);
+    if (box_log2 == 6) return launch_latent<true, TREE, 6>(maps, a, max_ctas, s);
+    if (box_log2 == 5) return launch_latent<true, TREE, 5>(maps, a, max_ctas, s);
+    return launch_latent<true, TREE, 4>(maps, a, max_ctas, s);
   };
   return tree.bits ? launch(std::true_type()) : launch(std::false_type());
 }

@@ -195,7 +195,8 @@ struct Shared {
 
 // Stores 8 bytes in a CTA of the cluster and counts them on an mbarrier there.
 __device__ __forceinline__ void st_async(uint32_t addr, int64_t v, uint32_t bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(addr),
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                   addr),
                "l"(v), "r"(bar)
                : "memory");
 }

@@ -162,7 +162,7 @@ def test_attention_other_shapes(case, shape, dtype, bs, kind):
     check_tree(dims, od, qsl, lens, mask, q, cache, table, o, lse)
 
 
-@pytest.mark.parametrize("bs", [1, 5, 8, 24, 100, 256])
+@pytest.mark.parametrize("bs", [1, 5, 8, 24, 32, 96, 100, 256])
 @pytest.mark.parametrize("H", [128, 4])
 def test_attention_block_sizes(H, bs):
     lens, ql = [301, 30, 130], [12, 9, 8]
@@ -175,7 +175,7 @@ def test_attention_block_sizes(H, bs):
     check_tree(dims, od, qsl, lens, mask, q, cache, table, o, lse)
 
 
-@pytest.mark.parametrize("shape,dtype,H,bs", [(LARGE, "bf16", 128, 64), (LARGE, "bf16", 128, 8), (LARGE, "bf16", 40, 16),
+@pytest.mark.parametrize("shape,dtype,H,bs", [(LARGE, "bf16", 128, 64), (LARGE, "bf16", 128, 32), (LARGE, "bf16", 128, 8), (LARGE, "bf16", 40, 16),
                                               (LARGE, "bf16", 3, 64), (SMALL, "f32", 3, 16)])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 def test_rows_that_are_not_finite_reach_only_nodes_that_see_them(shape, dtype, H, bs, value):
