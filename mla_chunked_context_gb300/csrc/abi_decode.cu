@@ -274,11 +274,12 @@ extern "C" int mla_verify_tree(int32_t dtype, int32_t num_tokens, int32_t num_se
   if (vocab > kMost || num_tokens > kMost || num_seqs > kMost) return MLA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return MLA_OK;
   const int es = elem_bytes(dtype);
-  if (!query_start_loc || !path || !num_kept || !next_tokens ||
-      (uniform == nullptr) != (uniform_next == nullptr) || !aligned4(path) ||
+  if (!query_start_loc || !path || !num_kept || !next_tokens || !aligned4(path) ||
       !aligned4(num_kept) || !aligned4(next_tokens) || !aligned4(query_start_loc))
     return MLA_ERR_INVALID;
-  if (num_tokens > 0 && (!target || !tokens || !parents || !aligned_to(target, es) ||
+  if (num_tokens > 0 && (!target || !tokens || !parents ||
+                         (uniform == nullptr) != (uniform_next == nullptr) ||
+                         !aligned_to(target, es) ||
                          !aligned_to(draft, es) || !aligned4(tokens) || !aligned4(parents) ||
                          !aligned4(uniform) || !aligned4(uniform_next)))
     return MLA_ERR_INVALID;
