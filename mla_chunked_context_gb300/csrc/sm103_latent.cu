@@ -39,17 +39,18 @@
 // it asks for before it waits for the scores.
 // Measured, 64 keys at 1.6-1.95 GHz: single 3380 clocks, of which HBM's rate
 // takes 3200 (128 sequences of up to 8192 keys, 32 heads: 110 us, 83% of copy
-// bandwidth); pair 1700 with pages of 64 (16 x 4096 keys, trees of 32 nodes, 128
-// heads: 445 us, 1300 TFLOP/s, 69% of the bf16 rate, 77% of what the power limit
-// lets it keep up) and about 2000 with pages of 16 (24 sequences x 4 tokens x 128
-// heads: 80 us, 52%).  The pair's MMAs take 1425 of that.  They, the copies into
-// shared memory (545 lines of 128 bytes a tile) and the softmax (290) want 2080 of
-// its cycles, so these hold the pair form, with one token a sequence too: 128
-// sequences of 4096 keys take 130 us, their bytes 94.  Not faster: K in three
-// column groups with barriers of their own (550 us for 437); S and P V with one
-// commit each for all that waits for them; new tokens' rows looked at a tile
-// later (463 for 445).  A launch has some 10000 clocks around its tiles: finding
-// its share, the first loads, the last rows out, and the joining kernel.
+// bandwidth); pair 1700 with pages of 64 and about 2000 with pages of 16 (24
+// sequences x 4 tokens x 128 heads: 79 us, 52% of the bf16 rate).  The pair's MMAs
+// take 1425 of that.  They, the copies into shared memory (545 lines of 128 bytes
+// a tile) and the softmax (306) want 2040 of its cycles, so these hold the pair
+// form, with one token a sequence too: 128 sequences of 4096 keys take 130 us,
+// their bytes 94.  Where such work lasts, power does: 16 x 4096 keys with trees of
+// 32 nodes, 128 heads, take 445-460 us, 1260-1300 TFLOP/s, at 1370 of 1400 W and
+// 1.8 GHz (matrix products of the library keep up 1690 at 1.44 GHz).  Not faster:
+// K in three column groups with barriers of their own (550 us for 437); S and P V
+// with one commit each for all that waits for them; new tokens' rows looked at a
+// tile later (463 for 445).  A launch has some 10000 clocks around its tiles:
+// finding its share, the first loads, the last rows out, and the joining kernel.
 // Warps: 0 K loads, 1 V loads (pair), 2 MMA issue, 3 query loads and prefetches
 // to L2, 4-11 softmax and epilogue (two a quarter of tensor memory's lanes).
 #include <algorithm>
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   float *xmax = reinterpret_cast<float *>(smem + Q_BYTES + C::KV_BYTES + C::P_BYTES);  // [2][256]
   uint64_t *bars = reinterpret_cast<uint64_t *>(xmax + 512);
   const uint32_t k_full = smem_u32(bars), k_empty = k_full + 16, v_full = k_full + 32,
-                 v_empty = k_full + 48, s_full = k_full + 64, s_empty = k_full + 80,
+                 v_empty = k_full + 48, s_full = k_full + 64,
                  p_full = k_full + 96, pv_done = k_full + 112, q_full = k_full + 128,
                  q_empty = k_full + 136, done = k_full + 144, v_own = k_full + 376;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
@@ -593,7 +594,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(v_full + 8 * i, TREE && PAIR ? 2 : 1);
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(s_empty + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
       mbar_init(p_full + 8 * i, PAIR ? 2 * SWARPS : SWARPS);
       mbar_init(pv_done + 8 * i, 1);
     }
@@ -834,21 +834,25 @@ __global__ void __launch_bounds__(THREADS, 1)
           auto ready = [&] {
             return mbar_test(k_full + 8 * st, parity) && (t > w.t0 || mbar_test(q_full, n & 1));
           };
-          bool behind = g > 0;
-          if (behind && !ready()) {
+          bool behind = g > 0, landed = ready();
+          if (behind && !landed) {
             const long long c0 = clock64();
-            while (PAIR && !mbar_test(p_full + 8 * (st ^ 1), ((g - 1) >> 1) & 1) && !ready() &&
-                   clock64() - c0 < kWaitCycles) {
-            }
-            if (!PAIR || !ready()) {
+            while (PAIR && !mbar_test(p_full + 8 * (st ^ 1), ((g - 1) >> 1) & 1) && !landed &&
+                   clock64() - c0 < kWaitCycles)
+              landed = ready();
+            if (!PAIR || !landed) {
               ok = second(g - 1, first);
               if (!ok) break;
               behind = false;
             }
           }
-          ok = (t > w.t0 || mbar_wait(q_full, n & 1)) &&
-               mbar_wait(s_empty + 8 * st, parity ^ 1) && mbar_wait(k_full + 8 * st, parity);
-          if (!ok) break;
+          // (a wait takes this thread some 100 clocks even where there is nothing
+          // to wait for.  That the S of two tiles before has been read is known
+          // from its P.)
+          if (!landed) {
+            ok = (t > w.t0 || mbar_wait(q_full, n & 1)) && mbar_wait(k_full + 8 * st, parity);
+            if (!ok) break;
+          }
           tc_fence_after();
           const uint32_t d = tmem + S_COL + st * SC, k = k_lo + st * K_STEP;
 #pragma unroll
@@ -879,7 +883,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int tid = threadIdx.x - 128, tl = tid & 127;  // tl: tensor-memory lane
     const int part = tid >> 7, half = tl >> 6, rl = tl & 63;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
-    const uint32_t s_empty_lead = lead(s_empty), p_full_lead = lead(p_full);
+    const uint32_t p_full_lead = lead(p_full);
     if (tid == 0 && rank == 0) a.desc[2 * cluster] = make_int4(0, 0, 0, 0);
     // the tiles' maxima and the pieces' sums, over the four threads of a row
     RowJoin<STHREADS> row_join(xmax, tid);
@@ -911,13 +915,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_ld16(t_s, s);
         tmem_wait_ld();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR)
-            mbar_arrive_cluster_relaxed(s_empty_lead + 8 * sb);
-          else
-            mbar_arrive(s_empty + 8 * sb);
-        }
         if (TREE ? mixed || nvis < NC : nvis < NC) {
 #pragma unroll
           for (int c = 0; c < NC; ++c)
