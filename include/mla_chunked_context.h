@@ -707,10 +707,11 @@ int mla_tree_attn(const mla_dims_t *d, int32_t num_seqs,
  *   num_kept  device int32 [num_seqs].  A sequence without new tokens has 0 and
  *             next_tokens -1.
  *   Values are held in units of 2^-45 (before r is divided by its sum): the
- *   results are those of exact sums but for borders nearer than vocab * 2^-45.  They have to be at least 0 and less
- *   than 2, a row's sum less than 512 (probabilities' is 1); what a row that is
- *   not gives is not specified, but its tokens are below vocab.  Greedy: NaN
- *   counts as -infinity, and a row of nothing else gives token 0.
+ *   results are those of exact sums but for borders nearer than vocab * 2^-45.
+ *   They have to be at least 0 and less than 2, a row's sum less than 512
+ *   (probabilities' is 1); what a row that is not gives is not specified, but
+ *   its tokens are below vocab.  Greedy: NaN counts as -infinity, and a row of
+ *   nothing else gives token 0.
  *   A sequence's first 1024 nodes are looked at; more set MLA_STATUS_BAD_TREE,
  *   as does a child whose token is outside [0, vocab) (it is passed over).
  *   Errors: MLA_ERR_UNSUPPORTED for a vocabulary beyond 2^24 or more than 2^24
