@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(full_lead + 8 * st);
+          if (lane == 0) mbar_arrive_remote(full_lead + 8 * st);  // (as P is handed on)
         }
         if (!is_v && lane == 0) *progress = g + 1;
       }

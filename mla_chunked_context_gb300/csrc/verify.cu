@@ -33,13 +33,13 @@
 // its sequence with the most rejections: 64 trees read 119 rows, 20 us of HBM,
 // but one of them 11, a row at some 7000 clocks once the others are done.  (More
 // bytes on their way, by a ring in shared memory or by prefetches, did not
-// shorten that.)  A cluster of up to 8 CTAs takes a sequence; each
-// walks the tree by itself (the same numbers, the same steps) over values
-// gathered at the start, sums its part of a row, and tells the others through
-// distributed shared memory.  For the next token the sums of CTAs, of warps, then of 32 lanes'
-// 16-byte pieces are searched by one warp of one CTA.  Where a warp's part of a
-// row is four pieces a lane or less it stays in registers for the sums that
-// follow at the same node.
+// shorten that.)  A cluster of up to 8 CTAs takes a sequence; each walks the tree
+// by itself (the same numbers, the same steps) over values gathered at the start,
+// sums its part of a row, and tells the others through distributed shared memory.
+// For the next token the sums of CTAs, of warps, then of 32 lanes' 16-byte pieces
+// are searched by one warp of one CTA.  Where a warp's part of a row is four
+// pieces a lane or less it stays in registers for the sums that follow at the
+// same node.
 #include <type_traits>
 
 #include "sm103.cuh"
@@ -115,7 +115,7 @@ __device__ __forceinline__ int64_t left_of(Two t, float p, float q) {
   return units(hi, lo);
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {  // |v| < 2^70
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {  // by 22, 22 and 20 bits
   const uint32_t a = __reduce_add_sync(0xffffffffu, uint32_t(v) & 0x3fffff);
   const uint32_t b = __reduce_add_sync(0xffffffffu, uint32_t(v >> 22) & 0x3fffff);
   const int c = __reduce_add_sync(0xffffffffu, int(v >> 44));
@@ -181,11 +181,11 @@ struct Shared {
   float p[NODES], q[NODES];
   int token[NODES];
   int16_t parent[NODES], path[NODES];
-  int16_t out[NODES];  // nodes whose tokens are taken out of the row
-  uint8_t first[NODES];  // whether it is kept as its parent's first child
-  int64_t warp[MAX_WARPS];             // sums of warps
-  int64_t cta[2][MAX_CLUSTER];         // of the cluster's CTAs; greedy: largest value and place
-  uint64_t bar[2];                     // their arrival
+  int16_t out[NODES];           // nodes whose tokens are taken out of the row
+  uint8_t first[NODES];         // whether it is kept as its parent's first child
+  int64_t warp[MAX_WARPS];      // sums of warps; greedy: largest value and place
+  int64_t cta[2][MAX_CLUSTER];  // the same of the cluster's CTAs
+  uint64_t bar[2];              // their arrival
   // what the walk asks of the row, and then of the search
   Two t;
   int cur, kept, finish, gone, minus_q;
