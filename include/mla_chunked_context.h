@@ -731,7 +731,8 @@ int mla_verify_tree(int32_t dtype, int32_t num_tokens, int32_t num_seqs,
  *   (device int32 [num_seqs], nullable; not seq_lens itself).  All rows are
  *   taken before any is overwritten.
  *   kv_caches  host array of num_layers device pointers, each [num_blocks,
- *              block_size, L+P] in dtype, 16-byte aligned, no two the same.
+ *              block_size, L+P] in dtype, 16-byte aligned; no two may
+ *              share memory (MLA_ERR_INVALID: rows would move twice).
  *   path       device int32 [num_seqs, path_ld], as mla_verify_tree leaves it:
  *              an entry has to be at least its place d and less than n, else
  *              nothing moves for it and MLA_STATUS_BAD_TREE is set; so it is

@@ -658,8 +658,8 @@ def mla_commit_tree(dims: Dims, path, num_kept, query_start_loc, seq_lens, kv_ca
                     stream=None) -> None:
     """Moves the cache rows of the kept nodes (mla_verify_tree's path and
     num_kept) behind the cached tokens, and writes the new lengths.  kv_caches:
-    the layers' caches as a list, or one; num_tokens: what query_start_loc is
-    clamped to, as the other calls do (None: not clamped)."""
+    the layers' caches as a list (no two sharing memory), or one; num_tokens:
+    what query_start_loc is clamped to, as the other calls do (None: not clamped)."""
     rc = (_decode or _native()).commit(dims, path, num_kept, query_start_loc, seq_lens, kv_caches,
                                        block_table, new_seq_lens, num_tokens, dev_status, stream)
     if rc:

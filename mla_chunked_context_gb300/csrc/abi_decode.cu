@@ -79,6 +79,22 @@ bool aligned_to(const void *p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & uintptr_t(bytes - 1)) == 0;
 }
 
+// Do two of n caches of `bytes` share memory?  (As a rule a list rises or falls.)
+bool share_memory(void *const *caches, int n, int64_t bytes) {
+  auto apart = [&](int i, int j) {
+    const int64_t d = int64_t(reinterpret_cast<uintptr_t>(caches[j])) -
+                      int64_t(reinterpret_cast<uintptr_t>(caches[i]));
+    return d >= bytes ? 1 : -d >= bytes ? -1 : 0;
+  };
+  int way = 0;
+  for (int i = 0; i + 1 < n; ++i) way += apart(i, i + 1);
+  if (way == n - 1 || way == 1 - n) return false;
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (!apart(i, j)) return true;
+  return false;
+}
+
 // mla_latent_attn, and with a mask mla_tree_attn
 int attend(const mla_dims_t *d, int causal, const TreeMask &tree, int num_seqs,
            const int32_t *query_start_loc, const int32_t *seq_lens, int num_tokens,
@@ -306,6 +322,9 @@ extern "C" int mla_commit_tree(const mla_dims_t *d, int32_t num_seqs, int32_t nu
     return MLA_ERR_INVALID;
   for (int32_t l = 0; l < num_layers; ++l)
     if (!kv_caches[l] || !aligned16(kv_caches[l])) return MLA_ERR_INVALID;
+  const int64_t row = int64_t(d->kv_lora_rank + d->qk_rope_dim) * elem_bytes(d->dtype);
+  if (num_blocks > 0 && share_memory(kv_caches, num_layers, row * d->block_size * num_blocks))
+    return MLA_ERR_INVALID;
   return launch_commit(*d, path, path_ld, num_kept, num_tokens, num_seqs, query_start_loc, seq_lens,
                        kv_caches, num_layers, num_blocks, block_table, block_table_stride,
                        new_seq_lens, dev_status, static_cast<cudaStream_t>(stream));

@@ -268,3 +268,24 @@ def test_chained_calls_back_to_back():
         ref_lens = TR.commit(ref, table.numpy(), qsl, full, path.cpu().numpy(), kept.tolist(), 16)
     assert len_d[0].tolist() == [v + n for v in ref_lens]
     assert same(cache.cpu(), torch.from_numpy(ref).float())
+
+
+def test_commit_takes_layers_in_any_order_but_none_twice():
+    """Views of one allocation, in an order that neither rises nor falls; a cache
+    listed twice, whose rows would move twice, is refused and stays as it was."""
+    rng = np.random.default_rng(29)
+    dims, _ = make_dims(SMALL, 2, 16, "f32")
+    cache, table = make_cache(rng, [40], 16, SMALL[0] + SMALL[1], dims.dtype)
+    whole = torch.stack([cache + l for l in range(4)]).to(DEV)
+    before, new = whole.clone(), i32([0])
+    path, kept, qsl, lens = i32([[0, 2, 4, 5]]), i32([4]), i32([0, 8]), i32([40])
+    for bad in ([whole[0], whole[0]], [whole[2], whole[1], whole[3], whole[1]]):
+        with pytest.raises(M.MlaError, match="invalid argument"):
+            M.mla_commit_tree(dims, path, kept, qsl, lens, bad, table.to(DEV), new)
+    assert torch.equal(whole.view(torch.int32), before.view(torch.int32)) and new.item() == 0
+    M.mla_commit_tree(dims, path, kept, qsl, lens, [whole[l] for l in (2, 0, 3, 1)], table.to(DEV), new)
+    for l in range(4):
+        ref = before[l].cpu().numpy()
+        TR.commit(ref, table.numpy(), [0, 8], [40], [[0, 2, 4, 5]], [4], 16)
+        assert (whole[l].cpu().numpy().view(np.int32) == ref.view(np.int32)).all()
+    assert new.item() == 36

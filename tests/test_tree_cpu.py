@@ -100,6 +100,19 @@ def test_commit_refuses(change, code):
     assert commit(dims(), **change) == code
 
 
+@pytest.mark.parametrize("caches,blocks,code", [
+    # a cache has blocks * 16 rows of 80 float32, blocks * 5120 bytes
+    ((4096, 4096), 4, INVALID), ((4096, 4096 + 4 * 5120 - 16), 4, INVALID), ((4 * 5120, 4096), 4, INVALID),
+    ((4096, 4096 + 4 * 5120), 4, None), ((4096 + 4 * 5120, 4096), 4, None), ((4096, 4096), 0, None),
+    ((1 << 20, 0x7FFFFFF0), 1 << 30, INVALID),
+])
+def test_commit_refuses_caches_that_share_memory(caches, blocks, code):
+    if code is None and torch.cuda.is_available():
+        pytest.skip("would launch on these addresses")
+    rc = commit(dims(), caches=caches, blocks=blocks)
+    assert rc == code if code is not None else rc != INVALID
+
+
 def test_bindings_refuse():
     d, z, i = M.Dims(2, 64, 16, 32, 32, 16, 0.1, torch.float32), torch.zeros, dict(dtype=torch.int32)
     m = z(3, 1, dtype=torch.int64)
