@@ -652,6 +652,8 @@ int mla_latent_attn(const mla_dims_t *d, int32_t causal, int32_t num_seqs,
  *   tree_mask[t]: bit j % 64 of word j / 64 set when node j is i or an ancestor
  *             of i; device uint64 [T, mask_words], 8-byte aligned.  Nodes from
  *             64 * mask_words on have no bit and set MLA_STATUS_BAD_TREE.
+ *             Nodes from 16384 of a sequence on count as without a parent and
+ *             set it too.
  *   positions[t] = seq_lens[r] - n + depth of i, device int32 [T], nullable
  *             (and seq_lens with it). */
 int mla_tree_layout(int32_t num_tokens, int32_t num_seqs,

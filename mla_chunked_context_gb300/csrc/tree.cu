@@ -9,7 +9,9 @@
 // Layout: a few hundred bytes a sequence, so it is bound by a launch and its
 // dependent loads (locations, parents).  A block has a sequence's parents in
 // shared memory and each thread walks up from a node of its own; ancestors
-// come in falling order, so one word of the mask is held at a time.
+// come in falling order, so one word of the mask is held at a time.  A walk is as long
+// as its node is deep: nodes from LIMIT on have no parent, which bounds a call
+// that is no tree anybody drafts.
 //
 // Commit: every moved row is read and written once in every layer; all layers
 // go in one launch, their addresses in its parameters.  A path's indices are at
@@ -23,6 +25,7 @@ namespace mla {
 namespace {
 
 constexpr int LAYOUT_THREADS = 128, STAGED = 1024;  // parents held in shared memory
+constexpr int LIMIT = 16384;
 
 __global__ void __launch_bounds__(LAYOUT_THREADS)
     tree_layout_kernel(const int32_t *parents, const int32_t *qsl, const int32_t *seq_lens, int T,
@@ -35,11 +38,11 @@ __global__ void __launch_bounds__(LAYOUT_THREADS)
   const int n = q1 - q0;
   if (n <= 0) return;
   const int len = seq_lens ? max(__ldg(seq_lens + r), 0) : 0;
-  bool bad = n > 64 * words;
+  bool bad = n > LIMIT || n > 64 * int64_t(words);
   // a parent that is no earlier node of the sequence counts as none
   auto fetch = [&](int i) {
     const int p = __ldg(parents + q0 + i);
-    if (p >= -1 && p < i) return p;
+    if (p >= -1 && p < i && i < LIMIT) return p;
     bad = true;
     return -1;
   };

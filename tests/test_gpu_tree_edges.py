@@ -270,6 +270,22 @@ def test_chained_calls_back_to_back():
     assert same(cache.cpu(), torch.from_numpy(ref).float())
 
 
+@pytest.mark.parametrize("n,W", [(16384, 256), (16385, 257), (40000, 1)])
+def test_layout_of_long_chains(n, W):
+    """Nodes from 16384 on count as without a parent."""
+    mask = torch.full((n, W), 0x0707, dtype=torch.int64, device=DEV)
+    pos, status = i32([-77] * n), status_word()
+    M.mla_tree_layout(i32(chain(n)), i32([0, n]), i32([n + 5]), mask, pos, status)
+    most = min(n, 16384)
+    assert status.item() == (M.MLA_STATUS_BAD_TREE if n > 16384 else 0)
+    assert pos.tolist() == list(range(5, 5 + most)) + [5] * (n - most)
+    bits = np.arange(64 * W)
+    for i in (0, 1, 63, 64, 1023, 1024, 1025, 9999, most - 1, n - 1):
+        want = bits <= i if i < most else bits == i
+        got = np.unpackbits(mask[i].cpu().numpy().view(np.uint8), bitorder="little").astype(bool)
+        assert (got == want).all()
+
+
 def test_commit_takes_layers_in_any_order_but_none_twice():
     """Views of one allocation, in an order that neither rises nor falls; a cache
     listed twice, whose rows would move twice, is refused and stays as it was."""
