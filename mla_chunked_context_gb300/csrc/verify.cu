@@ -33,7 +33,7 @@
 // its sequence with the most rejections: 64 trees read 119 rows, 20 us of HBM,
 // but one of them 11, a row at some 7000 clocks once the others are done.  (More
 // bytes on their way, by a ring in shared memory or by prefetches, did not
-// shorten that.)  A cluster of up to 8 CTAs takes a sequence; each walks the tree
+// shorten that.)  A cluster of 2 to 8 CTAs takes a sequence; each walks the tree
 // by itself (the same numbers, the same steps) over values gathered at the start,
 // sums its part of a row, and tells the others through distributed shared memory.
 // For the next token the sums of CTAs, of warps, then of 32 lanes' 16-byte pieces
@@ -596,8 +596,10 @@ int launch_verify(const void *p, int64_t p_ld, const void *q, int64_t q_ld, int 
                   const float *u, const float *u_next, int32_t *path, int path_ld, int32_t *kept,
                   int32_t *next, int32_t *status, cudaStream_t s) {
   VerifyArgs a{p, q, p_ld, q_ld, tokens, parents, qsl, u, u_next, path, kept, next, status,
-               T, V, path_ld, 0, 5};
-  // Clusters of 8 while four CTAs an SM are no fewer than them all.  1024 threads
+               T, V, path_ld, 1, 5};
+  // Clusters of 8 while four CTAs an SM are no fewer than them all, but of two at
+  // least: the kernel's stores to a cluster's shared memory fault in a launch that
+  // has no clusters (more than 304 sequences each on a CTA of its own).  1024 threads
   // an SM: a CTA has 32 to 8 warps, or 16 at least where 8 would have more than U
   // pieces a lane each (8 and 16: 64 trees, V 131072 50 and 45 us, 109 chains of 9,
   // greedy, 98294 49 and 43; 126 trees, 2066 in bf16 14 and 19, 58 single nodes,
