@@ -42,6 +42,7 @@
 // same node.
 #include <type_traits>
 
+#include "left_units.h"
 #include "sm103.cuh"
 
 namespace mla {
@@ -62,26 +63,8 @@ struct VerifyArgs {
   int T, V, path_ld, cluster_log2, warps_log2;
 };
 
-// A number in two floats (some 46 bits): |lo| is at most half a step of hi.
-struct Two {
-  float hi, lo;
-};
-
-// Values in units of 2^-45 (0 <= w < 2): w = hi * 2^-22 + lo * 2^-45.
-constexpr float GRID = 2.f, FINE = 1.5f / 4194304.f;
-constexpr uint32_t GRID_BITS = 0x40000000u, FINE_BITS = 0x34C00000u;
-constexpr int64_t ONE = int64_t(1) << 45;
-__device__ __forceinline__ int64_t units(uint32_t hi, uint32_t lo) {
-  return (int64_t(int32_t(hi)) << 23) + int32_t(lo);
-}
-// A sum of units as a number; a fraction and its part of a sum, rounded down.
-// (By conversions of 32 bits: those of 64 are slow.)
-__device__ __forceinline__ Two number(int64_t v) {  // 0 <= v < 2^54
-  const int a = int(v >> 24);
-  const float hi = float(a);
-  const float lo = float(a - int(hi)) * 16777216.f + float(int(v & 0xffffff));
-  return {hi * (1.f / 2097152.f), lo * (1.f / 35184372088832.f)};
-}
+// A fraction in units of 2^-64, and its part of a sum, rounded down.  (By
+// conversions of 32 bits: those of 64 are slow.)
 __device__ __forceinline__ uint64_t fraction(float x) {  // 0 <= x < 1, in 2^-64
   const float y = x * 4294967296.f;
   const uint32_t hi = __float2uint_rz(y);
@@ -90,29 +73,6 @@ __device__ __forceinline__ uint64_t fraction(float x) {  // 0 <= x < 1, in 2^-64
 }
 __device__ __forceinline__ int64_t part(uint64_t x, int64_t v) {
   return int64_t(__umul64hi(x, uint64_t(v)));
-}
-
-// Adds one value, max(p - t q, 0) or (without Q) p, to hi and lo.  What the grid
-// leaves of it, p - i - t q, has one rounding, of 2^-24 of that little.  (Integer
-// instructions, minima and choices have half the rate of float32 sums, hence no
-// more of them than this.)
-template <bool Q>
-__device__ __forceinline__ void add_left(Two t, float p, float q, uint32_t &hi, uint32_t &lo) {
-  const float d = Q ? __fmaf_rn(-t.hi, q, p) : p;
-  const float g = __fadd_rn(d, GRID);
-  float rest = __fsub_rn(p, __fsub_rn(g, GRID));
-  if (Q) rest = __fmaf_rn(-t.lo, q, __fmaf_rn(-t.hi, q, rest));
-  const float f = __fadd_rn(rest, FINE);
-  if (!Q || d > 0.f) {
-    hi += __float_as_uint(g) - GRID_BITS;
-    lo += __float_as_uint(f) - FINE_BITS;
-  }
-}
-template <bool Q>
-__device__ __forceinline__ int64_t left_of(Two t, float p, float q) {
-  uint32_t hi = 0, lo = 0;
-  add_left<Q>(t, p, q, hi, lo);
-  return units(hi, lo);
 }
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {  // by 22, 22 and 20 bits
@@ -391,7 +351,7 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
     };
     // the walk's state, the same in all lanes of warp 0
     int cur = 0, after = 0, kept = 1, tried = 0;
-    int64_t t = 0;     // in units
+    uint64_t t = 0;    // in units; below 2^64 for 1023 sums below 512
     Two t_two{0.f, 0.f};
     int64_t mass = 0;  // of what is left, from the first rejection on
     bool told = true;  // it is of what is left now
