@@ -708,8 +708,11 @@ int mla_tree_attn(const mla_dims_t *d, int32_t num_seqs,
  *             path_ld nodes are kept: the path_ld-th is taken for a leaf.
  *   num_kept  device int32 [num_seqs].  A sequence without new tokens has 0 and
  *             next_tokens -1.
- *   Values are held in units of 2^-45 (before r is divided by its sum): the
- *   results are those of exact sums but for borders nearer than vocab * 2^-45.
+ *   Values of r before it is divided by its sum (p, then max(p - t q, 0) with t = 1
+ *   and more) are held in units of 2^-45, to half a unit without draft rows, to 1.1
+ *   units with them (1.4 where p is above 1): the results are those of exact sums
+ *   but for borders nearer than vocab * 2^-45, with draft rows (that sum to 2 at
+ *   most) nearer than 1.4 k vocab * 2^-45 after k siblings rejected at the node.
  *   They have to be at least 0 and less than 2, a row's sum less than 512
  *   (probabilities' is 1); what a row that is not gives is not specified, but
  *   its tokens are below vocab.  Greedy: NaN counts as -infinity, and a row of

@@ -38,8 +38,8 @@ struct Two {
 };
 
 // Values in units of 2^-45 (0 <= w < 2): w = hi * 2^-22 + lo * 2^-45.
-constexpr float GRID = 2.f, FINE = 1.5f / 4194304.f;
-constexpr uint32_t GRID_BITS = 0x40000000u, FINE_BITS = 0x34C00000u;
+constexpr float GRID = 2.f, CARRY = 3.f, FINE = 1.5f / 4194304.f;
+constexpr uint32_t GRID_BITS = 0x40000000u, CARRY_BITS = 0x40400000u, FINE_BITS = 0x34C00000u;
 constexpr uint64_t ONE = uint64_t(1) << 45;
 MLA_LEFT_FN int64_t units(uint32_t hi, uint32_t lo) {
   return (int64_t(int32_t(hi)) << 23) + int32_t(lo);
@@ -52,19 +52,26 @@ MLA_LEFT_FN Two number(uint64_t v) {
   return {hi * UNIT, lo * UNIT};
 }
 
-// Adds one value, max(p - t q, 0) or (without Q) p, to hi and lo.  What the grid
-// leaves of it, p - i - t q, has one rounding, of 2^-24 of that little.  (Integer
-// instructions, minima and choices have half the rate of float32 sums, hence no
-// more of them than this.)
+// Adds one value, max(p - t q, 0) or (without Q) p, to hi and lo.  With Q the grid's
+// step i comes from a difference that was rounded twice, so what it leaves, p - i -
+// t q, may be twice half a step: a second step carries that over before the rest is
+// read off.  That rest has two roundings, of 2^-47 each for p up to 1.
 template <bool Q>
 MLA_LEFT_FN void add_left(Two t, float p, float q, uint32_t &hi, uint32_t &lo) {
-  const float d = Q ? fma_once(-t.hi, q, p) : p;
-  const float g = add_once(d, GRID);
-  float rest = add_once(p, -add_once(g, -GRID));
-  if (Q) rest = fma_once(-t.lo, q, fma_once(-t.hi, q, rest));
-  const float f = add_once(rest, FINE);
-  if (!Q || d > 0.f) {
+  if (!Q) {
+    const float g = add_once(p, GRID);
     hi += bits_of(g) - GRID_BITS;
+    lo += bits_of(add_once(add_once(p, -add_once(g, -GRID)), FINE)) - FINE_BITS;
+    return;
+  }
+  const float d = fma_once(-t.lo, q, fma_once(-t.hi, q, p));
+  const float g = add_once(d, GRID);
+  const float rest = fma_once(-t.lo, q, fma_once(-t.hi, q, add_once(p, -add_once(g, -GRID))));
+  const float c = add_once(rest, CARRY);
+  const float f = add_once(add_once(rest, -add_once(c, -CARRY)), FINE);
+  if (d > 0.f) {
+    hi += bits_of(g) - GRID_BITS;
+    hi += bits_of(c) - CARRY_BITS;
     lo += bits_of(f) - FINE_BITS;
   }
 }

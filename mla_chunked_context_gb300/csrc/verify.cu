@@ -17,13 +17,14 @@
 //
 // The results are whole numbers that have to be the same whatever the order of
 // sums, and a vocabulary's cumulated float32 sum is off by more than a token's
-// share.  So a value is rounded to units of 2^-45, as two integers (what adding
-// 2, and then 1.5 * 2^-22, leaves in a float32's low bits), and sums are sums of
-// integers: exact, in any order, and the same at every level of the search for
-// the next token.  (Pairs of float32 with 64-bit floating point for the walk,
+// share.  So a value is rounded to units of 2^-45, as two integers (left_units.h:
+// what adding 2, and then 1.5 * 2^-22, leaves in a float32's low bits), and sums are
+// sums of integers: exact, in any order, and the same at every level of the search
+// for the next token.  (Pairs of float32 with 64-bit floating point for the walk,
 // which has a 64th of float32's rate here, took 22 us for a chain of 5 over
 // 32000 tokens, 149 for 64 trees of 16 over 131072 and 58 for 24 of up to 21 over
-// 100003 in bf16; this 5.7, 45 and 12.)
+// 100003 in bf16; this 5.9, 50 and 12.  With one step less for p - t q, which is then
+// off by up to 2^-25 where the grid's step ties, 5.7 and 46.)
 //
 // Only the rows where a child was rejected and the last node's row are read,
 // one row at a time as each depends on the walk: a call of few sequences is

@@ -1,5 +1,6 @@
 """Verification at its borders: more sequences than fit the device at once; siblings
-rejected one after the other, against the rule in exact fractions."""
+rejected one after the other and random numbers right beside each border, against
+the rule in exact fractions."""
 
 from fractions import Fraction
 
@@ -87,3 +88,75 @@ def test_many_rejected_siblings_of_heavy_rows(kids, dtype):
     tokens = [0] + [2 * (i % 200) + 1 for i in range(kids)]
     check([p] * 2 * n, [q] * 2 * n, tokens + tokens[:-1] + [46], [-1] + [0] * kids + [-1] + [0] * kids, [0, n, 2 * n],
           [0.5] * 2 * n, [0.1234, 0.9876], 2, dtype)
+
+
+def neighbours(x):
+    """The float32 values on either side of a fraction in [0, 1)."""
+    a = np.float32(float(x))
+    if Fraction(float(a)) > x:
+        a = np.nextafter(a, np.float32(-1))
+    return [v for v in (a, np.nextafter(a, np.float32(2))) if 0 <= v < 1]
+
+
+def rounded(x, dtype):
+    return torch.from_numpy(np.float32(x)).to(dtype).float().numpy()
+
+
+def beside_borders(rng, V, kids, dtype):
+    """A root with `kids` children: rows, tokens drawn from the draft, and random
+    numbers that are the float32 next to the border of each test (mostly on the side
+    of a rejection) and of the next token; and how many children are rejected.  None
+    where one is nearer to its border than what the call promises: 1.1 units of 2^-45
+    a value and rejection, of what is left before it is divided by its sum."""
+    n = kids + 1
+    z = rng.normal(size=(n, V)) * rng.uniform(0.5, 4)
+    soft = lambda x: np.exp(x) / np.exp(x).sum(1, keepdims=True)  # noqa: E731
+    p = rounded(soft(z + rng.uniform(0.05, 0.8) * rng.normal(size=(n, V))), dtype)
+    q = rounded(np.minimum(soft(z), 0.95), dtype)
+    weight = q[0].astype(np.float64) / q[0].astype(np.float64).sum()
+    tokens = [0] + [int(x) for x in rng.choice(V, kids, p=weight)]
+    u = np.full(n, 0.5, np.float32)
+    left, draft = ([Fraction(float(x)) for x in row[0]] for row in (p, q))
+    scale, last, rejected = Fraction(1), 0, 0
+    for i in range(1, n):
+        x, room = tokens[i], Fraction(11, 10) * (rejected + 1) * V / 2 ** 45
+        if left[x] and draft[x]:
+            near = neighbours(left[x] / draft[x])
+            u[i] = near[-1 if rng.random() < 0.8 else 0] if near else 0.999
+            if abs(Fraction(float(u[i])) * draft[x] - left[x]) * scale <= room:
+                return None
+        if Fraction(float(u[i])) * draft[x] < left[x]:
+            last, left, scale = i, [Fraction(float(v)) for v in p[i]], Fraction(1)
+            break
+        left = [max(a - b, Fraction(0)) for a, b in zip(left, draft)]
+        total = sum(left)
+        if not total:
+            return None
+        left, scale, rejected = [a / total for a in left], scale * total, rejected + 1
+    ends, run = [], Fraction(0)
+    for a in left:
+        run += a
+        if a:
+            ends.append(run)
+    near = neighbours(ends[rng.integers(len(ends))] / run) or [np.float32(0.5)]
+    un = near[rng.integers(len(near))]
+    room = Fraction(11, 10) * (rejected + 1) * V / 2 ** 45
+    if min(abs(Fraction(float(un)) * run - e) for e in ends) * scale <= room:
+        return None
+    return p, q, tokens, [-1] + [0] * kids, u, un, rejected if not last else 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,count", [(2, 2400), (5, 2400), (12, 2400), (40, 2400), (3001, 100)])
+def test_random_numbers_beside_the_borders(V, count, dtype):
+    rng = np.random.default_rng(V)
+    P, Q, tok, par, qsl, u, un, deep = [], [], [], [], [0], [], [], []
+    for k in range(count):
+        made = beside_borders(rng, V, 1 + k % 6, dtype)
+        if made:
+            P += list(made[0]); Q += list(made[1]); tok += made[2]; par += made[3]; u += list(made[4]); un.append(made[5])
+            qsl.append(len(tok))
+            deep.append(made[6])
+    if 2 < V < 100:                                  # (of two tokens one rejection leaves one)
+        assert len(deep) > 0.8 * count and max(deep) >= 5 and sum(d >= 2 for d in deep) > 0.1 * count
+    check(P, Q, tok, par, qsl, u, un, 3, dtype)

@@ -75,3 +75,53 @@ def test_threshold_in_two_floats(run):
         assert abs(lo) <= half_step(hi), t
         off = abs(Fraction(hi) + Fraction(lo) - exact)
         assert off <= exact / 2 ** 49 and (off == 0 or t >= 1 << 48), t
+
+
+def values(rng, most, n):
+    """(t, p, q): p up to `most`; q at random, near p / t, and where p - t q is near
+    the middle between two steps of the first grid, 2^-22."""
+    out = []
+    for t in thresholds(rng, n):
+        x = t / 2.0 ** UNIT
+        p = min(f32(most * rng.choice([rng.random(), 2 ** rng.uniform(-40, 0)])), 2 - 2.0 ** -23)
+        k = rng.random()
+        if k < 0.25:
+            q = rng.random()
+        elif k < 0.5:
+            q = p / x * (1 + rng.choice([-1, 1]) * 2 ** rng.uniform(-26, 0))
+        elif k < 0.75:
+            q = p / x * rng.random()
+        else:
+            q = max(0.0, (p - (2 * rng.randrange(1 << 21) + 1) * 2.0 ** -23) / x)
+        out.append((t, p, f32(q)))
+    return out
+
+
+@pytest.mark.parametrize("most,bound", [(1.0, Fraction(17, 16)), (2.0, Fraction(22, 16))])
+def test_values_in_units(run, most, bound):
+    """In units of 2^-45.  What the grid's step i leaves of p - t.hi q is at most
+    2^-23 (half a step) and the difference's two roundings (2^-25 each for p up to 1,
+    2^-24 up to 2) and t.lo q (2^-24, 2^-23): 2^-22 for p up to 1 and less than 2^-21
+    up to 2, so its rounding is off by a quarter of a unit (a half); then without t.lo
+    q, at most 2^-22, a quarter; the reading of the rest a half; t's two floats 2^-49
+    t q, a sixteenth (an eighth).  Values of p alone: the reading."""
+    cases = values(random.Random(int(most)), most, 40000)
+    for (t, p, q), (_, _, got, plain) in zip(cases, run(cases)):
+        v = max(Fraction(p) - Fraction(t, 1 << UNIT) * Fraction(q), Fraction(0)) * 2 ** UNIT
+        assert abs(v - got) <= bound, (t, p, q, float(v), got)
+        assert abs(Fraction(p) * 2 ** UNIT - plain) <= Fraction(1, 2), p
+
+
+def test_values_at_the_middles_of_the_grid(run):
+    """t = 1 and p - q in the middle between two steps, or beside it by less than the
+    difference's own rounding."""
+    rng = random.Random(7)
+    cases = []
+    for _ in range(30000):
+        q = f32(2 ** rng.uniform(-12, -1))
+        p = f32(q + (2 * rng.randrange(1 << 21) + 1) * 2.0 ** -23)
+        if p <= 1:
+            cases.append((1 << UNIT, p, q))
+    assert len(cases) > 5000
+    for (_, p, q), (_, _, got, _) in zip(cases, run(cases)):
+        assert abs((Fraction(p) - Fraction(q)) * 2 ** UNIT - got) <= 1, (p, q)
