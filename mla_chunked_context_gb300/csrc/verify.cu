@@ -53,6 +53,7 @@ constexpr int MAX_WARPS = 32;
 constexpr int NODES = 1024;  // of a sequence
 constexpr int MAX_CLUSTER = 8;
 constexpr int U = 4;         // pieces a lane has in flight
+constexpr uint64_t NEVER = ~uint64_t(0);
 enum Mode { kDraft, kPoint, kGreedy };
 
 struct VerifyArgs {
@@ -138,7 +139,7 @@ struct Pieces {
 
 struct Shared {
   // of a node: u q (or u) as a fraction; p and q of its token in its parent's rows
-  uint64_t uq[NODES];
+  uint64_t uq[NODES];  // (NEVER: 1 or more, which no part of a sum exceeds)
   float p[NODES], q[NODES];
   int token[NODES];
   int16_t parent[NODES], path[NODES];
@@ -217,8 +218,10 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
       sh.p[i] = p;
       sh.q[i] = q;
       sh.first[i] = y < p || (y == p && rest < 0.f);  // u q < p, exactly
-      sh.uq[i] = y < 1.f ? fraction(y) + uint64_t(__float2ll_rn(rest * 18446744073709551616.f))
-                         : ~uint64_t(0);
+      sh.uq[i] = y < 1.f || (y == 1.f && rest < 0.f)
+                     ? (y < 1.f ? fraction(y) : 0) +
+                           uint64_t(__float2ll_rn(rest * 18446744073709551616.f))
+                     : NEVER;
     }
   }
   if (bad && rank == 0 && a.status) atomicOr(a.status, MLA_STATUS_BAD_TREE);
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(1024, 1) verify_kernel(const VerifyArgs a) {
               for (int i = lane; i < tried; i += 32) again = again || sh.token[sh.out[i]] == x;
               w = __any_sync(0xffffffffu, again) ? 0 : left_of<false>(Two(), sh.p[c], 0.f);
             }
-            keep = part(sh.uq[c], mass) < w;
+            keep = sh.uq[c] != NEVER && part(sh.uq[c], mass) < w;
           }
           if (keep) {
             if (lane == 0) sh.path[kept] = int16_t(c);

@@ -160,3 +160,22 @@ def test_random_numbers_beside_the_borders(V, count, dtype):
     if 2 < V < 100:                                  # (of two tokens one rejection leaves one)
         assert len(deep) > 0.8 * count and max(deep) >= 5 and sum(d >= 2 for d in deep) > 0.1 * count
     check(P, Q, tok, par, qsl, u, un, 3, dtype)
+
+
+def test_products_from_one_on():
+    """Draft values above 1.  The first sibling leaves token 0 alone, r(0) = 1: the
+    second one is rejected where u q is 1 or more, even by less than float32 sees,
+    and kept where it is less by that little."""
+    step = 2.0 ** -23
+    rows = [([1.5, 0.1], [1.25, 0.5], 0.95), ([1.5, 0.1], [1 + 1000 * step, 0.5], 1 - 1000 * step),
+            ([1.5, 0.1], [1 + 1001 * step, 0.5], 1 - 1000.5 * step), ([1.75, 0.1], [1.5, 0.5], 0.5)]
+    P, Q, u = [], [], []
+    for p, q, x in rows:
+        P += [p] * 3
+        Q += [q] * 3
+        u += [0.5, 0.9, x]
+    R = len(rows)
+    check(P, Q, [0, 1, 0] * R, [-1, 0, 0] * R, list(range(0, 3 * R + 1, 3)), u, [0.5] * R, 3)
+    kept = [walk(P[3 * r:3 * r + 3], Q[3 * r:3 * r + 3], [0, 1, 0], [-1, 0, 0], np.float32(u[3 * r:3 * r + 3]), 0.5, 3)[0]
+            for r in range(R)]
+    assert kept == [[0], [0, 2], [0], [0, 2]]
