@@ -647,6 +647,8 @@ int mla_latent_attn(const mla_dims_t *d, int32_t causal, int32_t num_seqs,
  *             tokens).  Any other value counts as -1 and sets
  *             MLA_STATUS_BAD_TREE.
  * All calls only enqueue kernels on `stream` and may be captured into a graph.
+ * No output may overlap an input or another output (but mla_commit_tree moves rows
+ * within its caches).
  *
  * mla_tree_layout: per node t, node i of sequence r,
  *   tree_mask[t]: bit j % 64 of word j / 64 set when node j is i or an ancestor
@@ -733,8 +735,9 @@ int mla_verify_tree(int32_t dtype, int32_t num_tokens, int32_t num_seqs,
 /* mla_commit_tree: per sequence r with n new tokens, for d < num_kept[r], the
  *   cache row of position base + path[r][d] goes to position base + d, base =
  *   seq_lens[r] - n, in every layer; new_seq_lens[r] = base + num_kept[r]
- *   (device int32 [num_seqs], nullable; not seq_lens itself).  All rows are
- *   taken before any is overwritten.
+ *   (device int32 [num_seqs], nullable).  It must not share memory with seq_lens
+ *   (MLA_ERR_INVALID) nor with the call's other integers (MLA_ERR_UNSUPPORTED).
+ *   All rows are taken before any is overwritten.
  *   kv_caches  host array of num_layers device pointers, each [num_blocks,
  *              block_size, L+P] in dtype, 16-byte aligned; no two may
  *              share memory (MLA_ERR_INVALID: rows would move twice).

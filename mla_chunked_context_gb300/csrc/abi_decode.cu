@@ -95,6 +95,12 @@ bool share_memory(void *const *caches, int n, int64_t bytes) {
   return false;
 }
 
+// Do n and m 32-bit integers share memory?
+bool overlap(const int32_t *a, int64_t n, const int32_t *b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + uintptr_t(m) * 4 && y < x + uintptr_t(n) * 4;
+}
+
 // mla_latent_attn, and with a mask mla_tree_attn
 int attend(const mla_dims_t *d, int causal, const TreeMask &tree, int num_seqs,
            const int32_t *query_start_loc, const int32_t *seq_lens, int num_tokens,
@@ -318,13 +324,21 @@ extern "C" int mla_commit_tree(const mla_dims_t *d, int32_t num_seqs, int32_t nu
     return MLA_ERR_INVALID;
   if (num_seqs == 0) return MLA_OK;
   if (!path || !num_kept || !query_start_loc || !seq_lens || !block_table ||
-      (num_layers > 0 && !kv_caches) || new_seq_lens == seq_lens)
+      (num_layers > 0 && !kv_caches) ||
+      (new_seq_lens && overlap(new_seq_lens, num_seqs, seq_lens, num_seqs)))
     return MLA_ERR_INVALID;
   for (int32_t l = 0; l < num_layers; ++l)
     if (!kv_caches[l] || !aligned16(kv_caches[l])) return MLA_ERR_INVALID;
   const int64_t row = int64_t(d->kv_lora_rank + d->qk_rope_dim) * elem_bytes(d->dtype);
   if (num_blocks > 0 && share_memory(kv_caches, num_layers, row * d->block_size * num_blocks))
     return MLA_ERR_INVALID;
+  // blocks of other layers still read these when a sequence's new length is written
+  const int64_t R = num_seqs;
+  if (new_seq_lens &&
+      (overlap(new_seq_lens, R, num_kept, R) || overlap(new_seq_lens, R, query_start_loc, R + 1) ||
+       overlap(new_seq_lens, R, path, R * path_ld) ||
+       overlap(new_seq_lens, R, block_table, R * block_table_stride)))
+    return MLA_ERR_UNSUPPORTED;
   return launch_commit(*d, path, path_ld, num_kept, num_tokens, num_seqs, query_start_loc, seq_lens,
                        kv_caches, num_layers, num_blocks, block_table, block_table_stride,
                        new_seq_lens, dev_status, static_cast<cudaStream_t>(stream));

@@ -1,0 +1,32 @@
+"""Trees of drafted tokens without a GPU: arguments that share memory, and the order
+of TreeDecode's calls."""
+
+import ctypes as C
+
+import pytest
+import torch
+
+import mla_chunked_context_gb300 as M
+from mla_chunked_context_gb300 import _lib
+
+from test_abi_cpu import built_library  # noqa: F401  (builds the library when it is stale)
+from test_decode_cpu import INVALID, UNSUPPORTED, dims
+
+
+def commit(new, R=3, path=1 << 20, path_ld=4, kept=2 << 20, qsl=3 << 20, lens=4 << 20, table=5 << 20, stride=2):
+    arr = (C.c_void_p * 1)(8 << 20)
+    p = C.c_void_p
+    return _lib.lib().mla_commit_tree(C.byref(dims()), R, 3, p(path), path_ld, p(kept), p(qsl), p(lens), arr, 1, 4,
+                                      p(table), stride, p(new), None, None)
+
+
+@pytest.mark.parametrize("at,size,code", [(4 << 20, 3, INVALID), (2 << 20, 3, UNSUPPORTED), (3 << 20, 4, UNSUPPORTED),
+                                          (1 << 20, 12, UNSUPPORTED), (5 << 20, 6, UNSUPPORTED)])
+def test_commit_refuses_new_lengths_over_its_inputs(at, size, code):
+    """Three new lengths over `size` integers: the same, the first or the last one in
+    common; right beside them is no overlap."""
+    for shift in (0, -2, size - 1):
+        assert commit(at + 4 * shift) == code, shift
+    if not torch.cuda.is_available():                # (would launch on these addresses)
+        for shift in (-3, size):
+            assert commit(at + 4 * shift) not in (INVALID, UNSUPPORTED), shift
