@@ -123,6 +123,12 @@ class LatentDecode:
                         self.workspace, o_lat, lse, dev_status, stream)
 
 
+def _capturing(stream) -> bool:
+    import torch
+    with torch.cuda.stream(stream):  # (None: the current one)
+        return torch.cuda.is_current_stream_capturing()
+
+
 class TreeDecode(LatentDecode):
     """LatentDecode for steps whose new tokens are trees of drafts: ``plan``
     once a step, then the call for each layer, ``verify`` with the target's
@@ -144,7 +150,7 @@ class TreeDecode(LatentDecode):
         self.positions = i32(self.max_tokens)
         self.path, self.num_kept = i32(self.max_seqs, int(max_path)), i32(self.max_seqs)
         self.next_tokens = i32(self.max_seqs)
-        self._step = None
+        self._step, self._verified, self._captured = None, False, False
 
     def plan(self, parents, query_start_loc, seq_lens, dev_status=None, stream=None):
         """The step's trees (mla_tree_layout); the layers' calls and verify use
@@ -155,7 +161,7 @@ class TreeDecode(LatentDecode):
                              f"{self.max_tokens} of {self.max_seqs}")
         mla_tree_layout(parents, query_start_loc, seq_lens, self.tree_mask[:T],
                         self.positions[:T], dev_status, stream)
-        self._step = (T, R, parents, query_start_loc, seq_lens)
+        self._step, self._verified = (T, R, parents, query_start_loc, seq_lens), False
 
     def _planned(self):
         if self._step is None:
@@ -186,10 +192,15 @@ class TreeDecode(LatentDecode):
         out = self.path[:R], self.num_kept[:R], self.next_tokens[:R]
         mla_verify_tree(target, draft, tokens, parents, query_start_loc, uniform, uniform_next,
                         *out, dev_status, stream)
+        self._verified = True
+        self._captured = self._captured or _capturing(stream)
         return out
 
     def commit(self, kv_caches, block_table, new_seq_lens=None, dev_status=None, stream=None):
-        """mla_commit_tree of what verify kept, in all layers' caches."""
+        """mla_commit_tree of what verify kept of the planned trees, in all layers'
+        caches.  (A captured verify may have been replayed since the plan.)"""
         T, R, _, query_start_loc, seq_lens = self._planned()
+        if not (self._verified or self._captured):
+            raise ValueError("TreeDecode: verify comes before commit")
         mla_commit_tree(self.dims, self.path[:R], self.num_kept[:R], query_start_loc, seq_lens,
                         kv_caches, block_table, new_seq_lens, T, dev_status, stream)

@@ -30,3 +30,41 @@ def test_commit_refuses_new_lengths_over_its_inputs(at, size, code):
     if not torch.cuda.is_available():                # (would launch on these addresses)
         for shift in (-3, size):
             assert commit(at + 4 * shift) not in (INVALID, UNSUPPORTED), shift
+
+
+def planned(monkeypatch, capturing, max_tokens=4):
+    """A TreeDecode on the CPU whose calls only note that they were made, and the
+    notes."""
+    made = []
+    for name in ("mla_tree_layout", "mla_verify_tree", "mla_commit_tree"):
+        monkeypatch.setattr(M, name, lambda *a, name=name: made.append(name))
+    monkeypatch.setattr(M, "_capturing", lambda stream: capturing)
+    d = M.Dims(2, 64, 16, 32, 32, 16, 0.1, torch.float32)
+    return M.TreeDecode(d, max_tokens, 2, device="cpu"), made
+
+
+def plan(dec):
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    dec.plan(z(3), z(3), z(2))
+
+
+def test_commit_wants_a_verification_of_the_planned_trees(monkeypatch):
+    """Else it would commit the path of the step before."""
+    dec, made = planned(monkeypatch, False)
+    for _ in range(2):
+        plan(dec)
+        with pytest.raises(ValueError, match="verify comes before commit"):
+            dec.commit([], None)
+        dec.verify(None, None)
+        dec.commit([], None)
+        dec.commit([], None)                         # other layers' caches
+    assert made == ["mla_tree_layout", "mla_verify_tree", "mla_commit_tree", "mla_commit_tree"] * 2
+
+
+def test_a_captured_verification_may_be_replayed_between_plan_and_commit(monkeypatch):
+    dec, made = planned(monkeypatch, True)
+    plan(dec)
+    dec.verify(None, None)
+    plan(dec)
+    dec.commit([], None)
+    assert made[-1] == "mla_commit_tree"
