@@ -133,14 +133,18 @@ class TreeDecode(LatentDecode):
     """LatentDecode for steps whose new tokens are trees of drafts: ``plan``
     once a step, then the call for each layer, ``verify`` with the target's
     rows, ``commit``.  It holds what these hand on: the trees' masks and rope
-    positions (nodes up to 64 * mask_words a sequence), the kept paths of up to
-    max_path nodes, num_kept and next_tokens.  All of it is on the device, and a
-    captured step can be replayed with other trees of the same numbers of tokens."""
+    positions, the kept paths of up to max_path nodes, num_kept and next_tokens.
+    Masks have room for 64 * mask_words nodes a sequence; by default for as many as
+    max_tokens and the verification, which looks at 1024, allow.  (What fits fewer
+    is only told by dev_status.)  All of it is on the device, and a captured step can
+    be replayed with other trees of the same numbers of tokens."""
 
-    def __init__(self, dims: Dims, max_tokens: int, max_seqs: int, mask_words: int = 1,
+    def __init__(self, dims: Dims, max_tokens: int, max_seqs: int, mask_words=None,
                  max_path: int = 16, device="cuda"):
         import torch
         super().__init__(dims, max_tokens, max_seqs, device)
+        if mask_words is None:
+            mask_words = max(1, -(-min(self.max_tokens, 1024) // 64))
 
         def i32(*shape):
             return torch.zeros(*shape, dtype=torch.int32, device=device)

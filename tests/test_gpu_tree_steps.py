@@ -1,4 +1,4 @@
-"""TreeDecode's order of calls on the device."""
+"""TreeDecode on the device: its calls' order, trees of more than 64 nodes."""
 
 import numpy as np
 import pytest
@@ -7,8 +7,9 @@ import torch
 import mla_chunked_context_gb300 as M
 from oracle import tree as TR
 
-from test_gpu_decode import DEV, SMALL, _cuda, _no_device_errors, i32, loc, make_cache, make_dims  # noqa: F401
-from test_gpu_tree import drafted, same
+from test_gpu_decode import (DEV, SMALL, _cuda, _no_device_errors, i32, loc, make_cache,  # noqa: F401
+                             make_dims, normal)
+from test_gpu_tree import chain, check_tree, drafted, same, tree
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,24 @@ def test_a_captured_verification_between_an_eager_plan_and_commit(own_stream):
             assert path[r, :kept[r]].tolist() == line and dec.next_tokens[r].item() == nxt
         assert new.tolist() == TR.commit(ref, table.numpy(), qsl, lens, path, kept, 16)
         assert same(cache_d.cpu(), torch.from_numpy(ref).float())
+
+
+def test_a_tree_of_more_than_64_nodes_keeps_its_masks():
+    """Without a word about masks, and a step's attention over them."""
+    rng = np.random.default_rng(4)
+    dims, od = make_dims(SMALL, 2, 16, "f32")
+    L, P, Dn, Dv = SMALL
+    ql, lens = [100, 3], [130, 40]
+    T, qsl = sum(ql), loc(ql)
+    parents = tree(rng, 100) + chain(3)
+    cache, table = make_cache(rng, lens, 16, L + P, dims.dtype)
+    dec, status = M.TreeDecode(dims, T, 2, device=DEV), i32([0])
+    dec.plan(i32(parents), i32(qsl), i32(lens), status)
+    mask, pos = TR.layout(parents, qsl, lens, 2)
+    assert (dec.tree_mask.cpu().numpy() == mask).all() and (dec.positions.cpu().numpy() == pos).all()
+    q, w = normal(rng, T, 2, Dn + P, std=0.5), normal(rng, 2 * (Dn + Dv), L, std=0.1)
+    out, lse = torch.empty(T, 2, Dv, device=DEV), torch.empty(2, T, device=DEV)
+    after = cache.to(DEV)
+    dec(q.to(DEV), normal(rng, T, L + P).to(DEV), None, after, table.to(DEV), w.to(DEV), out, lse, dev_status=status)
+    assert status.item() == 0
+    check_tree(dims, od, qsl, lens, mask, dec.q_latent, after.cpu(), table, dec.o_latent, lse)

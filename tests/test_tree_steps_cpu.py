@@ -68,3 +68,10 @@ def test_a_captured_verification_may_be_replayed_between_plan_and_commit(monkeyp
     plan(dec)
     dec.commit([], None)
     assert made[-1] == "mla_commit_tree"
+
+
+@pytest.mark.parametrize("tokens,words", [(1, 1), (64, 1), (65, 2), (200, 4), (1024, 16), (5000, 16)])
+def test_masks_have_room_for_any_tree_that_is_verified(tokens, words):
+    d = M.Dims(1, 16, 0, 8, 8, 16, 0.1, torch.float32)
+    assert M.TreeDecode(d, tokens, 2, device="cpu").tree_mask.shape == (tokens, words)
+    assert M.TreeDecode(d, tokens, 2, mask_words=3, device="cpu").tree_mask.shape == (tokens, 3)
