@@ -606,8 +606,10 @@ int mla_expand_output(const mla_dims_t *d, const void *o_latent,
  *   q_latent device [T, H, L+P], o_latent device [T, H, L], both in dtype;
  *   lse device float32 [H, T], nullable.  A row that sees no key gets 0 and
  *   -inf.  Cache rows past seq_lens are never used.  A cache row that is not
- *   finite reaches only the tokens that see it: it makes them NaN (or weighs
- *   nothing where its score is -inf).  No output may overlap an input.
+ *   finite reaches only the tokens that see it: it makes o_latent and lse NaN
+ *   where its score is NaN or +inf; where it is -inf, it weighs nothing, but
+ *   columns of o_latent in which the row is infinite may be NaN.  No output may
+ *   overlap an input.
  *   workspace: device, 16-byte aligned, mla_latent_attn_workspace_bytes bytes
  *   (partial results of key ranges: one size for the tensor-core shape,
  *   whatever the batch; 0 bytes and NULL otherwise); nothing in it has to be
@@ -669,8 +671,8 @@ int mla_tree_layout(int32_t num_tokens, int32_t num_seqs,
  *   and new token i of the sequence where bit i of its tree_mask row is set (its
  *   own one too only then; bits past the mask's words count as 0).  Any bits
  *   will do, also such as are no tree's.  Everything else, the workspace
- *   (mla_latent_attn_workspace_bytes) among it, as there; a cache row that is
- *   not finite reaches only the tokens that see it. */
+ *   (mla_latent_attn_workspace_bytes) and rows that are not finite among it, as
+ *   there. */
 int mla_tree_attn(const mla_dims_t *d, int32_t num_seqs,
                   const int32_t *query_start_loc, const int32_t *seq_lens,
                   const uint64_t *tree_mask, int32_t mask_words,

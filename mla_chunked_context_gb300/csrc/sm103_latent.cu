@@ -509,7 +509,7 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
 
 // Keys that some rows of a unit see and others do not: where a value row is not
 // finite, zeros have to stand for it, as a weight of 0 would not hide it.  (The
-// rows that see it are NaN by their scores.)  Which of a tile's keys [from, to)
+// rows that see it are NaN by their scores, or, -inf, weigh it nothing.)  Which of a tile's keys [from, to)
 // are not finite in the 256 columns from byte `col`; by a warp, whose lanes have
 // the cache rows of groups of 2^bl keys in row0, row1.  (Not inlined, like the
 // next: inlined, they cost every tile's loads a little, 1.5% of the whole.)
