@@ -158,7 +158,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 // The same arrive at the default scope: for handing over shared memory of the
 // arriving thread's own CTA that it wrote and passed to the async proxy
 // (fence.proxy.async) before -- the waiter only issues MMAs, which read it
-// through that proxy.  The cluster-scope release costs some 2000 clocks a
+// through that proxy.  (That this scope suffices for the other CTA's waiter is an
+// assumption: PTX states it for the cluster's only.)  The cluster-scope release costs some 2000 clocks a
 // tile in a loop that has nothing else to make visible.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");

@@ -41,11 +41,12 @@
 // takes 3200 (128 sequences of up to 8192 keys, 32 heads: 110 us, 83% of copy
 // bandwidth); pair 1700 with pages of 64 and about 2000 with pages of 16 (24
 // sequences x 4 tokens x 128 heads: 79 us, 52% of the bf16 rate).  The pair's MMAs
-// take 1425 of that.  They, the copies into shared memory (545 lines of 128 bytes
-// a tile) and the softmax (306) want 2040 of its cycles, so these hold the pair
-// form, with one token a sequence too: 128 sequences of 4096 keys take 130 us,
-// their bytes 94.  Where such work lasts, power does: 16 x 4096 keys with trees of
-// 32 nodes, 128 heads, take 445-460 us, 1260-1300 TFLOP/s, at 1370 of 1400 W and
+// alone take 1425 of that.  Counted a tile and CTA, in lines of 128 bytes of shared
+// memory: 1193 by the tensor pipe, 306 by the softmax; the copies write 545 more,
+// whether through the same port is not known.  HBM does not hold the pair form with
+// one token a sequence either: 128 sequences of 4096 keys take 130 us, their bytes
+// 94.  Where such work lasts, power does: 16 x 4096 keys with trees of
+// 32 nodes, 128 heads, take 440-460 us, 1260-1310 TFLOP/s, at 1370 of 1400 W and
 // 1.8 GHz (matrix products of the library keep up 1690 at 1.44 GHz).  Not faster:
 // K in three column groups with barriers of their own (550 us for 437); S and P V
 // with one commit each for all that waits for them; new tokens' rows looked at a
@@ -715,7 +716,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(full_lead + 8 * st);  // (as P is handed on)
+          // As P is handed on: an arrive of CTA scope after the proxy fence, of which
+          // it is taken, beyond what PTX states, that it suffices for the even CTA's
+          // MMAs, as they read this CTA's rows through the async proxy.
+          if (lane == 0) mbar_arrive_remote(full_lead + 8 * st);
         }
         if (!is_v && lane == 0) *progress = g + 1;
       }

@@ -28,13 +28,13 @@
 //
 // Only the rows where a child was rejected and the last node's row are read,
 // one row at a time as each depends on the walk: a call of few sequences is
-// bound by latency (of 10500 clocks for a chain: 2900 to the gathered values,
-// 2200 for the walk, 2600 for the row, 1400 for the cluster's sums, 1400 for the
+// bound by latency (of 11500 clocks for a chain: 3100 to the gathered values,
+// 2500 for the walk, 2700 for the row, 1400 for the cluster's sums, 1500 for the
 // next token; much of each is code fetched for the first time), one of many by
 // its sequence with the most rejections: 64 trees read 119 rows, 20 us of HBM,
-// but one of them 11, a row at some 7000 clocks once the others are done.  (More
-// bytes on their way, by a ring in shared memory or by prefetches, did not
-// shorten that.)  A cluster of 2 to 8 CTAs takes a sequence; each walks the tree
+// but one of them 11, each some 9000 clocks once the others are done (2200 for the
+// walk, 5500 for the row, 1200 for the sums).  (More bytes on their way, by a ring
+// in shared memory or by prefetches, did not shorten that.)  A cluster of 2 to 8 CTAs takes a sequence; each walks the tree
 // by itself (the same numbers, the same steps) over values gathered at the start,
 // sums its part of a row, and tells the others through distributed shared memory.
 // For the next token the sums of CTAs, of warps, then of 32 lanes' 16-byte pieces
@@ -565,9 +565,9 @@ int launch_verify(const void *p, int64_t p_ld, const void *q, int64_t q_ld, int 
   // least: the kernel's stores to a cluster's shared memory fault in a launch that
   // has no clusters (more than 304 sequences each on a CTA of its own).  1024 threads
   // an SM: a CTA has 32 to 8 warps, or 16 at least where 8 would have more than U
-  // pieces a lane each (8 and 16: 64 trees, V 131072 50 and 45 us, 109 chains of 9,
-  // greedy, 98294 49 and 43; 126 trees, 2066 in bf16 14 and 19, 58 single nodes,
-  // 57225 in bf16 5.5 and 8.1).
+  // pieces a lane each (8 and 16: 64 trees, V 131072 55 and 49.5 us, 109 chains of 9,
+  // greedy, 98294 86 and 70; 126 trees of 9, 2066 in bf16 15.7 and 20, 58 single
+  // nodes, 57225 in bf16 7.4 and 10.5, 1000 trees of 5, 2066 26 and 45).
   const int sms = num_sms();
   while (2 << a.cluster_log2 <= MAX_CLUSTER && (int64_t(R) * 2 << a.cluster_log2) <= 4 * sms)
     ++a.cluster_log2;
