@@ -15,7 +15,7 @@ from test_gpu_decode import (F, LARGE, SMALL, _cuda, _no_device_errors, f64, loc
                              normal, run_attn, unit, within)
 from test_gpu_tree import chain, run_tree, tree
 
-pytestmark = pytest.mark.gpu
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
 
 
 def attend(q, cache, table, sees, r, od):

@@ -1,4 +1,5 @@
-"""TreeDecode on the device: its calls' order, trees of more than 64 nodes."""
+"""Steps of trees on the device: the order of TreeDecode's calls, trees of more than
+64 nodes, calls of many sequences."""
 
 import numpy as np
 import pytest
@@ -7,9 +8,9 @@ import torch
 import mla_chunked_context_gb300 as M
 from oracle import tree as TR
 
-from test_gpu_decode import (DEV, SMALL, _cuda, _no_device_errors, i32, loc, make_cache,  # noqa: F401
-                             make_dims, normal)
-from test_gpu_tree import chain, check_tree, drafted, same, tree
+from test_gpu_decode import (DEV, LARGE, SMALL, _cuda, _no_device_errors, i32, loc,  # noqa: F401
+                             make_cache, make_dims, normal)
+from test_gpu_tree import chain, check_tree, drafted, run_tree, same, tree
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,41 @@ def test_a_tree_of_more_than_64_nodes_keeps_its_masks():
     dec(q.to(DEV), normal(rng, T, L + P).to(DEV), None, after, table.to(DEV), w.to(DEV), out, lse, dev_status=status)
     assert status.item() == 0
     check_tree(dims, od, qsl, lens, mask, dec.q_latent, after.cpu(), table, dec.o_latent, lse)
+
+
+@pytest.mark.parametrize("H,bs", [(48, 64), (48, 16), (4, 64)])
+def test_attention_of_more_sequences_than_a_block_has_threads(H, bs):
+    """500 sequences, some without tokens: pairs (72 rows a sequence) and single CTAs."""
+    rng = np.random.default_rng(H + bs)
+    dims, od = make_dims(LARGE, H, bs, "bf16")
+    ql = [int(x) for x in rng.integers(0, 4, size=500)]
+    lens = [int(x) for x in rng.integers(3, 150, size=500)]
+    qsl = loc(ql)
+    mask, _ = TR.layout(sum((tree(rng, n) for n in ql), []), qsl, lens, 1)
+    cache, table = make_cache(rng, lens, bs, 576, dims.dtype)
+    q = normal(rng, qsl[-1], H, 576, std=0.4, dtype=dims.dtype)
+    o, lse = run_tree(dims, qsl, lens, mask, q, cache, table)
+    check_tree(dims, od, qsl, lens, mask, q, cache, table, o, lse)
+
+
+def test_layout_and_commit_of_many_sequences():
+    rng = np.random.default_rng(12)
+    dims, _ = make_dims(SMALL, 1, 16, "f32")
+    R = 3000
+    ql, lens = [int(x) for x in rng.integers(0, 9, R)], [int(x) for x in rng.integers(9, 40, R)]
+    qsl, parents = loc(ql), sum((tree(rng, n) for n in ql), [])
+    mask, pos = torch.zeros(qsl[-1], 1, dtype=torch.int64, device=DEV), i32([0] * qsl[-1])
+    M.mla_tree_layout(i32(parents), i32(qsl), i32(lens), mask, pos)
+    ref, rpos = TR.layout(parents, qsl, lens, 1)
+    assert (mask.cpu().numpy() == ref).all() and (pos.cpu().numpy() == rpos).all()
+    paths = [TR.ancestors(parents[qsl[r]:qsl[r + 1]])[-1] if n else [] for r, n in enumerate(ql)]
+    paths = [p if not p or p[0] == 0 else [0] for p in paths]
+    path = torch.tensor([p + [-1] * (8 - len(p)) for p in paths], dtype=torch.int32)
+    kept = [len(p) for p in paths]
+    cache, table = make_cache(rng, lens, 16, SMALL[0] + SMALL[1], dims.dtype)
+    layers, new = [cache.to(DEV), (cache + 1).to(DEV)], i32([0] * R)
+    M.mla_commit_tree(dims, path.to(DEV), i32(kept), i32(qsl), i32(lens), layers, table.to(DEV), new)
+    for got, first in zip(layers, (cache, cache + 1)):
+        want = first.numpy().copy()
+        assert new.tolist() == TR.commit(want, table.numpy(), qsl, lens, path.numpy(), kept, 16)
+        assert same(got.cpu(), torch.from_numpy(want))
